@@ -57,7 +57,7 @@
 extern "C" {
 #endif
 
-#define NVFP4_ABI_VERSION 6
+#define NVFP4_ABI_VERSION 7
 
 /* Exported symbols: the library builds with hidden visibility by default. */
 #if defined(NVFP4_BUILD) && defined(__GNUC__)
@@ -89,6 +89,21 @@ typedef enum nvfp4_status {
 /* nvfp4_prepare_weights flags */
 #define NVFP4_PREP_PLAIN 0
 #define NVFP4_PREP_W13_INTERLEAVE 1 /* rows [0,N/2) gate, [N/2,N) up -> 64 gate + 64 up per 128 */
+
+/* element types of the 16-bit and fp32 operands of the dense feed-forward operators */
+#define NVFP4_DT_BF16 0
+#define NVFP4_DT_FP16 1
+#define NVFP4_DT_FP32 2
+
+/* activations of nvfp4_gated_linear */
+#define NVFP4_ACT_SILU 0      /* g / (1 + exp(-g))                                         */
+#define NVFP4_ACT_GELU 1      /* g Phi(g), Phi the normal distribution function (erf)      */
+#define NVFP4_ACT_GELU_TANH 2 /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2           */
+
+/* gates of nvfp4_residual_norm */
+#define NVFP4_GATE_NONE 0
+#define NVFP4_GATE_CHANNEL 1 /* (groups, K): one value per channel of M / groups rows      */
+#define NVFP4_GATE_ROW 2     /* (M): one value per row                                     */
 
 /* device fault flags returned by nvfp4_get_device_error */
 #define NVFP4_DEVERR_BAD_EXPERT_ID 1  /* a top-k id outside [0, E); the entry was dropped  */
@@ -360,6 +375,95 @@ NVFP4_API nvfp4_status nvfp4_moe_w2(int64_t T, int64_t H, int64_t I, int64_t E, 
 NVFP4_API nvfp4_status nvfp4_moe_finalize(int64_t T, int64_t H, int64_t I, int64_t E, int topk,
                                 int has_shared, void *y, void *ws, size_t ws_bytes,
                                 void *stream);
+
+/* ============================================================================
+ * Dense feed-forward operators around the experts: an 8-bit block-scaled linear, a gated
+ * linear with its gradients, and the norms, gate and residual sum between two blocks with
+ * their gradients.  The conventions above hold (device pointers, no allocation, caller's
+ * workspace, programmatic dependent launch, 16-byte aligned pointers); element types are
+ * given by NVFP4_DT_*.  No input may overlap an output unless a call says so.  M, N, K, T, H
+ * and I are below 2^24, a product of two of them below 2^40.
+ * ============================================================================ */
+
+/* ------------------------------------------- FP8 block-scaled linear (128)
+ * e4m3 operands with fp32 scales: one per 128 consecutive K elements of a row of x, one per
+ * 128 x 128 block of W (the last block of a row or column may be partial).
+ *   s = fl32(max |x| / 448) over the block, q = e4m3_rne_satfinite(fl32(x / s)), q = 0 if s == 0
+ *   y[m, n] = sum_b xs[b, m] w_s[n / 128, b] sum_{k in b} q[m, k] w[n, k]       (fp32 sums)
+ * A block that holds a NaN or an infinity makes every output of its rows NaN.
+ * x (M, K), row stride ldx (a multiple of 8), bf16 or fp16; q (M, K) codes, contiguous;
+ * xs (ceil(K / 128), lds) fp32, xs[b * lds + m], lds >= M a multiple of 4 (every row,
+ * the last included, is readable up to M rounded up to 4; entries m >= M are not written and do not
+ * matter); w (N, K) codes and w_s (ceil(N / 128), ceil(K / 128)), both
+ * row-major as checkpoints store them: no preparation.  y (M, N) contiguous in `dtype`.
+ * K % 16 == 0; any N; K % 16 == 0 for the weight quantiser too (ldw a multiple of 8). */
+NVFP4_API nvfp4_status nvfp4_fp8_quantize_act(const void *x, int dtype, int64_t M, int64_t K, int64_t ldx,
+                                              uint8_t *q, float *xs, int64_t lds, void *stream);
+NVFP4_API nvfp4_status nvfp4_fp8_quantize_weight(const void *w, int dtype, int64_t N, int64_t K, int64_t ldw,
+                                                 uint8_t *q, float *w_s, void *stream);
+NVFP4_API nvfp4_status nvfp4_fp8_gemm(const uint8_t *xq, const float *xs, int64_t lds, int64_t M, int64_t K,
+                                      int64_t N, const uint8_t *w, const float *w_s, int dtype, void *y,
+                                      void *stream);
+/* The quantiser and the product in one call; the workspace holds the codes and scales. */
+NVFP4_API size_t nvfp4_fp8_linear_workspace_bytes(int64_t M, int64_t K);
+NVFP4_API nvfp4_status nvfp4_fp8_linear(const void *x, int dtype, int64_t M, int64_t K, int64_t ldx, int64_t N,
+                                        const uint8_t *w, const float *w_s, void *y, void *ws, size_t ws_bytes,
+                                        void *stream);
+
+/* ------------------------------------------------------------ gated linear
+ * h = act(x Wg^T) * (x Wu^T): both projections, the activation and the product in one kernel.
+ * x (T, H), row stride ldx (a multiple of 8); w_gate and w_up (I, H) contiguous; h (T, I)
+ * contiguous; all bf16 or all fp16 (`dtype`).  gu, if not NULL, receives the fp32
+ * pre-activations (T, 2I), g in columns [0, I) and u in [I, 2I): the input of the backward.
+ * H % 8 == 0, I % 8 == 0. */
+NVFP4_API nvfp4_status nvfp4_gated_linear(const void *x, int dtype, int64_t T, int64_t H, int64_t ldx, int64_t I,
+                                          const void *w_gate, const void *w_up, int act, void *h, float *gu,
+                                          void *stream);
+/* Gradients of h: dg = dh u act'(g) and du = dh act(g), rounded to `dtype`, then
+ *   dx = dg Wg + du Wu (T, H),  dw_gate = dg^T x (I, H),  dw_up = du^T x (I, H)
+ * with fp32 sums, contiguous, in `dtype`.  dx may be NULL, and dw_gate and dw_up may both be
+ * NULL: that product is then left out.  dh (T, I) has row stride lddh (a multiple of 8).
+ * With T == 0 the weight gradients are zero.  Workspace: [dg | du]. */
+NVFP4_API size_t nvfp4_gated_linear_backward_workspace_bytes(int64_t T, int64_t I);
+NVFP4_API nvfp4_status nvfp4_gated_linear_backward(const void *dh, int64_t lddh, const void *x, int64_t ldx,
+                                                   int dtype, int64_t T, int64_t H, int64_t I,
+                                                   const void *w_gate, const void *w_up, int act, const float *gu,
+                                                   void *dx, void *dw_gate, void *dw_up, void *ws,
+                                                   size_t ws_bytes, void *stream);
+
+/* ----------------------------------------------------------- residual norm
+ * The boundary between two blocks of a layer: the norm after the block, its gate and residual
+ * scale, the residual sum, and the norm before the next block.  Per row, in fp32:
+ *   n = f rstd(f) gamma_after        (n = f if gamma_after is NULL)
+ *   r_out = r + scale gate n
+ *   y = r_out rstd(r_out) gamma_before   (from r_out before its rounding; none if NULL)
+ * with rstd(v) = 1 / sqrt(mean(v^2) + eps).  f (M, K) with row stride ldf, gammas (K) and the gate
+ * in `dtype` (bf16 or fp16); r (M, K) with row stride ldr and r_out (M, K) contiguous in
+ * `r_dtype`: `dtype` or fp32.  gate_kind NVFP4_GATE_CHANNEL: gate (gate_groups, K) contiguous, row
+ * m uses gate[m / (M / gate_groups)], M % gate_groups == 0; NVFP4_GATE_ROW: gate (M).
+ * y (M, K) contiguous in `dtype`.  stats, if not NULL: fp32 (M, 2) = rstd(f), rstd(r_out) (0 where
+ * a norm is absent), the input of the backward.  r_out may be r (same stride K).
+ * K % 8 == 0, K <= 16384; row strides a multiple of 8. */
+NVFP4_API nvfp4_status nvfp4_residual_norm(const void *f, int dtype, const void *r, int r_dtype, int64_t M,
+                                           int64_t K, int64_t ldf, int64_t ldr, const void *gamma_after,
+                                           const void *gate, int gate_kind, int64_t gate_groups, float scale,
+                                           const void *gamma_before, float eps, void *r_out, void *y,
+                                           float *stats, void *stream);
+/* Gradients, from the gradients dr_out of r_out (r_dtype, row stride lddr) and dy of y (dtype, row
+ * stride lddy); either may be NULL (zero).  f, r, the parameters and stats are the forward's.
+ * df (M, K) in dtype, dr (M, K) in r_dtype, contiguous; dgamma_after (K), dgamma_before (K) and
+ * dgate (the gate's shape) in fp32, each sum over rows in a fixed order; each of the three may be
+ * NULL, and has to be where its parameter is absent.  With M == 0 the parameter gradients are zero. */
+NVFP4_API size_t nvfp4_residual_norm_backward_workspace_bytes(int64_t M, int64_t K, int64_t gate_groups,
+                                                              int r_dtype);
+NVFP4_API nvfp4_status nvfp4_residual_norm_backward(const void *dr_out, int64_t lddr, const void *dy, int64_t lddy,
+                                                    const void *f, int dtype, const void *r, int r_dtype,
+                                                    int64_t M, int64_t K, int64_t ldf, int64_t ldr,
+                                                    const float *stats, const void *gamma_after, const void *gate,
+                                                    int gate_kind, int64_t gate_groups, float scale,
+                                                    const void *gamma_before, void *df, void *dr,
+                                                    float *dgamma_after, float *dgate, float *dgamma_before,
+                                                    void *ws, size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------ diagnostics
  * Runs one CTA that waits on a shared-memory barrier nothing arrives at, with

@@ -35,9 +35,18 @@ DEVERR_BAD_EXPERT_ID = 1
 DEVERR_PIPELINE_TIMEOUT = 2
 DEVERR_INTERNAL = 4
 LINEAR_NOALLOC_MAX_BYTES = 4 << 20
+DT_BF16 = 0
+DT_FP16 = 1
+DT_FP32 = 2
+ACT_SILU = 0
+ACT_GELU = 1
+ACT_GELU_TANH = 2
+GATE_NONE = 0
+GATE_CHANNEL = 1
+GATE_ROW = 2
 
 
-ABI_VERSION = 6  # NVFP4_ABI_VERSION of the header these signatures follow
+ABI_VERSION = 7  # NVFP4_ABI_VERSION of the header these signatures follow
 
 
 class MoeWsLayout(Structure):
@@ -80,6 +89,20 @@ _SIGNATURES = {
     "nvfp4_moe_w13": (c_int, [I64, I64, I64, I64, c_int, P, P, P, P, P, P, P, P, P, P, c_size_t, P]),
     "nvfp4_moe_w2": (c_int, [I64, I64, I64, I64, c_int, P, P, P, P, P, P, P, P, P, c_size_t, P]),
     "nvfp4_moe_finalize": (c_int, [I64, I64, I64, I64, c_int, c_int, P, P, c_size_t, P]),
+    "nvfp4_fp8_quantize_act": (c_int, [P, c_int, I64, I64, I64, P, P, I64, P]),
+    "nvfp4_fp8_quantize_weight": (c_int, [P, c_int, I64, I64, I64, P, P, P]),
+    "nvfp4_fp8_gemm": (c_int, [P, P, I64, I64, I64, I64, P, P, c_int, P, P]),
+    "nvfp4_fp8_linear_workspace_bytes": (c_size_t, [I64, I64]),
+    "nvfp4_fp8_linear": (c_int, [P, c_int, I64, I64, I64, I64, P, P, P, P, c_size_t, P]),
+    "nvfp4_gated_linear": (c_int, [P, c_int, I64, I64, I64, I64, P, P, c_int, P, P, P]),
+    "nvfp4_gated_linear_backward_workspace_bytes": (c_size_t, [I64, I64]),
+    "nvfp4_gated_linear_backward": (c_int, [P, I64, P, I64, c_int, I64, I64, I64, P, P, c_int, P, P, P, P, P, c_size_t,
+                                            P]),
+    "nvfp4_residual_norm": (c_int, [P, c_int, P, c_int, I64, I64, I64, I64, P, P, c_int, I64, c_float, P, c_float, P, P,
+                                    P, P]),
+    "nvfp4_residual_norm_backward_workspace_bytes": (c_size_t, [I64, I64, I64, c_int]),
+    "nvfp4_residual_norm_backward": (c_int, [P, I64, P, I64, P, c_int, P, c_int, I64, I64, I64, I64, P, P, P, c_int,
+                                             I64, c_float, P, P, P, P, P, P, P, c_size_t, P]),
     "nvfp4_debug_wait_timeout": (c_int, [c_uint32, P]),
 }
 

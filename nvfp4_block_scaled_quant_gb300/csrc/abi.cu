@@ -7,14 +7,13 @@
 #include <cstring>
 #include <mutex>
 
-#include "internal.h"
+#include "abi_util.h"
 
 namespace nvfp4 {
-namespace {
 
 // ---------------------------------------------------------------- error reporting
 
-thread_local char g_last_error[512] = "";
+static thread_local char g_last_error[512] = "";
 
 nvfp4_status fail(nvfp4_status st, const char *fn, const char *fmt, ...) {
   int n = std::snprintf(g_last_error, sizeof(g_last_error), "%s: ", fn);
@@ -30,32 +29,13 @@ nvfp4_status cuda_fail(const char *fn, cudaError_t e, const char *what) {
   return fail(NVFP4_ERR_CUDA, fn, "%s: %s", what, cudaGetErrorString(e));
 }
 
-#define NV_REQUIRE(cond, status, ...) \
-  do {                                \
-    if (!(cond)) return fail(status, __func__, __VA_ARGS__); \
-  } while (0)
-
-#define NV_CUDA(expr, what)                          \
-  do {                                               \
-    cudaError_t e_ = (expr);                         \
-    if (e_ != cudaSuccess) return cuda_fail(__func__, e_, what); \
-  } while (0)
-
-bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
 // ---------------------------------------------------------------- per-device state
 
-__device__ uint32_t g_device_flags;
+static __device__ uint32_t g_device_flags;
 
 constexpr int kMaxDevices = 64;
-struct DeviceInfo {
-  bool ready = false;
-  bool supported = false;
-  int sms = 0;
-  uint32_t *flags = nullptr;
-};
-DeviceInfo g_dev[kMaxDevices];
-std::mutex g_dev_mutex;
+static DeviceInfo g_dev[kMaxDevices];
+static std::mutex g_dev_mutex;
 
 nvfp4_status device_info(const char *fn, DeviceInfo **out) {
   int dev = 0;
@@ -94,7 +74,7 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t
                                   const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-nvfp4_status get_encoder(const char *fn, EncodeTiledFn *out) {
+static nvfp4_status get_encoder(const char *fn, EncodeTiledFn *out) {
   static EncodeTiledFn encode = nullptr;
   static std::once_flag once;
   static cudaError_t err = cudaSuccess;
@@ -109,11 +89,9 @@ nvfp4_status get_encoder(const char *fn, EncodeTiledFn *out) {
   return NVFP4_OK;
 }
 
-// 2-D byte tensor (rows x row_bytes, row stride ld_bytes) read in boxes of
-// 128 bytes x box_rows with the 128-byte swizzle.
 nvfp4_status make_map(const char *fn, CUtensorMap *m, const void *base, int64_t row_bytes,
-                      int64_t rows, int64_t ld_bytes, int box_rows, int box_bytes = 128,
-                      CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B) {
+                      int64_t rows, int64_t ld_bytes, int box_rows, int box_bytes,
+                      CUtensorMapSwizzle swizzle) {
   EncodeTiledFn encode;
   nvfp4_status st = get_encoder(fn, &encode);
   if (st != NVFP4_OK) return st;
@@ -130,6 +108,8 @@ nvfp4_status make_map(const char *fn, CUtensorMap *m, const void *base, int64_t 
   return NVFP4_OK;
 }
 
+namespace {
+
 // Prepared (tile-major) weights of rows x K: blocks of 128 rows x 128 bytes, read through a
 // map of 128-byte rows with 128-row boxes.
 nvfp4_status make_weight_map(const char *fn, CUtensorMap *m, const void *w, int64_t rows, int64_t K) {
@@ -143,9 +123,6 @@ nvfp4_status make_weight_slice_map(const char *fn, CUtensorMap *m, const void *w
   const int64_t slabs = (K / 2 + 127) / 128;
   return make_map(fn, m, w, 128, rows * slabs, 128, 128, 32, CU_TENSOR_MAP_SWIZZLE_32B);
 }
-
-size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
-int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
 size_t sf_bytes(int64_t rows, int64_t K) {
   return static_cast<size_t>(round_up(rows, 128)) * static_cast<size_t>(round_up(K / 16, 4));
@@ -218,6 +195,8 @@ nvfp4_status check_moe_shape(const char *fn, int64_t T, int64_t H, int64_t I, in
   return NVFP4_OK;
 }
 
+}  // namespace
+
 nvfp4_status check_ws(const char *fn, const void *ws, size_t ws_bytes, size_t need) {
   if (ws_bytes < need)
     return fail(NVFP4_ERR_WORKSPACE, fn, "workspace of %zu bytes, %zu needed", ws_bytes, need);
@@ -225,6 +204,8 @@ nvfp4_status check_ws(const char *fn, const void *ws, size_t ws_bytes, size_t ne
   if (!aligned(ws, 256)) return fail(NVFP4_ERR_MISALIGNED, fn, "workspace must be 256-byte aligned");
   return NVFP4_OK;
 }
+
+namespace {
 
 template <typename T>
 T *at(void *ws, size_t off) {

@@ -1,0 +1,431 @@
+// Tensor-bound GEMM on CTA pairs (tcgen05 cta_group::2) shared by the FP8 block-scaled linear
+// and the gated linear's forward and backward products.
+//
+// One output tile per pair has 256 rows (128 per CTA, the lanes of its tensor memory) and 256
+// accumulator columns.  A K block is 128 bytes of every operand row: each CTA stages 128 rows of A
+// and 128 rows of B per block (32 KB), a ring of kTStages blocks deep.  A one-SM tile of 128 x 256
+// would stage 48 KB for the same work: the L2 -> SM operand stream is what bounds tiles of this
+// size, so the pair's sharing of B matters.
+//
+// Warps of each CTA: 0 = TMA producer, 1 = MMA issuer (the even CTA's, for both), 2..9 = epilogue
+// (two per 32-lane quarter of tensor memory, 128 columns each).
+//
+//   Op::kFp8    A = xq (M, K) e4m3, B = wq (N, K) e4m3.  The scales change every 128 K, so every K
+//               block is a product of its own: the issuer alternates between two accumulators, and
+//               the epilogue warps add block * (sa[m, b] * sw[n / 128, b]) to fp32 registers (128
+//               columns per thread) while the next block runs.  Scaling in registers keeps the
+//               scales arbitrary fp32 values; nothing is rounded until the output.
+//   Op::kGated  A = x (M, K), B = 128 rows of Wg (even CTA) and the matching 128 of Wu (odd CTA):
+//               columns 0..127 of the accumulator are g, 128..255 u of the same outputs.
+//   Op::kDx     A = [dg | du] in two segments of K = I, B = Wg, then Wu, read along their rows
+//               (MN-major B): dx = dg Wg + du Wu.
+//   Op::kDw     A = [dg | du]^T (MN-major), B = x^T (MN-major), K = tokens: rows 0..I-1 are dWg,
+//               rows I..2I-1 dWu.
+//
+// Every wait is bounded: a role that gives up raises NVFP4_DEVERR_PIPELINE_TIMEOUT, the copies in
+// flight are given time to land, and every thread of the pair meets at the final cluster barrier.
+#pragma once
+
+#include <atomic>
+
+#include "mma16x8.cuh"
+
+namespace nvfp4 {
+
+enum class TileOp : int { kFp8 = 0, kGated = 1, kDx = 2, kDw = 3 };
+
+struct TileArgs {
+  int M, N;        // output rows and columns (kGated: N = I; kDw: M = 2I, N = H)
+  int k_blocks;    // 128-byte K blocks of one segment
+  int segments;    // 1, or 2 (kDx)
+  const float *sa; // kFp8: (K blocks, ld_sa) activation scales
+  int64_t ld_sa;
+  const float *sw; // kFp8: (ceil(N / 128), K blocks) weight scales
+  void *out;       // 16-bit (M, N), row stride ldo; kDw: dWg
+  void *out2;      // kDw: dWu
+  int64_t ldo;
+  float *save;     // kGated: fp32 (M, 2N) pre-activations [g | u], or null
+  uint32_t *err;
+};
+
+constexpr int kTRows = 256, kTCols = 256, kTHalf = 128;
+constexpr int kTStages = 6;
+constexpr int kTOperandBytes = kTHalf * 128;  // 16 KiB: 128 rows x 128 bytes
+constexpr int kTStageBytes = 2 * kTOperandBytes;
+constexpr int kTEpiWarps = 8;
+constexpr int kTThreads = (2 + kTEpiWarps) * 32;
+constexpr size_t kTSmem = 1024 + static_cast<size_t>(kTStages) * kTStageBytes + 256;
+constexpr uint32_t kTTmemCols = 512;  // two accumulators of 256 columns
+constexpr int kTGroupM = 8;           // m tiles walked together, so that a wave shares rows of B in L2
+static_assert(kTSmem <= 232448, "per-block shared memory limit");
+static_assert((2 * kTStages + 4) * 8 + 8 <= 256, "barrier region");
+
+template <TileOp kOp, class T, int kAct>
+__global__ void __launch_bounds__(kTThreads, 1)
+    tile_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
+                     const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
+                     const TileArgs args) {
+  constexpr bool kFp8 = kOp == TileOp::kFp8;
+  constexpr bool kAMn = kOp == TileOp::kDw;
+  constexpr bool kBMn = kOp == TileOp::kDw || kOp == TileOp::kDx;
+  constexpr int kOutCols = kOp == TileOp::kGated ? kTHalf : kTCols;  // output columns of a tile
+  constexpr uint32_t kFmt = kFp8 ? 0u : (T::kCode == NVFP4_DT_BF16 ? 1u : 0u);
+  constexpr uint32_t kIdesc = mma_idesc(kFmt, kAMn, kBMn, kTRows, kTCols);
+
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                              ~static_cast<uintptr_t>(1023));
+  uint8_t *sA = smem;
+  uint8_t *sB = sA + kTStages * kTOperandBytes;
+  uint64_t *full = reinterpret_cast<uint64_t *>(sB + kTStages * kTOperandBytes);  // used in the even CTA
+  uint64_t *empty = full + kTStages;
+  uint64_t *tfull = empty + kTStages;   // [2]
+  uint64_t *tempty = tfull + 2;         // [2], used in the even CTA
+  uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(tempty + 2);
+  volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kTStages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&tfull[b], 1);
+      mbar_init(&tempty[b], 2 * kTEpiWarps);
+    }
+    *abort_flag = 0;
+    fence_barrier_init();
+  }
+  if (warp == 0 && lane == 0) {
+    prefetch_tensormap(&tmA0);
+    prefetch_tensormap(&tmB0);
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(tmem_holder, kTTmemCols);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are initialised and their tensor memory allocated
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  pdl_wait();
+  pdl_trigger();
+
+  const int m_tiles = (args.M + kTRows - 1) / kTRows;
+  const int n_tiles = (args.N + kOutCols - 1) / kOutCols;
+  const int total = m_tiles * n_tiles;
+  const int k_blocks = args.k_blocks * args.segments;
+  const int clusters = static_cast<int>(gridDim.x) / 2, cluster_id = static_cast<int>(blockIdx.x) / 2;
+  // after a wait that gave up: the time that copies and MMAs in flight need, many times over
+  auto settle = [] {
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 10000000ull) {
+    }
+  };
+  auto tile_at = [&](int idx, int &mt, int &nt) {
+    const int per_group = kTGroupM * n_tiles, g = idx / per_group, in = idx - g * per_group;
+    const int rows = min(kTGroupM, m_tiles - g * kTGroupM);
+    nt = in / rows;
+    mt = g * kTGroupM + (in - nt * rows);
+  };
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ TMA producer
+      const uint64_t pol = policy_evict_normal();
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int idx = cluster_id; ok && idx < total; idx += clusters) {
+        int mt, nt;
+        tile_at(idx, mt, nt);
+        const int a_row = mt * kTRows + static_cast<int>(rank) * kTHalf;
+        const int b_row = kOp == TileOp::kGated ? nt * kTHalf : nt * kTCols + static_cast<int>(rank) * kTHalf;
+        const CUtensorMap *mapA = &tmA0, *mapB = kOp == TileOp::kGated && rank ? &tmB1 : &tmB0;
+        int kb = 0, seg = 0;
+        for (int it = 0; it < k_blocks; ++it, ++kb) {
+          if (kOp == TileOp::kDx && kb == args.k_blocks) {
+            kb = 0;
+            seg = 1;
+          }
+          if (kOp == TileOp::kDx && seg) {
+            mapA = &tmA1;
+            mapB = &tmB1;
+          }
+          if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, args.err, kPipelineTimeoutNs)) {
+            ok = false;
+            break;
+          }
+          // both CTAs' copies complete on the even CTA's barrier, which expects all of them
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kTStageBytes);
+          const uint32_t bar = cluster_addr(&full[stage], 0);
+          uint8_t *a = sA + stage * kTOperandBytes, *b = sB + stage * kTOperandBytes;
+          if constexpr (kAMn) {  // 64 K rows of 64 elements, two boxes side by side along M
+            tma_load_2d_pair(a, mapA, a_row * 2, kb * 64, bar, pol);
+            tma_load_2d_pair(a + 8192, mapA, a_row * 2 + 128, kb * 64, bar, pol);
+          } else {
+            tma_load_2d_pair(a, mapA, kb * 128, a_row, bar, pol);
+          }
+          if constexpr (kBMn) {
+            tma_load_2d_pair(b, mapB, b_row * 2, kb * 64, bar, pol);
+            tma_load_2d_pair(b + 8192, mapB, b_row * 2 + 128, kb * 64, bar, pol);
+          } else {
+            tma_load_2d_pair(b, mapB, kb * 128, b_row, bar, pol);
+          }
+          if (++stage == kTStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      if (!ok) settle();  // copies in flight may complete on the other CTA's barrier
+    }
+  } else if (warp == 1) {
+    if (rank == 0 && lane == 0) {
+      // ------------------------------------------------------------ MMA issuer
+      const uint32_t a0 = smem_u32(sA), b0 = smem_u32(sB);
+      // K-major rows of 128 bytes: 8-row groups 1024 bytes apart, a K step is 32 bytes on.
+      // MN-major boxes (64 elements x 64 K rows): boxes 8192 bytes apart along MN, 8-K groups 1024
+      // bytes apart, a K step of 16 rows is 2048 bytes on.
+      constexpr uint32_t kAStep = kAMn ? 2048 / 16 : 32 / 16, kBStep = kBMn ? 2048 / 16 : 32 / 16;
+      int stage = 0;
+      uint32_t phase = 0;
+      uint32_t acc = 0;  // accumulators handed to the epilogue so far
+      bool ok = true;
+      for (int idx = cluster_id; ok && idx < total; idx += clusters) {
+        for (int it = 0; it < k_blocks; ++it) {
+          const uint32_t buf = acc & 1;
+          if ((kFp8 || it == 0) &&
+              !mbar_wait_bounded_cluster(&tempty[buf], ((acc >> 1) & 1) ^ 1, abort_flag, args.err, kPipelineTimeoutNs)) {
+            ok = false;
+            break;
+          }
+          if (!mbar_wait_bounded_cluster(&full[stage], phase, abort_flag, args.err, kPipelineTimeoutNs)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t ad = smem_desc(a0 + stage * kTOperandBytes, kAMn ? 8192 : 16, 1024, 2);
+          const uint64_t bd = smem_desc(b0 + stage * kTOperandBytes, kBMn ? 8192 : 16, 1024, 2);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            tc_mma<kFp8, true>(tmem_base + buf * kTCols, ad + j * kAStep, bd + j * kBStep, kIdesc,
+                               kFp8 ? j != 0 : (it | j) != 0);
+          tc_commit_pair(&empty[stage], 0x3);
+          if (kFp8 || it == k_blocks - 1) {
+            tc_commit_pair(&tfull[buf], 0x3);
+            ++acc;
+          }
+          if (++stage == kTStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        }
+      }
+      // every MMA issued has completed before the pair frees its tensor memory: the last commits
+      // arrive on tfull, which this thread follows to the end
+      if (!ok) {
+        settle();
+      } else if (acc) {
+        volatile int never = 0;
+        mbar_wait_bounded(&tfull[(acc - 1) & 1], ((acc - 1) >> 1) & 1, &never, nullptr, 100000000ull);
+      }
+    }
+  } else {
+    // -------------------------------------------------------------- epilogue
+    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const uint32_t tempty_leader = cluster_addr(tempty, 0);
+    const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
+    uint32_t acc = 0;
+    bool ok = true;
+    auto wait_acc = [&]() {
+      ok = mbar_wait_bounded(&tfull[acc & 1], (acc >> 1) & 1, abort_flag, args.err, kPipelineTimeoutNs);
+      ok = __all_sync(0xffffffffu, ok);
+      tc_fence_after();
+      return ok;
+    };
+    auto release = [&]() {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster_relaxed(tempty_leader + (acc & 1) * 8);
+      ++acc;
+    };
+    const bool vec = (args.ldo & 7) == 0;
+    for (int idx = cluster_id; ok && idx < total; idx += clusters) {
+      int mt, nt;
+      tile_at(idx, mt, nt);
+      const int row = mt * kTRows + static_cast<int>(rank) * kTHalf + quarter * 32 + lane;
+      const bool row_ok = row < args.M;
+      if constexpr (kFp8) {
+        const int n0 = nt * kTCols + half * kTHalf;
+        // scales of the next K block are fetched one block ahead; a half past N is computed on zeros
+        const float *sa = args.sa + row;
+        const float *sw = args.sw + static_cast<int64_t>(min(n0, args.N - 1) / 128) * k_blocks;
+        float next_a = row_ok ? __ldg(sa) : 0.f, next_w = __ldg(sw);
+        uint64_t sum[64];
+#pragma unroll
+        for (int i = 0; i < 64; ++i) sum[i] = 0;
+        for (int kb = 0; kb < k_blocks; ++kb) {
+          const float f = next_a * next_w;
+          const uint64_t f2 = pack_f32x2(f, f);
+          if (kb + 1 < k_blocks) {
+            next_a = row_ok ? __ldg(sa + (kb + 1) * args.ld_sa) : 0.f;
+            next_w = __ldg(sw + kb + 1);
+          }
+          if (!wait_acc()) break;
+          const uint32_t t = lanes + (acc & 1) * kTCols + half * kTHalf;
+          uint32_t r[2][16];
+          tmem_ld16(t, r[0]);
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            tmem_ld_wait();
+            if (c < 7)
+              tmem_ld16(t + (c + 1) * 16, r[(c + 1) & 1]);
+            else
+              release();
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              sum[c * 8 + i] = fma_f32x2(pack_f32x2(__uint_as_float(r[c & 1][2 * i]), __uint_as_float(r[c & 1][2 * i + 1])),
+                                         f2, sum[c * 8 + i]);
+          }
+        }
+        if (!ok) break;
+        if (row_ok) {
+          uint16_t *dst = static_cast<uint16_t *>(args.out) + row * args.ldo + n0;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) unpack_f32x2(sum[c * 8 + i], v[2 * i], v[2 * i + 1]);
+            store16<T>(dst + c * 16, v, args.N - n0 - c * 16, vec);
+          }
+        }
+      } else if constexpr (kOp == TileOp::kGated) {
+        if (!wait_acc()) break;
+        const int n0 = nt * kTHalf + half * 64;
+        const uint32_t t = lanes + (acc & 1) * kTCols + half * 64;
+        uint16_t *dst = static_cast<uint16_t *>(args.out) + row * args.ldo + n0;
+        float *save = args.save ? args.save + static_cast<int64_t>(row) * 2 * args.N + n0 : nullptr;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t g[16], u[16];
+          tmem_ld16(t + c * 16, g);
+          tmem_ld16(t + kTHalf + c * 16, u);
+          tmem_ld_wait();
+          if (c == 3) release();
+          const int left = args.N - n0 - c * 16;
+          if (row_ok && left > 0) {
+            float h[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) h[i] = act_fwd<kAct>(__uint_as_float(g[i])) * __uint_as_float(u[i]);
+            store16<T>(dst + c * 16, h, left, vec);
+            if (save) {  // N % 8 == 0: whole groups of 4 columns exist or do not
+#pragma unroll
+              for (int i = 0; i < 16; i += 4)
+                if (i < left) {
+                  *reinterpret_cast<uint4 *>(save + c * 16 + i) = make_uint4(g[i], g[i + 1], g[i + 2], g[i + 3]);
+                  *reinterpret_cast<uint4 *>(save + args.N + c * 16 + i) = make_uint4(u[i], u[i + 1], u[i + 2], u[i + 3]);
+                }
+            }
+          }
+          __syncwarp();
+        }
+      } else {
+        if (!wait_acc()) break;
+        const int n0 = nt * kTCols + half * kTHalf;
+        const uint32_t t = lanes + (acc & 1) * kTCols + half * kTHalf;
+        uint16_t *dst = static_cast<uint16_t *>(args.out) + row * args.ldo + n0;
+        if constexpr (kOp == TileOp::kDw) {  // rows I..2I-1 belong to the second output
+          const int split = args.M / 2;
+          if (row >= split) dst = static_cast<uint16_t *>(args.out2) + (row - split) * args.ldo + n0;
+        }
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t r[16];
+          tmem_ld16(t + c * 16, r);
+          tmem_ld_wait();
+          if (c == 7) release();
+          float v[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+          if (row_ok) store16<T>(dst + c * 16, v, args.N - n0 - c * 16, vec);
+        }
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // the pair's MMAs have drained and both epilogues have read their accumulators
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem_base, kTTmemCols);
+}
+
+// Clusters of two that fit on the current device at once (0 if the query fails), and the launch.
+template <class K>
+int tile_gemm_max_clusters(K kernel) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kTSmem)) !=
+      cudaSuccess)
+    return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * 1024);
+  cfg.blockDim = dim3(kTThreads);
+  cfg.dynamicSmemBytes = kTSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess) return 0;
+  return n;
+}
+
+template <TileOp kOp, class T, int kAct>
+cudaError_t launch_tile_gemm_as(const CUtensorMap &a0, const CUtensorMap &a1, const CUtensorMap &b0,
+                                const CUtensorMap &b1, const TileArgs &args, cudaStream_t s) {
+  auto kernel = tile_gemm_kernel<kOp, T, kAct>;
+  static std::atomic<int> fit[64];  // per device; the kernel's shared-memory limit is set with the query
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  int n = fit[dev].load();
+  if (n <= 0) {
+    n = tile_gemm_max_clusters(kernel);
+    if (n <= 0) {
+      const cudaError_t last = cudaGetLastError();
+      return last != cudaSuccess ? last : cudaErrorLaunchOutOfResources;
+    }
+    fit[dev].store(n);
+  }
+  const int out_cols = kOp == TileOp::kGated ? kTHalf : kTCols;
+  const int64_t tiles = ((static_cast<int64_t>(args.M) + kTRows - 1) / kTRows) *
+                        ((static_cast<int64_t>(args.N) + out_cols - 1) / out_cols);
+  // a balanced grid: every wave of tiles, the last included, is (nearly) full
+  const int64_t waves = (tiles + n - 1) / n;
+  const int clusters = static_cast<int>((tiles + waves - 1) / waves);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * clusters);
+  cfg.blockDim = dim3(kTThreads);
+  cfg.dynamicSmemBytes = kTSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, a0, a1, b0, b1, args);
+}
+
+}  // namespace nvfp4

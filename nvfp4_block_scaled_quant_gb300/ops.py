@@ -287,6 +287,278 @@ def moe_finalize(T: int, topk: int, W: MoEWeights, y, workspace, stream=None):
          workspace.numel(), _stream(stream))
 
 
+# --------------------------------------------------------------------------- dense feed-forward operators
+#
+# The operators around the experts: bf16 or fp16 tensors, rows with any stride that is a multiple of
+# 8 elements where a call says "strided rows", everything else contiguous.  They keep no autograd
+# graph: a backward pass is its own call.  With ``stream`` given, outputs and scratch are allocated
+# for that stream and the inputs are marked as used on it.
+
+_DT = {torch.bfloat16: _lib.DT_BF16, torch.float16: _lib.DT_FP16}
+_ACT = {"silu": _lib.ACT_SILU, "gelu": _lib.ACT_GELU, "gelu_tanh": _lib.ACT_GELU_TANH}
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+class _Place:
+    """The device of a call's tensors (all the same) as the current one, and its stream."""
+
+    def __init__(self, stream, *tensors: Optional[torch.Tensor]):
+        first = tensors[0]
+        for t in tensors:
+            if t is None:
+                continue
+            if not t.is_cuda:
+                raise ValueError("nvfp4 ops take CUDA tensors only (no CPU fallback)")
+            if t.device != first.device:
+                raise ValueError("tensors on different devices")
+        self.device = first.device
+        self._guards = []
+        if first.get_device() != torch.cuda.current_device():
+            self._guards.append(torch.cuda.device(first.device))
+        if stream is not None:
+            if stream.device != first.device:
+                raise ValueError("stream of another device")
+            self._guards.append(torch.cuda.stream(stream))
+            for t in tensors:
+                if t is not None:
+                    t.record_stream(stream)
+
+    def __enter__(self):
+        for g in self._guards:
+            g.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *exc):
+        for g in reversed(self._guards):
+            g.__exit__(*exc)
+
+
+def _kind(x: torch.Tensor, what: str) -> int:
+    d = _DT.get(x.dtype)
+    if d is None:
+        raise ValueError(f"{what} must be bf16 or fp16, got {x.dtype}")
+    return d
+
+
+def _ld(t: torch.Tensor, what: str, rows: Optional[int] = None, cols: Optional[int] = None, dtype=None) -> int:
+    """Row stride of a 2-D tensor of strided rows (a single row's stride does not matter)."""
+    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected ({rows if rows is not None else 'rows'}, "
+                         f"{cols if cols is not None else 'columns'})")
+    if dtype is not None and t.dtype != dtype:
+        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
+    if t.stride(1) != 1 and t.shape[1] > 1:
+        raise ValueError(f"{what}: the elements of a row must be contiguous")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+def _whole(t: torch.Tensor, what: str, shape, dtypes) -> int:
+    """Data pointer of a contiguous tensor of the given shape and type."""
+    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes:
+        raise ValueError(f"{what} has shape {tuple(t.shape)} and type {t.dtype}, expected {tuple(shape)} {dtypes}")
+    if not t.is_contiguous():
+        raise ValueError(f"{what} must be contiguous")
+    return t.data_ptr()
+
+
+def fp8_quantize_act(x: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """x (M, K) strided rows -> (q (M, K) float8_e4m3fn, s (ceil(K / 128), M) fp32).
+
+    One scale per 128 consecutive K elements of a row, s = max|x| / 448, q = e4m3(x / s).  s is a view
+    of rows padded to a multiple of four, as ``fp8_gemm`` wants them.  K % 16 == 0.
+    """
+    with _Place(stream, x) as st:
+        ld = _ld(x, "x")
+        M, K = x.shape
+        q = torch.empty(M, K, dtype=torch.float8_e4m3fn, device=x.device)
+        lds = (M + 3) // 4 * 4
+        s = torch.empty((K + 127) // 128, lds, dtype=torch.float32, device=x.device)
+        call("nvfp4_fp8_quantize_act", x.data_ptr(), _kind(x, "x"), M, K, ld, q.data_ptr(), s.data_ptr(), lds, st)
+        return q, s[:, :M]
+
+
+def fp8_quantize_weight(w: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """w (N, K) strided rows -> (q (N, K) float8_e4m3fn, s (ceil(N / 128), ceil(K / 128)) fp32): one
+    scale per 128 x 128 block, the layout checkpoints store.  Once, at load time.  K % 16 == 0."""
+    with _Place(stream, w) as st:
+        ld = _ld(w, "w")
+        N, K = w.shape
+        q = torch.empty(N, K, dtype=torch.float8_e4m3fn, device=w.device)
+        s = torch.empty((N + 127) // 128, (K + 127) // 128, dtype=torch.float32, device=w.device)
+        call("nvfp4_fp8_quantize_weight", w.data_ptr(), _kind(w, "w"), N, K, ld, q.data_ptr(), s.data_ptr(), st)
+        return q, s
+
+
+def _fp8_weight(w: torch.Tensor, w_s: torch.Tensor, K: int) -> Tuple[int, int, int]:
+    if w.dim() != 2:
+        raise ValueError("w must be 2-D")
+    N = w.shape[0]
+    return (N, _whole(w, "w", (N, K), _CODES),
+            _whole(w_s, "w_s", ((N + 127) // 128, (K + 127) // 128), (torch.float32,)))
+
+
+def fp8_gemm(xq: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, w_s: torch.Tensor, dtype=torch.bfloat16,
+             out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y (M, N) = deq(xq) deq(w)^T of quantised activations (``fp8_quantize_act``) and weights, in
+    bf16 or fp16; the scales apply to fp32 sums of one 128-wide K block each."""
+    with _Place(stream, xq, xs, w, w_s, out) as st:
+        if xq.dim() != 2 or xs.dim() != 2:
+            raise ValueError("xq and xs must be 2-D")
+        M, K = xq.shape
+        N, wp, wsp = _fp8_weight(w, w_s, K)
+        KB = (K + 127) // 128
+        lds = xs.stride(0) if KB > 1 else max(xs.stride(0), (M + 3) // 4 * 4)
+        room = xs.untyped_storage().nbytes() // 4 - xs.storage_offset()
+        if xs.dtype != torch.float32 or tuple(xs.shape) != (KB, M) or (M > 1 and xs.stride(1) != 1):
+            raise ValueError(f"xs must be fp32 ({KB}, {M}) with contiguous rows")
+        if M and room < (KB - 1) * lds + (M + 3) // 4 * 4:
+            raise ValueError("the rows of xs must be padded to a multiple of four scales")
+        if dtype not in _DT:
+            raise ValueError(f"output type {dtype}")
+        y = out if out is not None else torch.empty(M, N, dtype=dtype, device=xq.device)
+        call("nvfp4_fp8_gemm", _whole(xq, "xq", (M, K), _CODES), xs.data_ptr(), lds, M, K, N, wp, wsp, _DT[dtype],
+             _whole(y, "out", (M, N), (dtype,)), st)
+        return y
+
+
+def fp8_linear(x: torch.Tensor, w: torch.Tensor, w_s: torch.Tensor, out: Optional[torch.Tensor] = None,
+               workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y (M, N) = deq(quantize(x)) deq(w)^T in x's type: x (M, K) strided rows, w (N, K) e4m3 codes
+    with w_s (ceil(N / 128), ceil(K / 128)) fp32 scales as checkpoints store them."""
+    with _Place(stream, x, w, w_s, out, workspace) as st:
+        ld = _ld(x, "x")
+        M, K = x.shape
+        N, wp, wsp = _fp8_weight(w, w_s, K)
+        y = out if out is not None else torch.empty(M, N, dtype=x.dtype, device=x.device)
+        n = int(lib().nvfp4_fp8_linear_workspace_bytes(M, K))
+        ws = workspace if workspace is not None else _u8(n, device=x.device)
+        call("nvfp4_fp8_linear", x.data_ptr(), _kind(x, "x"), M, K, ld, N, wp, wsp,
+             _whole(y, "out", (M, N), (x.dtype,)), _whole(ws, "workspace", (ws.numel(),), (torch.uint8,)), ws.numel(),
+             st)
+        return y
+
+
+def _gated_args(x, w_gate, w_up, activation):
+    if activation not in _ACT:
+        raise ValueError(f"activation {activation!r}, expected one of {sorted(_ACT)}")
+    ld = _ld(x, "x")
+    if w_gate.dim() != 2:
+        raise ValueError("w_gate must be 2-D")
+    T, H = x.shape
+    I = w_gate.shape[0]
+    return (T, H, I, ld, _kind(x, "x"), _whole(w_gate, "w_gate", (I, H), (x.dtype,)),
+            _whole(w_up, "w_up", (I, H), (x.dtype,)), _ACT[activation])
+
+
+def gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, activation: str = "silu",
+                 save: bool = False, out: Optional[torch.Tensor] = None, stream=None):
+    """h (T, I) = act(x w_gate^T) * (x w_up^T): x (T, H) strided rows, weights (I, H), one type.
+
+    ``activation``: "silu", "gelu" (erf) or "gelu_tanh".  With ``save`` returns (h, gu), gu (T, 2I) the
+    fp32 pre-activations [g | u] that ``gated_linear_backward`` takes.  H % 8 == 0, I % 8 == 0.
+    """
+    with _Place(stream, x, w_gate, w_up, out) as st:
+        T, H, I, ld, kind, gp, up, act = _gated_args(x, w_gate, w_up, activation)
+        h = out if out is not None else torch.empty(T, I, dtype=x.dtype, device=x.device)
+        gu = torch.empty(T, 2 * I, dtype=torch.float32, device=x.device) if save else None
+        call("nvfp4_gated_linear", x.data_ptr(), kind, T, H, ld, I, gp, up, act, _whole(h, "out", (T, I), (x.dtype,)),
+             _ptr(gu), st)
+        return (h, gu) if save else h
+
+
+def gated_linear_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
+                          gu: torch.Tensor, activation: str = "silu", need_dx: bool = True, need_dw: bool = True,
+                          workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients (dx (T, H), dw_gate (I, H), dw_up (I, H)) of ``gated_linear`` from dh (T, I) strided
+    rows and the saved gu; those not asked for are None."""
+    with _Place(stream, x, dh, w_gate, w_up, gu, workspace) as st:
+        T, H, I, ld, kind, gp, up, act = _gated_args(x, w_gate, w_up, activation)
+        lddh = _ld(dh, "dh", T, I, x.dtype)
+        gup = _whole(gu, "gu", (T, 2 * I), (torch.float32,))
+        dx = torch.empty(T, H, dtype=x.dtype, device=x.device) if need_dx else None
+        dwg = torch.empty(I, H, dtype=x.dtype, device=x.device) if need_dw else None
+        dwu = torch.empty(I, H, dtype=x.dtype, device=x.device) if need_dw else None
+        n = int(lib().nvfp4_gated_linear_backward_workspace_bytes(T, I))
+        ws = workspace if workspace is not None else _u8(n, device=x.device)
+        call("nvfp4_gated_linear_backward", dh.data_ptr(), lddh, x.data_ptr(), ld, kind, T, H, I, gp, up, act, gup,
+             _ptr(dx), _ptr(dwg), _ptr(dwu), _whole(ws, "workspace", (ws.numel(),), (torch.uint8,)), ws.numel(), st)
+        return dx, dwg, dwu
+
+
+def _norm_args(f, r, gamma_after, gate, gamma_before):
+    ldf, kind = _ld(f, "f"), _kind(f, "f")
+    M, K = f.shape
+    if r.dtype != f.dtype and r.dtype != torch.float32:
+        raise ValueError(f"r must be {f.dtype} or fp32, got {r.dtype}")
+    ldr = _ld(r, "r", M, K)
+    rkind = _lib.DT_FP32 if r.dtype == torch.float32 else kind
+    ga = None if gamma_after is None else _whole(gamma_after, "gamma_after", (K,), (f.dtype,))
+    gb = None if gamma_before is None else _whole(gamma_before, "gamma_before", (K,), (f.dtype,))
+    if gate is None:
+        return M, K, ldf, ldr, kind, rkind, ga, None, _lib.GATE_NONE, 0, gb
+    if gate.dim() == 2 and tuple(gate.shape) == (M, 1):
+        return M, K, ldf, ldr, kind, rkind, ga, _whole(gate, "gate", (M, 1), (f.dtype,)), _lib.GATE_ROW, 0, gb
+    groups = 1 if gate.dim() == 1 else gate.shape[0]
+    gp = _whole(gate, "gate", (K,) if gate.dim() == 1 else (groups, K), (f.dtype,))
+    if groups == 0 or M % groups:
+        raise ValueError(f"{M} rows do not split into {groups} groups")
+    return M, K, ldf, ldr, kind, rkind, ga, gp, _lib.GATE_CHANNEL, groups, gb
+
+
+def residual_norm(f: torch.Tensor, r: torch.Tensor, gamma_after: Optional[torch.Tensor] = None,
+                  gate: Optional[torch.Tensor] = None, scale: float = 1.0,
+                  gamma_before: Optional[torch.Tensor] = None, eps: float = 1e-6, save: bool = False,
+                  out: Optional[torch.Tensor] = None, stream=None):
+    """The boundary between two blocks: returns (r_out, y), with ``save`` (r_out, y, stats).
+
+    n = rmsnorm(f; gamma_after) (f without gamma_after), r_out = r + scale * gate * n, y =
+    rmsnorm(r_out; gamma_before) from the unrounded sum (None without gamma_before).  f (M, K) and r
+    (M, K; f's type or fp32) strided rows; gate (K,), (groups, K) for M / groups consecutive rows each,
+    or (M, 1).  ``out`` receives r_out and may be r.  K % 8 == 0, K <= 16384.
+    """
+    with _Place(stream, f, r, gamma_after, gate, gamma_before, out) as st:
+        M, K, ldf, ldr, kind, rkind, ga, gp, gkind, groups, gb = _norm_args(f, r, gamma_after, gate, gamma_before)
+        r_out = out if out is not None else torch.empty(M, K, dtype=r.dtype, device=f.device)
+        y = torch.empty(M, K, dtype=f.dtype, device=f.device) if gb is not None else None
+        stats = torch.empty(M, 2, dtype=torch.float32, device=f.device) if save else None
+        call("nvfp4_residual_norm", f.data_ptr(), kind, r.data_ptr(), rkind, M, K, ldf, ldr, ga, gp, gkind, groups, scale,
+             gb, eps, _whole(r_out, "out", (M, K), (r.dtype,)), _ptr(y), _ptr(stats), st)
+        return (r_out, y, stats) if save else (r_out, y)
+
+
+def residual_norm_backward(dr_out: Optional[torch.Tensor], dy: Optional[torch.Tensor], f: torch.Tensor,
+                           r: torch.Tensor, stats: torch.Tensor, gamma_after: Optional[torch.Tensor] = None,
+                           gate: Optional[torch.Tensor] = None, scale: float = 1.0,
+                           gamma_before: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                           workspace: Optional[torch.Tensor] = None, stream=None):
+    """Gradients (df, dr, dgamma_after, dgate, dgamma_before) of ``residual_norm``; the parameters' are
+    fp32 in their own shapes, None where the parameter is absent.
+
+    dr_out (r's type) and dy (f's type) are the gradients of r_out and y, strided rows; either may be
+    None (zero).  The other arguments are the forward's (eps is already in ``stats``).
+    """
+    with _Place(stream, f, r, dr_out, dy, stats, gamma_after, gate, gamma_before, workspace) as st:
+        M, K, ldf, ldr, kind, rkind, ga, gp, gkind, groups, gb = _norm_args(f, r, gamma_after, gate, gamma_before)
+        if dy is not None and gb is None:
+            raise ValueError("dy without gamma_before")
+        lddr = K if dr_out is None else _ld(dr_out, "dr_out", M, K, r.dtype)
+        lddy = K if dy is None else _ld(dy, "dy", M, K, f.dtype)
+        sp = _whole(stats, "stats", (M, 2), (torch.float32,))
+        df = torch.empty(M, K, dtype=f.dtype, device=f.device)
+        dr = torch.empty(M, K, dtype=r.dtype, device=f.device)
+
+        def grad(p):
+            return None if p is None else torch.empty(p.shape, dtype=torch.float32, device=f.device)
+
+        dga, dgate, dgb = grad(gamma_after), grad(gate), grad(gamma_before)
+        n = int(lib().nvfp4_residual_norm_backward_workspace_bytes(M, K, max(groups, 1), rkind))
+        ws = workspace if workspace is not None else _u8(n, device=f.device)
+        call("nvfp4_residual_norm_backward", _ptr(dr_out), lddr, _ptr(dy), lddy, f.data_ptr(), kind, r.data_ptr(), rkind,
+             M, K, ldf, ldr, sp, ga, gp, gkind, groups, scale, gb, df.data_ptr(), dr.data_ptr(), _ptr(dga), _ptr(dgate),
+             _ptr(dgb), _whole(ws, "workspace", (ws.numel(),), (torch.uint8,)), ws.numel(), st)
+        return df, dr, dga, dgate, dgb
+
+
 # --------------------------------------------------------------------------- diagnostics
 
 def device_error(stream=None) -> Tuple[int, int]:
