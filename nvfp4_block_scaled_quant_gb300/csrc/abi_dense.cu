@@ -400,6 +400,7 @@ nvfp4_status nvfp4_residual_norm(const void *f, int dtype, const void *r, int r_
   a.stats = stats;
   a.M = M;
   a.K = static_cast<int>(K);
+  a.err = d->flags;
   NV_CUDA(launch_residual_norm(a, dtype, r_dtype == NVFP4_DT_FP32, d->sms, static_cast<cudaStream_t>(stream)),
           "residual norm launch");
   return NVFP4_OK;

@@ -329,6 +329,7 @@ struct NormArgs {
   float *stats;               // (M, 2) rstd(f), rstd(r'), or null
   int64_t M;
   int K;
+  uint32_t *err;
 };
 struct NormGradArgs {
   const void *dr_out, *dy;    // or null
@@ -354,8 +355,9 @@ struct NormGradPlan {
   int slices, slice_cols, threads, stages, parts, ctas, smem;
 };
 constexpr int64_t kNormMaxK = 16384;
-constexpr int kNormSlice = 8192;     // columns of a CTA in the backward (8 per thread)
-constexpr int kNormMaxSlices = 2;
+constexpr int kNormGradThreads = 896; // threads of a backward CTA: 72 registers each
+constexpr int kNormSlice = 8 * kNormGradThreads;  // columns of a backward CTA (8 per thread)
+constexpr int kNormMaxSlices = 3;    // ceil(kNormMaxK / kNormSlice)
 constexpr int kNormMaxStages = 4;
 constexpr int kNormMaxSmem = 225 * 1024;
 constexpr int kNormSms = 152;        // the plan must not depend on the device: it sizes the workspace

@@ -42,17 +42,33 @@ struct Fp16 {
 };
 
 // 16 fp32 values -> 16 elements at dst, of which the first `left` exist; vec: dst is 16-byte aligned.
+// A 32-byte aligned dst takes one 256-bit store (a whole sector per lane).
 template <class T>
 __device__ __forceinline__ void store16(uint16_t *dst, const float (&v)[16], int left, bool vec) {
   if (vec && left >= 16) {
-    uint4 *d = reinterpret_cast<uint4 *>(dst);
-    d[0] = make_uint4(T::pack(v[0], v[1]), T::pack(v[2], v[3]), T::pack(v[4], v[5]), T::pack(v[6], v[7]));
-    d[1] = make_uint4(T::pack(v[8], v[9]), T::pack(v[10], v[11]), T::pack(v[12], v[13]), T::pack(v[14], v[15]));
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = T::pack(v[2 * i], v[2 * i + 1]);
+    if ((reinterpret_cast<uintptr_t>(dst) & 31) == 0) {
+      st_global_v8(dst, w);
+    } else {
+      uint4 *d = reinterpret_cast<uint4 *>(dst);
+      d[0] = make_uint4(w[0], w[1], w[2], w[3]);
+      d[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < 16; ++i)
       if (i < left) dst[i] = T::one(v[i]);
   }
+}
+
+// A read-only load that stays where it is written: an ordinary load may be moved down to its first
+// use, which undoes a prefetch.
+__device__ __forceinline__ float ld_early(const float *p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
 }
 
 // ---------------------------------------------------------------- packed fp32
@@ -84,7 +100,28 @@ __device__ __forceinline__ void tma_load_2d_pair(void *smem_dst, const CUtensorM
       : "memory");
 }
 
+// 32 lanes x 32 consecutive 32-bit columns: thread i receives lane (base lane + i).
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32"
+      " {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23,"
+      " %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+
 // ---------------------------------------------------------------- MMA
+
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred P;\n\telect.sync _|P, 0xffffffff;\n\tselp.u32 %0, 1, 0, P;\n\t}" : "=r"(p));
+  return p != 0;
+}
 
 // Instruction descriptor of kind::f16 and kind::f8f6f4: fp32 accumulator, operand format
 // `fmt` on both sides (f16: 0 = fp16, 1 = bf16; f8f6f4: 0 = e4m3), MN-major flags, M and N.

@@ -56,6 +56,32 @@ struct Res {
   }
 };
 
+// The same four elements at a time.
+template <class T, bool kF32>
+struct Four {
+  static __device__ __forceinline__ void load(const void *p, int64_t i, float (&v)[4]) {
+    if constexpr (kF32) {
+      const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+    } else {
+      const uint2 a = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
+      v[0] = T::lo(a.x), v[1] = T::hi(a.x), v[2] = T::lo(a.y), v[3] = T::hi(a.y);
+    }
+  }
+  static __device__ __forceinline__ void store(void *p, int64_t i, const float (&v)[4]) {
+    if constexpr (kF32)
+      *reinterpret_cast<float4 *>(static_cast<float *>(p) + i) = make_float4(v[0], v[1], v[2], v[3]);
+    else
+      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + i) = make_uint2(T::pack(v[0], v[1]), T::pack(v[2], v[3]));
+  }
+};
+// Element i of four packed 16-bit values.
+template <class T>
+__device__ __forceinline__ float at4(const uint2 w, int i) {
+  const uint32_t x = i < 2 ? w.x : w.y;
+  return (i & 1) ? T::hi(x) : T::lo(x);
+}
+
 // 8 values of an optional 16-bit row vector, `otherwise` where it is absent.
 template <class T>
 __device__ __forceinline__ void load_opt(const uint16_t *p, int i, float otherwise, float (&v)[8]) {
@@ -86,16 +112,21 @@ __device__ __forceinline__ float block_sum(float v, float *red) {
   return warp_sum(lane < warps ? red[lane] : 0.f);
 }
 
+// The group of rows that row m belongs to (row counts are below 2^24).
+__device__ __forceinline__ uint32_t group_of(int64_t m, int64_t rows_per_group) {
+  return static_cast<uint32_t>(m) / static_cast<uint32_t>(rows_per_group);
+}
+
 __device__ __forceinline__ float rstd_of(float sum, int K, float eps) {
   return __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(sum, static_cast<float>(K)) + eps));
 }
 
 // ---------------------------------------------------------------- forward
 
-// A row per CTA at a time; kChunks groups of 8 columns per thread stay in registers over both
-// reductions, so memory is read once.
+// Few rows: one row per CTA, kChunks groups of 8 columns per thread, in registers over both
+// reductions.
 template <class T, bool kR32, int kChunks>
-__global__ void __launch_bounds__(kChunks == 4 ? 512 : 1024, 1) residual_norm_kernel(const NormArgs a) {
+__global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const NormArgs a) {
   __shared__ float red[2][32];
   pdl_wait();
   pdl_trigger();
@@ -108,7 +139,7 @@ __global__ void __launch_bounds__(kChunks == 4 ? 512 : 1024, 1) residual_norm_ke
       gm *= T::up(__ldg(gate + m));
       gate = nullptr;
     } else if (gate) {
-      gate += m / a.rows_per_group * a.K;
+      gate += static_cast<int64_t>(group_of(m, a.rows_per_group)) * a.K;
     }
     uint4 fv[kChunks];
     float rv[kChunks][8];
@@ -176,19 +207,133 @@ __global__ void __launch_bounds__(kChunks == 4 ? 512 : 1024, 1) residual_norm_ke
   }
 }
 
+// Many rows: each CTA walks its rows through a ring in shared memory (one bulk copy per row and
+// tensor), so the next rows load while this one passes its two reductions.  16 columns per thread
+// and two CTAs per SM at most widths: one CTA's reductions overlap the other's.
+template <class T, bool kR32, int kChunks>
+__global__ void __launch_bounds__(1024, 1) residual_norm_rows_kernel(const NormArgs a, int stages) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) &
+                                              ~static_cast<uintptr_t>(127));
+  __shared__ float red[2][32];
+  __shared__ uint64_t full[kNormMaxStages];
+  __shared__ int s_abort;
+  volatile int *abort_flag = &s_abort;
+  const int chunks = a.K / 8, nt = static_cast<int>(blockDim.x), tid = static_cast<int>(threadIdx.x);
+  const uint32_t n16 = static_cast<uint32_t>(a.K) * 2u, nr = static_cast<uint32_t>(a.K) * Res<T, kR32>::kBytes;
+  const uint32_t stage_bytes = n16 + nr;
+  if (tid == 0) {
+    for (int s = 0; s < stages; ++s) mbar_init(&full[s], 1);
+    s_abort = 0;
+    fence_barrier_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  pdl_trigger();
+  const uint64_t pol = policy_evict_first();
+  auto load_row = [&](int64_t m, int s) {
+    mbar_arrive_expect_tx(&full[s], stage_bytes);
+    uint8_t *d = smem + s * stage_bytes;
+    bulk_load(d, static_cast<const uint16_t *>(a.f) + m * a.ldf, n16, &full[s], pol);
+    bulk_load(d + n16, static_cast<const uint8_t *>(a.r) + m * a.ldr * Res<T, kR32>::kBytes, nr, &full[s], pol);
+  };
+  const int64_t step = gridDim.x;
+  if (tid == 0)
+    for (int s = 0; s < stages && blockIdx.x + s * step < a.M; ++s) load_row(blockIdx.x + s * step, s);
+  int s = 0;
+  uint32_t phase = 0;
+  const uint16_t *gate0 = static_cast<const uint16_t *>(a.gate);
+  float next_gm = a.gate_kind == NVFP4_GATE_ROW && blockIdx.x < a.M ? T::up(__ldg(gate0 + blockIdx.x)) : 1.f;
+  for (int64_t m = blockIdx.x; m < a.M; m += step) {
+    const float gm = a.scale * next_gm;
+    if (a.gate_kind == NVFP4_GATE_ROW && m + step < a.M) next_gm = T::up(__ldg(gate0 + m + step));
+    const uint16_t *gate = a.gate_kind == NVFP4_GATE_CHANNEL ? gate0 + static_cast<int64_t>(group_of(m, a.rows_per_group)) * a.K : nullptr;
+    // a wait that gives up raises the fault flag; every barrier below is still met
+    mbar_wait_bounded(&full[s], phase, abort_flag, a.err, kPipelineTimeoutNs);
+    const uint8_t *d = smem + s * stage_bytes;
+    float v[kChunks][8];
+    float sum = 0.f;
+    float ia = 1.f;
+    if (a.ga) {
+#pragma unroll
+      for (int u = 0; u < kChunks; ++u) {
+        const int c = tid + u * nt;
+        if (c < chunks) {
+          Res<T, false>::load(d, c * 8, v[u]);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sum += v[u][i] * v[u][i];
+        }
+      }
+      ia = rstd_of(block_sum(sum, red[0]), a.K, a.eps);
+    }
+    sum = 0.f;
+#pragma unroll
+    for (int u = 0; u < kChunks; ++u) {
+      const int c = tid + u * nt;
+      if (c < chunks) {
+        float x[8], w[8];
+        if (!a.ga) Res<T, false>::load(d, c * 8, v[u]);
+        load_opt<T>(static_cast<const uint16_t *>(a.ga), c * 8, 1.f, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[u][i] *= ia * w[i];
+        load_opt<T>(gate, c * 8, 1.f, w);
+        Res<T, kR32>::load(d + n16, c * 8, x);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          v[u][i] = x[i] + gm * w[i] * v[u][i];
+          sum += v[u][i] * v[u][i];
+        }
+        Res<T, kR32>::store(a.r_out, m * a.ldr_out + c * 8, v[u]);
+      }
+    }
+    float ib = 0.f;
+    if (a.gb) {
+      ib = rstd_of(block_sum(sum, red[1]), a.K, a.eps);  // its barrier: every thread has read the stage
+    } else {
+      __syncthreads();
+    }
+    if (tid == 0 && m + stages * step < a.M) load_row(m + stages * step, s);
+    if (++s == stages) {
+      s = 0;
+      phase ^= 1;
+    }
+    if (a.gb) {
+#pragma unroll
+      for (int u = 0; u < kChunks; ++u) {
+        const int c = tid + u * nt;
+        if (c < chunks) {
+          float gb[8];
+          load_opt<T>(static_cast<const uint16_t *>(a.gb), c * 8, 1.f, gb);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[u][i] *= ib * gb[i];
+          Res<T, false>::store(a.y, m * a.K + c * 8, v[u]);
+        }
+      }
+      // red[1] is written again only after the next row's first barrier, or this one without ga
+      if (!a.ga) __syncthreads();
+    }
+    if (a.stats && tid == 0) *reinterpret_cast<float2 *>(a.stats + 2 * m) = make_float2(a.ga ? ia : 0.f, ib);
+  }
+  if (*abort_flag) {  // copies in flight land before the CTA's memory goes
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 10000000ull) {
+    }
+  }
+}
+
 // ---------------------------------------------------------------- backward
 
 // Rows stream through a ring in shared memory (one bulk copy per row and tensor), so the next rows
 // load while this one is reduced; registers hold the parameter gradients.  A row of more than
 // kNormSlice columns is split over the CTAs of a cluster, which exchange the three sums.
-constexpr int kNbRedFloats = 3 * 32;
+constexpr int kNbRedFloats = 4 * 32;  // three sums of up to 32 warps each, and a row of zeros
 
 template <class T, bool kR32>
-__global__ void __launch_bounds__(1024, 1) residual_norm_backward_kernel(const NormGradArgs a) {
+__global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_kernel(const NormGradArgs a) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) &
                                               ~static_cast<uintptr_t>(127));
-  __shared__ float red[2][kNbRedFloats];
+  __shared__ __align__(16) float red[2][kNbRedFloats];
   __shared__ float peer_sums[2][kNormMaxSlices][3];
   __shared__ uint64_t full[kNormMaxStages];
   __shared__ int s_abort;
@@ -196,9 +341,10 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_backward_kernel(const N
 
   const int slice = static_cast<int>(blockIdx.x) % a.slices, part = static_cast<int>(blockIdx.x) / a.slices;
   const int k0 = slice * a.slice_cols, cols = min(a.slice_cols, a.K - k0);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = static_cast<int>(blockDim.x) >> 5;
-  const int c = static_cast<int>(threadIdx.x) * 8;  // this thread's columns of the slice
-  const bool live = c < cols;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // this thread's columns of the slice: two groups of four, each contiguous over the block
+  const int col[2] = {static_cast<int>(threadIdx.x) * 4, static_cast<int>(blockDim.x + threadIdx.x) * 4};
+  const bool live[2] = {col[0] < cols, col[1] < cols};
   // ring stage: f, dy (16 bits), r, dr' (16 or 32 bits), each slice_cols wide
   const int b16 = a.slice_cols * 2, br = a.slice_cols * Res<T, kR32>::kBytes;
   const int stage_bytes = 2 * b16 + 2 * br;
@@ -207,6 +353,7 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_backward_kernel(const N
     s_abort = 0;
     fence_barrier_init();
   }
+  for (int i = static_cast<int>(threadIdx.x); i < 2 * kNbRedFloats; i += static_cast<int>(blockDim.x)) red[0][i] = 0.f;
   __syncthreads();
   pdl_wait();
   pdl_trigger();
@@ -239,68 +386,103 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_backward_kernel(const N
     for (int64_t m = m_first; m < m_last && m < m_first + a.stages; ++m) load_row(m);
 
   const uint16_t *gp = static_cast<const uint16_t *>(a.gate);
+  const bool row_gate = a.gate_kind == NVFP4_GATE_ROW, channel_gate = a.gate_kind == NVFP4_GATE_CHANNEL;
   const float inv_k = 1.f / static_cast<float>(a.K);
-  float acc_a[8], acc_b[8], acc_g[8];
+  // parameters of the thread's columns, packed as stored; the gate's change with the group of rows
+  uint2 ga[2], gb[2], gk[2];
+  const uint32_t one = T::pack(1.f, 1.f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) acc_a[i] = acc_b[i] = acc_g[i] = 0.f;
+  for (int h = 0; h < 2; ++h) {
+    ga[h] = gk[h] = make_uint2(one, one);
+    gb[h] = make_uint2(0u, 0u);
+    if (live[h]) {
+      if (a.ga) ga[h] = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.ga) + k0 + col[h]));
+      if (a.gb) gb[h] = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.gb) + k0 + col[h]));
+    }
+  }
+  float acc_a[2][4], acc_b[2][4], acc_g[2][4];
+#pragma unroll
+  for (int h = 0; h < 2; ++h)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc_a[h][i] = acc_b[h][i] = acc_g[h][i] = 0.f;
+
+  int64_t group = 0;
+  int64_t rows_left = 0;  // rows of the current group still to come, this one included
+  int s = 0;
+  uint32_t phase = 0;
+  // a row's statistics and gate are fetched one row ahead
+  float2 next_st = make_float2(0.f, 0.f);
+  float next_gate = 1.f;
+  auto fetch_row = [&](int64_t m) {
+    next_st = __ldg(reinterpret_cast<const float2 *>(a.stats) + m);
+    if (row_gate) next_gate = T::up(__ldg(gp + m));
+  };
+  if (m_first < m_last) fetch_row(m_first);
 
   for (int64_t m = m_first; m < m_last; ++m) {
-    const int64_t i_row = m - m_first;
-    const int s = static_cast<int>(i_row % a.stages);
-    const int pb = static_cast<int>(i_row & 1);
-    // a wait that gives up leaves this CTA's results undefined and the fault flag raised, but every
-    // barrier below is still met
-    mbar_wait_bounded(&full[s], static_cast<uint32_t>(i_row / a.stages) & 1u, abort_flag, a.err, kPipelineTimeoutNs);
-    const uint8_t *d = smem + s * stage_bytes;
-    const float2 st = __ldg(reinterpret_cast<const float2 *>(a.stats) + m);
-    const float ia = a.ga ? st.x : 1.f, ib = st.y;
-    float gm = a.scale;
-    const uint16_t *gate = gp;
-    if (a.gate_kind == NVFP4_GATE_ROW) {
-      gm *= T::up(__ldg(gp + m));
-      gate = nullptr;
-    } else if (gp) {
-      gate += m / a.rows_per_group * a.K + k0;
-    }
-
-    // one column: q, rh, v and dr' (fh = f ia and n = fh ga are recomputed where needed)
-    float fv[8], rv[8], dyv[8], drv[8], ga[8], gb[8], gk[8];
-    float c2 = 0.f, sa = 0.f, sc = 0.f;
-    auto fetch = [&]() {
-      Res<T, false>::load(d, c, fv);
-      Res<T, kR32>::load(d + 2 * b16, c, rv);
+    const int pb = static_cast<int>((m - m_first) & 1);
+    const float ia = a.ga ? next_st.x : 1.f, ib = next_st.y, gm = a.scale * next_gate;
+    if (m + 1 < m_last) fetch_row(m + 1);
+    if (rows_left == 0) {  // the first row of this CTA or of a group
+      group = group_of(m, a.rows_per_group);
+      rows_left = min((group + 1) * a.rows_per_group, m_last) - m;
+      if (channel_gate) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) dyv[i] = drv[i] = 0.f;
-      if (a.dy) Res<T, false>::load(d + b16, c, dyv);
-      if (a.dr_out) Res<T, kR32>::load(d + 2 * b16 + br, c, drv);
-      load_opt<T>(a.ga ? static_cast<const uint16_t *>(a.ga) + k0 : nullptr, c, 1.f, ga);
-      load_opt<T>(a.gb ? static_cast<const uint16_t *>(a.gb) + k0 : nullptr, c, 0.f, gb);
-      load_opt<T>(gate, c, 1.f, gk);
-    };
-    if (live) {
-      fetch();
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float q = gk[i] * (fv[i] * ia * ga[i]);
-        const float rh = (rv[i] + gm * q) * ib, v = dyv[i] * gb[i];
-        c2 += v * rh;
-        sa += q * (drv[i] + ib * v);
-        sc += q * rh;
+        for (int h = 0; h < 2; ++h)
+          if (live[h]) gk[h] = __ldg(reinterpret_cast<const uint2 *>(gp + group * a.K + k0 + col[h]));
       }
     }
-    c2 = warp_sum(c2);
-    sa = warp_sum(sa);
-    sc = warp_sum(sc);
-    if (lane == 0) {
-      red[pb][warp] = c2;
-      red[pb][32 + warp] = sa;
-      red[pb][64 + warp] = sc;
+    --rows_left;
+    // a wait that gives up leaves this CTA's results undefined and the fault flag raised, but every
+    // barrier below is still met
+    mbar_wait_bounded(&full[s], phase, abort_flag, a.err, kPipelineTimeoutNs);
+    const uint8_t *d = smem + s * stage_bytes;
+    float fv[4], rv[4], dyv[4], drv[4], w[4];
+    auto fetch = [&](int h) {
+      Four<T, false>::load(d, col[h], fv);
+      Four<T, kR32>::load(d + 2 * b16, col[h], rv);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dyv[i] = drv[i] = 0.f;
+      if (a.dy) Four<T, false>::load(d + b16, col[h], dyv);
+      if (a.dr_out) Four<T, kR32>::load(d + 2 * b16 + br, col[h], drv);
+    };
+    float c2 = 0.f, sa = 0.f, sc = 0.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      if (live[h]) {
+        fetch(h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float q = at4<T>(gk[h], i) * (fv[i] * ia * at4<T>(ga[h], i));
+          const float rh = (rv[i] + gm * q) * ib, v = dyv[i] * at4<T>(gb[h], i);
+          c2 += v * rh;
+          sa += q * (drv[i] + ib * v);
+          sc += q * rh;
+        }
+      }
+    }
+    // the three sums over the block: lanes 8 j .. 8 j + 7 carry sum j from the second step on
+    {
+      const bool up16 = lane & 16, up8 = lane & 8;
+      const float x = up16 ? c2 : sc, y = up16 ? sa : 0.f;
+      float lo = (up16 ? sc : c2) + __shfl_xor_sync(0xffffffffu, x, 16);
+      float hi = (up16 ? 0.f : sa) + __shfl_xor_sync(0xffffffffu, y, 16);
+      float t = (up8 ? hi : lo) + __shfl_xor_sync(0xffffffffu, up8 ? lo : hi, 8);
+#pragma unroll
+      for (int o = 4; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      if ((lane & 7) == 0) red[pb][(lane >> 3) * 32 + warp] = t;
     }
     __syncthreads();  // also: every thread is done with the previous row's stage
-    if (threadIdx.x == 0 && i_row > 0 && m - 1 + a.stages < m_last) load_row(m - 1 + a.stages);
-    c2 = warp_sum(lane < warps ? red[pb][lane] : 0.f);
-    sa = warp_sum(lane < warps ? red[pb][32 + lane] : 0.f);
-    sc = warp_sum(lane < warps ? red[pb][64 + lane] : 0.f);
+    if (threadIdx.x == 0 && m > m_first && m - 1 + a.stages < m_last) load_row(m - 1 + a.stages);
+    {
+      const float4 v = *reinterpret_cast<const float4 *>(&red[pb][lane * 4]);
+      float t = (v.x + v.y) + (v.z + v.w);
+#pragma unroll
+      for (int o = 4; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+      c2 = __shfl_sync(0xffffffffu, t, 0);
+      sa = __shfl_sync(0xffffffffu, t, 8);
+      sc = __shfl_sync(0xffffffffu, t, 16);
+    }
     if (a.slices > 1) {  // the other slices' sums, by rank
       if (threadIdx.x < static_cast<unsigned>(a.slices)) {
         const uint32_t at = cluster_addr(&peer_sums[pb][slice][0], threadIdx.x);
@@ -318,46 +500,51 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_backward_kernel(const N
       }
     }
     const float mean2 = c2 * inv_k;
-    const float S = sa - ib * mean2 * sc;                // sum q dR
-    const float mean1 = gm * S * inv_k;                  // mean of fh times the gradient of fh
-    if (a.gate_kind == NVFP4_GATE_ROW && a.dgate && threadIdx.x == 0 && slice == 0) a.dgate[m] = a.scale * S;
-    if (live) {
-      fetch();
-      float dr[8], df[8];
+    const float S = sa - ib * mean2 * sc;  // sum q dR
+    const float mean1 = gm * S * inv_k;    // mean of fh times the gradient of fh
+    if (row_gate && a.dgate && threadIdx.x == 0 && slice == 0) a.dgate[m] = a.scale * S;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float fh = fv[i] * ia, n = fh * ga[i];
-        const float rh = (rv[i] + gm * gk[i] * n) * ib, v = dyv[i] * gb[i];
-        dr[i] = drv[i] + ib * (v - rh * mean2);
-        const float sdr = gm * dr[i];
-        acc_b[i] += dyv[i] * rh;
-        acc_g[i] += sdr * n;
-        const float dn = sdr * gk[i];
-        acc_a[i] += dn * fh;
-        df[i] = a.ga ? ia * (dn * ga[i] - fh * mean1) : dn;
-      }
-      Res<T, kR32>::store(a.dr, m * a.K + k0 + c, dr);
-      Res<T, false>::store(a.df, m * a.K + k0 + c, df);
-      // the end of a group of rows: its gate gradient
-      if (a.gate_kind == NVFP4_GATE_CHANNEL && a.dgate && (m + 1 == m_last || (m + 1) % a.rows_per_group == 0)) {
-        const int64_t at = (a.parts > 1 ? part : m / a.rows_per_group) * a.K + k0 + c;
-        float *dst = (a.parts > 1 ? a.part_g : a.dgate) + at;
-        reinterpret_cast<float4 *>(dst)[0] = make_float4(acc_g[0], acc_g[1], acc_g[2], acc_g[3]);
-        reinterpret_cast<float4 *>(dst)[1] = make_float4(acc_g[4], acc_g[5], acc_g[6], acc_g[7]);
+    for (int h = 0; h < 2; ++h) {
+      if (live[h]) {
+        fetch(h);
+        float df[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) acc_g[i] = 0.f;
+        for (int i = 0; i < 4; ++i) {
+          const float fh = fv[i] * ia, g = at4<T>(ga[h], i), k = at4<T>(gk[h], i), n = fh * g;
+          const float rh = (rv[i] + gm * k * n) * ib, v = dyv[i] * at4<T>(gb[h], i);
+          acc_b[h][i] += dyv[i] * rh;
+          w[i] = drv[i] + ib * (v - rh * mean2);
+          const float sdr = gm * w[i];
+          acc_g[h][i] += sdr * n;
+          const float dn = sdr * k;
+          acc_a[h][i] += dn * fh;
+          df[i] = a.ga ? ia * (dn * g - fh * mean1) : dn;
+        }
+        Four<T, kR32>::store(a.dr, m * a.K + k0 + col[h], w);
+        Four<T, false>::store(a.df, m * a.K + k0 + col[h], df);
       }
+    }
+    if (rows_left == 0 && channel_gate && a.dgate) {  // the end of a group of rows: its gate gradient
+      const int64_t at = (a.parts > 1 ? part : group) * a.K + k0;
+      float *dst = (a.parts > 1 ? a.part_g : a.dgate) + at;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        if (live[h]) Four<T, true>::store(dst, col[h], acc_g[h]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc_g[h][i] = 0.f;
+      }
+    }
+    if (++s == a.stages) {
+      s = 0;
+      phase ^= 1;
     }
   }
-  if (live) {
-    const int64_t at = static_cast<int64_t>(part) * a.K + k0 + c;
-    if (a.part_a) {
-      reinterpret_cast<float4 *>(a.part_a + at)[0] = make_float4(acc_a[0], acc_a[1], acc_a[2], acc_a[3]);
-      reinterpret_cast<float4 *>(a.part_a + at)[1] = make_float4(acc_a[4], acc_a[5], acc_a[6], acc_a[7]);
-    }
-    if (a.part_b) {
-      reinterpret_cast<float4 *>(a.part_b + at)[0] = make_float4(acc_b[0], acc_b[1], acc_b[2], acc_b[3]);
-      reinterpret_cast<float4 *>(a.part_b + at)[1] = make_float4(acc_b[4], acc_b[5], acc_b[6], acc_b[7]);
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    if (live[h]) {
+      const int64_t at = static_cast<int64_t>(part) * a.K + k0;
+      if (a.part_a) Four<T, true>::store(a.part_a + at, col[h], acc_a[h]);
+      if (a.part_b) Four<T, true>::store(a.part_b + at, col[h], acc_b[h]);
     }
   }
   if (*abort_flag) {  // copies in flight land before the CTA's memory goes
@@ -409,17 +596,36 @@ __global__ void __launch_bounds__(256) partial_sum_kernel(const SumJobs jobs) {
 template <class T, bool kR32>
 cudaError_t norm_forward(const NormArgs &a, int sms, cudaStream_t s) {
   const int chunks = a.K / 8;
-  // few rows: as many threads as the row has chunks (latency); many rows: four chunks per thread,
-  // more CTAs per SM and more loads in flight per thread
-  const int per = a.M <= 2 * sms ? (chunks <= 1024 ? 1 : 2) : (chunks <= 128 ? 1 : chunks <= 512 ? 2 : 4);
-  const int threads = ((chunks + per - 1) / per + 31) / 32 * 32;
-  const int64_t cap = static_cast<int64_t>(sms) * 16;
-  const dim3 grid(static_cast<unsigned>(a.M < cap ? a.M : cap)), block(threads);
-  switch (per) {
-    case 1: return launch_pdl(residual_norm_kernel<T, kR32, 1>, grid, block, 0, s, a);
-    case 2: return launch_pdl(residual_norm_kernel<T, kR32, 2>, grid, block, 0, s, a);
+  if (a.M <= 2 * sms) {  // few rows: as many threads as the row has chunks, straight from memory (latency)
+    const int per = chunks <= 1024 ? 1 : 2;
+    const dim3 grid(static_cast<unsigned>(a.M)), block(((chunks + per - 1) / per + 31) / 32 * 32);
+    return per == 1 ? launch_pdl(residual_norm_kernel<T, kR32, 1>, grid, block, 0, s, a)
+                    : launch_pdl(residual_norm_kernel<T, kR32, 2>, grid, block, 0, s, a);
   }
-  return launch_pdl(residual_norm_kernel<T, kR32, 4>, grid, block, 0, s, a);
+  const int per = chunks <= 64 ? 1 : 2;
+  const int threads = ((chunks + per - 1) / per + 31) / 32 * 32;
+  const int stage = a.K * (2 + Res<T, kR32>::kBytes);
+  int per_sm = 1024 / threads;
+  if (per_sm > 16) per_sm = 16;
+  int stages = (kNormMaxSmem / per_sm - 2048) / stage;
+  while (stages < 2 && per_sm > 1) stages = (kNormMaxSmem / --per_sm - 2048) / stage;
+  if (stages > kNormMaxStages) stages = kNormMaxStages;
+  if (stages < 1) stages = 1;
+  const int smem = 128 + stages * stage;
+  const int64_t cap = static_cast<int64_t>(sms) * per_sm;
+  const dim3 grid(static_cast<unsigned>(a.M < cap ? a.M : cap)), block(threads);
+  auto kernel = per == 1 ? residual_norm_rows_kernel<T, kR32, 1> : residual_norm_rows_kernel<T, kR32, 2>;
+  static std::atomic<bool> ready[64][2];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!ready[dev][per - 1].load()) {
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMaxSmem);
+    if (e != cudaSuccess) return e;
+    ready[dev][per - 1].store(true);
+  }
+  return launch_pdl(kernel, grid, block, smem, s, a, stages);
 }
 
 template <class T, bool kR32>
@@ -474,7 +680,7 @@ NormGradPlan norm_grad_plan(int64_t M, int64_t K, int64_t groups, bool r32) {
   p.threads = (p.slice_cols / 8 + 31) / 32 * 32;
   const int stage = p.slice_cols * (r32 ? 12 : 8);
   // narrow rows: several CTAs per SM share its shared memory
-  int per_sm = 1024 / p.threads;
+  int per_sm = kNormGradThreads / p.threads;
   if (per_sm > 8) per_sm = 8;
   if (per_sm < 1) per_sm = 1;
   const int budget = (kNormMaxSmem - 1024) / per_sm - 1024;

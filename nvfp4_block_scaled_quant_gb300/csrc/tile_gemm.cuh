@@ -7,14 +7,20 @@
 // would stage 48 KB for the same work: the L2 -> SM operand stream is what bounds tiles of this
 // size, so the pair's sharing of B matters.
 //
-// Warps of each CTA: 0 = TMA producer, 1 = MMA issuer (the even CTA's, for both), 2..9 = epilogue
+// Warps of each CTA: 0 = TMA producer, 1 (and 2 for FP8) = MMA issuer (the even CTA's, for both),
+// 4..11 = epilogue
 // (two per 32-lane quarter of tensor memory, 128 columns each).
 //
 //   Op::kFp8    A = xq (M, K) e4m3, B = wq (N, K) e4m3.  The scales change every 128 K, so every K
-//               block is a product of its own: the issuer alternates between two accumulators, and
-//               the epilogue warps add block * (sa[m, b] * sw[n / 128, b]) to fp32 registers (128
-//               columns per thread) while the next block runs.  Scaling in registers keeps the
+//               block is a product of its own: two issuers take the blocks in turn into an accumulator
+//               each, and the epilogue warps add block * (sa[m, b] * sw[n / 128, b]) to fp32 registers
+//               (128 columns per thread) while the next block runs.  Scaling in registers keeps the
 //               scales arbitrary fp32 values; nothing is rounded until the output.
+//               4096 x 7168 x 7168: 161 us, 2.6 PF/s.  A block takes 0.41 us where its MMAs take 0.26:
+//               an accumulator's way to the epilogue and back (commit, wait, read, release, wait) is
+//               longer than the other's MMAs.  Measured and left: four accumulators of 128 columns (two
+//               issuers; 8 warps 200 us, 16 warps 175 us), 16 epilogue warps on 256 columns, two batches
+//               of columns in flight, activation scales through a shared-memory ring.
 //   Op::kGated  A = x (M, K), B = 128 rows of Wg (even CTA) and the matching 128 of Wu (odd CTA):
 //               columns 0..127 of the accumulator are g, 128..255 u of the same outputs.
 //   Op::kDx     A = [dg | du] in two segments of K = I, B = Wg, then Wu, read along their rows
@@ -52,16 +58,29 @@ constexpr int kTRows = 256, kTCols = 256, kTHalf = 128;
 constexpr int kTStages = 6;
 constexpr int kTOperandBytes = kTHalf * 128;  // 16 KiB: 128 rows x 128 bytes
 constexpr int kTStageBytes = 2 * kTOperandBytes;
+constexpr int kTEpiWarp0 = 4;  // epilogue warps start on a multiple of four: a warp reads lane quarter warp % 4
+template <TileOp kOp>
 constexpr int kTEpiWarps = 8;
-constexpr int kTThreads = (2 + kTEpiWarps) * 32;
+template <TileOp kOp>
+constexpr int kTThreads = (kTEpiWarp0 + kTEpiWarps<kOp>)*32;
+template <TileOp kOp>
+constexpr int kTIssuers = kOp == TileOp::kFp8 ? 2 : 1;
+// kFp8: registers per thread.  The launch gives every warp 168 (three warps on each quarter of an
+// SM); the epilogue's 128 sums, scales and accumulator columns in flight take more, which the first four
+// warps give up.
+constexpr int kTLaunchRegs = 168, kTLightRegs = 56, kTEpiRegs = 224;
+static_assert(kTEpiWarp0 * kTLightRegs + kTEpiWarps<TileOp::kFp8> * kTEpiRegs <=
+                  (kTEpiWarp0 + kTEpiWarps<TileOp::kFp8>)*kTLaunchRegs,
+              "register split within what the block was launched with");
 constexpr size_t kTSmem = 1024 + static_cast<size_t>(kTStages) * kTStageBytes + 256;
 constexpr uint32_t kTTmemCols = 512;  // two accumulators of 256 columns
+constexpr int kAhead = 4;             // kFp8: K blocks that a thread's scales are fetched ahead
 constexpr int kTGroupM = 8;           // m tiles walked together, so that a wave shares rows of B in L2
 static_assert(kTSmem <= 232448, "per-block shared memory limit");
-static_assert((2 * kTStages + 4) * 8 + 8 <= 256, "barrier region");
+static_assert((2 * kTStages + 8) * 8 + 8 <= 256, "barrier region");
 
 template <TileOp kOp, class T, int kAct>
-__global__ void __launch_bounds__(kTThreads, 1)
+__global__ void __launch_bounds__(kTThreads<kOp>, 1)
     tile_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
                      const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
                      const TileArgs args) {
@@ -80,7 +99,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
   uint64_t *full = reinterpret_cast<uint64_t *>(sB + kTStages * kTOperandBytes);  // used in the even CTA
   uint64_t *empty = full + kTStages;
   uint64_t *tfull = empty + kTStages;   // [2]
-  uint64_t *tempty = tfull + 2;         // [2], used in the even CTA
+  uint64_t *tempty = tfull + 2;     // [2], used in the even CTA
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(tempty + 2);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
 
@@ -94,7 +113,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
-      mbar_init(&tempty[b], 2 * kTEpiWarps);
+      mbar_init(&tempty[b], 2 * 8);  // the eight warps of each CTA that read it
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -133,6 +152,12 @@ __global__ void __launch_bounds__(kTThreads, 1)
     mt = g * kTGroupM + (in - nt * rows);
   };
 
+  if constexpr (kFp8) {
+    if (warp < kTEpiWarp0)
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTLightRegs));
+    else
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTEpiRegs));
+  }
   if (warp == 0) {
     if (lane == 0) {
       // ------------------------------------------------------------ TMA producer
@@ -184,60 +209,65 @@ __global__ void __launch_bounds__(kTThreads, 1)
       }
       if (!ok) settle();  // copies in flight may complete on the other CTA's barrier
     }
-  } else if (warp == 1) {
-    if (rank == 0 && lane == 0) {
-      // ------------------------------------------------------------ MMA issuer
+  } else if (warp < kTEpiWarp0) {
+    if (rank == 0 && warp <= kTIssuers<kOp>) {
+      // ------------------------------------------------------------ MMA issuers
+      // The whole warp waits and one elected lane issues: in an elect.sync branch an MMA takes its
+      // issuer about 32 cycles, from a `lane == 0` branch about its execution time, and the waits
+      // and commits between K blocks then leave the tensor pipe idle.
       const uint32_t a0 = smem_u32(sA), b0 = smem_u32(sB);
       // K-major rows of 128 bytes: 8-row groups 1024 bytes apart, a K step is 32 bytes on.
       // MN-major boxes (64 elements x 64 K rows): boxes 8192 bytes apart along MN, 8-K groups 1024
       // bytes apart, a K step of 16 rows is 2048 bytes on.
       constexpr uint32_t kAStep = kAMn ? 2048 / 16 : 32 / 16, kBStep = kBMn ? 2048 / 16 : 32 / 16;
-      int stage = 0;
+      // kFp8: the two issuers take the blocks in turn, issuer i into accumulator i
+      const int iss = warp - 1;
+      constexpr int kIssuers = kTIssuers<kOp>;
+      const int tiles = cluster_id < total ? (total - 1 - cluster_id) / clusters + 1 : 0;
+      const int64_t blocks = static_cast<int64_t>(tiles) * k_blocks;  // of this launch
+      int stage = iss, it = iss;
       uint32_t phase = 0;
-      uint32_t acc = 0;  // accumulators handed to the epilogue so far
+      uint32_t acc = iss;  // the accumulator's turn: the block (kFp8) or the tile
       bool ok = true;
-      for (int idx = cluster_id; ok && idx < total; idx += clusters) {
-        for (int it = 0; it < k_blocks; ++it) {
-          const uint32_t buf = acc & 1;
-          if ((kFp8 || it == 0) &&
-              !mbar_wait_bounded_cluster(&tempty[buf], ((acc >> 1) & 1) ^ 1, abort_flag, args.err, kPipelineTimeoutNs)) {
-            ok = false;
-            break;
-          }
-          if (!mbar_wait_bounded_cluster(&full[stage], phase, abort_flag, args.err, kPipelineTimeoutNs)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
+      for (int64_t g = iss; ok && g < blocks; g += kIssuers) {
+        if (kFp8 || it == 0)
+          ok = mbar_wait_bounded_cluster(&tempty[acc & 1], ((acc >> 1) & 1) ^ 1, abort_flag, args.err, kPipelineTimeoutNs);
+        ok = ok && mbar_wait_bounded_cluster(&full[stage], phase, abort_flag, args.err, kPipelineTimeoutNs);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        const bool done = kFp8 || it == k_blocks - 1;
+        if (elect_one()) {
           const uint64_t ad = smem_desc(a0 + stage * kTOperandBytes, kAMn ? 8192 : 16, 1024, 2);
           const uint64_t bd = smem_desc(b0 + stage * kTOperandBytes, kBMn ? 8192 : 16, 1024, 2);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
-            tc_mma<kFp8, true>(tmem_base + buf * kTCols, ad + j * kAStep, bd + j * kBStep, kIdesc,
+            tc_mma<kFp8, true>(tmem_base + (acc & 1) * kTCols, ad + j * kAStep, bd + j * kBStep, kIdesc,
                                kFp8 ? j != 0 : (it | j) != 0);
           tc_commit_pair(&empty[stage], 0x3);
-          if (kFp8 || it == k_blocks - 1) {
-            tc_commit_pair(&tfull[buf], 0x3);
-            ++acc;
-          }
-          if (++stage == kTStages) {
-            stage = 0;
-            phase ^= 1;
-          }
+          if (done) tc_commit_pair(&tfull[acc & 1], 0x3);
+        }
+        __syncwarp();
+        if (done) acc += kIssuers;
+        it = !kFp8 && done ? 0 : it + 1;
+        if ((stage += kIssuers) >= kTStages) {
+          stage -= kTStages;
+          phase ^= 1;
         }
       }
-      // every MMA issued has completed before the pair frees its tensor memory: the last commits
-      // arrive on tfull, which this thread follows to the end
+      // every MMA issued has completed before the pair frees its tensor memory: the last commit
+      // arrives on tfull, which this warp follows to the end
       if (!ok) {
         settle();
-      } else if (acc) {
+      } else if (acc >= kIssuers) {
         volatile int never = 0;
-        mbar_wait_bounded(&tfull[(acc - 1) & 1], ((acc - 1) >> 1) & 1, &never, nullptr, 100000000ull);
+        const uint32_t last = acc - kIssuers;
+        mbar_wait_bounded(&tfull[last & 1], (last >> 1) & 1, &never, nullptr, 100000000ull);
       }
     }
   } else {
     // -------------------------------------------------------------- epilogue
-    const int quarter = warp & 3, half = (warp - 2) >> 2;
+    const int quarter = warp & 3, half = (warp - kTEpiWarp0) >> 2;
     const uint32_t tempty_leader = cluster_addr(tempty, 0);
     const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16);
     uint32_t acc = 0;
@@ -255,55 +285,66 @@ __global__ void __launch_bounds__(kTThreads, 1)
       ++acc;
     };
     const bool vec = (args.ldo & 7) == 0;
+    // kFp8: the sums of this thread's row, columns out_n0 .. out_n0 + 127
+    float sum[kFp8 ? 128 : 1];
+    int out_row = 0, out_n0 = 0;
+    auto store_tile = [&]() {
+      if constexpr (kFp8) {
+        if (out_row < args.M) {
+          uint16_t *dst = static_cast<uint16_t *>(args.out) + out_row * args.ldo + out_n0;
+#pragma unroll
+          for (int c = 0; c < 8; ++c) {
+            float v[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) v[i] = sum[c * 16 + i];
+            store16<T>(dst + c * 16, v, args.N - out_n0 - c * 16, vec);
+          }
+        }
+      }
+    };
     for (int idx = cluster_id; ok && idx < total; idx += clusters) {
       int mt, nt;
       tile_at(idx, mt, nt);
       const int row = mt * kTRows + static_cast<int>(rank) * kTHalf + quarter * 32 + lane;
       const bool row_ok = row < args.M;
       if constexpr (kFp8) {
-        const int n0 = nt * kTCols + half * kTHalf;
-        // scales of the next K block are fetched one block ahead; a half past N is computed on zeros
-        const float *sa = args.sa + row;
+        const int n0 = nt * kTCols + half * kTHalf;  // a warp's 128 columns share one weight scale
+        // Scales are fetched ahead: under the operand stream a load takes longer than a block.  The
+        // thread's row's activation scales kAhead blocks ahead (the loop is unrolled, so that no
+        // register in flight is moved); a lane holds every 32nd weight scale.  Rows past M and
+        // columns past N read the last one's.
+        const float *sa = args.sa + min(row, args.M - 1);
         const float *sw = args.sw + static_cast<int64_t>(min(n0, args.N - 1) / 128) * k_blocks;
-        float next_a = row_ok ? __ldg(sa) : 0.f, next_w = __ldg(sw);
-        uint64_t sum[64];
+        float w = ld_early(sw + min(lane, k_blocks - 1)), a[kAhead];
 #pragma unroll
-        for (int i = 0; i < 64; ++i) sum[i] = 0;
-        for (int kb = 0; kb < k_blocks; ++kb) {
-          const float f = next_a * next_w;
-          const uint64_t f2 = pack_f32x2(f, f);
-          if (kb + 1 < k_blocks) {
-            next_a = row_ok ? __ldg(sa + (kb + 1) * args.ld_sa) : 0.f;
-            next_w = __ldg(sw + kb + 1);
-          }
-          if (!wait_acc()) break;
-          const uint32_t t = lanes + (acc & 1) * kTCols + half * kTHalf;
-          uint32_t r[2][16];
-          tmem_ld16(t, r[0]);
+        for (int u = 0; u < kAhead; ++u) a[u] = ld_early(sa + min(u, k_blocks - 1) * args.ld_sa);
+        if (idx != cluster_id) store_tile();  // the previous tile, while this one's first block is made
+        out_row = row;
+        out_n0 = n0;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            tmem_ld_wait();
-            if (c < 7)
-              tmem_ld16(t + (c + 1) * 16, r[(c + 1) & 1]);
-            else
-              release();
+        for (int i = 0; i < 128; ++i) sum[i] = 0.f;
+        for (int kb0 = 0; ok && kb0 < k_blocks; kb0 += kAhead) {
+          if ((kb0 & 31) == 0 && kb0) w = ld_early(sw + min(kb0 + lane, k_blocks - 1));
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-              sum[c * 8 + i] = fma_f32x2(pack_f32x2(__uint_as_float(r[c & 1][2 * i]), __uint_as_float(r[c & 1][2 * i + 1])),
-                                         f2, sum[c * 8 + i]);
+          for (int u = 0; u < kAhead; ++u) {
+            if (kb0 + u >= k_blocks) break;
+            const float f = a[u] * __shfl_sync(0xffffffffu, w, (kb0 + u) & 31);
+            a[u] = ld_early(sa + min(kb0 + u + kAhead, k_blocks - 1) * args.ld_sa);
+            if (!wait_acc()) break;
+            const uint32_t t = lanes + (acc & 1) * kTCols + half * kTHalf;
+            // scalar FMAs: the packed form (fma.rn.f32x2) has no higher rate here and cost 16% more time
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+              uint32_t r[16];
+              tmem_ld16(t + c * 16, r);
+              tmem_ld_wait();
+              if (c == 7) release();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) sum[c * 16 + i] = fmaf(__uint_as_float(r[i]), f, sum[c * 16 + i]);
+            }
           }
         }
         if (!ok) break;
-        if (row_ok) {
-          uint16_t *dst = static_cast<uint16_t *>(args.out) + row * args.ldo + n0;
-#pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            float v[16];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) unpack_f32x2(sum[c * 8 + i], v[2 * i], v[2 * i + 1]);
-            store16<T>(dst + c * 16, v, args.N - n0 - c * 16, vec);
-          }
-        }
       } else if constexpr (kOp == TileOp::kGated) {
         if (!wait_acc()) break;
         const int n0 = nt * kTHalf + half * 64;
@@ -356,6 +397,7 @@ __global__ void __launch_bounds__(kTThreads, 1)
         }
       }
     }
+    if (ok && cluster_id < total) store_tile();
   }
 
   tc_fence_before();
@@ -367,13 +409,13 @@ __global__ void __launch_bounds__(kTThreads, 1)
 
 // Clusters of two that fit on the current device at once (0 if the query fails), and the launch.
 template <class K>
-int tile_gemm_max_clusters(K kernel) {
+int tile_gemm_max_clusters(K kernel, int threads) {
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kTSmem)) !=
       cudaSuccess)
     return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * 1024);
-  cfg.blockDim = dim3(kTThreads);
+  cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = kTSmem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -398,7 +440,7 @@ cudaError_t launch_tile_gemm_as(const CUtensorMap &a0, const CUtensorMap &a1, co
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   int n = fit[dev].load();
   if (n <= 0) {
-    n = tile_gemm_max_clusters(kernel);
+    n = tile_gemm_max_clusters(kernel, kTThreads<kOp>);
     if (n <= 0) {
       const cudaError_t last = cudaGetLastError();
       return last != cudaSuccess ? last : cudaErrorLaunchOutOfResources;
@@ -413,7 +455,7 @@ cudaError_t launch_tile_gemm_as(const CUtensorMap &a0, const CUtensorMap &a1, co
   const int clusters = static_cast<int>((tiles + waves - 1) / waves);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * clusters);
-  cfg.blockDim = dim3(kTThreads);
+  cfg.blockDim = dim3(kTThreads<kOp>);
   cfg.dynamicSmemBytes = kTSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];

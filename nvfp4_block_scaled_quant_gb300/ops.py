@@ -299,38 +299,34 @@ _ACT = {"silu": _lib.ACT_SILU, "gelu": _lib.ACT_GELU, "gelu_tanh": _lib.ACT_GELU
 _CODES = (torch.float8_e4m3fn, torch.uint8)
 
 
-class _Place:
-    """The device of a call's tensors (all the same) as the current one, and its stream."""
+def _here(stream, *tensors: Optional[torch.Tensor]) -> int:
+    """Raw handle of the current stream if the call can run as it stands, -1 if ``_elsewhere`` has to
+    switch to the given stream or to the tensors' device first; refuses mixed or CPU tensors."""
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("tensors on different devices")
+    if dev < 0:
+        raise ValueError("nvfp4 ops take CUDA tensors only (no CPU fallback)")
+    if stream is not None or dev != torch._C._cuda_getDevice():
+        return -1
+    return torch._C._cuda_getCurrentRawStream(dev)
 
-    def __init__(self, stream, *tensors: Optional[torch.Tensor]):
-        first = tensors[0]
+
+def _elsewhere(stream, tensors, run):
+    """``run()`` with the tensors' device current and on ``stream`` (if given), which the tensors are
+    marked as used on; outputs and scratch then belong to that stream too."""
+    device = next(t for t in tensors if t is not None).device
+    with torch.cuda.device(device):
+        if stream is None:
+            return run()
+        if stream.device != device:
+            raise ValueError("stream of another device")
         for t in tensors:
-            if t is None:
-                continue
-            if not t.is_cuda:
-                raise ValueError("nvfp4 ops take CUDA tensors only (no CPU fallback)")
-            if t.device != first.device:
-                raise ValueError("tensors on different devices")
-        self.device = first.device
-        self._guards = []
-        if first.get_device() != torch.cuda.current_device():
-            self._guards.append(torch.cuda.device(first.device))
-        if stream is not None:
-            if stream.device != first.device:
-                raise ValueError("stream of another device")
-            self._guards.append(torch.cuda.stream(stream))
-            for t in tensors:
-                if t is not None:
-                    t.record_stream(stream)
-
-    def __enter__(self):
-        for g in self._guards:
-            g.__enter__()
-        return torch.cuda.current_stream().cuda_stream
-
-    def __exit__(self, *exc):
-        for g in reversed(self._guards):
-            g.__exit__(*exc)
+            if t is not None:
+                t.record_stream(stream)
+        with torch.cuda.stream(stream):
+            return run()
 
 
 def _kind(x: torch.Tensor, what: str) -> int:
@@ -340,25 +336,42 @@ def _kind(x: torch.Tensor, what: str) -> int:
     return d
 
 
-def _ld(t: torch.Tensor, what: str, rows: Optional[int] = None, cols: Optional[int] = None, dtype=None) -> int:
+def _ld(t: torch.Tensor, what: str, rows: int, cols: int, dtype=None) -> int:
     """Row stride of a 2-D tensor of strided rows (a single row's stride does not matter)."""
-    if t.dim() != 2 or (rows is not None and t.shape[0] != rows) or (cols is not None and t.shape[1] != cols):
-        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected ({rows if rows is not None else 'rows'}, "
-                         f"{cols if cols is not None else 'columns'})")
-    if dtype is not None and t.dtype != dtype:
-        raise ValueError(f"{what} must be {dtype}, got {t.dtype}")
-    if t.stride(1) != 1 and t.shape[1] > 1:
+    if t.shape != (rows, cols) or (dtype is not None and t.dtype != dtype):
+        raise ValueError(f"{what} has shape {tuple(t.shape)} and type {t.dtype}, expected ({rows}, {cols}) "
+                         f"{dtype if dtype is not None else ''}")
+    ld, one = t.stride()
+    if one != 1 and cols > 1:
         raise ValueError(f"{what}: the elements of a row must be contiguous")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+    return ld if rows > 1 else cols
+
+
+def _size(t: torch.Tensor, what: str):
+    """(rows, columns) of a 2-D tensor."""
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what} must be 2-D, got {tuple(shape)}")
+    return shape
 
 
 def _whole(t: torch.Tensor, what: str, shape, dtypes) -> int:
     """Data pointer of a contiguous tensor of the given shape and type."""
-    if tuple(t.shape) != tuple(shape) or t.dtype not in dtypes:
-        raise ValueError(f"{what} has shape {tuple(t.shape)} and type {t.dtype}, expected {tuple(shape)} {dtypes}")
+    if t.shape != shape or t.dtype not in dtypes:
+        raise ValueError(f"{what} has shape {tuple(t.shape)} and type {t.dtype}, expected {shape} {dtypes}")
     if not t.is_contiguous():
         raise ValueError(f"{what} must be contiguous")
     return t.data_ptr()
+
+
+def _scratch(workspace: Optional[torch.Tensor], query: str, like: torch.Tensor, *sizes: int):
+    """The caller's workspace or a new one of the size that the query returns, and its bytes."""
+    if workspace is None:
+        n = getattr(lib(), query)(*sizes)
+        return torch.empty(n, dtype=torch.uint8, device=like.device), n
+    n = workspace.numel()
+    _whole(workspace, "workspace", (n,), (torch.uint8,))
+    return workspace, n
 
 
 def fp8_quantize_act(x: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -367,32 +380,34 @@ def fp8_quantize_act(x: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.
     One scale per 128 consecutive K elements of a row, s = max|x| / 448, q = e4m3(x / s).  s is a view
     of rows padded to a multiple of four, as ``fp8_gemm`` wants them.  K % 16 == 0.
     """
-    with _Place(stream, x) as st:
-        ld = _ld(x, "x")
-        M, K = x.shape
-        q = torch.empty(M, K, dtype=torch.float8_e4m3fn, device=x.device)
-        lds = (M + 3) // 4 * 4
-        s = torch.empty((K + 127) // 128, lds, dtype=torch.float32, device=x.device)
-        call("nvfp4_fp8_quantize_act", x.data_ptr(), _kind(x, "x"), M, K, ld, q.data_ptr(), s.data_ptr(), lds, st)
-        return q, s[:, :M]
+    st = _here(stream, x)
+    if st < 0:
+        return _elsewhere(stream, (x,), lambda: fp8_quantize_act(x))
+    M, K = _size(x, "x")
+    ld = _ld(x, "x", M, K)
+    q = torch.empty(M, K, dtype=torch.float8_e4m3fn, device=x.device)
+    lds = (M + 3) // 4 * 4
+    s = torch.empty((K + 127) // 128, lds, dtype=torch.float32, device=x.device)
+    call("nvfp4_fp8_quantize_act", x.data_ptr(), _kind(x, "x"), M, K, ld, q.data_ptr(), s.data_ptr(), lds, st)
+    return q, s[:, :M]
 
 
 def fp8_quantize_weight(w: torch.Tensor, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
     """w (N, K) strided rows -> (q (N, K) float8_e4m3fn, s (ceil(N / 128), ceil(K / 128)) fp32): one
     scale per 128 x 128 block, the layout checkpoints store.  Once, at load time.  K % 16 == 0."""
-    with _Place(stream, w) as st:
-        ld = _ld(w, "w")
-        N, K = w.shape
-        q = torch.empty(N, K, dtype=torch.float8_e4m3fn, device=w.device)
-        s = torch.empty((N + 127) // 128, (K + 127) // 128, dtype=torch.float32, device=w.device)
-        call("nvfp4_fp8_quantize_weight", w.data_ptr(), _kind(w, "w"), N, K, ld, q.data_ptr(), s.data_ptr(), st)
-        return q, s
+    st = _here(stream, w)
+    if st < 0:
+        return _elsewhere(stream, (w,), lambda: fp8_quantize_weight(w))
+    N, K = _size(w, "w")
+    ld = _ld(w, "w", N, K)
+    q = torch.empty(N, K, dtype=torch.float8_e4m3fn, device=w.device)
+    s = torch.empty((N + 127) // 128, (K + 127) // 128, dtype=torch.float32, device=w.device)
+    call("nvfp4_fp8_quantize_weight", w.data_ptr(), _kind(w, "w"), N, K, ld, q.data_ptr(), s.data_ptr(), st)
+    return q, s
 
 
 def _fp8_weight(w: torch.Tensor, w_s: torch.Tensor, K: int) -> Tuple[int, int, int]:
-    if w.dim() != 2:
-        raise ValueError("w must be 2-D")
-    N = w.shape[0]
+    N = _size(w, "w")[0]
     return (N, _whole(w, "w", (N, K), _CODES),
             _whole(w_s, "w_s", ((N + 127) // 128, (K + 127) // 128), (torch.float32,)))
 
@@ -401,51 +416,52 @@ def fp8_gemm(xq: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, w_s: torch.Ten
              out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y (M, N) = deq(xq) deq(w)^T of quantised activations (``fp8_quantize_act``) and weights, in
     bf16 or fp16; the scales apply to fp32 sums of one 128-wide K block each."""
-    with _Place(stream, xq, xs, w, w_s, out) as st:
-        if xq.dim() != 2 or xs.dim() != 2:
-            raise ValueError("xq and xs must be 2-D")
-        M, K = xq.shape
-        N, wp, wsp = _fp8_weight(w, w_s, K)
-        KB = (K + 127) // 128
-        lds = xs.stride(0) if KB > 1 else max(xs.stride(0), (M + 3) // 4 * 4)
-        room = xs.untyped_storage().nbytes() // 4 - xs.storage_offset()
-        if xs.dtype != torch.float32 or tuple(xs.shape) != (KB, M) or (M > 1 and xs.stride(1) != 1):
-            raise ValueError(f"xs must be fp32 ({KB}, {M}) with contiguous rows")
-        if M and room < (KB - 1) * lds + (M + 3) // 4 * 4:
-            raise ValueError("the rows of xs must be padded to a multiple of four scales")
-        if dtype not in _DT:
-            raise ValueError(f"output type {dtype}")
-        y = out if out is not None else torch.empty(M, N, dtype=dtype, device=xq.device)
-        call("nvfp4_fp8_gemm", _whole(xq, "xq", (M, K), _CODES), xs.data_ptr(), lds, M, K, N, wp, wsp, _DT[dtype],
-             _whole(y, "out", (M, N), (dtype,)), st)
-        return y
+    st = _here(stream, xq, xs, w, w_s, out)
+    if st < 0:
+        return _elsewhere(stream, (xq, xs, w, w_s, out), lambda: fp8_gemm(xq, xs, w, w_s, dtype, out))
+    M, K = _size(xq, "xq")
+    _size(xs, "xs")
+    N, wp, wsp = _fp8_weight(w, w_s, K)
+    KB = (K + 127) // 128
+    lds = xs.stride(0) if KB > 1 else max(xs.stride(0), (M + 3) // 4 * 4)
+    room = xs.untyped_storage().nbytes() // 4 - xs.storage_offset()
+    if xs.dtype != torch.float32 or tuple(xs.shape) != (KB, M) or (M > 1 and xs.stride(1) != 1):
+        raise ValueError(f"xs must be fp32 ({KB}, {M}) with contiguous rows")
+    if M and room < (KB - 1) * lds + (M + 3) // 4 * 4:
+        raise ValueError("the rows of xs must be padded to a multiple of four scales")
+    if dtype not in _DT:
+        raise ValueError(f"output type {dtype}")
+    y = out if out is not None else torch.empty(M, N, dtype=dtype, device=xq.device)
+    call("nvfp4_fp8_gemm", _whole(xq, "xq", (M, K), _CODES), xs.data_ptr(), lds, M, K, N, wp, wsp, _DT[dtype],
+         _whole(y, "out", (M, N), (dtype,)), st)
+    return y
 
 
 def fp8_linear(x: torch.Tensor, w: torch.Tensor, w_s: torch.Tensor, out: Optional[torch.Tensor] = None,
                workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y (M, N) = deq(quantize(x)) deq(w)^T in x's type: x (M, K) strided rows, w (N, K) e4m3 codes
     with w_s (ceil(N / 128), ceil(K / 128)) fp32 scales as checkpoints store them."""
-    with _Place(stream, x, w, w_s, out, workspace) as st:
-        ld = _ld(x, "x")
-        M, K = x.shape
-        N, wp, wsp = _fp8_weight(w, w_s, K)
-        y = out if out is not None else torch.empty(M, N, dtype=x.dtype, device=x.device)
-        n = int(lib().nvfp4_fp8_linear_workspace_bytes(M, K))
-        ws = workspace if workspace is not None else _u8(n, device=x.device)
-        call("nvfp4_fp8_linear", x.data_ptr(), _kind(x, "x"), M, K, ld, N, wp, wsp,
-             _whole(y, "out", (M, N), (x.dtype,)), _whole(ws, "workspace", (ws.numel(),), (torch.uint8,)), ws.numel(),
-             st)
-        return y
+    st = _here(stream, x, w, w_s, out, workspace)
+    if st < 0:
+        return _elsewhere(stream, (x, w, w_s, out, workspace), lambda: fp8_linear(x, w, w_s, out, workspace))
+    M, K = _size(x, "x")
+    ld = _ld(x, "x", M, K)
+    N, wp, wsp = _fp8_weight(w, w_s, K)
+    if out is not None:
+        _whole(out, "out", (M, N), (x.dtype,))
+    y = out if out is not None else torch.empty(M, N, dtype=x.dtype, device=x.device)
+    ws, ws_bytes = _scratch(workspace, "nvfp4_fp8_linear_workspace_bytes", x, M, K)
+    call("nvfp4_fp8_linear", x.data_ptr(), _kind(x, "x"), M, K, ld, N, wp, wsp, y.data_ptr(), ws.data_ptr(), ws_bytes,
+         st)
+    return y
 
 
 def _gated_args(x, w_gate, w_up, activation):
     if activation not in _ACT:
         raise ValueError(f"activation {activation!r}, expected one of {sorted(_ACT)}")
-    ld = _ld(x, "x")
-    if w_gate.dim() != 2:
-        raise ValueError("w_gate must be 2-D")
-    T, H = x.shape
-    I = w_gate.shape[0]
+    T, H = _size(x, "x")
+    ld = _ld(x, "x", T, H)
+    I = _size(w_gate, "w_gate")[0]
     return (T, H, I, ld, _kind(x, "x"), _whole(w_gate, "w_gate", (I, H), (x.dtype,)),
             _whole(w_up, "w_up", (I, H), (x.dtype,)), _ACT[activation])
 
@@ -457,13 +473,16 @@ def gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, acti
     ``activation``: "silu", "gelu" (erf) or "gelu_tanh".  With ``save`` returns (h, gu), gu (T, 2I) the
     fp32 pre-activations [g | u] that ``gated_linear_backward`` takes.  H % 8 == 0, I % 8 == 0.
     """
-    with _Place(stream, x, w_gate, w_up, out) as st:
-        T, H, I, ld, kind, gp, up, act = _gated_args(x, w_gate, w_up, activation)
-        h = out if out is not None else torch.empty(T, I, dtype=x.dtype, device=x.device)
-        gu = torch.empty(T, 2 * I, dtype=torch.float32, device=x.device) if save else None
-        call("nvfp4_gated_linear", x.data_ptr(), kind, T, H, ld, I, gp, up, act, _whole(h, "out", (T, I), (x.dtype,)),
-             _ptr(gu), st)
-        return (h, gu) if save else h
+    st = _here(stream, x, w_gate, w_up, out)
+    if st < 0:
+        return _elsewhere(stream, (x, w_gate, w_up, out), lambda: gated_linear(x, w_gate, w_up, activation, save, out))
+    T, H, I, ld, kind, gp, up, act = _gated_args(x, w_gate, w_up, activation)
+    if out is not None:
+        _whole(out, "out", (T, I), (x.dtype,))
+    h = out if out is not None else torch.empty(T, I, dtype=x.dtype, device=x.device)
+    gu = torch.empty(T, 2 * I, dtype=torch.float32, device=x.device) if save else None
+    call("nvfp4_gated_linear", x.data_ptr(), kind, T, H, ld, I, gp, up, act, h.data_ptr(), _ptr(gu), st)
+    return (h, gu) if save else h
 
 
 def gated_linear_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
@@ -471,23 +490,25 @@ def gated_linear_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tenso
                           workspace: Optional[torch.Tensor] = None, stream=None):
     """Gradients (dx (T, H), dw_gate (I, H), dw_up (I, H)) of ``gated_linear`` from dh (T, I) strided
     rows and the saved gu; those not asked for are None."""
-    with _Place(stream, x, dh, w_gate, w_up, gu, workspace) as st:
-        T, H, I, ld, kind, gp, up, act = _gated_args(x, w_gate, w_up, activation)
-        lddh = _ld(dh, "dh", T, I, x.dtype)
-        gup = _whole(gu, "gu", (T, 2 * I), (torch.float32,))
-        dx = torch.empty(T, H, dtype=x.dtype, device=x.device) if need_dx else None
-        dwg = torch.empty(I, H, dtype=x.dtype, device=x.device) if need_dw else None
-        dwu = torch.empty(I, H, dtype=x.dtype, device=x.device) if need_dw else None
-        n = int(lib().nvfp4_gated_linear_backward_workspace_bytes(T, I))
-        ws = workspace if workspace is not None else _u8(n, device=x.device)
-        call("nvfp4_gated_linear_backward", dh.data_ptr(), lddh, x.data_ptr(), ld, kind, T, H, I, gp, up, act, gup,
-             _ptr(dx), _ptr(dwg), _ptr(dwu), _whole(ws, "workspace", (ws.numel(),), (torch.uint8,)), ws.numel(), st)
-        return dx, dwg, dwu
+    st = _here(stream, x, dh, w_gate, w_up, gu, workspace)
+    if st < 0:
+        return _elsewhere(stream, (x, dh, w_gate, w_up, gu, workspace),
+                          lambda: gated_linear_backward(dh, x, w_gate, w_up, gu, activation, need_dx, need_dw, workspace))
+    T, H, I, ld, kind, gp, up, act = _gated_args(x, w_gate, w_up, activation)
+    lddh = _ld(dh, "dh", T, I, x.dtype)
+    gup = _whole(gu, "gu", (T, 2 * I), (torch.float32,))
+    dx = torch.empty(T, H, dtype=x.dtype, device=x.device) if need_dx else None
+    dwg = torch.empty(I, H, dtype=x.dtype, device=x.device) if need_dw else None
+    dwu = torch.empty(I, H, dtype=x.dtype, device=x.device) if need_dw else None
+    ws, ws_bytes = _scratch(workspace, "nvfp4_gated_linear_backward_workspace_bytes", x, T, I)
+    call("nvfp4_gated_linear_backward", dh.data_ptr(), lddh, x.data_ptr(), ld, kind, T, H, I, gp, up, act, gup,
+         _ptr(dx), _ptr(dwg), _ptr(dwu), ws.data_ptr(), ws_bytes, st)
+    return dx, dwg, dwu
 
 
 def _norm_args(f, r, gamma_after, gate, gamma_before):
-    ldf, kind = _ld(f, "f"), _kind(f, "f")
-    M, K = f.shape
+    M, K = _size(f, "f")
+    ldf, kind = _ld(f, "f", M, K), _kind(f, "f")
     if r.dtype != f.dtype and r.dtype != torch.float32:
         raise ValueError(f"r must be {f.dtype} or fp32, got {r.dtype}")
     ldr = _ld(r, "r", M, K)
@@ -516,14 +537,19 @@ def residual_norm(f: torch.Tensor, r: torch.Tensor, gamma_after: Optional[torch.
     (M, K; f's type or fp32) strided rows; gate (K,), (groups, K) for M / groups consecutive rows each,
     or (M, 1).  ``out`` receives r_out and may be r.  K % 8 == 0, K <= 16384.
     """
-    with _Place(stream, f, r, gamma_after, gate, gamma_before, out) as st:
-        M, K, ldf, ldr, kind, rkind, ga, gp, gkind, groups, gb = _norm_args(f, r, gamma_after, gate, gamma_before)
-        r_out = out if out is not None else torch.empty(M, K, dtype=r.dtype, device=f.device)
-        y = torch.empty(M, K, dtype=f.dtype, device=f.device) if gb is not None else None
-        stats = torch.empty(M, 2, dtype=torch.float32, device=f.device) if save else None
-        call("nvfp4_residual_norm", f.data_ptr(), kind, r.data_ptr(), rkind, M, K, ldf, ldr, ga, gp, gkind, groups, scale,
-             gb, eps, _whole(r_out, "out", (M, K), (r.dtype,)), _ptr(y), _ptr(stats), st)
-        return (r_out, y, stats) if save else (r_out, y)
+    st = _here(stream, f, r, gamma_after, gate, gamma_before, out)
+    if st < 0:
+        return _elsewhere(stream, (f, r, gamma_after, gate, gamma_before, out),
+                          lambda: residual_norm(f, r, gamma_after, gate, scale, gamma_before, eps, save, out))
+    M, K, ldf, ldr, kind, rkind, ga, gp, gkind, groups, gb = _norm_args(f, r, gamma_after, gate, gamma_before)
+    if out is not None:
+        _whole(out, "out", (M, K), (r.dtype,))
+    r_out = out if out is not None else torch.empty(M, K, dtype=r.dtype, device=r.device)
+    y = torch.empty(M, K, dtype=f.dtype, device=f.device) if gb is not None else None
+    stats = torch.empty(M, 2, dtype=torch.float32, device=f.device) if save else None
+    call("nvfp4_residual_norm", f.data_ptr(), kind, r.data_ptr(), rkind, M, K, ldf, ldr, ga, gp, gkind, groups, scale,
+         gb, eps, r_out.data_ptr(), _ptr(y), _ptr(stats), st)
+    return (r_out, y, stats) if save else (r_out, y)
 
 
 def residual_norm_backward(dr_out: Optional[torch.Tensor], dy: Optional[torch.Tensor], f: torch.Tensor,
@@ -537,26 +563,29 @@ def residual_norm_backward(dr_out: Optional[torch.Tensor], dy: Optional[torch.Te
     dr_out (r's type) and dy (f's type) are the gradients of r_out and y, strided rows; either may be
     None (zero).  The other arguments are the forward's (eps is already in ``stats``).
     """
-    with _Place(stream, f, r, dr_out, dy, stats, gamma_after, gate, gamma_before, workspace) as st:
-        M, K, ldf, ldr, kind, rkind, ga, gp, gkind, groups, gb = _norm_args(f, r, gamma_after, gate, gamma_before)
-        if dy is not None and gb is None:
-            raise ValueError("dy without gamma_before")
-        lddr = K if dr_out is None else _ld(dr_out, "dr_out", M, K, r.dtype)
-        lddy = K if dy is None else _ld(dy, "dy", M, K, f.dtype)
-        sp = _whole(stats, "stats", (M, 2), (torch.float32,))
-        df = torch.empty(M, K, dtype=f.dtype, device=f.device)
-        dr = torch.empty(M, K, dtype=r.dtype, device=f.device)
+    st = _here(stream, f, r, dr_out, dy, stats, gamma_after, gate, gamma_before, workspace)
+    if st < 0:
+        return _elsewhere(stream, (f, r, dr_out, dy, stats, gamma_after, gate, gamma_before, workspace),
+                          lambda: residual_norm_backward(dr_out, dy, f, r, stats, gamma_after, gate, scale, gamma_before,
+                                                         eps, workspace))
+    M, K, ldf, ldr, kind, rkind, ga, gp, gkind, groups, gb = _norm_args(f, r, gamma_after, gate, gamma_before)
+    if dy is not None and gb is None:
+        raise ValueError("dy without gamma_before")
+    lddr = K if dr_out is None else _ld(dr_out, "dr_out", M, K, r.dtype)
+    lddy = K if dy is None else _ld(dy, "dy", M, K, f.dtype)
+    sp = _whole(stats, "stats", (M, 2), (torch.float32,))
+    df = torch.empty(M, K, dtype=f.dtype, device=f.device)
+    dr = torch.empty(M, K, dtype=r.dtype, device=r.device)
 
-        def grad(p):
-            return None if p is None else torch.empty(p.shape, dtype=torch.float32, device=f.device)
+    def grad(p):
+        return None if p is None else torch.empty(p.shape, dtype=torch.float32, device=f.device)
 
-        dga, dgate, dgb = grad(gamma_after), grad(gate), grad(gamma_before)
-        n = int(lib().nvfp4_residual_norm_backward_workspace_bytes(M, K, max(groups, 1), rkind))
-        ws = workspace if workspace is not None else _u8(n, device=f.device)
-        call("nvfp4_residual_norm_backward", _ptr(dr_out), lddr, _ptr(dy), lddy, f.data_ptr(), kind, r.data_ptr(), rkind,
-             M, K, ldf, ldr, sp, ga, gp, gkind, groups, scale, gb, df.data_ptr(), dr.data_ptr(), _ptr(dga), _ptr(dgate),
-             _ptr(dgb), _whole(ws, "workspace", (ws.numel(),), (torch.uint8,)), ws.numel(), st)
-        return df, dr, dga, dgate, dgb
+    dga, dgate, dgb = grad(gamma_after), grad(gate), grad(gamma_before)
+    ws, ws_bytes = _scratch(workspace, "nvfp4_residual_norm_backward_workspace_bytes", f, M, K, max(groups, 1), rkind)
+    call("nvfp4_residual_norm_backward", _ptr(dr_out), lddr, _ptr(dy), lddy, f.data_ptr(), kind, r.data_ptr(), rkind,
+         M, K, ldf, ldr, sp, ga, gp, gkind, groups, scale, gb, df.data_ptr(), dr.data_ptr(), _ptr(dga), _ptr(dgate),
+         _ptr(dgb), ws.data_ptr(), ws_bytes, st)
+    return df, dr, dga, dgate, dgb
 
 
 # --------------------------------------------------------------------------- diagnostics
