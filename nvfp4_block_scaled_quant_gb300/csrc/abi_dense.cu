@@ -19,34 +19,63 @@ bool dims_ok(int64_t a, int64_t b) { return a < kMaxDim && b < kMaxDim && a * b 
   NV_REQUIRE(dims_ok(a, b), NVFP4_ERR_UNSUPPORTED_SHAPE, "sizes too large: %lld x %lld", (long long)(a), \
              (long long)(b))
 
+// Estimated times (in units of 10 ns) that choose between the GEMMs.  The coefficients were fitted to
+// times on a GB300 over M = 16 .. 2048 and five (K, N) between 512 x 512 and 7168 x 7168; they rank
+// the choices, nothing else depends on them.
+struct Cost {
+  int64_t start;             // of a launch
+  int64_t block256, block128;  // a K block of a 256- or 128-column pair tile
+  int64_t tile;              // a tile's start and end
+  int64_t tok_start[4], tok_block[4];  // weight-streaming GEMM of 16, 32, 64, 128 tokens
+};
+constexpr Cost kFp8Cost = {200, 46, 32, 160, {220, 250, 350, 500}, {40, 45, 60, 110}};
+constexpr Cost kGatedCost = {250, 33, 24, 200, {220, 250, 330, 0}, {50, 65, 78, 0}};
+
 // How the weight-streaming GEMM covers M tokens and N features: token tiles of `tok` columns and
-// clusters of `splits` CTAs along K.  The cost of a choice is its waves of CTAs (two per SM) times a
-// CTA's K blocks plus a fixed part (start-up, reduction) of about four blocks.
+// clusters of `splits` CTAs along K.  A choice costs its waves of CTAs (two per SM) times a CTA's K
+// blocks plus a fixed part (start-up, reduction) of about four.
 struct StreamPlan {
   int tok, splits;
+  int64_t cost;
 };
-StreamPlan stream_plan(int64_t M, int64_t N, int k_blocks, int max_tok, int sms) {
-  StreamPlan p;
-  p.tok = 16;
-  while (p.tok < max_tok && p.tok < M) p.tok *= 2;
+StreamPlan stream_plan(int64_t M, int64_t N, int k_blocks, int max_tok, int sms, const Cost &c) {
+  StreamPlan p = {16, 0, 0};
+  int size = 0;
+  while (p.tok < max_tok && p.tok < M) p.tok *= 2, ++size;
   const int64_t tiles = ((N + 127) / 128) * ((M + p.tok - 1) / p.tok);
   int64_t best = 0;
-  p.splits = 0;
   for (int s = 1; s <= kStreamMaxSplit && s <= k_blocks; ++s) {
     const int64_t waves = (tiles * s + 2 * sms - 1) / (2 * sms);
-    const int64_t cost = waves * ((k_blocks + s - 1) / s + 4);
-    if (p.splits == 0 || cost < best) {
-      best = cost;
+    const int64_t blocks = waves * ((k_blocks + s - 1) / s + 4);
+    if (p.splits == 0 || blocks < best) {
+      best = blocks;
       p.splits = s;
     }
   }
+  p.cost = c.tok_start[size] + best * c.tok_block[size];
   return p;
 }
 
-// Rows up to which the weight-streaming GEMM runs (more go to the 256-row tiles).
-constexpr int64_t kFp8StreamMaxM = 256;
+// Accumulator columns of the pair tiles for M x N outputs: 256, or 128 where the waves of tiles (one
+// pair per two SMs) then take less time.  out_cols: output columns of a 256-column tile.
+struct TilePlan {
+  int cols;
+  int64_t cost;
+};
+TilePlan tile_plan(int64_t M, int64_t N, int k_blocks, int out_cols, int sms, const Cost &c) {
+  const int64_t m = (M + kTRows - 1) / kTRows, pairs = sms / 2;
+  const int64_t w = m * ((N + out_cols - 1) / out_cols), n = m * ((N + out_cols / 2 - 1) / (out_cols / 2));
+  const int64_t cost_w = (w + pairs - 1) / pairs * (k_blocks * c.block256 + c.tile);
+  const int64_t cost_n = (n + pairs - 1) / pairs * (k_blocks * c.block128 + c.tile);
+  return cost_n < cost_w ? TilePlan{128, c.start + cost_n} : TilePlan{256, c.start + cost_w};
+}
+
+// The weight-streaming GEMM is considered up to kStreamMaxM rows (its token tiles re-read the weights),
+// and taken up to kStreamMinM whatever the estimates: a pair tile's 128-row boxes of a tensor of 64
+// rows or fewer load at half speed (1536 -> 16384: 22 us for M = 64, 10.5 us for M = 100).
+constexpr int64_t kStreamMinM = 64;
+constexpr int64_t kStreamMaxM = 256;
 constexpr int kFp8StreamTok = 128;
-constexpr int64_t kGatedStreamMaxM = 128;
 constexpr int kGatedStreamTok = 64;
 
 nvfp4_status fp8_gemm_impl(const char *fn, DeviceInfo *d, const uint8_t *xq, const float *xs, int64_t lds, int64_t M,
@@ -55,8 +84,9 @@ nvfp4_status fp8_gemm_impl(const char *fn, DeviceInfo *d, const uint8_t *xq, con
   const int k_blocks = static_cast<int>((K + 127) / 128);
   CUtensorMap mx, mw;
   nvfp4_status st;
-  if (M <= kFp8StreamMaxM) {
-    const StreamPlan p = stream_plan(M, N, k_blocks, kFp8StreamTok, d->sms);
+  const TilePlan tp = tile_plan(M, N, k_blocks, 256, d->sms, kFp8Cost);
+  const StreamPlan p = stream_plan(M, N, k_blocks, kFp8StreamTok, d->sms, kFp8Cost);
+  if (M <= kStreamMinM || (M <= kStreamMaxM && p.cost <= tp.cost)) {
     if ((st = make_map(fn, &mx, xq, K, M, K, p.tok)) != NVFP4_OK) return st;
     if ((st = make_map(fn, &mw, w, K, N, K, 128)) != NVFP4_OK) return st;
     StreamArgs a = {};
@@ -73,7 +103,7 @@ nvfp4_status fp8_gemm_impl(const char *fn, DeviceInfo *d, const uint8_t *xq, con
     return NVFP4_OK;
   }
   if ((st = make_map(fn, &mx, xq, K, M, K, kTHalf)) != NVFP4_OK) return st;
-  if ((st = make_map(fn, &mw, w, K, N, K, kTHalf)) != NVFP4_OK) return st;
+  if ((st = make_map(fn, &mw, w, K, N, K, tp.cols / 2)) != NVFP4_OK) return st;
   TileArgs a = {};
   a.M = static_cast<int>(M);
   a.N = static_cast<int>(N);
@@ -85,7 +115,7 @@ nvfp4_status fp8_gemm_impl(const char *fn, DeviceInfo *d, const uint8_t *xq, con
   a.out = y;
   a.ldo = N;
   a.err = d->flags;
-  NV_CUDA(launch_fp8_tile_gemm(mx, mw, a, dtype, s), "FP8 tile GEMM launch");
+  NV_CUDA(launch_fp8_tile_gemm(mx, mw, a, dtype, tp.cols, s), "FP8 tile GEMM launch");
   return NVFP4_OK;
 }
 
@@ -107,7 +137,8 @@ struct Fp8Ws {
   int64_t lds;
 };
 Fp8Ws fp8_ws(int64_t M, int64_t K) {
-  Fp8Ws w;
+  Fp8Ws w = {};
+  if (M <= kFp8FusedMaxM) return w;  // quantised in the GEMM
   w.lds = round_up(M, 4);
   w.q = 0;
   w.s = align256(static_cast<size_t>(M) * static_cast<size_t>(K));
@@ -198,6 +229,24 @@ nvfp4_status nvfp4_fp8_linear(const void *x, int dtype, int64_t M, int64_t K, in
   if ((st = device_info(__func__, &d)) != NVFP4_OK) return st;
   if (M == 0) return NVFP4_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (M <= kFp8FusedMaxM) {
+    CUtensorMap mw;
+    if ((st = make_map(__func__, &mw, w, K, N, K, 128)) != NVFP4_OK) return st;
+    StreamArgs a = {};
+    a.M = static_cast<int>(M);
+    a.N = static_cast<int>(N);
+    a.K = static_cast<int>(K);
+    a.k_blocks = static_cast<int>((K + 127) / 128);
+    a.sw = w_s;
+    a.out = y;
+    a.ldo = N;
+    a.x = x;
+    a.ldx = ldx;
+    a.err = d->flags;
+    const StreamPlan p = stream_plan(M, N, a.k_blocks, kFp8FusedMaxM, d->sms, kFp8Cost);
+    NV_CUDA(launch_fp8_stream_linear(mw, a, dtype, p.tok, p.splits, s), "FP8 linear launch");
+    return NVFP4_OK;
+  }
   uint8_t *q = static_cast<uint8_t *>(ws) + L.q;
   float *xs = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + L.s);
   NV_CUDA(launch_fp8_quantize_act(x, dtype, M, K, ldx, q, xs, L.lds, d->sms, s), "FP8 quantise launch");
@@ -238,10 +287,13 @@ nvfp4_status nvfp4_gated_linear(const void *x, int dtype, int64_t T, int64_t H, 
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int k_blocks = static_cast<int>((H + 63) / 64);
   CUtensorMap mx, mg, mu;
-  if ((st = make_map(__func__, &mg, w_gate, H * 2, I, H * 2, 128)) != NVFP4_OK) return st;
-  if ((st = make_map(__func__, &mu, w_up, H * 2, I, H * 2, 128)) != NVFP4_OK) return st;
-  if (T <= kGatedStreamMaxM) {
-    const StreamPlan p = stream_plan(T, I, k_blocks, kGatedStreamTok, d->sms);
+  const TilePlan tp = tile_plan(T, I, k_blocks, 128, d->sms, kGatedCost);
+  const StreamPlan p = stream_plan(T, I, k_blocks, kGatedStreamTok, d->sms, kGatedCost);
+  const bool stream_weights = T <= kStreamMinM || (T <= kStreamMaxM && p.cost <= tp.cost);
+  const int cols = stream_weights ? 256 : tp.cols;
+  if ((st = make_map(__func__, &mg, w_gate, H * 2, I, H * 2, cols / 2)) != NVFP4_OK) return st;
+  if ((st = make_map(__func__, &mu, w_up, H * 2, I, H * 2, cols / 2)) != NVFP4_OK) return st;
+  if (stream_weights) {
     if ((st = make_map(__func__, &mx, x, H * 2, T, ldx * 2, p.tok)) != NVFP4_OK) return st;
     StreamArgs a = {};
     a.M = static_cast<int>(T);
@@ -264,7 +316,7 @@ nvfp4_status nvfp4_gated_linear(const void *x, int dtype, int64_t T, int64_t H, 
   a.ldo = I;
   a.save = gu;
   a.err = d->flags;
-  NV_CUDA(launch_gated_tile_gemm(mx, mg, mu, a, dtype, act, s), "gated tile GEMM launch");
+  NV_CUDA(launch_gated_tile_gemm(mx, mg, mu, a, dtype, act, cols, s), "gated tile GEMM launch");
   return NVFP4_OK;
 }
 
@@ -313,7 +365,8 @@ nvfp4_status nvfp4_gated_linear_backward(const void *dh, int64_t lddh, const voi
     a.out = dx;
     a.ldo = H;
     a.err = d->flags;
-    NV_CUDA(launch_gated_dx_gemm(mdg, mdu, mg, mu, a, dtype, s), "input gradient launch");
+    const int cols = tile_plan(T, H, 2 * a.k_blocks, 256, d->sms, kGatedCost).cols;
+    NV_CUDA(launch_gated_dx_gemm(mdg, mdu, mg, mu, a, dtype, cols, s), "input gradient launch");
   }
   if (dw_gate) {
     CUtensorMap ma, mx;
@@ -328,7 +381,8 @@ nvfp4_status nvfp4_gated_linear_backward(const void *dh, int64_t lddh, const voi
     a.out2 = dw_up;
     a.ldo = H;
     a.err = d->flags;
-    NV_CUDA(launch_gated_dw_gemm(ma, mx, a, dtype, s), "weight gradient launch");
+    const int cols = tile_plan(2 * I, H, a.k_blocks, 256, d->sms, kGatedCost).cols;
+    NV_CUDA(launch_gated_dw_gemm(ma, mx, a, dtype, cols, s), "weight gradient launch");
   }
   return NVFP4_OK;
 }

@@ -9,6 +9,7 @@
 // divides in IEEE fp32.  A NaN in a block gives a NaN scale (the maximum is taken over the bits of
 // |x|, where NaN orders above infinity) and an infinity an infinite one: either way every output of
 // that row is NaN, never a finite number made from a dropped NaN.
+#include "fp8_encode.cuh"
 #include "stream_gemm.cuh"
 #include "tile_gemm.cuh"
 
@@ -20,26 +21,6 @@ constexpr int kFqThreads = 256;
 constexpr int kFqGroup = 16;                         // lanes of one 128-element block (8 elements each)
 constexpr int kFqRows = kFqThreads / kFqGroup;       // rows of a CTA
 constexpr int kFqUnroll = 4;                         // blocks of a row in flight per lane
-
-__device__ __forceinline__ uint32_t max_abs16(const uint4 v) {
-  uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
-  return max(m & 0xFFFFu, m >> 16);
-}
-
-__device__ __forceinline__ uint32_t e4m3x2(float a, float b) {
-  return static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3));
-}
-
-// 8 elements -> 8 codes
-template <class T>
-__device__ __forceinline__ uint2 encode8(const uint4 v, float s) {
-  if (s == 0.f) return make_uint2(0u, 0u);
-  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-  uint32_t c[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) c[i] = e4m3x2(__fdiv_rn(T::lo(w[i]), s), __fdiv_rn(T::hi(w[i]), s));
-  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-}
 
 // One pass over x: a 16-lane group holds one block of one row, 16 rows per CTA, so that the scales
 // of a block column leave as 64 consecutive bytes.  Bound by memory (2 bytes in, 1 out per element).
@@ -126,16 +107,16 @@ cudaError_t launch_fp8_quantize_weight(const void *w, int dtype, int64_t N, int6
                     ldw, q, s);
 }
 
-cudaError_t launch_fp8_tile_gemm(const CUtensorMap &a, const CUtensorMap &b, const TileArgs &args, int dtype,
+cudaError_t launch_fp8_tile_gemm(const CUtensorMap &a, const CUtensorMap &b, const TileArgs &args, int dtype, int cols,
                                  cudaStream_t s) {
-  return dtype == NVFP4_DT_BF16 ? launch_tile_gemm_as<TileOp::kFp8, Bf16, 0>(a, a, b, b, args, s)
-                                : launch_tile_gemm_as<TileOp::kFp8, Fp16, 0>(a, a, b, b, args, s);
+  return dtype == NVFP4_DT_BF16 ? launch_tile_gemm_as<TileOp::kFp8, Bf16, 0>(a, a, b, b, args, cols, s)
+                                : launch_tile_gemm_as<TileOp::kFp8, Fp16, 0>(a, a, b, b, args, cols, s);
 }
 
 cudaError_t launch_fp8_stream_gemm(const CUtensorMap &w, const CUtensorMap &x, const StreamArgs &args, int dtype,
                                    int tok, int splits, cudaStream_t s) {
-#define NVFP4_TOK(n)                                                                          \
-  case n:                                                                                     \
+#define NVFP4_TOK(n)                                                                                   \
+  case n:                                                                                              \
     return dtype == NVFP4_DT_BF16 ? launch_stream_gemm_as<true, Bf16, 0, n>(w, w, x, args, splits, s) \
                                   : launch_stream_gemm_as<true, Fp16, 0, n>(w, w, x, args, splits, s)
   switch (tok) {
@@ -143,6 +124,20 @@ cudaError_t launch_fp8_stream_gemm(const CUtensorMap &w, const CUtensorMap &x, c
     NVFP4_TOK(32);
     NVFP4_TOK(64);
     NVFP4_TOK(128);
+  }
+#undef NVFP4_TOK
+  return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_fp8_stream_linear(const CUtensorMap &w, const StreamArgs &args, int dtype, int tok, int splits,
+                                     cudaStream_t s) {
+#define NVFP4_TOK(n)                                                                                         \
+  case n:                                                                                                    \
+    return dtype == NVFP4_DT_BF16 ? launch_stream_gemm_as<true, Bf16, 0, n, true>(w, w, w, args, splits, s) \
+                                  : launch_stream_gemm_as<true, Fp16, 0, n, true>(w, w, w, args, splits, s)
+  switch (tok) {
+    NVFP4_TOK(16);
+    NVFP4_TOK(32);
   }
 #undef NVFP4_TOK
   return cudaErrorInvalidValue;

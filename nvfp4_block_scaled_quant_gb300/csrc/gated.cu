@@ -72,9 +72,9 @@ cudaError_t launch_gated_grad(const void *dh, int64_t lddh, const float *gu, int
 }
 
 cudaError_t launch_gated_tile_gemm(const CUtensorMap &x, const CUtensorMap &wg, const CUtensorMap &wu,
-                                   const TileArgs &args, int dtype, int act, cudaStream_t s) {
-  NVFP4_BY_ACT(return dtype == NVFP4_DT_BF16 ? (launch_tile_gemm_as<TileOp::kGated, Bf16, kAct>(x, x, wg, wu, args, s))
-                                             : (launch_tile_gemm_as<TileOp::kGated, Fp16, kAct>(x, x, wg, wu, args, s)));
+                                   const TileArgs &args, int dtype, int act, int cols, cudaStream_t s) {
+  NVFP4_BY_ACT(return dtype == NVFP4_DT_BF16 ? (launch_tile_gemm_as<TileOp::kGated, Bf16, kAct>(x, x, wg, wu, args, cols, s))
+                                             : (launch_tile_gemm_as<TileOp::kGated, Fp16, kAct>(x, x, wg, wu, args, cols, s)));
 }
 
 template <int kTok>
@@ -96,15 +96,15 @@ cudaError_t launch_gated_stream_gemm(const CUtensorMap &x, const CUtensorMap &wg
 }
 
 cudaError_t launch_gated_dx_gemm(const CUtensorMap &dg, const CUtensorMap &du, const CUtensorMap &wg,
-                                 const CUtensorMap &wu, const TileArgs &args, int dtype, cudaStream_t s) {
-  return dtype == NVFP4_DT_BF16 ? launch_tile_gemm_as<TileOp::kDx, Bf16, 0>(dg, du, wg, wu, args, s)
-                                : launch_tile_gemm_as<TileOp::kDx, Fp16, 0>(dg, du, wg, wu, args, s);
+                                 const CUtensorMap &wu, const TileArgs &args, int dtype, int cols, cudaStream_t s) {
+  return dtype == NVFP4_DT_BF16 ? launch_tile_gemm_as<TileOp::kDx, Bf16, 0>(dg, du, wg, wu, args, cols, s)
+                                : launch_tile_gemm_as<TileOp::kDx, Fp16, 0>(dg, du, wg, wu, args, cols, s);
 }
 
-cudaError_t launch_gated_dw_gemm(const CUtensorMap &dgu, const CUtensorMap &x, const TileArgs &args, int dtype,
+cudaError_t launch_gated_dw_gemm(const CUtensorMap &dgu, const CUtensorMap &x, const TileArgs &args, int dtype, int cols,
                                  cudaStream_t s) {
-  return dtype == NVFP4_DT_BF16 ? launch_tile_gemm_as<TileOp::kDw, Bf16, 0>(dgu, dgu, x, x, args, s)
-                                : launch_tile_gemm_as<TileOp::kDw, Fp16, 0>(dgu, dgu, x, x, args, s);
+  return dtype == NVFP4_DT_BF16 ? launch_tile_gemm_as<TileOp::kDw, Bf16, 0>(dgu, dgu, x, x, args, cols, s)
+                                : launch_tile_gemm_as<TileOp::kDw, Fp16, 0>(dgu, dgu, x, x, args, cols, s);
 }
 
 }  // namespace nvfp4

@@ -300,21 +300,25 @@ cudaError_t launch_fp8_quantize_act(const void *x, int dtype, int64_t M, int64_t
                                     int64_t lds, int sms, cudaStream_t st);
 cudaError_t launch_fp8_quantize_weight(const void *w, int dtype, int64_t N, int64_t K, int64_t ldw, uint8_t *q,
                                        float *s, cudaStream_t st);
-cudaError_t launch_fp8_tile_gemm(const CUtensorMap &a, const CUtensorMap &b, const TileArgs &args, int dtype,
+cudaError_t launch_fp8_tile_gemm(const CUtensorMap &a, const CUtensorMap &b, const TileArgs &args, int dtype, int cols,
                                  cudaStream_t s);
 cudaError_t launch_fp8_stream_gemm(const CUtensorMap &w, const CUtensorMap &x, const StreamArgs &args, int dtype,
                                    int tok, int splits, cudaStream_t s);
+// The same with the activations quantised in the GEMM (args.x, tok 16 or 32).
+cudaError_t launch_fp8_stream_linear(const CUtensorMap &w, const StreamArgs &args, int dtype, int tok, int splits,
+                                     cudaStream_t s);
+constexpr int64_t kFp8FusedMaxM = 32;
 
 // ---------------------------------------------------------------- gated linear
 cudaError_t launch_gated_tile_gemm(const CUtensorMap &x, const CUtensorMap &wg, const CUtensorMap &wu,
-                                   const TileArgs &args, int dtype, int act, cudaStream_t s);
+                                   const TileArgs &args, int dtype, int act, int cols, cudaStream_t s);
 cudaError_t launch_gated_stream_gemm(const CUtensorMap &x, const CUtensorMap &wg, const CUtensorMap &wu,
                                      const StreamArgs &args, int dtype, int act, int tok, int splits, cudaStream_t s);
 cudaError_t launch_gated_grad(const void *dh, int64_t lddh, const float *gu, int64_t M, int64_t I, int dtype, int act,
                               void *dgu, int sms, cudaStream_t s);
 cudaError_t launch_gated_dx_gemm(const CUtensorMap &dg, const CUtensorMap &du, const CUtensorMap &wg,
-                                 const CUtensorMap &wu, const TileArgs &args, int dtype, cudaStream_t s);
-cudaError_t launch_gated_dw_gemm(const CUtensorMap &dgu, const CUtensorMap &x, const TileArgs &args, int dtype,
+                                 const CUtensorMap &wu, const TileArgs &args, int dtype, int cols, cudaStream_t s);
+cudaError_t launch_gated_dw_gemm(const CUtensorMap &dgu, const CUtensorMap &x, const TileArgs &args, int dtype, int cols,
                                  cudaStream_t s);
 
 // ---------------------------------------------------------------- residual norm
@@ -360,6 +364,7 @@ constexpr int kNormSlice = 8 * kNormGradThreads;  // columns of a backward CTA (
 constexpr int kNormMaxSlices = 3;    // ceil(kNormMaxK / kNormSlice)
 constexpr int kNormMaxStages = 4;
 constexpr int kNormMaxSmem = 225 * 1024;
+constexpr int kNormGradRows = 4;     // rows of a backward CTA aimed at when there are few
 constexpr int kNormSms = 152;        // the plan must not depend on the device: it sizes the workspace
 NormGradPlan norm_grad_plan(int64_t M, int64_t K, int64_t groups, bool r32);
 cudaError_t launch_residual_norm(const NormArgs &a, int dtype, bool r32, int sms, cudaStream_t s);

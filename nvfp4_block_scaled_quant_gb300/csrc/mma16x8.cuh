@@ -81,10 +81,31 @@ __device__ __forceinline__ uint64_t pack_f32x2(float a, float b) {
 __device__ __forceinline__ void unpack_f32x2(uint64_t d, float &a, float &b) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(d));
 }
+__device__ __forceinline__ uint64_t mul_f32x2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ uint64_t fma_f32x2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t d;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
+}
+
+// ---------------------------------------------------------------- meeting points
+
+// __syncthreads and the cluster barrier for warps that come from role branches: the barrier instructions
+// (and the .aligned tensor-memory instructions around them) need converged warps, and the lanes of
+// a warp may leave a wait one after the other.
+__device__ __forceinline__ void block_meet() {
+  __syncwarp();
+  __syncthreads();
+  __syncwarp();
+}
+__device__ __forceinline__ void cluster_meet() {
+  __syncwarp();
+  cluster_sync();
+  __syncwarp();
 }
 
 // ---------------------------------------------------------------- TMA for a CTA pair

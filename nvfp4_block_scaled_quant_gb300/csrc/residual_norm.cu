@@ -6,13 +6,14 @@
 //
 // with rstd(v) = 1 / sqrt(mean(v^2) + eps) over a row, all in fp32, and its backward pass.
 //
-// Backward of one row, with fh = f rstd(f), rh = r' rstd(r'), v = dy gb, and the sums over the row
-//   c2 = sum v rh,  A = sum q (dr' + ib v),  C = sum q rh,  q = n gate (n alone for a gate per row):
-//   dR    = dr' + ib (v - rh c2 / K)           the gradient of r' (and of r)
-//   S     = sum q dR = A - ib c2 C / K
-//   dgate = scale dR n                         (a gate per row: scale S)
-//   df    = ia (scale gate dR ga - fh scale [gate] S / K)
-//   dga  += scale gate dR fh,   dgb += dy rh
+// Backward of one row, with w = ga gate (ga alone for a gate per row), ia = rstd(f), ib = rstd(r'),
+// c = scale ia (times the row's gate), t = w f, R = r + c t (which is r'), u = dr' + ib dy gb, and the
+// sums over the row C2 = sum dy gb R, A = sum t u, C = sum t R:
+//   kappa = ib^3 C2 / K,  dR = u - kappa R               the gradient of r' (and of r)
+//   S     = sum (ia t) dR = ia (A - kappa C)
+//   df    = c w dR - f ia^2 (c / ia) S / K                (the second term is the norm's)
+//   dgate = ga z, dga = gate z with z = sum over rows of c f dR; for a gate per row dgate = scale S
+//   dgb   = sum over rows of ib dy R
 // S is linear in dR, so the three sums come from one sweep and one reduction over the block.
 // rstd(f) and rstd(r') are kept by the forward (8 bytes per row); everything else is recomputed.
 //
@@ -56,30 +57,71 @@ struct Res {
   }
 };
 
-// The same four elements at a time.
-template <class T, bool kF32>
-struct Four {
-  static __device__ __forceinline__ void load(const void *p, int64_t i, float (&v)[4]) {
-    if constexpr (kF32) {
-      const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i);
-      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
-    } else {
-      const uint2 a = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
-      v[0] = T::lo(a.x), v[1] = T::hi(a.x), v[2] = T::lo(a.y), v[3] = T::hi(a.y);
-    }
-  }
-  static __device__ __forceinline__ void store(void *p, int64_t i, const float (&v)[4]) {
-    if constexpr (kF32)
-      *reinterpret_cast<float4 *>(static_cast<float *>(p) + i) = make_float4(v[0], v[1], v[2], v[3]);
-    else
-      *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + i) = make_uint2(T::pack(v[0], v[1]), T::pack(v[2], v[3]));
-  }
+// Pairs of fp32 values: two elements per instruction, where the number of instructions is what bounds
+// a kernel (the many-row kernels: about as many as the memory leaves time for).
+struct Two {
+  uint64_t v;
 };
-// Element i of four packed 16-bit values.
+__device__ __forceinline__ Two two(float a, float b) { return {pack_f32x2(a, b)}; }
+__device__ __forceinline__ Two both(float a) { return {pack_f32x2(a, a)}; }
+__device__ __forceinline__ Two operator*(Two a, Two b) { return {mul_f32x2(a.v, b.v)}; }
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) { return {fma_f32x2(a.v, b.v, c.v)}; }
+__device__ __forceinline__ float sum2(Two a) {
+  float x, y;
+  unpack_f32x2(a.v, x, y);
+  return x + y;
+}
 template <class T>
-__device__ __forceinline__ float at4(const uint2 w, int i) {
-  const uint32_t x = i < 2 ? w.x : w.y;
-  return (i & 1) ? T::hi(x) : T::lo(x);
+__device__ __forceinline__ Two two_of(uint32_t w) {
+  return two(T::lo(w), T::hi(w));
+}
+template <class T>
+__device__ __forceinline__ uint32_t pack_two(Two a) {
+  float x, y;
+  unpack_f32x2(a.v, x, y);
+  return T::pack(x, y);
+}
+
+// kPairs pairs of elements at element i: fp32, or the 16-bit type T.
+template <class T, bool kF32, int kPairs>
+__device__ __forceinline__ void load_pairs(const void *p, int64_t i, Two (&v)[kPairs]) {
+  if constexpr (kF32) {
+#pragma unroll
+    for (int k = 0; k < kPairs; k += 2) {
+      const float4 a = *reinterpret_cast<const float4 *>(static_cast<const float *>(p) + i + 2 * k);
+      v[k] = two(a.x, a.y), v[k + 1] = two(a.z, a.w);
+    }
+  } else if constexpr (kPairs == 2) {
+    const uint2 a = *reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(p) + i);
+    v[0] = two_of<T>(a.x), v[1] = two_of<T>(a.y);
+  } else {
+    const uint4 a = *reinterpret_cast<const uint4 *>(static_cast<const uint16_t *>(p) + i);
+    v[0] = two_of<T>(a.x), v[1] = two_of<T>(a.y), v[2] = two_of<T>(a.z), v[3] = two_of<T>(a.w);
+  }
+}
+template <class T, bool kF32, int kPairs>
+__device__ __forceinline__ void store_pairs(void *p, int64_t i, const Two (&v)[kPairs]) {
+  if constexpr (kF32) {
+#pragma unroll
+    for (int k = 0; k < kPairs; k += 2) {
+      float4 a;
+      unpack_f32x2(v[k].v, a.x, a.y);
+      unpack_f32x2(v[k + 1].v, a.z, a.w);
+      *reinterpret_cast<float4 *>(static_cast<float *>(p) + i + 2 * k) = a;
+    }
+  } else if constexpr (kPairs == 2) {
+    *reinterpret_cast<uint2 *>(static_cast<uint16_t *>(p) + i) = make_uint2(pack_two<T>(v[0]), pack_two<T>(v[1]));
+  } else {
+    *reinterpret_cast<uint4 *>(static_cast<uint16_t *>(p) + i) =
+        make_uint4(pack_two<T>(v[0]), pack_two<T>(v[1]), pack_two<T>(v[2]), pack_two<T>(v[3]));
+  }
+}
+// The same of an optional row vector of parameters: `otherwise` where it is absent.
+template <class T, int kPairs>
+__device__ __forceinline__ void load_params(const void *p, int64_t i, float otherwise, Two (&v)[kPairs]) {
+#pragma unroll
+  for (int k = 0; k < kPairs; ++k) v[k] = both(otherwise);
+  if (p) load_pairs<T, false, kPairs>(p, i, v);
 }
 
 // 8 values of an optional 16-bit row vector, `otherwise` where it is absent.
@@ -210,8 +252,11 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const NormArgs a
 // Many rows: each CTA walks its rows through a ring in shared memory (one bulk copy per row and
 // tensor), so the next rows load while this one passes its two reductions.  16 columns per thread
 // and two CTAs per SM at most widths: one CTA's reductions overlap the other's.
-template <class T, bool kR32, int kChunks>
-__global__ void __launch_bounds__(1024, 1) residual_norm_rows_kernel(const NormArgs a, int stages) {
+// kThreads, kCtas: most threads of a CTA and CTAs per SM, which set the registers per thread: the
+// parameters of a thread's columns stay in registers (the ring leaves little of the SM's memory to
+// its cache, and re-reading them for every row cost as much as the rows).
+template <class T, bool kR32, int kChunks, int kThreads, int kCtas>
+__global__ void __launch_bounds__(kThreads, kCtas) residual_norm_rows_kernel(const NormArgs a, int stages) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) &
                                               ~static_cast<uintptr_t>(127));
@@ -243,52 +288,71 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_rows_kernel(const NormA
   int s = 0;
   uint32_t phase = 0;
   const uint16_t *gate0 = static_cast<const uint16_t *>(a.gate);
+  const bool channel_gate = a.gate_kind == NVFP4_GATE_CHANNEL;
+  // w = ga gate and gb of the thread's columns: r' = r + (scale rstd(f)) w f, y = (rstd(r') r') gb
+  Two w[kChunks][4], gb[kChunks][4];
+  auto load_w = [&](int64_t g) {
+#pragma unroll
+    for (int u = 0; u < kChunks; ++u) {
+      const int c = tid + u * nt;
+      Two gate[4];
+      const bool live = c < chunks;
+      load_params<T, 4>(live ? a.ga : nullptr, c * 8, 1.f, w[u]);
+      load_params<T, 4>(live && channel_gate ? gate0 + g * a.K : nullptr, c * 8, 1.f, gate);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[u][i] = w[u][i] * gate[i];
+    }
+  };
+  load_w(0);
+#pragma unroll
+  for (int u = 0; u < kChunks; ++u)
+    load_params<T, 4>(tid + u * nt < chunks ? a.gb : nullptr, (tid + u * nt) * 8, 1.f, gb[u]);
+  int64_t group = 0;
   float next_gm = a.gate_kind == NVFP4_GATE_ROW && blockIdx.x < a.M ? T::up(__ldg(gate0 + blockIdx.x)) : 1.f;
   for (int64_t m = blockIdx.x; m < a.M; m += step) {
     const float gm = a.scale * next_gm;
     if (a.gate_kind == NVFP4_GATE_ROW && m + step < a.M) next_gm = T::up(__ldg(gate0 + m + step));
-    const uint16_t *gate = a.gate_kind == NVFP4_GATE_CHANNEL ? gate0 + static_cast<int64_t>(group_of(m, a.rows_per_group)) * a.K : nullptr;
+    if (channel_gate) {
+      const int64_t g = group_of(m, a.rows_per_group);
+      if (g != group) {
+        group = g;
+        load_w(g);
+      }
+    }
     // a wait that gives up raises the fault flag; every barrier below is still met
     mbar_wait_bounded(&full[s], phase, abort_flag, a.err, kPipelineTimeoutNs);
     const uint8_t *d = smem + s * stage_bytes;
-    float v[kChunks][8];
-    float sum = 0.f;
-    float ia = 1.f;
-    if (a.ga) {
-#pragma unroll
-      for (int u = 0; u < kChunks; ++u) {
-        const int c = tid + u * nt;
-        if (c < chunks) {
-          Res<T, false>::load(d, c * 8, v[u]);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) sum += v[u][i] * v[u][i];
-        }
-      }
-      ia = rstd_of(block_sum(sum, red[0]), a.K, a.eps);
-    }
-    sum = 0.f;
+    Two v[kChunks][4];
+    Two sum = both(0.f);
 #pragma unroll
     for (int u = 0; u < kChunks; ++u) {
       const int c = tid + u * nt;
       if (c < chunks) {
-        float x[8], w[8];
-        if (!a.ga) Res<T, false>::load(d, c * 8, v[u]);
-        load_opt<T>(static_cast<const uint16_t *>(a.ga), c * 8, 1.f, w);
+        load_pairs<T, false, 4>(d, c * 8, v[u]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[u][i] *= ia * w[i];
-        load_opt<T>(gate, c * 8, 1.f, w);
-        Res<T, kR32>::load(d + n16, c * 8, x);
+        for (int i = 0; i < 4; ++i) sum = fma2(v[u][i], v[u][i], sum);
+      }
+    }
+    const float ia = a.ga ? rstd_of(block_sum(sum2(sum), red[0]), a.K, a.eps) : 1.f;
+    const Two c1 = both(gm * ia);
+    sum = both(0.f);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          v[u][i] = x[i] + gm * w[i] * v[u][i];
-          sum += v[u][i] * v[u][i];
+    for (int u = 0; u < kChunks; ++u) {
+      const int c = tid + u * nt;
+      if (c < chunks) {
+        Two x[4];
+        load_pairs<T, kR32, 4>(d + n16, c * 8, x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          v[u][i] = fma2(c1, v[u][i] * w[u][i], x[i]);
+          sum = fma2(v[u][i], v[u][i], sum);
         }
-        Res<T, kR32>::store(a.r_out, m * a.ldr_out + c * 8, v[u]);
+        store_pairs<T, kR32, 4>(a.r_out, m * a.ldr_out + c * 8, v[u]);
       }
     }
     float ib = 0.f;
     if (a.gb) {
-      ib = rstd_of(block_sum(sum, red[1]), a.K, a.eps);  // its barrier: every thread has read the stage
+      ib = rstd_of(block_sum(sum2(sum), red[1]), a.K, a.eps);  // its barrier: every thread has read the stage
     } else {
       __syncthreads();
     }
@@ -302,11 +366,9 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_rows_kernel(const NormA
       for (int u = 0; u < kChunks; ++u) {
         const int c = tid + u * nt;
         if (c < chunks) {
-          float gb[8];
-          load_opt<T>(static_cast<const uint16_t *>(a.gb), c * 8, 1.f, gb);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) v[u][i] *= ib * gb[i];
-          Res<T, false>::store(a.y, m * a.K + c * 8, v[u]);
+          for (int i = 0; i < 4; ++i) v[u][i] = (v[u][i] * both(ib)) * gb[u][i];
+          store_pairs<T, false, 4>(a.y, m * a.K + c * 8, v[u]);
         }
       }
       // red[1] is written again only after the next row's first barrier, or this one without ga
@@ -388,24 +450,16 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
   const uint16_t *gp = static_cast<const uint16_t *>(a.gate);
   const bool row_gate = a.gate_kind == NVFP4_GATE_ROW, channel_gate = a.gate_kind == NVFP4_GATE_CHANNEL;
   const float inv_k = 1.f / static_cast<float>(a.K);
-  // parameters of the thread's columns, packed as stored; the gate's change with the group of rows
-  uint2 ga[2], gb[2], gk[2];
-  const uint32_t one = T::pack(1.f, 1.f);
+  // Per thread and column: w = ga gate (it changes with the group of rows) and gb; the sums over rows
+  // of dy rh (dgb) and z = scale ia f dR, of which both dga = gate z and dgate = ga z are multiples.
+  Two w[2][2], gb[2][2], acc_a[2][2], acc_b[2][2], acc_z[2][2];
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    ga[h] = gk[h] = make_uint2(one, one);
-    gb[h] = make_uint2(0u, 0u);
-    if (live[h]) {
-      if (a.ga) ga[h] = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.ga) + k0 + col[h]));
-      if (a.gb) gb[h] = __ldg(reinterpret_cast<const uint2 *>(static_cast<const uint16_t *>(a.gb) + k0 + col[h]));
-    }
+    load_params<T, 2>(live[h] ? a.gb : nullptr, k0 + col[h], 0.f, gb[h]);
+    if (!a.gb) gb[h][0] = gb[h][1] = both(0.f);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) acc_a[h][i] = acc_b[h][i] = acc_z[h][i] = both(0.f);
   }
-  float acc_a[2][4], acc_b[2][4], acc_g[2][4];
-#pragma unroll
-  for (int h = 0; h < 2; ++h)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) acc_a[h][i] = acc_b[h][i] = acc_g[h][i] = 0.f;
-
   int64_t group = 0;
   int64_t rows_left = 0;  // rows of the current group still to come, this one included
   int s = 0;
@@ -426,10 +480,13 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
     if (rows_left == 0) {  // the first row of this CTA or of a group
       group = group_of(m, a.rows_per_group);
       rows_left = min((group + 1) * a.rows_per_group, m_last) - m;
-      if (channel_gate) {
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
-          if (live[h]) gk[h] = __ldg(reinterpret_cast<const uint2 *>(gp + group * a.K + k0 + col[h]));
+      for (int h = 0; h < 2; ++h) {
+        Two gate[2];
+        load_params<T, 2>(live[h] ? a.ga : nullptr, k0 + col[h], 1.f, w[h]);
+        load_params<T, 2>(live[h] && channel_gate ? gp + group * a.K : nullptr, k0 + col[h], 1.f, gate);
+        w[h][0] = w[h][0] * gate[0];
+        w[h][1] = w[h][1] * gate[1];
       }
     }
     --rows_left;
@@ -437,30 +494,37 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
     // barrier below is still met
     mbar_wait_bounded(&full[s], phase, abort_flag, a.err, kPipelineTimeoutNs);
     const uint8_t *d = smem + s * stage_bytes;
-    float fv[4], rv[4], dyv[4], drv[4], w[4];
+    // With t = w f and R = r + (gm ia) t (so q = ia t and rh = ib R), and u = dr' + ib dy gb:
+    //   C2 = sum dy gb R, A = sum t u, C = sum t R
+    const Two c1 = both(gm * ia), ib2 = both(ib);
+    Two fv[2], tv[2], rv[2], dyv[2], uv[2];
     auto fetch = [&](int h) {
-      Four<T, false>::load(d, col[h], fv);
-      Four<T, kR32>::load(d + 2 * b16, col[h], rv);
+      load_pairs<T, false, 2>(d, col[h], fv);
+      load_pairs<T, kR32, 2>(d + 2 * b16, col[h], rv);
+      dyv[0] = dyv[1] = uv[0] = uv[1] = both(0.f);
+      if (a.dy) load_pairs<T, false, 2>(d + b16, col[h], dyv);
+      if (a.dr_out) load_pairs<T, kR32, 2>(d + 2 * b16 + br, col[h], uv);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dyv[i] = drv[i] = 0.f;
-      if (a.dy) Four<T, false>::load(d + b16, col[h], dyv);
-      if (a.dr_out) Four<T, kR32>::load(d + 2 * b16 + br, col[h], drv);
+      for (int i = 0; i < 2; ++i) {
+        tv[i] = fv[i] * w[h][i];
+        rv[i] = fma2(c1, tv[i], rv[i]);
+      }
     };
-    float c2 = 0.f, sa = 0.f, sc = 0.f;
+    Two s2 = both(0.f), sA = both(0.f), sC = both(0.f);
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (live[h]) {
         fetch(h);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float q = at4<T>(gk[h], i) * (fv[i] * ia * at4<T>(ga[h], i));
-          const float rh = (rv[i] + gm * q) * ib, v = dyv[i] * at4<T>(gb[h], i);
-          c2 += v * rh;
-          sa += q * (drv[i] + ib * v);
-          sc += q * rh;
+        for (int i = 0; i < 2; ++i) {
+          const Two v = dyv[i] * gb[h][i];
+          s2 = fma2(v, rv[i], s2);
+          sA = fma2(tv[i], fma2(ib2, v, uv[i]), sA);
+          sC = fma2(tv[i], rv[i], sC);
         }
       }
     }
+    float c2 = sum2(s2), sa = sum2(sA), sc = sum2(sC);
     // the three sums over the block: lanes 8 j .. 8 j + 7 carry sum j from the second step on
     {
       const bool up16 = lane & 16, up8 = lane & 8;
@@ -490,8 +554,7 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 4), "f"(sa) : "memory");
         asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at + 8), "f"(sc) : "memory");
       }
-      __syncwarp();
-      cluster_sync();
+      cluster_meet();
       c2 = sa = sc = 0.f;
       for (int r = 0; r < a.slices; ++r) {
         c2 += peer_sums[pb][r][0];
@@ -499,39 +562,44 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
         sc += peer_sums[pb][r][2];
       }
     }
-    const float mean2 = c2 * inv_k;
-    const float S = sa - ib * mean2 * sc;  // sum q dR
-    const float mean1 = gm * S * inv_k;    // mean of fh times the gradient of fh
+    // dR = u - kappa R, S = sum q dR, df = (gm ia) w dR - lambda f
+    const float kappa = ib * ib * ib * (c2 * inv_k);
+    const float S = ia * (sa - kappa * sc);
+    const Two nk = both(-kappa), nl = both(a.ga ? -ia * ia * (gm * S * inv_k) : 0.f);
     if (row_gate && a.dgate && threadIdx.x == 0 && slice == 0) a.dgate[m] = a.scale * S;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       if (live[h]) {
         fetch(h);
-        float df[4];
+        Two df[2];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float fh = fv[i] * ia, g = at4<T>(ga[h], i), k = at4<T>(gk[h], i), n = fh * g;
-          const float rh = (rv[i] + gm * k * n) * ib, v = dyv[i] * at4<T>(gb[h], i);
-          acc_b[h][i] += dyv[i] * rh;
-          w[i] = drv[i] + ib * (v - rh * mean2);
-          const float sdr = gm * w[i];
-          acc_g[h][i] += sdr * n;
-          const float dn = sdr * k;
-          acc_a[h][i] += dn * fh;
-          df[i] = a.ga ? ia * (dn * g - fh * mean1) : dn;
+        for (int i = 0; i < 2; ++i) {
+          acc_b[h][i] = fma2(ib2 * dyv[i], rv[i], acc_b[h][i]);
+          uv[i] = fma2(nk, rv[i], fma2(ib2, dyv[i] * gb[h][i], uv[i]));
+          const Two sdr = c1 * uv[i];
+          acc_z[h][i] = fma2(sdr, fv[i], acc_z[h][i]);
+          df[i] = fma2(nl, fv[i], sdr * w[h][i]);
         }
-        Four<T, kR32>::store(a.dr, m * a.K + k0 + col[h], w);
-        Four<T, false>::store(a.df, m * a.K + k0 + col[h], df);
+        store_pairs<T, kR32, 2>(a.dr, m * a.K + k0 + col[h], uv);
+        store_pairs<T, false, 2>(a.df, m * a.K + k0 + col[h], df);
       }
     }
-    if (rows_left == 0 && channel_gate && a.dgate) {  // the end of a group of rows: its gate gradient
+    if (rows_left == 0) {  // the end of a group of rows
       const int64_t at = (a.parts > 1 ? part : group) * a.K + k0;
-      float *dst = (a.parts > 1 ? a.part_g : a.dgate) + at;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        if (live[h]) Four<T, true>::store(dst, col[h], acc_g[h]);
+        if (live[h]) {
+          Two x[2], gate[2];
+          load_params<T, 2>(channel_gate ? gp + group * a.K : nullptr, k0 + col[h], 1.f, gate);
+          load_params<T, 2>(a.ga, k0 + col[h], 1.f, x);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc_g[h][i] = 0.f;
+          for (int i = 0; i < 2; ++i) {
+            acc_a[h][i] = fma2(gate[i], acc_z[h][i], acc_a[h][i]);
+            x[i] = x[i] * acc_z[h][i];
+            acc_z[h][i] = both(0.f);
+          }
+          if (channel_gate && a.dgate) store_pairs<T, true, 2>((a.parts > 1 ? a.part_g : a.dgate) + at, col[h], x);
+        }
       }
     }
     if (++s == a.stages) {
@@ -543,8 +611,8 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
   for (int h = 0; h < 2; ++h) {
     if (live[h]) {
       const int64_t at = static_cast<int64_t>(part) * a.K + k0;
-      if (a.part_a) Four<T, true>::store(a.part_a + at, col[h], acc_a[h]);
-      if (a.part_b) Four<T, true>::store(a.part_b + at, col[h], acc_b[h]);
+      if (a.part_a) store_pairs<T, true, 2>(a.part_a + at, col[h], acc_a[h]);
+      if (a.part_b) store_pairs<T, true, 2>(a.part_b + at, col[h], acc_b[h]);
     }
   }
   if (*abort_flag) {  // copies in flight land before the CTA's memory goes
@@ -552,12 +620,13 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
     while (global_timer_ns() - t0 < 10000000ull) {
     }
   }
-  if (a.slices > 1) cluster_sync();  // no CTA leaves while another writes its sums
+  if (a.slices > 1) cluster_meet();  // no CTA leaves while another writes its sums
 }
 
-// out[j, k] = sum over `count` partial rows of part[j * count + p, k], in a fixed order: a warp's 32
-// lanes take 32 columns, the 8 warps of a CTA every eighth row.  blockIdx.y: the output row j;
-// blockIdx.z: which of the (at most three) sums.
+// out[j, k] = sum over `count` partial rows of part[j * count + p, k], in a fixed order: a thread takes
+// four columns and every 16th row, eight rows of loads in flight, and the 16 are added at the end.
+// blockIdx.y: the output rows of all (at most three) sums, one after the other; a CTA that finds
+// nothing to do still costs its launch, so none is made for them.
 struct SumJob {
   const float *part;
   float *out;
@@ -568,26 +637,36 @@ struct SumJobs {
   SumJob job[3];
   int K;
 };
-__global__ void __launch_bounds__(256) partial_sum_kernel(const SumJobs jobs) {
-  __shared__ float red[8][32];
+constexpr int kSumCols = 16;  // threads of a CTA along K: 64 columns
+constexpr int kSumRows = 16;  // along the partial rows
+__global__ void __launch_bounds__(kSumCols *kSumRows) partial_sum_kernel(const SumJobs jobs) {
+  __shared__ float4 red[kSumRows][kSumCols];
   pdl_wait();
   pdl_trigger();
-  const SumJob j = jobs.job[blockIdx.z];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, k = static_cast<int>(blockIdx.x) * 32 + lane;
-  for (int row = blockIdx.y; row < j.rows; row += gridDim.y) {
-    float s = 0.f;
+  const int tx = threadIdx.x % kSumCols, ty = threadIdx.x / kSumCols;
+  const int k = (static_cast<int>(blockIdx.x) * kSumCols + tx) * 4;
+  const int total = jobs.job[0].rows + jobs.job[1].rows + jobs.job[2].rows;
+  for (int at = blockIdx.y; at < total; at += gridDim.y) {
+    int row = at, z = 0;
+    while (row >= jobs.job[z].rows) row -= jobs.job[z++].rows;
+    const SumJob j = jobs.job[z];
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     if (k < jobs.K) {
       const float *p = j.part + static_cast<int64_t>(row) * j.count * jobs.K + k;
-#pragma unroll 4
-      for (int i = warp; i < j.count; i += 8) s += __ldg(p + static_cast<int64_t>(i) * jobs.K);
+#pragma unroll 8
+      for (int i = ty; i < j.count; i += kSumRows) {
+        const float4 v = __ldcg(reinterpret_cast<const float4 *>(p + static_cast<int64_t>(i) * jobs.K));
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+      }
     }
-    red[warp][lane] = s;
+    red[ty][tx] = s;
     __syncthreads();
-    if (warp == 0 && k < jobs.K) {
-      s = 0.f;
-#pragma unroll
-      for (int w = 0; w < 8; ++w) s += red[w][lane];
-      j.out[static_cast<int64_t>(row) * jobs.K + k] = s;
+    if (ty == 0 && k < jobs.K) {
+      for (int w = 1; w < kSumRows; ++w) {
+        const float4 v = red[w][tx];
+        s.x += v.x, s.y += v.y, s.z += v.z, s.w += v.w;
+      }
+      *reinterpret_cast<float4 *>(j.out + static_cast<int64_t>(row) * jobs.K + k) = s;
     }
     __syncthreads();
   }
@@ -602,11 +681,13 @@ cudaError_t norm_forward(const NormArgs &a, int sms, cudaStream_t s) {
     return per == 1 ? launch_pdl(residual_norm_kernel<T, kR32, 1>, grid, block, 0, s, a)
                     : launch_pdl(residual_norm_kernel<T, kR32, 2>, grid, block, 0, s, a);
   }
-  const int per = chunks <= 64 ? 1 : 2;
-  const int threads = ((chunks + per - 1) / per + 31) / 32 * 32;
+  // 16 columns per thread.  Up to 448 threads (K = 7168) two CTAs share an SM with 72 registers a
+  // thread; more threads take one CTA per SM.
+  const int threads = ((chunks + 1) / 2 + 31) / 32 * 32;
+  const bool wide = threads > 448;
   const int stage = a.K * (2 + Res<T, kR32>::kBytes);
-  int per_sm = 1024 / threads;
-  if (per_sm > 16) per_sm = 16;
+  int per_sm = wide ? 1 : 896 / threads;
+  if (per_sm > 12) per_sm = 12;
   int stages = (kNormMaxSmem / per_sm - 2048) / stage;
   while (stages < 2 && per_sm > 1) stages = (kNormMaxSmem / --per_sm - 2048) / stage;
   if (stages > kNormMaxStages) stages = kNormMaxStages;
@@ -614,16 +695,16 @@ cudaError_t norm_forward(const NormArgs &a, int sms, cudaStream_t s) {
   const int smem = 128 + stages * stage;
   const int64_t cap = static_cast<int64_t>(sms) * per_sm;
   const dim3 grid(static_cast<unsigned>(a.M < cap ? a.M : cap)), block(threads);
-  auto kernel = per == 1 ? residual_norm_rows_kernel<T, kR32, 1> : residual_norm_rows_kernel<T, kR32, 2>;
+  auto kernel = wide ? residual_norm_rows_kernel<T, kR32, 2, 1024, 1> : residual_norm_rows_kernel<T, kR32, 2, 448, 2>;
   static std::atomic<bool> ready[64][2];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!ready[dev][per - 1].load()) {
+  if (!ready[dev][wide].load()) {
     e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kNormMaxSmem);
     if (e != cudaSuccess) return e;
-    ready[dev][per - 1].store(true);
+    ready[dev][wide].store(true);
   }
   return launch_pdl(kernel, grid, block, smem, s, a, stages);
 }
@@ -659,15 +740,16 @@ cudaError_t norm_backward(const NormGradArgs &a, const NormGradPlan &p, cudaStre
   if (e != cudaSuccess) return e;
   SumJobs jobs = {};
   jobs.K = a.K;
-  int n = 0, rows = 1;
+  int n = 0, rows = 0;
   if (a.part_a) jobs.job[n++] = {a.part_a, a.dga, 1, p.ctas};
   if (a.part_b) jobs.job[n++] = {a.part_b, a.dgb, 1, p.ctas};
   if (a.part_g) {
     jobs.job[n++] = {a.part_g, a.dgate, static_cast<int>(a.groups), a.parts};
-    rows = static_cast<int>(a.groups);
   }
+  for (int i = 0; i < n; ++i) rows += jobs.job[i].rows;
   if (n == 0) return cudaSuccess;
-  return launch_pdl(partial_sum_kernel, dim3((a.K + 31) / 32, rows < 1024 ? rows : 1024, n), dim3(256), 0, s, jobs);
+  return launch_pdl(partial_sum_kernel, dim3((a.K + 4 * kSumCols - 1) / (4 * kSumCols), rows < 1024 ? rows : 1024),
+                    dim3(kSumCols * kSumRows), 0, s, jobs);
 }
 
 }  // namespace
@@ -694,7 +776,13 @@ NormGradPlan norm_grad_plan(int64_t M, int64_t K, int64_t groups, bool r32) {
     p.parts = 1;
     p.ctas = static_cast<int>(want);
   } else {
-    int64_t parts = want / (groups > 0 ? groups : 1);
+    // few rows per CTA cost more in partial sums than they save: at least kNormGradRows each, as
+    // long as every SM still has a CTA
+    const int64_t base = static_cast<int64_t>(kNormSms) / p.slices;
+    int64_t goal = M / kNormGradRows;
+    if (goal < base) goal = base;
+    if (goal > want) goal = want;
+    int64_t parts = goal / (groups > 0 ? groups : 1);
     if (parts > rows_per_group) parts = rows_per_group;
     if (parts < 1) parts = 1;
     p.parts = static_cast<int>(parts);

@@ -6,7 +6,9 @@
 // is split over the CTAs of a cluster so that enough weight bytes are in flight on every SM even
 // where there are few 128-row tiles.  A stage of the ring is one 128-byte K block: 128 weight rows
 // (kGated: 128 rows of Wg and 128 of Wu), kTok token rows, and for FP8 the block's token scales.
-// Two CTAs fit on an SM.
+// Two CTAs fit on an SM.  (Measured and left: a ring twice as deep and one CTA per SM for launches of at
+// most one CTA per SM.  A cluster of eight then needs eight whole SMs of one GPC: one token 7168 -> 2 x
+// 2048 in bf16 took 22 us instead of 16.)
 //
 // The CTAs of a cluster hold partial sums of the same outputs; each leaves its partial in its own
 // shared memory, and after a cluster barrier each adds its share of the token columns over all
@@ -15,12 +17,17 @@
 // FP8: the product of one K block goes to one of kBufs accumulators, and the epilogue warps add it
 // to fp32 registers times sw[tile, b] * sa[b, token] (a 128-row weight tile has one scale per block).
 //
+// kQuant (FP8, at most 32 tokens): four more warps quantise the 16-bit activations into the ring
+// themselves, with the quantiser kernel's arithmetic, so that a decoded token takes one launch.  Every
+// CTA quantises its K blocks of all tokens; that pays while the tokens are few.
+//
 // Warps: 0 = TMA producer, 1 = MMA issuer, 2..5 = epilogue (one 32-lane quarter of tensor memory
-// each).  Every wait is bounded, as in the tile GEMM.
+// each), 6..9 = quantisers (kQuant).  Every wait is bounded, as in the tile GEMM.
 #pragma once
 
 #include <atomic>
 
+#include "fp8_encode.cuh"
 #include "mma16x8.cuh"
 
 namespace nvfp4 {
@@ -34,17 +41,22 @@ struct StreamArgs {
   void *out;       // 16-bit (M, N), row stride ldo
   int64_t ldo;
   float *save;     // kGated: fp32 (M, 2N) [g | u], or null
+  const void *x;   // kQuant: 16-bit activations (M, K), row stride ldx
+  int64_t ldx;
+  int K;           // kQuant
   uint32_t *err;
 };
 
-template <bool kFp8, int kTok>
+template <bool kFp8, int kTok, bool kQuant>
 struct StreamCfg {
   static constexpr int kOperands = kFp8 ? 1 : 2;  // weight tiles per stage (gate and up)
   static constexpr int kWBytes = 128 * 128;
   static constexpr int kXBytes = kTok * 128;
   static constexpr int kSBytes = kFp8 ? kTok * 4 : 0;
   static constexpr int kStageBytes = kOperands * kWBytes + kXBytes;
-  static constexpr int kStages = (104 * 1024) / (kStageBytes + kSBytes);
+  static constexpr int kStages = 104 * 1024 / (kStageBytes + kSBytes);
+  static constexpr int kQuantWarps = kQuant ? 4 : 0;
+  static constexpr int kThreads = 192 + kQuantWarps * 32;
   static constexpr int kBufs = kFp8 ? (kTok <= 64 ? 4 : 2) : 1;
   static constexpr int kCols = kFp8 ? kBufs * kTok : 2 * kTok;  // accumulator columns
   static constexpr uint32_t kTmemCols = kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
@@ -54,18 +66,18 @@ struct StreamCfg {
   static_assert(kPartialBytes <= kRing, "the partial sums fit where the ring was");
   static_assert(kCols <= 256, "two CTAs share the SM's 512 tensor-memory columns");
   static_assert(2 * (kSmem + 1024) <= 233472, "two CTAs per SM");
+  static_assert(!kQuant || (kFp8 && kTok <= 32), "the quantisers hold a few tokens of four K blocks in registers");
   static_assert((2 * kStages + 2 * kBufs) * 8 + 8 <= 256, "barrier region");
   static_assert(kTok % 16 == 0 && kStages >= 2, "MMA N and ring");
 };
 
-constexpr int kStreamGemmThreads = 192;
 constexpr int kStreamMaxSplit = 8;  // portable cluster size
 
-template <bool kFp8, class T, int kAct, int kTok>
-__global__ void __launch_bounds__(kStreamGemmThreads, 2)
+template <bool kFp8, class T, int kAct, int kTok, bool kQuant>
+__global__ void __launch_bounds__(StreamCfg<kFp8, kTok, kQuant>::kThreads, 2)
     stream_gemm_kernel(const __grid_constant__ CUtensorMap tmW0, const __grid_constant__ CUtensorMap tmW1,
                        const __grid_constant__ CUtensorMap tmX, const StreamArgs args, const int splits) {
-  using C = StreamCfg<kFp8, kTok>;
+  using C = StreamCfg<kFp8, kTok, kQuant>;
   constexpr uint32_t kFmt = kFp8 ? 0u : (T::kCode == NVFP4_DT_BF16 ? 1u : 0u);
   constexpr uint32_t kIdesc = mma_idesc(kFmt, false, false, 128, kTok);
 
@@ -88,7 +100,7 @@ __global__ void __launch_bounds__(kStreamGemmThreads, 2)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 1 + C::kQuantWarps);
       // FP8: the epilogue also reads the stage's token scales
       mbar_init(&empty[s], kFp8 ? 5 : 1);
     }
@@ -101,14 +113,15 @@ __global__ void __launch_bounds__(kStreamGemmThreads, 2)
   }
   if (warp == 0 && lane == 0) {
     prefetch_tensormap(&tmW0);
-    prefetch_tensormap(&tmX);
+    if constexpr (!kQuant) prefetch_tensormap(&tmX);
   }
+  __syncwarp();
   if (warp == 1) {
     tmem_alloc(tmem_holder, C::kTmemCols);
     tmem_relinquish();
   }
   tc_fence_before();
-  __syncthreads();
+  block_meet();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   pdl_wait();
@@ -130,7 +143,7 @@ __global__ void __launch_bounds__(kStreamGemmThreads, 2)
       // ------------------------------------------------------------ TMA producer
       const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
       // token scales that exist from m0 on, rounded up to whole 16 bytes (a row of scales is padded)
-      const uint32_t s_bytes = kFp8 ? static_cast<uint32_t>(min(kTok, (args.M - m0 + 3) & ~3)) * 4u : 0u;
+      const uint32_t s_bytes = kFp8 && !kQuant ? static_cast<uint32_t>(min(kTok, (args.M - m0 + 3) & ~3)) * 4u : 0u;
       int stage = 0;
       uint32_t phase = 0;
       bool ok = true;
@@ -139,12 +152,20 @@ __global__ void __launch_bounds__(kStreamGemmThreads, 2)
           ok = false;
           break;
         }
-        mbar_arrive_expect_tx(&full[stage], C::kStageBytes + s_bytes);
+        mbar_arrive_expect_tx(&full[stage], C::kStageBytes - (kQuant ? C::kXBytes : 0) + s_bytes);
         uint8_t *w = sW + stage * C::kOperands * C::kWBytes;
         tma_load_2d(w, &tmW0, kb * 128, tile * 128, &full[stage], pol_w);
         if constexpr (!kFp8) tma_load_2d(w + C::kWBytes, &tmW1, kb * 128, tile * 128, &full[stage], pol_w);
-        tma_load_2d(sX + stage * C::kXBytes, &tmX, kb * 128, m0, &full[stage], pol_x);
-        if constexpr (kFp8) bulk_load(sS + stage * kTok, args.sa + kb * args.ld_sa + m0, s_bytes, &full[stage], pol_x);
+        if constexpr (!kQuant) tma_load_2d(sX + stage * C::kXBytes, &tmX, kb * 128, m0, &full[stage], pol_x);
+        if constexpr (kFp8 && !kQuant) bulk_load(sS + stage * kTok, args.sa + kb * args.ld_sa + m0, s_bytes, &full[stage], pol_x);
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1;
+        }
+      }
+      // no commit is on its way to a barrier of this CTA when it exits
+      for (int i = 0; ok && i < C::kStages; ++i) {
+        ok = mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, args.err, kPipelineTimeoutNs);
         if (++stage == C::kStages) {
           stage = 0;
           phase ^= 1;
@@ -153,23 +174,19 @@ __global__ void __launch_bounds__(kStreamGemmThreads, 2)
       if (!ok) settle();
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ MMA issuer
-      const uint32_t w0 = smem_u32(sW), x0 = smem_u32(sX);
-      int stage = 0;
-      uint32_t phase = 0, n = 0;
-      bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        const uint32_t buf = kFp8 ? n % C::kBufs : 0;
-        if (kFp8 && !mbar_wait_bounded(&tempty[buf], ((n / C::kBufs) & 1) ^ 1, abort_flag, args.err, kPipelineTimeoutNs)) {
-          ok = false;
-          break;
-        }
-        if (!mbar_wait_bounded(&full[stage], phase, abort_flag, args.err, kPipelineTimeoutNs)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
+    // -------------------------------------------------------------- MMA issuer (one elected lane issues)
+    const uint32_t w0 = smem_u32(sW), x0 = smem_u32(sX);
+    int stage = 0;
+    uint32_t phase = 0, n = 0;
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      const uint32_t buf = kFp8 ? n % C::kBufs : 0;
+      if (kFp8) ok = mbar_wait_bounded(&tempty[buf], ((n / C::kBufs) & 1) ^ 1, abort_flag, args.err, kPipelineTimeoutNs);
+      ok = ok && mbar_wait_bounded(&full[stage], phase, abort_flag, args.err, kPipelineTimeoutNs);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      if (elect_one()) {
         const uint64_t xd = smem_desc(x0 + stage * C::kXBytes, 16, 1024, 2);
 #pragma unroll
         for (int o = 0; o < C::kOperands; ++o) {
@@ -180,15 +197,67 @@ __global__ void __launch_bounds__(kStreamGemmThreads, 2)
                                 kFp8 ? j != 0 : (kb != kb0 || j != 0));
         }
         tc_commit(&empty[stage]);
-        if (kFp8) tc_commit(&tfull[buf]);
-        ++n;
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1;
+        if (kFp8 || kb == kb1 - 1) tc_commit(&tfull[buf]);
+      }
+      __syncwarp();
+      ++n;
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    if (!ok) settle();
+  } else if (kQuant && warp >= 6) {
+    // -------------------------------------------------------------- quantisers
+    // 16 lanes hold one token's 128 elements of a K block, so the four warps take eight tokens at a
+    // time.  The loads of kGroup K blocks are in flight together: one memory latency per group,
+    // behind the ring.  Columns of tokens past M are left as they are: they feed no output.
+    if constexpr (kQuant) {
+      constexpr int kGroup = 4, kPasses = kTok / 8;
+      const int gl = lane & 15, slot = (warp - 6) * 2 + (lane >> 4);
+      const uint16_t *x = static_cast<const uint16_t *>(args.x);
+      int stage = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (int g0 = kb0; ok && g0 < kb1; g0 += kGroup) {
+        uint4 v[kGroup][kPasses];
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u)
+#pragma unroll
+          for (int p = 0; p < kPasses; ++p) {
+            const int tok = m0 + p * 8 + slot, k = (g0 + u) * 128 + gl * 8;
+            v[u][p] = make_uint4(0u, 0u, 0u, 0u);
+            if (g0 + u < kb1 && tok < args.M && k < args.K)
+              v[u][p] = __ldg(reinterpret_cast<const uint4 *>(x + tok * args.ldx + k));
+          }
+#pragma unroll
+        for (int u = 0; u < kGroup; ++u) {
+          if (g0 + u >= kb1) break;
+          ok = mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, args.err, kPipelineTimeoutNs);
+          ok = __all_sync(0xffffffffu, ok);
+          if (!ok) break;
+#pragma unroll
+          for (int p = 0; p < kPasses; ++p) {
+            const int row = p * 8 + slot;
+            uint32_t a = max_abs16(v[u][p]);
+#pragma unroll
+            for (int o = 8; o; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+            const float sc = __fdiv_rn(T::up(a), 448.f);
+            if (m0 + row < args.M) {  // rows of 128 bytes, 16-byte chunks swizzled by the row
+              uint8_t *d = sX + stage * C::kXBytes + row * 128 + (((gl >> 1) ^ (row & 7)) << 4) + (gl & 1) * 8;
+              *reinterpret_cast<uint2 *>(d) = encode8<T>(v[u][p], sc);
+              if (gl == 0) sS[stage * kTok + row] = sc;
+            }
+          }
+          fence_proxy_async_shared();  // the codes are read by the tensor core
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&full[stage]);
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
         }
       }
-      if (!kFp8) tc_commit(&tfull[0]);
-      if (!ok) settle();
     }
   } else {
     // -------------------------------------------------------------- epilogue: this CTA's sums
@@ -260,15 +329,15 @@ __global__ void __launch_bounds__(kStreamGemmThreads, 2)
 
   // ---------------------------------------------------------------- reduction over the ranks
   tc_fence_before();
-  __syncthreads();
-  if (splits > 1) cluster_sync();
+  block_meet();
+  if (splits > 1) cluster_meet();
   tc_fence_after();
   if (warp == 1) tmem_dealloc(tmem_base, C::kTmemCols);
   if (*abort_flag == 0) {
     const int j0 = kTok * rank / splits, j1 = kTok * (rank + 1) / splits;
     const uint32_t base = smem_u32(smem);
     const int live = min(j1, args.M - m0);
-    for (int e = static_cast<int>(threadIdx.x) + j0 * 128; e < live * 128; e += kStreamGemmThreads) {
+    for (int e = static_cast<int>(threadIdx.x) + j0 * 128; e < live * 128; e += C::kThreads) {
       const int j = e >> 7, f = tile * 128 + (e & 127);
       float va[kStreamMaxSplit], vb[kStreamMaxSplit];  // every rank's load is in flight before the sums
 #pragma unroll
@@ -302,14 +371,14 @@ __global__ void __launch_bounds__(kStreamGemmThreads, 2)
       }
     }
   }
-  if (splits > 1) cluster_sync();  // no CTA leaves while another reads its partial sums
+  if (splits > 1) cluster_meet();  // no CTA leaves while another reads its partial sums
 }
 
-template <bool kFp8, class T, int kAct, int kTok>
+template <bool kFp8, class T, int kAct, int kTok, bool kQuant = false>
 cudaError_t launch_stream_gemm_as(const CUtensorMap &w0, const CUtensorMap &w1, const CUtensorMap &x,
                                   const StreamArgs &args, int splits, cudaStream_t s) {
-  using C = StreamCfg<kFp8, kTok>;
-  auto kernel = stream_gemm_kernel<kFp8, T, kAct, kTok>;
+  using C = StreamCfg<kFp8, kTok, kQuant>;
+  auto kernel = stream_gemm_kernel<kFp8, T, kAct, kTok, kQuant>;
   static std::atomic<bool> ready[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -323,7 +392,7 @@ cudaError_t launch_stream_gemm_as(const CUtensorMap &w0, const CUtensorMap &w1, 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>((args.N + 127) / 128 * splits),
                      static_cast<unsigned>((args.M + kTok - 1) / kTok));
-  cfg.blockDim = dim3(kStreamGemmThreads);
+  cfg.blockDim = dim3(C::kThreads);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[2];

@@ -1,15 +1,15 @@
 // Tensor-bound GEMM on CTA pairs (tcgen05 cta_group::2) shared by the FP8 block-scaled linear
 // and the gated linear's forward and backward products.
 //
-// One output tile per pair has 256 rows (128 per CTA, the lanes of its tensor memory) and 256
+// One output tile per pair has 256 rows (128 per CTA, the lanes of its tensor memory) and 256 (or 128)
 // accumulator columns.  A K block is 128 bytes of every operand row: each CTA stages 128 rows of A
-// and 128 rows of B per block (32 KB), a ring of kTStages blocks deep.  A one-SM tile of 128 x 256
+// and half of the tile's rows of B per block (32 KB), a ring of kStages blocks deep.  A one-SM tile of 128 x 256
 // would stage 48 KB for the same work: the L2 -> SM operand stream is what bounds tiles of this
 // size, so the pair's sharing of B matters.
 //
-// Warps of each CTA: 0 = TMA producer, 1 (and 2 for FP8) = MMA issuer (the even CTA's, for both),
-// 4..11 = epilogue
-// (two per 32-lane quarter of tensor memory, 128 columns each).
+// Warps of each CTA: 0 = TMA producer, 1 (and 2 for FP8) = MMA issuer (the even CTA's, for both), 3 = tensor memory,
+// 4..11 =
+// epilogue (two per 32-lane quarter of tensor memory, half of the columns each).
 //
 //   Op::kFp8    A = xq (M, K) e4m3, B = wq (N, K) e4m3.  The scales change every 128 K, so every K
 //               block is a product of its own: two issuers take the blocks in turn into an accumulator
@@ -21,12 +21,17 @@
 //               longer than the other's MMAs.  Measured and left: four accumulators of 128 columns (two
 //               issuers; 8 warps 200 us, 16 warps 175 us), 16 epilogue warps on 256 columns, two batches
 //               of columns in flight, activation scales through a shared-memory ring.
-//   Op::kGated  A = x (M, K), B = 128 rows of Wg (even CTA) and the matching 128 of Wu (odd CTA):
-//               columns 0..127 of the accumulator are g, 128..255 u of the same outputs.
+//   Op::kGated  A = x (M, K), B = rows of Wg (even CTA) and the matching rows of Wu (odd CTA):
+//               the first half of the accumulator's columns is g, the second u of the same outputs.
 //   Op::kDx     A = [dg | du] in two segments of K = I, B = Wg, then Wu, read along their rows
 //               (MN-major B): dx = dg Wg + du Wu.
 //   Op::kDw     A = [dg | du]^T (MN-major), B = x^T (MN-major), K = tokens: rows 0..I-1 are dWg,
 //               rows I..2I-1 dWu.
+//
+// Launched in plain stream order, without programmatic dependent launch, and it does not let its
+// successor start early: two pair kernels that overlap that way, one taking over the SMs and tensor memory
+// that the other leaves cluster by cluster, stopped making progress once in some thousand launches.
+// It costs about 2 us per launch.
 //
 // Every wait is bounded: a role that gives up raises NVFP4_DEVERR_PIPELINE_TIMEOUT, the copies in
 // flight are given time to land, and every thread of the pair meets at the final cluster barrier.
@@ -54,10 +59,23 @@ struct TileArgs {
   uint32_t *err;
 };
 
-constexpr int kTRows = 256, kTCols = 256, kTHalf = 128;
-constexpr int kTStages = 6;
-constexpr int kTOperandBytes = kTHalf * 128;  // 16 KiB: 128 rows x 128 bytes
-constexpr int kTStageBytes = 2 * kTOperandBytes;
+constexpr int kTRows = 256, kTHalf = 128;
+// kCols accumulator columns of a tile, half of them staged by either CTA: 256, or 128 where 256 x 256
+// tiles would leave SMs idle (tile_plan).
+template <int kCols>
+struct TileCfg {
+  static constexpr int kStages = kCols == 256 ? 6 : 8;
+  static constexpr int kABytes = kTHalf * 128;      // 128 rows x 128 bytes
+  static constexpr int kBBytes = kCols / 2 * 128;   // kCols / 2 rows x 128 bytes
+  static constexpr int kStageBytes = kABytes + kBBytes;
+  static constexpr int kRing = kStages * kStageBytes;
+  static constexpr uint32_t kTmemCols = 2 * kCols;  // two accumulators
+  static constexpr int kStoreBytes = 8 * 32 * 36;   // kFp8: a warp's 32 rows of 16 columns on their way out
+  static constexpr size_t kSmem = 1024 + kRing + 256 + kStoreBytes;
+  static_assert(kSmem <= 232448, "per-block shared memory limit");
+  static_assert((2 * kStages + 4) * 8 + 8 <= 256, "barrier region");
+};
+constexpr int kTAllocWarp = 3;  // owns the tensor memory; it has no other role, so it is never diverged
 constexpr int kTEpiWarp0 = 4;  // epilogue warps start on a multiple of four: a warp reads lane quarter warp % 4
 template <TileOp kOp>
 constexpr int kTEpiWarps = 8;
@@ -72,22 +90,19 @@ constexpr int kTLaunchRegs = 168, kTLightRegs = 56, kTEpiRegs = 224;
 static_assert(kTEpiWarp0 * kTLightRegs + kTEpiWarps<TileOp::kFp8> * kTEpiRegs <=
                   (kTEpiWarp0 + kTEpiWarps<TileOp::kFp8>)*kTLaunchRegs,
               "register split within what the block was launched with");
-constexpr size_t kTSmem = 1024 + static_cast<size_t>(kTStages) * kTStageBytes + 256;
-constexpr uint32_t kTTmemCols = 512;  // two accumulators of 256 columns
 constexpr int kAhead = 4;             // kFp8: K blocks that a thread's scales are fetched ahead
 constexpr int kTGroupM = 8;           // m tiles walked together, so that a wave shares rows of B in L2
-static_assert(kTSmem <= 232448, "per-block shared memory limit");
-static_assert((2 * kTStages + 8) * 8 + 8 <= 256, "barrier region");
-
-template <TileOp kOp, class T, int kAct>
+template <TileOp kOp, class T, int kAct, int kTCols>
 __global__ void __launch_bounds__(kTThreads<kOp>, 1)
     tile_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
                      const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
                      const TileArgs args) {
+  using C = TileCfg<kTCols>;
+  constexpr int kBRows = kTCols / 2;  // rows of B staged by a CTA
   constexpr bool kFp8 = kOp == TileOp::kFp8;
   constexpr bool kAMn = kOp == TileOp::kDw;
   constexpr bool kBMn = kOp == TileOp::kDw || kOp == TileOp::kDx;
-  constexpr int kOutCols = kOp == TileOp::kGated ? kTHalf : kTCols;  // output columns of a tile
+  constexpr int kOutCols = kOp == TileOp::kGated ? kBRows : kTCols;  // output columns of a tile
   constexpr uint32_t kFmt = kFp8 ? 0u : (T::kCode == NVFP4_DT_BF16 ? 1u : 0u);
   constexpr uint32_t kIdesc = mma_idesc(kFmt, kAMn, kBMn, kTRows, kTCols);
 
@@ -95,19 +110,20 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                               ~static_cast<uintptr_t>(1023));
   uint8_t *sA = smem;
-  uint8_t *sB = sA + kTStages * kTOperandBytes;
-  uint64_t *full = reinterpret_cast<uint64_t *>(sB + kTStages * kTOperandBytes);  // used in the even CTA
-  uint64_t *empty = full + kTStages;
-  uint64_t *tfull = empty + kTStages;   // [2]
+  uint8_t *sB = sA + C::kStages * C::kABytes;
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::kRing);  // used in the even CTA
+  uint64_t *empty = full + C::kStages;
+  uint64_t *tfull = empty + C::kStages;   // [2]
   uint64_t *tempty = tfull + 2;     // [2], used in the even CTA
   uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(tempty + 2);
   volatile int *abort_flag = reinterpret_cast<volatile int *>(tmem_holder + 1);
+  uint16_t *s_store = reinterpret_cast<uint16_t *>(smem + C::kRing + 256);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_ctarank();
 
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kTStages; ++s) {
+    for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -122,17 +138,16 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
     prefetch_tensormap(&tmA0);
     prefetch_tensormap(&tmB0);
   }
-  if (warp == 1) {
-    tmem_alloc_pair(tmem_holder, kTTmemCols);
+  __syncwarp();
+  if (warp == kTAllocWarp) {
+    tmem_alloc_pair(tmem_holder, C::kTmemCols);
     tmem_relinquish_pair();
   }
   tc_fence_before();
-  __syncthreads();
-  cluster_sync();  // both CTAs' barriers are initialised and their tensor memory allocated
+  block_meet();
+  cluster_meet();  // both CTAs' barriers are initialised and their tensor memory allocated
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  pdl_wait();
-  pdl_trigger();
 
   const int m_tiles = (args.M + kTRows - 1) / kTRows;
   const int n_tiles = (args.N + kOutCols - 1) / kOutCols;
@@ -169,7 +184,7 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
         int mt, nt;
         tile_at(idx, mt, nt);
         const int a_row = mt * kTRows + static_cast<int>(rank) * kTHalf;
-        const int b_row = kOp == TileOp::kGated ? nt * kTHalf : nt * kTCols + static_cast<int>(rank) * kTHalf;
+        const int b_row = kOp == TileOp::kGated ? nt * kBRows : nt * kTCols + static_cast<int>(rank) * kBRows;
         const CUtensorMap *mapA = &tmA0, *mapB = kOp == TileOp::kGated && rank ? &tmB1 : &tmB0;
         int kb = 0, seg = 0;
         for (int it = 0; it < k_blocks; ++it, ++kb) {
@@ -186,9 +201,9 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
             break;
           }
           // both CTAs' copies complete on the even CTA's barrier, which expects all of them
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * kTStageBytes);
+          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::kStageBytes);
           const uint32_t bar = cluster_addr(&full[stage], 0);
-          uint8_t *a = sA + stage * kTOperandBytes, *b = sB + stage * kTOperandBytes;
+          uint8_t *a = sA + stage * C::kABytes, *b = sB + stage * C::kBBytes;
           if constexpr (kAMn) {  // 64 K rows of 64 elements, two boxes side by side along M
             tma_load_2d_pair(a, mapA, a_row * 2, kb * 64, bar, pol);
             tma_load_2d_pair(a + 8192, mapA, a_row * 2 + 128, kb * 64, bar, pol);
@@ -197,14 +212,23 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
           }
           if constexpr (kBMn) {
             tma_load_2d_pair(b, mapB, b_row * 2, kb * 64, bar, pol);
-            tma_load_2d_pair(b + 8192, mapB, b_row * 2 + 128, kb * 64, bar, pol);
+            if constexpr (kBRows == 128) tma_load_2d_pair(b + 8192, mapB, b_row * 2 + 128, kb * 64, bar, pol);
           } else {
             tma_load_2d_pair(b, mapB, kb * 128, b_row, bar, pol);
           }
-          if (++stage == kTStages) {
+          if (++stage == C::kStages) {
             stage = 0;
             phase ^= 1;
           }
+        }
+      }
+      // Neither CTA may exit with a commit on its way to one of its barriers (the commits of the even
+      // CTA's issuer arrive on both CTAs'): the ring is followed until every stage is free again.
+      for (int i = 0; ok && i < C::kStages; ++i) {
+        ok = mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, args.err, kPipelineTimeoutNs);
+        if (++stage == C::kStages) {
+          stage = 0;
+          phase ^= 1;
         }
       }
       if (!ok) settle();  // copies in flight may complete on the other CTA's barrier
@@ -238,8 +262,8 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
         tc_fence_after();
         const bool done = kFp8 || it == k_blocks - 1;
         if (elect_one()) {
-          const uint64_t ad = smem_desc(a0 + stage * kTOperandBytes, kAMn ? 8192 : 16, 1024, 2);
-          const uint64_t bd = smem_desc(b0 + stage * kTOperandBytes, kBMn ? 8192 : 16, 1024, 2);
+          const uint64_t ad = smem_desc(a0 + stage * C::kABytes, kAMn ? 8192 : 16, 1024, 2);
+          const uint64_t bd = smem_desc(b0 + stage * C::kBBytes, kBMn ? 8192 : 16, 1024, 2);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             tc_mma<kFp8, true>(tmem_base + (acc & 1) * kTCols, ad + j * kAStep, bd + j * kBStep, kIdesc,
@@ -250,20 +274,18 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
         __syncwarp();
         if (done) acc += kIssuers;
         it = !kFp8 && done ? 0 : it + 1;
-        if ((stage += kIssuers) >= kTStages) {
-          stage -= kTStages;
+        if ((stage += kIssuers) >= C::kStages) {
+          stage -= C::kStages;
           phase ^= 1;
         }
       }
-      // every MMA issued has completed before the pair frees its tensor memory: the last commit
-      // arrives on tfull, which this warp follows to the end
-      if (!ok) {
-        settle();
-      } else if (acc >= kIssuers) {
-        volatile int never = 0;
-        const uint32_t last = acc - kIssuers;
-        mbar_wait_bounded(&tfull[last & 1], (last >> 1) & 1, &never, nullptr, 100000000ull);
-      }
+      // Every accumulator has come back, so every MMA has completed before the pair frees its tensor
+      // memory, and no release of the other CTA's epilogue is on its way to this CTA's barriers.
+      for (int64_t turn = static_cast<int64_t>(acc) - 2; ok && turn < acc; ++turn)
+        if (turn >= 0 && (!kFp8 || (turn & 1) == iss))
+          ok = mbar_wait_bounded_cluster(&tempty[turn & 1], static_cast<uint32_t>(turn >> 1) & 1, abort_flag, args.err,
+                                         kPipelineTimeoutNs);
+      if (!ok) settle();
     }
   } else {
     // -------------------------------------------------------------- epilogue
@@ -285,19 +307,35 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
       ++acc;
     };
     const bool vec = (args.ldo & 7) == 0;
-    // kFp8: the sums of this thread's row, columns out_n0 .. out_n0 + 127
-    float sum[kFp8 ? 128 : 1];
+    // kFp8: the sums of this thread's row, kBRows columns from out_n0 on
+    float sum[kFp8 ? kBRows : 1];
     int out_row = 0, out_n0 = 0;
     auto store_tile = [&]() {
       if constexpr (kFp8) {
-        if (out_row < args.M) {
-          uint16_t *dst = static_cast<uint16_t *>(args.out) + out_row * args.ldo + out_n0;
 #pragma unroll
-          for (int c = 0; c < 8; ++c) {
-            float v[16];
+        for (int c = 0; c < kBRows / 16; ++c) {
+          float v[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) v[i] = sum[c * 16 + i];
-            store16<T>(dst + c * 16, v, args.N - out_n0 - c * 16, vec);
+          for (int i = 0; i < 16; ++i) v[i] = sum[c * 16 + i];
+          const int left = args.N - out_n0 - c * 16;
+          if (vec) {
+            if (out_row < args.M)
+              store16<T>(static_cast<uint16_t *>(args.out) + out_row * args.ldo + out_n0 + c * 16, v, left, true);
+          } else if (left > 0) {
+            // rows of any alignment: through shared memory, so that 16 lanes write 16 consecutive
+            // elements (a lane per row would touch 32 sectors with every 2-byte store)
+            uint16_t *mine = s_store + (warp - kTEpiWarp0) * 32 * 18;
+            uint32_t *w = reinterpret_cast<uint32_t *>(mine + lane * 18);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = T::pack(v[2 * i], v[2 * i + 1]);
+            __syncwarp();
+            const int at = lane & 15;
+            for (int r = lane >> 4; r < 32; r += 2) {
+              const int row = out_row - lane + r;
+              if (row < args.M && at < left)
+                static_cast<uint16_t *>(args.out)[row * args.ldo + out_n0 + c * 16 + at] = mine[r * 18 + at];
+            }
+            __syncwarp();
           }
         }
       }
@@ -308,7 +346,7 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
       const int row = mt * kTRows + static_cast<int>(rank) * kTHalf + quarter * 32 + lane;
       const bool row_ok = row < args.M;
       if constexpr (kFp8) {
-        const int n0 = nt * kTCols + half * kTHalf;  // a warp's 128 columns share one weight scale
+        const int n0 = nt * kTCols + half * kBRows;  // a warp's columns share one weight scale
         // Scales are fetched ahead: under the operand stream a load takes longer than a block.  The
         // thread's row's activation scales kAhead blocks ahead (the loop is unrolled, so that no
         // register in flight is moved); a lane holds every 32nd weight scale.  Rows past M and
@@ -322,7 +360,7 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
         out_row = row;
         out_n0 = n0;
 #pragma unroll
-        for (int i = 0; i < 128; ++i) sum[i] = 0.f;
+        for (int i = 0; i < kBRows; ++i) sum[i] = 0.f;
         for (int kb0 = 0; ok && kb0 < k_blocks; kb0 += kAhead) {
           if ((kb0 & 31) == 0 && kb0) w = ld_early(sw + min(kb0 + lane, k_blocks - 1));
 #pragma unroll
@@ -331,14 +369,14 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
             const float f = a[u] * __shfl_sync(0xffffffffu, w, (kb0 + u) & 31);
             a[u] = ld_early(sa + min(kb0 + u + kAhead, k_blocks - 1) * args.ld_sa);
             if (!wait_acc()) break;
-            const uint32_t t = lanes + (acc & 1) * kTCols + half * kTHalf;
+            const uint32_t t = lanes + (acc & 1) * kTCols + half * kBRows;
             // scalar FMAs: the packed form (fma.rn.f32x2) has no higher rate here and cost 16% more time
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
+            for (int c = 0; c < kBRows / 16; ++c) {
               uint32_t r[16];
               tmem_ld16(t + c * 16, r);
               tmem_ld_wait();
-              if (c == 7) release();
+              if (c == kBRows / 16 - 1) release();
 #pragma unroll
               for (int i = 0; i < 16; ++i) sum[c * 16 + i] = fmaf(__uint_as_float(r[i]), f, sum[c * 16 + i]);
             }
@@ -347,17 +385,17 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
         if (!ok) break;
       } else if constexpr (kOp == TileOp::kGated) {
         if (!wait_acc()) break;
-        const int n0 = nt * kTHalf + half * 64;
-        const uint32_t t = lanes + (acc & 1) * kTCols + half * 64;
+        const int n0 = nt * kBRows + half * (kBRows / 2);
+        const uint32_t t = lanes + (acc & 1) * kTCols + half * (kBRows / 2);
         uint16_t *dst = static_cast<uint16_t *>(args.out) + row * args.ldo + n0;
         float *save = args.save ? args.save + static_cast<int64_t>(row) * 2 * args.N + n0 : nullptr;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        for (int c = 0; c < kBRows / 32; ++c) {
           uint32_t g[16], u[16];
           tmem_ld16(t + c * 16, g);
-          tmem_ld16(t + kTHalf + c * 16, u);
+          tmem_ld16(t + kBRows + c * 16, u);
           tmem_ld_wait();
-          if (c == 3) release();
+          if (c == kBRows / 32 - 1) release();
           const int left = args.N - n0 - c * 16;
           if (row_ok && left > 0) {
             float h[16];
@@ -377,19 +415,20 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
         }
       } else {
         if (!wait_acc()) break;
-        const int n0 = nt * kTCols + half * kTHalf;
-        const uint32_t t = lanes + (acc & 1) * kTCols + half * kTHalf;
+        const int n0 = nt * kTCols + half * kBRows;
+        const uint32_t t = lanes + (acc & 1) * kTCols + half * kBRows;
         uint16_t *dst = static_cast<uint16_t *>(args.out) + row * args.ldo + n0;
         if constexpr (kOp == TileOp::kDw) {  // rows I..2I-1 belong to the second output
           const int split = args.M / 2;
           if (row >= split) dst = static_cast<uint16_t *>(args.out2) + (row - split) * args.ldo + n0;
         }
 #pragma unroll
-        for (int c = 0; c < 8; ++c) {
+        for (int c = 0; c < kBRows / 16; ++c) {
           uint32_t r[16];
+          __syncwarp();
           tmem_ld16(t + c * 16, r);
           tmem_ld_wait();
-          if (c == 7) release();
+          if (c == kBRows / 16 - 1) release();
           float v[16];
 #pragma unroll
           for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
@@ -401,22 +440,23 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
   }
 
   tc_fence_before();
-  __syncthreads();
-  cluster_sync();  // the pair's MMAs have drained and both epilogues have read their accumulators
+  block_meet();
+  cluster_meet();  // the pair's MMAs have drained and both epilogues have read their accumulators
   tc_fence_after();
-  if (warp == 1) tmem_dealloc_pair(tmem_base, kTTmemCols);
+  if (warp == kTAllocWarp) tmem_dealloc_pair(tmem_base, C::kTmemCols);
+  // Freeing a pair's tensor memory takes both CTAs: neither leaves before the other has done it.
+  cluster_meet();
 }
 
 // Clusters of two that fit on the current device at once (0 if the query fails), and the launch.
 template <class K>
-int tile_gemm_max_clusters(K kernel, int threads) {
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kTSmem)) !=
-      cudaSuccess)
+int tile_gemm_max_clusters(K kernel, int threads, size_t smem) {
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
     return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * 1024);
   cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = kTSmem;
+  cfg.dynamicSmemBytes = smem;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
@@ -429,10 +469,11 @@ int tile_gemm_max_clusters(K kernel, int threads) {
   return n;
 }
 
-template <TileOp kOp, class T, int kAct>
-cudaError_t launch_tile_gemm_as(const CUtensorMap &a0, const CUtensorMap &a1, const CUtensorMap &b0,
-                                const CUtensorMap &b1, const TileArgs &args, cudaStream_t s) {
-  auto kernel = tile_gemm_kernel<kOp, T, kAct>;
+template <TileOp kOp, class T, int kAct, int kTCols>
+cudaError_t launch_tile_gemm_cols(const CUtensorMap &a0, const CUtensorMap &a1, const CUtensorMap &b0,
+                                  const CUtensorMap &b1, const TileArgs &args, cudaStream_t s) {
+  using C = TileCfg<kTCols>;
+  auto kernel = tile_gemm_kernel<kOp, T, kAct, kTCols>;
   static std::atomic<int> fit[64];  // per device; the kernel's shared-memory limit is set with the query
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -440,14 +481,14 @@ cudaError_t launch_tile_gemm_as(const CUtensorMap &a0, const CUtensorMap &a1, co
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   int n = fit[dev].load();
   if (n <= 0) {
-    n = tile_gemm_max_clusters(kernel, kTThreads<kOp>);
+    n = tile_gemm_max_clusters(kernel, kTThreads<kOp>, C::kSmem);
     if (n <= 0) {
       const cudaError_t last = cudaGetLastError();
       return last != cudaSuccess ? last : cudaErrorLaunchOutOfResources;
     }
     fit[dev].store(n);
   }
-  const int out_cols = kOp == TileOp::kGated ? kTHalf : kTCols;
+  const int out_cols = kOp == TileOp::kGated ? kTCols / 2 : kTCols;
   const int64_t tiles = ((static_cast<int64_t>(args.M) + kTRows - 1) / kTRows) *
                         ((static_cast<int64_t>(args.N) + out_cols - 1) / out_cols);
   // a balanced grid: every wave of tiles, the last included, is (nearly) full
@@ -456,18 +497,25 @@ cudaError_t launch_tile_gemm_as(const CUtensorMap &a0, const CUtensorMap &a1, co
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * clusters);
   cfg.blockDim = dim3(kTThreads<kOp>);
-  cfg.dynamicSmemBytes = kTSmem;
+  cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = 2;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, kernel, a0, a1, b0, b1, args);
+}
+
+// cols: 256 or 128 accumulator columns per tile; B's tensor maps have boxes of cols / 2 rows
+// (K-major) or 64 columns (MN-major).
+template <TileOp kOp, class T, int kAct>
+cudaError_t launch_tile_gemm_as(const CUtensorMap &a0, const CUtensorMap &a1, const CUtensorMap &b0,
+                                const CUtensorMap &b1, const TileArgs &args, int cols, cudaStream_t s) {
+  return cols == 256 ? launch_tile_gemm_cols<kOp, T, kAct, 256>(a0, a1, b0, b1, args, s)
+                     : launch_tile_gemm_cols<kOp, T, kAct, 128>(a0, a1, b0, b1, args, s);
 }
 
 }  // namespace nvfp4

@@ -365,10 +365,11 @@ def _whole(t: torch.Tensor, what: str, shape, dtypes) -> int:
 
 
 def _scratch(workspace: Optional[torch.Tensor], query: str, like: torch.Tensor, *sizes: int):
-    """The caller's workspace or a new one of the size that the query returns, and its bytes."""
+    """The caller's workspace or a new one of the size that the query returns (None for size 0), and
+    its bytes."""
     if workspace is None:
         n = getattr(lib(), query)(*sizes)
-        return torch.empty(n, dtype=torch.uint8, device=like.device), n
+        return (torch.empty(n, dtype=torch.uint8, device=like.device) if n else None), n
     n = workspace.numel()
     _whole(workspace, "workspace", (n,), (torch.uint8,))
     return workspace, n
@@ -451,8 +452,7 @@ def fp8_linear(x: torch.Tensor, w: torch.Tensor, w_s: torch.Tensor, out: Optiona
         _whole(out, "out", (M, N), (x.dtype,))
     y = out if out is not None else torch.empty(M, N, dtype=x.dtype, device=x.device)
     ws, ws_bytes = _scratch(workspace, "nvfp4_fp8_linear_workspace_bytes", x, M, K)
-    call("nvfp4_fp8_linear", x.data_ptr(), _kind(x, "x"), M, K, ld, N, wp, wsp, y.data_ptr(), ws.data_ptr(), ws_bytes,
-         st)
+    call("nvfp4_fp8_linear", x.data_ptr(), _kind(x, "x"), M, K, ld, N, wp, wsp, y.data_ptr(), _ptr(ws), ws_bytes, st)
     return y
 
 
@@ -502,7 +502,7 @@ def gated_linear_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tenso
     dwu = torch.empty(I, H, dtype=x.dtype, device=x.device) if need_dw else None
     ws, ws_bytes = _scratch(workspace, "nvfp4_gated_linear_backward_workspace_bytes", x, T, I)
     call("nvfp4_gated_linear_backward", dh.data_ptr(), lddh, x.data_ptr(), ld, kind, T, H, I, gp, up, act, gup,
-         _ptr(dx), _ptr(dwg), _ptr(dwu), ws.data_ptr(), ws_bytes, st)
+         _ptr(dx), _ptr(dwg), _ptr(dwu), _ptr(ws), ws_bytes, st)
     return dx, dwg, dwu
 
 
@@ -584,7 +584,7 @@ def residual_norm_backward(dr_out: Optional[torch.Tensor], dy: Optional[torch.Te
     ws, ws_bytes = _scratch(workspace, "nvfp4_residual_norm_backward_workspace_bytes", f, M, K, max(groups, 1), rkind)
     call("nvfp4_residual_norm_backward", _ptr(dr_out), lddr, _ptr(dy), lddy, f.data_ptr(), kind, r.data_ptr(), rkind,
          M, K, ldf, ldr, sp, ga, gp, gkind, groups, scale, gb, df.data_ptr(), dr.data_ptr(), _ptr(dga), _ptr(dgate),
-         _ptr(dgb), ws.data_ptr(), ws_bytes, st)
+         _ptr(dgb), _ptr(ws), ws_bytes, st)
     return df, dr, dga, dgate, dgb
 
 

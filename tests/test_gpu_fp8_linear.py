@@ -111,7 +111,8 @@ def test_quantize_weight_matches_definition(N, K):
         assert torch.equal(s, rs) and torch.equal(q.double(), rq)
 
 
-@pytest.mark.parametrize("M,K,N", [(1, 7168, 256), (7, 1536, 1000), (37, 1536, 640), (129, 1024, 129), (300, 2000, 400)])
+@pytest.mark.parametrize("M,K,N", [(1, 7168, 256), (7, 1536, 1000), (2, 16, 3), (16, 656, 130), (17, 2000, 77), (32, 1024, 8448),
+                                   (33, 1024, 260), (37, 1536, 640), (129, 1024, 129), (300, 2000, 400)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 def test_linear_random(M, K, N, dtype):
     g = torch.Generator(device=DEV).manual_seed(M + K)
@@ -136,7 +137,7 @@ def test_repeated_calls_give_the_same_bits():
             assert torch.equal(y, ops.fp8_linear(x, w, ws))
 
 
-@pytest.mark.parametrize("M", [3, 300])
+@pytest.mark.parametrize("M", [3, 40, 300])
 def test_nan_and_inf_stay_in_their_rows(M):
     g = torch.Generator(device=DEV).manual_seed(M)
     x = torch.randn(M, 512, generator=g, device=DEV).bfloat16()
@@ -150,7 +151,7 @@ def test_nan_and_inf_stay_in_their_rows(M):
     assert torch.equal(y[keep], clean[keep])
 
 
-@pytest.mark.parametrize("M", [5, 300])
+@pytest.mark.parametrize("M", [5, 50, 300])
 def test_strided_rows_and_given_buffers(M):
     g = torch.Generator(device=DEV).manual_seed(M)
     big = torch.randn(M, 1024 + 16, generator=g, device=DEV).bfloat16()
@@ -205,7 +206,7 @@ def test_refusals():
     for f in bad:
         with pytest.raises(ValueError):
             f()
-    for f in [lambda: ops.fp8_linear(x, w, ws, workspace=torch.empty(256, dtype=torch.uint8, device=DEV)),
+    for f in [lambda: ops.fp8_linear(x.repeat(16, 1), w, ws, workspace=torch.empty(256, dtype=torch.uint8, device=DEV)),
               lambda: ops.fp8_quantize_act(torch.zeros(4, 24, dtype=torch.bfloat16, device=DEV)),
               lambda: ops.fp8_quantize_act(torch.zeros(4, 36, dtype=torch.bfloat16, device=DEV)[:, :32]),
               lambda: ops.fp8_quantize_act(torch.zeros(1, 32, dtype=torch.bfloat16, device=DEV).expand(4, 32))]:
