@@ -1,0 +1,119 @@
+"""CPU checks of the dense feed-forward operators: the C ABI refuses bad arguments on the host, before any
+device is touched, with the right status and a message; workspace sizes; the torch layer's refusals."""
+
+import ctypes
+
+import pytest
+import torch
+
+from nvfp4_block_scaled_quant_gb300 import _lib, ops
+from nvfp4_block_scaled_quant_gb300 import build as B
+
+P = 1 << 20  # an aligned address that is never used: validation fails first
+BF, HF, F32 = _lib.DT_BF16, _lib.DT_FP16, _lib.DT_FP32
+
+
+@pytest.fixture(scope="module")
+def L():
+    B.build()
+    return _lib.lib()
+
+
+def refuses(L, name, args, want):
+    assert getattr(L, name)(*args) == want, (name, args, L.nvfp4_last_error_string())
+    assert L.nvfp4_last_error_string().startswith(name.encode())
+
+
+def changed(base, **kw):
+    """`base` (a dict in the order of the call's arguments) with some arguments replaced."""
+    return tuple({**base, **kw}.values())
+
+
+def test_fp8_quantisers(L):
+    a = dict(x=P, dtype=BF, M=4, K=256, ldx=256, q=P, xs=P, lds=4, stream=None)
+    for kw, st in [(dict(dtype=F32), 1), (dict(dtype=7), 1), (dict(M=-1), 1), (dict(K=0), 1), (dict(x=None), 1),
+                   (dict(q=None), 1), (dict(xs=None), 1), (dict(K=264), 2), (dict(K=1 << 24, ldx=1 << 24), 2),
+                   (dict(ldx=248), 3), (dict(ldx=260), 3), (dict(x=P + 2), 3), (dict(q=P + 8), 3), (dict(lds=3), 3), (dict(lds=6), 3)]:
+        refuses(L, "nvfp4_fp8_quantize_act", changed(a, **kw), st)
+    w = dict(w=P, dtype=HF, N=4, K=256, ldw=256, q=P, s=P, stream=None)
+    for kw, st in [(dict(N=0), 1), (dict(dtype=F32), 1), (dict(q=None), 1), (dict(K=24, ldw=24), 2), (dict(ldw=16), 3), (dict(w=P + 4), 3)]:
+        refuses(L, "nvfp4_fp8_quantize_weight", changed(w, **kw), st)
+
+
+def test_fp8_gemm_and_linear(L):
+    a = dict(xq=P, xs=P, lds=4, M=4, K=256, N=100, w=P, ws=P, dtype=BF, y=P, stream=None)
+    for kw, st in [(dict(N=0), 1), (dict(dtype=F32), 1), (dict(w=None), 1), (dict(y=None), 1), (dict(xs=None), 1), (dict(K=250), 2),
+                   (dict(N=1 << 24), 2), (dict(lds=2), 3), (dict(lds=5), 3), (dict(w=P + 8), 3), (dict(y=P + 2), 3)]:
+        refuses(L, "nvfp4_fp8_gemm", changed(a, **kw), st)
+    need = L.nvfp4_fp8_linear_workspace_bytes(100, 256)
+    assert need >= 100 * 256 + 2 * 100 * 4 and L.nvfp4_fp8_linear_workspace_bytes(32, 256) == 0
+    assert L.nvfp4_fp8_linear_workspace_bytes(100, 250) == 0 and L.nvfp4_fp8_linear_workspace_bytes(-1, 256) == 0
+    b = dict(x=P, dtype=BF, M=100, K=256, ldx=256, N=100, w=P, ws=P, y=P, work=P, bytes=need, stream=None)
+    for kw, st in [(dict(bytes=need - 1), 4), (dict(work=None), 1), (dict(work=P + 16), 3), (dict(N=-5), 1), (dict(w=None), 1),
+                   (dict(y=None), 1), (dict(x=P + 8), 3), (dict(K=255), 2)]:
+        refuses(L, "nvfp4_fp8_linear", changed(b, **kw), st)
+
+
+def test_gated_linear(L):
+    a = dict(x=P, dtype=BF, T=4, H=64, ldx=64, I=16, wg=P, wu=P, act=0, h=P, gu=None, stream=None)
+    for kw, st in [(dict(act=3), 1), (dict(act=-1), 1), (dict(dtype=F32), 1), (dict(T=-1), 1), (dict(wg=None), 1), (dict(h=None), 1),
+                   (dict(H=60, ldx=64), 2), (dict(I=12), 2), (dict(I=1 << 23), 2), (dict(ldx=56), 3), (dict(ldx=68), 3),
+                   (dict(wu=P + 8), 3), (dict(gu=P + 8), 3)]:
+        refuses(L, "nvfp4_gated_linear", changed(a, **kw), st)
+    need = L.nvfp4_gated_linear_backward_workspace_bytes(4, 16)
+    assert need == 256 and L.nvfp4_gated_linear_backward_workspace_bytes(4, 12) == 0
+    b = dict(dh=P, lddh=16, x=P, ldx=64, dtype=BF, T=4, H=64, I=16, wg=P, wu=P, act=0, gu=P, dx=P, dwg=P, dwu=P, ws=P, bytes=need,
+             stream=None)
+    for kw, st in [(dict(gu=None), 1), (dict(dh=None), 1), (dict(dwu=None), 1), (dict(dwg=None), 1), (dict(bytes=0), 4),
+                   (dict(lddh=8), 3), (dict(lddh=18), 3), (dict(dx=P + 2), 3), (dict(act=9), 1)]:
+        refuses(L, "nvfp4_gated_linear_backward", changed(b, **kw), st)
+
+
+def test_residual_norm(L):
+    a = dict(f=P, dtype=BF, r=P, rd=F32, M=6, K=64, ldf=64, ldr=64, ga=P, gate=P, kind=1, groups=3, scale=1.0, gb=P, eps=1e-6, ro=P, y=P,
+             stats=None, stream=None)
+    nan = float("nan")
+    for kw, st in [(dict(rd=HF), 1), (dict(dtype=F32), 1), (dict(M=-1), 1), (dict(f=None), 1), (dict(gate=None), 1), (dict(kind=0), 1),
+                   (dict(kind=5), 1), (dict(eps=-1.0), 1), (dict(eps=nan), 1), (dict(scale=nan), 1), (dict(ro=None), 1), (dict(y=None), 1),
+                   (dict(gb=None), 1), (dict(K=60), 2), (dict(K=16392, ldf=16392, ldr=16392), 2), (dict(groups=4), 2), (dict(groups=0), 2),
+                   (dict(ldf=56), 3), (dict(ldr=68), 3), (dict(ga=P + 8), 3), (dict(gate=P + 2), 3), (dict(y=P + 8), 3),
+                   (dict(ro=P, ldr=72), 3)]:
+        refuses(L, "nvfp4_residual_norm", changed(a, **kw), st)
+    need = L.nvfp4_residual_norm_backward_workspace_bytes(6, 64, 3, F32)
+    assert need > 0 and L.nvfp4_residual_norm_backward_workspace_bytes(6, 64, 4, F32) == 0
+    assert L.nvfp4_residual_norm_backward_workspace_bytes(0, 64, 1, F32) == 0
+    b = dict(dro=P, lddr=64, dy=P, lddy=64, f=P, dtype=BF, r=P, rd=F32, M=6, K=64, ldf=64, ldr=64, stats=P, ga=P, gate=P, kind=1, groups=3,
+             scale=1.0, gb=P, df=P, dr=P, dga=P, dgate=P, dgb=P, ws=P, bytes=need, stream=None)
+    for kw, st in [(dict(stats=None), 1), (dict(df=None), 1), (dict(gb=None), 1), (dict(ga=None), 1), (dict(gate=None, kind=0), 1),
+                   (dict(bytes=need - 1), 4), (dict(lddr=56), 3), (dict(lddy=66), 3), (dict(df=P + 8), 3), (dict(dga=P + 4), 3)]:
+        refuses(L, "nvfp4_residual_norm_backward", changed(b, **kw), st)
+
+
+@pytest.mark.parametrize("M,K,groups,kind", [(1, 8, 1, BF), (4096, 7168, 1, BF), (8192, 7168, 8, BF), (1001, 1544, 1, F32), (600, 64, 600, F32),
+                                             (3, 16384, 3, F32), (100000, 256, 4, BF)])
+def test_norm_workspace_holds_the_partial_sums(L, M, K, groups, kind):
+    """At most one row of K sums per CTA for each parameter, at most 152 x 8 CTAs: the size is bounded
+    whatever M, and it is a whole number of rows of three (or two) sums."""
+    n = L.nvfp4_residual_norm_backward_workspace_bytes(M, K, groups, kind)
+    row = 4 * K
+    assert 2 * row <= n <= 3 * (152 * 8 * row + 256)
+
+
+def test_valid_calls_without_a_gpu_fail_cleanly(L):
+    if torch.cuda.is_available():
+        pytest.skip("a GPU is present")
+    buf = ctypes.create_string_buffer(1 << 16)
+    p = (ctypes.addressof(buf) + 255) & ~255
+    calls = [("nvfp4_fp8_quantize_act", (p, BF, 4, 256, 256, p, p, 4, None)),
+             ("nvfp4_fp8_gemm", (p, p, 4, 4, 256, 8, p, p, BF, p, None)),
+             ("nvfp4_gated_linear", (p, BF, 4, 64, 64, 16, p, p, 0, p, None, None)),
+             ("nvfp4_residual_norm", (p, BF, p, BF, 4, 64, 64, 64, None, None, 0, 0, 1.0, None, 1e-6, p, None, None, None))]
+    for name, args in calls:
+        assert getattr(L, name)(*args) in (_lib.ERR_CUDA, _lib.ERR_UNSUPPORTED_DEVICE)
+
+
+def test_torch_layer_refuses_cpu_tensors():
+    x, w = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(16, 64, dtype=torch.bfloat16)
+    for f in [lambda: ops.fp8_quantize_act(x), lambda: ops.gated_linear(x, w, w), lambda: ops.residual_norm(x, x)]:
+        with pytest.raises(ValueError, match="CUDA"):
+            f()
