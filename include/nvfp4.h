@@ -405,8 +405,8 @@ NVFP4_API nvfp4_status nvfp4_fp8_gemm(const uint8_t *xq, const float *xs, int64_
                                       int64_t N, const uint8_t *w, const float *w_s, int dtype, void *y,
                                       void *stream);
 /* The quantiser and the product in one call, with the two calls' results bit for bit; the workspace
- * holds the codes and scales.  With M <= 32 the product quantises x itself: one launch, and no
- * workspace (its size is 0). */
+ * holds the codes and scales.  With few rows (M <= 16, or up to 64 of a small product) the product
+ * quantises x itself: one launch; up to 16 rows the workspace's size is 0. */
 NVFP4_API size_t nvfp4_fp8_linear_workspace_bytes(int64_t M, int64_t K);
 NVFP4_API nvfp4_status nvfp4_fp8_linear(const void *x, int dtype, int64_t M, int64_t K, int64_t ldx, int64_t N,
                                         const uint8_t *w, const float *w_s, void *y, void *ws, size_t ws_bytes,

@@ -132,13 +132,25 @@ nvfp4_status check_fp8_x(const char *fn, const void *x, int dtype, int64_t M, in
   return NVFP4_OK;
 }
 
+// Whether the weight-streaming GEMM quantises the activations itself.  That saves a launch (about 3 us
+// of GPU time, and of the host's), but every CTA encodes the rows of its K blocks again: it pays up to
+// one token tile of 16 rows, and up to 64 rows while the product is small.  GPU time in one launch / two:
+// 7168 -> 7168 of 1 row 9.1 / 13.3 us, of 8 rows 10.9 / 11.7, of 16 rows 14.9 / 13.2 (the host's time
+// still favours one), of 32 rows 24 / 14; 2000 -> 1136 of 24 rows 7.6 / 7.5, of 64 rows 8.2 / 8.8;
+// 512 x 512 of 24 rows 6.5 / 7.8, of 64 rows 6.6 / 9.0; 2048 -> 7168 of 32 rows 12.1 / 9.7.
+constexpr int64_t kFp8FusedM = 16, kFp8FusedSmallM = 64, kFp8FusedSmallMnk = int64_t(1) << 27;
+constexpr int kFp8FusedTok = 32;
+bool quantise_in_gemm(int64_t M, int64_t K, int64_t N) {
+  return M <= kFp8FusedM || (M <= kFp8FusedSmallM && M * N * K <= kFp8FusedSmallMnk);
+}
+
 struct Fp8Ws {
   size_t q, s, total;
   int64_t lds;
 };
 Fp8Ws fp8_ws(int64_t M, int64_t K) {
   Fp8Ws w = {};
-  if (M <= kFp8FusedMaxM) return w;  // quantised in the GEMM
+  if (M <= kFp8FusedM) return w;  // quantised in the GEMM
   w.lds = round_up(M, 4);
   w.q = 0;
   w.s = align256(static_cast<size_t>(M) * static_cast<size_t>(K));
@@ -229,7 +241,7 @@ nvfp4_status nvfp4_fp8_linear(const void *x, int dtype, int64_t M, int64_t K, in
   if ((st = device_info(__func__, &d)) != NVFP4_OK) return st;
   if (M == 0) return NVFP4_OK;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (M <= kFp8FusedMaxM) {
+  if (quantise_in_gemm(M, K, N)) {
     CUtensorMap mw;
     if ((st = make_map(__func__, &mw, w, K, N, K, 128)) != NVFP4_OK) return st;
     StreamArgs a = {};
@@ -243,8 +255,10 @@ nvfp4_status nvfp4_fp8_linear(const void *x, int dtype, int64_t M, int64_t K, in
     a.x = x;
     a.ldx = ldx;
     a.err = d->flags;
-    const StreamPlan p = stream_plan(M, N, a.k_blocks, kFp8FusedMaxM, d->sms, kFp8Cost);
-    NV_CUDA(launch_fp8_stream_linear(mw, a, dtype, p.tok, p.splits, s), "FP8 linear launch");
+    // the splits of the product after a quantiser: the same sums in the same order
+    const StreamPlan p = stream_plan(M, N, a.k_blocks, kFp8StreamTok, d->sms, kFp8Cost);
+    NV_CUDA(launch_fp8_stream_linear(mw, a, dtype, p.tok < kFp8FusedTok ? p.tok : kFp8FusedTok, p.splits, s),
+            "FP8 linear launch");
     return NVFP4_OK;
   }
   uint8_t *q = static_cast<uint8_t *>(ws) + L.q;

@@ -307,7 +307,6 @@ cudaError_t launch_fp8_stream_gemm(const CUtensorMap &w, const CUtensorMap &x, c
 // The same with the activations quantised in the GEMM (args.x, tok 16 or 32).
 cudaError_t launch_fp8_stream_linear(const CUtensorMap &w, const StreamArgs &args, int dtype, int tok, int splits,
                                      cudaStream_t s);
-constexpr int64_t kFp8FusedMaxM = 32;
 
 // ---------------------------------------------------------------- gated linear
 cudaError_t launch_gated_tile_gemm(const CUtensorMap &x, const CUtensorMap &wg, const CUtensorMap &wu,

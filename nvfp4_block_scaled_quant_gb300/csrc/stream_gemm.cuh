@@ -17,7 +17,7 @@
 // FP8: the product of one K block goes to one of kBufs accumulators, and the epilogue warps add it
 // to fp32 registers times sw[tile, b] * sa[b, token] (a 128-row weight tile has one scale per block).
 //
-// kQuant (FP8, at most 32 tokens): four more warps quantise the 16-bit activations into the ring
+// kQuant (FP8, tiles of at most 32 tokens): four more warps quantise the 16-bit activations into the ring
 // themselves, with the quantiser kernel's arithmetic, so that a decoded token takes one launch.  Every
 // CTA quantises its K blocks of all tokens; that pays while the tokens are few.
 //
@@ -66,12 +66,15 @@ struct StreamCfg {
   static_assert(kPartialBytes <= kRing, "the partial sums fit where the ring was");
   static_assert(kCols <= 256, "two CTAs share the SM's 512 tensor-memory columns");
   static_assert(2 * (kSmem + 1024) <= 233472, "two CTAs per SM");
-  static_assert(!kQuant || (kFp8 && kTok <= 32), "the quantisers hold a few tokens of four K blocks in registers");
+  static_assert(!kQuant || (kFp8 && kTok <= 32), "a quantiser holds all tokens of a K block in registers");
   static_assert((2 * kStages + 2 * kBufs) * 8 + 8 <= 256, "barrier region");
   static_assert(kTok % 16 == 0 && kStages >= 2, "MMA N and ring");
 };
 
 constexpr int kStreamMaxSplit = 8;  // portable cluster size
+
+// Quantising warps that share a K block of `rows` tokens, eight each (the last tile's rows may be fewer)
+__device__ __forceinline__ int quant_share(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 
 template <bool kFp8, class T, int kAct, int kTok, bool kQuant>
 __global__ void __launch_bounds__(StreamCfg<kFp8, kTok, kQuant>::kThreads, 2)
@@ -100,7 +103,7 @@ __global__ void __launch_bounds__(StreamCfg<kFp8, kTok, kQuant>::kThreads, 2)
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
-      mbar_init(&full[s], 1 + C::kQuantWarps);
+      mbar_init(&full[s], kQuant ? 1 + quant_share(min(kTok, args.M - m0)) : 1);
       // FP8: the epilogue also reads the stage's token scales
       mbar_init(&empty[s], kFp8 ? 5 : 1);
     }
@@ -209,53 +212,56 @@ __global__ void __launch_bounds__(StreamCfg<kFp8, kTok, kQuant>::kThreads, 2)
     if (!ok) settle();
   } else if (kQuant && warp >= 6) {
     // -------------------------------------------------------------- quantisers
-    // 16 lanes hold one token's 128 elements of a K block, so the four warps take eight tokens at a
-    // time.  The loads of kGroup K blocks are in flight together: one memory latency per group,
-    // behind the ring.  Columns of tokens past M are left as they are: they feed no output.
+    // A warp takes eight tokens of a K block, two at a time (16 lanes hold one token's 128 elements),
+    // so the four warps work on four, two or one blocks at once, for up to 8, 16 or more tokens: the
+    // latency of a block, a few hundred cycles of dependent steps, is shared by the blocks in work (one
+    // token 7168 -> 7168: 9.1 us, with the four warps on one block 15.5).  A register is loaded again,
+    // for the warp's next block, as soon as it is encoded.  Columns of tokens past M are left as they
+    // are: they feed no output.
     if constexpr (kQuant) {
-      constexpr int kGroup = 4, kPasses = kTok / 8;
-      const int gl = lane & 15, slot = (warp - 6) * 2 + (lane >> 4);
-      const uint16_t *x = static_cast<const uint16_t *>(args.x);
-      int stage = 0;
+      constexpr int kHold = 4;
+      static_assert(C::kStages >= C::kQuantWarps, "a warp's stages wrap at most once per step");
+      const int share = quant_share(min(kTok, args.M - m0)), step = C::kQuantWarps / share;
+      const int gl = lane & 15, row0 = (warp - 6) % share * 8 + (lane >> 4);
+      const uint16_t *x = static_cast<const uint16_t *>(args.x) + (m0 + row0) * args.ldx + gl * 8;
+      auto load = [&](int kb, int q) {
+        return m0 + row0 + q * 2 < args.M && kb < kb1 && kb * 128 + gl * 8 < args.K
+                   ? __ldg(reinterpret_cast<const uint4 *>(x + q * 2 * args.ldx + kb * 128))
+                   : make_uint4(0u, 0u, 0u, 0u);
+      };
+      int stage = (warp - 6) / share;
       uint32_t phase = 0;
-      bool ok = true;
-      for (int g0 = kb0; ok && g0 < kb1; g0 += kGroup) {
-        uint4 v[kGroup][kPasses];
+      uint4 v[kHold];
 #pragma unroll
-        for (int u = 0; u < kGroup; ++u)
+      for (int q = 0; q < kHold; ++q) v[q] = load(kb0 + stage, q);
+      for (int kb = kb0 + stage; kb < kb1; kb += step) {
+        bool ok = mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, args.err, kPipelineTimeoutNs);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
 #pragma unroll
-          for (int p = 0; p < kPasses; ++p) {
-            const int tok = m0 + p * 8 + slot, k = (g0 + u) * 128 + gl * 8;
-            v[u][p] = make_uint4(0u, 0u, 0u, 0u);
-            if (g0 + u < kb1 && tok < args.M && k < args.K)
-              v[u][p] = __ldg(reinterpret_cast<const uint4 *>(x + tok * args.ldx + k));
-          }
-#pragma unroll
-        for (int u = 0; u < kGroup; ++u) {
-          if (g0 + u >= kb1) break;
-          ok = mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, args.err, kPipelineTimeoutNs);
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
-#pragma unroll
-          for (int p = 0; p < kPasses; ++p) {
-            const int row = p * 8 + slot;
-            uint32_t a = max_abs16(v[u][p]);
+        for (int q = 0; q < kHold; ++q) {
+          const int row = row0 + q * 2;
+          const bool mine = m0 + row < args.M;
+          if (__any_sync(0xffffffffu, mine)) {
+            uint32_t a = max_abs16(v[q]);
 #pragma unroll
             for (int o = 8; o; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
             const float sc = __fdiv_rn(T::up(a), 448.f);
-            if (m0 + row < args.M) {  // rows of 128 bytes, 16-byte chunks swizzled by the row
+            if (mine) {  // rows of 128 bytes, 16-byte chunks swizzled by the row
               uint8_t *d = sX + stage * C::kXBytes + row * 128 + (((gl >> 1) ^ (row & 7)) << 4) + (gl & 1) * 8;
-              *reinterpret_cast<uint2 *>(d) = encode8<T>(v[u][p], sc);
+              *reinterpret_cast<uint2 *>(d) = encode8<T>(v[q], sc);
               if (gl == 0) sS[stage * kTok + row] = sc;
             }
           }
-          fence_proxy_async_shared();  // the codes are read by the tensor core
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&full[stage]);
-          if (++stage == C::kStages) {
-            stage = 0;
-            phase ^= 1;
-          }
+          v[q] = load(kb + step, q);
+        }
+        fence_proxy_async_shared();  // the codes are read by the tensor core
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&full[stage]);
+        stage += step;
+        if (stage >= C::kStages) {
+          stage -= C::kStages;
+          phase ^= 1;
         }
       }
     }

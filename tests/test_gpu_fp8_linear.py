@@ -112,7 +112,8 @@ def test_quantize_weight_matches_definition(N, K):
 
 
 @pytest.mark.parametrize("M,K,N", [(1, 7168, 256), (7, 1536, 1000), (2, 16, 3), (16, 656, 130), (17, 2000, 77), (32, 1024, 8448),
-                                   (33, 1024, 260), (37, 1536, 640), (129, 1024, 129), (300, 2000, 400)])
+                                   (33, 1024, 260), (37, 1536, 640), (24, 7168, 2700),
+                                   (48, 2000, 1136), (64, 512, 500), (64, 4096, 130), (129, 1024, 129), (300, 2000, 400)])
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
 def test_linear_random(M, K, N, dtype):
     g = torch.Generator(device=DEV).manual_seed(M + K)
