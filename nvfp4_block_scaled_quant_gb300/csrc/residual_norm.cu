@@ -398,6 +398,7 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
   __shared__ __align__(16) float red[2][kNbRedFloats];
   __shared__ float peer_sums[2][kNormMaxSlices][3];
   __shared__ uint64_t full[kNormMaxStages];
+  __shared__ unsigned done[kNormMaxStages];  // warps done with the stage
   __shared__ int s_abort;
   volatile int *abort_flag = &s_abort;
 
@@ -411,11 +412,19 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
   const int b16 = a.slice_cols * 2, br = a.slice_cols * Res<T, kR32>::kBytes;
   const int stage_bytes = 2 * b16 + 2 * br;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1);
+    for (int s = 0; s < a.stages; ++s) mbar_init(&full[s], 1), done[s] = 0;
     s_abort = 0;
     fence_barrier_init();
   }
   for (int i = static_cast<int>(threadIdx.x); i < 2 * kNbRedFloats; i += static_cast<int>(blockDim.x)) red[0][i] = 0.f;
+  // an absent gradient reads as zeros: no copy touches its part of the stages
+  for (int s = 0; s < a.stages; ++s) {
+    uint4 *d = reinterpret_cast<uint4 *>(smem + s * stage_bytes);
+    for (int i = static_cast<int>(threadIdx.x); i < b16 / 16 && !a.dy; i += static_cast<int>(blockDim.x))
+      d[b16 / 16 + i] = make_uint4(0u, 0u, 0u, 0u);
+    for (int i = static_cast<int>(threadIdx.x); i < br / 16 && !a.dr_out; i += static_cast<int>(blockDim.x))
+      d[(2 * b16 + br) / 16 + i] = make_uint4(0u, 0u, 0u, 0u);
+  }
   __syncthreads();
   pdl_wait();
   pdl_trigger();
@@ -432,8 +441,7 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
     m_last = a.groups * (part + 1) / ctas * a.rows_per_group;
   }
   const uint64_t pol = policy_evict_first();
-  auto load_row = [&](int64_t m) {
-    const int s = static_cast<int>((m - m_first) % a.stages);
+  auto load_row = [&](int64_t m, int s) {
     uint8_t *d = smem + s * stage_bytes;
     const uint32_t n16 = static_cast<uint32_t>(cols) * 2u, nr = static_cast<uint32_t>(cols) * Res<T, kR32>::kBytes;
     mbar_arrive_expect_tx(&full[s], n16 + nr + (a.dy ? n16 : 0u) + (a.dr_out ? nr : 0u));
@@ -445,7 +453,7 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
                 &full[s], pol);
   };
   if (threadIdx.x == 0)
-    for (int64_t m = m_first; m < m_last && m < m_first + a.stages; ++m) load_row(m);
+    for (int s = 0; s < a.stages && m_first + s < m_last; ++s) load_row(m_first + s, s);
 
   const uint16_t *gp = static_cast<const uint16_t *>(a.gate);
   const bool row_gate = a.gate_kind == NVFP4_GATE_ROW, channel_gate = a.gate_kind == NVFP4_GATE_CHANNEL;
@@ -501,9 +509,8 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
     auto fetch = [&](int h) {
       load_pairs<T, false, 2>(d, col[h], fv);
       load_pairs<T, kR32, 2>(d + 2 * b16, col[h], rv);
-      dyv[0] = dyv[1] = uv[0] = uv[1] = both(0.f);
-      if (a.dy) load_pairs<T, false, 2>(d + b16, col[h], dyv);
-      if (a.dr_out) load_pairs<T, kR32, 2>(d + 2 * b16 + br, col[h], uv);
+      load_pairs<T, false, 2>(d + b16, col[h], dyv);
+      load_pairs<T, kR32, 2>(d + 2 * b16 + br, col[h], uv);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         tv[i] = fv[i] * w[h][i];
@@ -536,8 +543,7 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
       for (int o = 4; o; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
       if ((lane & 7) == 0) red[pb][(lane >> 3) * 32 + warp] = t;
     }
-    __syncthreads();  // also: every thread is done with the previous row's stage
-    if (threadIdx.x == 0 && m > m_first && m - 1 + a.stages < m_last) load_row(m - 1 + a.stages);
+    __syncthreads();
     {
       const float4 v = *reinterpret_cast<const float4 *>(&red[pb][lane * 4]);
       float t = (v.x + v.y) + (v.z + v.w);
@@ -582,6 +588,15 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
         }
         store_pairs<T, kR32, 2>(a.dr, m * a.K + k0 + col[h], uv);
         store_pairs<T, false, 2>(a.df, m * a.K + k0 + col[h], df);
+      }
+    }
+    // the last warp that is done with the stage fills it again (the counter returns to zero)
+    __syncwarp();
+    if (lane == 0) {
+      __threadfence_block();
+      if (atomicInc(&done[s], (blockDim.x >> 5) - 1) == (blockDim.x >> 5) - 1 && m + a.stages < m_last) {
+        __threadfence_block();
+        load_row(m + a.stages, s);
       }
     }
     if (rows_left == 0) {  // the end of a group of rows
