@@ -257,9 +257,7 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const NormArgs a
 // its cache, and re-reading them for every row cost as much as the rows).
 template <class T, bool kR32, int kChunks, int kThreads, int kCtas>
 __global__ void __launch_bounds__(kThreads, kCtas) residual_norm_rows_kernel(const NormArgs a, int stages) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) &
-                                              ~static_cast<uintptr_t>(127));
+  extern __shared__ __align__(128) uint8_t smem[];  // used as declared: its loads are known to be shared ones
   __shared__ float red[2][32];
   __shared__ uint64_t full[kNormMaxStages];
   __shared__ int s_abort;
@@ -392,9 +390,7 @@ constexpr int kNbRedFloats = 4 * 32;  // three sums of up to 32 warps each, and 
 
 template <class T, bool kR32>
 __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_kernel(const NormGradArgs a) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 127) &
-                                              ~static_cast<uintptr_t>(127));
+  extern __shared__ __align__(128) uint8_t smem[];  // used as declared: its loads are known to be shared ones
   __shared__ __align__(16) float red[2][kNbRedFloats];
   __shared__ float peer_sums[2][kNormMaxSlices][3];
   __shared__ uint64_t full[kNormMaxStages];
@@ -707,7 +703,7 @@ cudaError_t norm_forward(const NormArgs &a, int sms, cudaStream_t s) {
   while (stages < 2 && per_sm > 1) stages = (kNormMaxSmem / --per_sm - 2048) / stage;
   if (stages > kNormMaxStages) stages = kNormMaxStages;
   if (stages < 1) stages = 1;
-  const int smem = 128 + stages * stage;
+  const int smem = stages * stage;
   const int64_t cap = static_cast<int64_t>(sms) * per_sm;
   const dim3 grid(static_cast<unsigned>(a.M < cap ? a.M : cap)), block(threads);
   auto kernel = wide ? residual_norm_rows_kernel<T, kR32, 2, 1024, 1> : residual_norm_rows_kernel<T, kR32, 2, 448, 2>;
@@ -784,8 +780,9 @@ NormGradPlan norm_grad_plan(int64_t M, int64_t K, int64_t groups, bool r32) {
   p.stages = budget / stage;
   if (p.stages > kNormMaxStages) p.stages = kNormMaxStages;
   if (p.stages < 1) p.stages = 1;
-  p.smem = 128 + p.stages * stage;
-  const int64_t want = static_cast<int64_t>(kNormSms) * per_sm / p.slices;
+  p.smem = p.stages * stage;
+  // one wave: of clusters of three with an SM per CTA, the GPU's partitions hold 46 at once (not 50)
+  const int64_t want = p.slices == 3 ? 46 : static_cast<int64_t>(kNormSms) * per_sm / p.slices;
   const int64_t rows_per_group = groups > 0 ? M / groups : M;
   if (groups >= want) {
     p.parts = 1;
@@ -793,7 +790,7 @@ NormGradPlan norm_grad_plan(int64_t M, int64_t K, int64_t groups, bool r32) {
   } else {
     // few rows per CTA cost more in partial sums than they save: at least kNormGradRows each, as
     // long as every SM still has a CTA
-    const int64_t base = static_cast<int64_t>(kNormSms) / p.slices;
+    const int64_t base = p.slices == 3 ? want : kNormSms / p.slices;
     int64_t goal = M / kNormGradRows;
     if (goal < base) goal = base;
     if (goal > want) goal = want;
