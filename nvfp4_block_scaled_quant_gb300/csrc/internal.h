@@ -358,9 +358,11 @@ struct NormGradPlan {
   int slices, slice_cols, threads, stages, parts, ctas, smem;
 };
 constexpr int64_t kNormMaxK = 16384;
-constexpr int kNormGradThreads = 896; // threads of a backward CTA: 72 registers each
-constexpr int kNormSlice = 8 * kNormGradThreads;  // columns of a backward CTA (8 per thread)
-constexpr int kNormMaxSlices = 3;    // ceil(kNormMaxK / kNormSlice)
+constexpr int kNormGradThreads = 512; // most threads of a backward CTA: 128 registers each
+constexpr int kNormGradGroups = 4;   // groups of four columns of a thread
+constexpr int kNormGradMaxCtas = 8;  // most backward CTAs of an SM
+constexpr int kNormSlice = 4 * kNormGradGroups * kNormGradThreads;  // columns of a backward CTA
+constexpr int kNormMaxSlices = 2;    // ceil(kNormMaxK / kNormSlice)
 constexpr int kNormMaxStages = 4;
 constexpr int kNormMaxSmem = 225 * 1024;
 constexpr int kNormGradRows = 4;     // rows of a backward CTA aimed at when there are few

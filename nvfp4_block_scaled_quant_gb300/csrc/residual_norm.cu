@@ -401,9 +401,14 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
   const int slice = static_cast<int>(blockIdx.x) % a.slices, part = static_cast<int>(blockIdx.x) / a.slices;
   const int k0 = slice * a.slice_cols, cols = min(a.slice_cols, a.K - k0);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  // this thread's columns of the slice: two groups of four, each contiguous over the block
-  const int col[2] = {static_cast<int>(threadIdx.x) * 4, static_cast<int>(blockDim.x + threadIdx.x) * 4};
-  const bool live[2] = {col[0] < cols, col[1] < cols};
+  // this thread's columns of the slice: groups of four, each contiguous over the block
+  int col[kNormGradGroups];
+  bool live[kNormGradGroups];
+#pragma unroll
+  for (int h = 0; h < kNormGradGroups; ++h) {
+    col[h] = static_cast<int>(blockDim.x * h + threadIdx.x) * 4;
+    live[h] = col[h] < cols;
+  }
   // ring stage: f, dy (16 bits), r, dr' (16 or 32 bits), each slice_cols wide
   const int b16 = a.slice_cols * 2, br = a.slice_cols * Res<T, kR32>::kBytes;
   const int stage_bytes = 2 * b16 + 2 * br;
@@ -422,6 +427,7 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
       d[(2 * b16 + br) / 16 + i] = make_uint4(0u, 0u, 0u, 0u);
   }
   __syncthreads();
+  if (a.slices > 1) cluster_meet();  // the other slices' memory may be written from here on
   pdl_wait();
   pdl_trigger();
 
@@ -456,9 +462,10 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
   const float inv_k = 1.f / static_cast<float>(a.K);
   // Per thread and column: w = ga gate (it changes with the group of rows) and gb; the sums over rows
   // of dy rh (dgb) and z = scale ia f dR, of which both dga = gate z and dgate = ga z are multiples.
-  Two w[2][2], gb[2][2], acc_a[2][2], acc_b[2][2], acc_z[2][2];
+  Two w[kNormGradGroups][2], gb[kNormGradGroups][2];
+  Two acc_a[kNormGradGroups][2], acc_b[kNormGradGroups][2], acc_z[kNormGradGroups][2];
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < kNormGradGroups; ++h) {
     load_params<T, 2>(live[h] ? a.gb : nullptr, k0 + col[h], 0.f, gb[h]);
     if (!a.gb) gb[h][0] = gb[h][1] = both(0.f);
 #pragma unroll
@@ -485,7 +492,7 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
       group = group_of(m, a.rows_per_group);
       rows_left = min((group + 1) * a.rows_per_group, m_last) - m;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kNormGradGroups; ++h) {
         Two gate[2];
         load_params<T, 2>(live[h] ? a.ga : nullptr, k0 + col[h], 1.f, w[h]);
         load_params<T, 2>(live[h] && channel_gate ? gp + group * a.K : nullptr, k0 + col[h], 1.f, gate);
@@ -515,7 +522,7 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
     };
     Two s2 = both(0.f), sA = both(0.f), sC = both(0.f);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < kNormGradGroups; ++h) {
       if (live[h]) {
         fetch(h);
 #pragma unroll
@@ -570,7 +577,7 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
     const Two nk = both(-kappa), nl = both(a.ga ? -ia * ia * (gm * S * inv_k) : 0.f);
     if (row_gate && a.dgate && threadIdx.x == 0 && slice == 0) a.dgate[m] = a.scale * S;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    for (int h = 0; h < kNormGradGroups; ++h) {
       if (live[h]) {
         fetch(h);
         Two df[2];
@@ -598,7 +605,7 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
     if (rows_left == 0) {  // the end of a group of rows
       const int64_t at = (a.parts > 1 ? part : group) * a.K + k0;
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      for (int h = 0; h < kNormGradGroups; ++h) {
         if (live[h]) {
           Two x[2], gate[2];
           load_params<T, 2>(channel_gate ? gp + group * a.K : nullptr, k0 + col[h], 1.f, gate);
@@ -619,7 +626,7 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
     }
   }
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
+  for (int h = 0; h < kNormGradGroups; ++h) {
     if (live[h]) {
       const int64_t at = static_cast<int64_t>(part) * a.K + k0;
       if (a.part_a) store_pairs<T, true, 2>(a.part_a + at, col[h], acc_a[h]);
@@ -770,19 +777,18 @@ NormGradPlan norm_grad_plan(int64_t M, int64_t K, int64_t groups, bool r32) {
   NormGradPlan p;
   p.slices = static_cast<int>((K + kNormSlice - 1) / kNormSlice);
   p.slice_cols = static_cast<int>(((K + p.slices - 1) / p.slices + 7) / 8 * 8);
-  p.threads = (p.slice_cols / 8 + 31) / 32 * 32;
+  p.threads = (p.slice_cols + 128 * kNormGradGroups - 1) / (128 * kNormGradGroups) * 32;
   const int stage = p.slice_cols * (r32 ? 12 : 8);
   // narrow rows: several CTAs per SM share its shared memory
   int per_sm = kNormGradThreads / p.threads;
-  if (per_sm > 8) per_sm = 8;
+  if (per_sm > kNormGradMaxCtas) per_sm = kNormGradMaxCtas;
   if (per_sm < 1) per_sm = 1;
   const int budget = (kNormMaxSmem - 1024) / per_sm - 1024;
   p.stages = budget / stage;
   if (p.stages > kNormMaxStages) p.stages = kNormMaxStages;
   if (p.stages < 1) p.stages = 1;
   p.smem = p.stages * stage;
-  // one wave: of clusters of three with an SM per CTA, the GPU's partitions hold 46 at once (not 50)
-  const int64_t want = p.slices == 3 ? 46 : static_cast<int64_t>(kNormSms) * per_sm / p.slices;
+  const int64_t want = static_cast<int64_t>(kNormSms) * per_sm / p.slices;
   const int64_t rows_per_group = groups > 0 ? M / groups : M;
   if (groups >= want) {
     p.parts = 1;
@@ -790,7 +796,7 @@ NormGradPlan norm_grad_plan(int64_t M, int64_t K, int64_t groups, bool r32) {
   } else {
     // few rows per CTA cost more in partial sums than they save: at least kNormGradRows each, as
     // long as every SM still has a CTA
-    const int64_t base = p.slices == 3 ? want : kNormSms / p.slices;
+    const int64_t base = kNormSms / p.slices;
     int64_t goal = M / kNormGradRows;
     if (goal < base) goal = base;
     if (goal > want) goal = want;
