@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(kFqThreads)
       uint32_t a = max_abs16(v[u]);
 #pragma unroll
       for (int o = kFqGroup / 2; o; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-      const float sc = __fdiv_rn(T::up(a), 448.f);
+      const float sc = scale_of<T>(a);
       const int k = (b0 + u) * 128 + gl * 8;
       if (row_ok && k < K) *reinterpret_cast<uint2 *>(q + m * K + k) = encode8<T>(v[u], sc);
       if (row_ok && gl == 0 && b0 + u < blocks) s[(b0 + u) * lds + m] = sc;
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(kFqThreads)
   __syncthreads();
 #pragma unroll
   for (int i = 0; i < kFqThreads / 32; ++i) a = max(a, red[i]);
-  const float sc = __fdiv_rn(T::up(a), 448.f);
+  const float sc = scale_of<T>(a);
   if (threadIdx.x == 0) s[static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x] = sc;
 #pragma unroll
   for (int i = 0; i < 128 / kFqRows; ++i) {

@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(StreamCfg<kFp8, kTok, kQuant>::kThreads, 2)
             uint32_t a = max_abs16(v[q]);
 #pragma unroll
             for (int o = 8; o; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
-            const float sc = __fdiv_rn(T::up(a), 448.f);
+            const float sc = scale_of<T>(a);
             if (mine) {  // rows of 128 bytes, 16-byte chunks swizzled by the row
               uint8_t *d = sX + stage * C::kXBytes + row * 128 + (((gl >> 1) ^ (row & 7)) << 4) + (gl & 1) * 8;
               *reinterpret_cast<uint2 *>(d) = encode8<T>(v[q], sc);

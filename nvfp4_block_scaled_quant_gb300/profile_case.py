@@ -9,6 +9,9 @@
     python -m nvfp4_block_scaled_quant_gb300.profile_case norm --M 128 --iters 3
     python -m nvfp4_block_scaled_quant_gb300.profile_case router --T 128 --iters 3
     python -m nvfp4_block_scaled_quant_gb300.profile_case quant --M 4096 --iters 3
+    python -m nvfp4_block_scaled_quant_gb300.profile_case fp8 --M 4096 --iters 3
+    python -m nvfp4_block_scaled_quant_gb300.profile_case gated --M 4096 --iters 3
+    python -m nvfp4_block_scaled_quant_gb300.profile_case resnorm --M 8192 --iters 3
 
 ``moe`` runs 128-token prefill chunks (hidden 7168, intermediate 2048, top-8
 Zipf(1.1) routing, shared expert; ``--T`` above 1 sets the batch instead, e.g.
@@ -22,7 +25,10 @@ weights are needed); ``norm`` the fused RMSNorm -> NVFP4 quantiser over hidden
 7168; ``router`` the router gate (384 experts, hidden 7168, top-8); ``quant``
 the activation quantiser over K = 7168 (M = 1024 .. 16384 are the large-GEMM
 sweep's activations); ``linear`` the dense 1536 -> 16384 linear and ``grouped`` the
-fixed-group 8 x (4096 -> 1024) linear at ``--M`` tokens.
+fixed-group 8 x (4096 -> 1024) linear at ``--M`` tokens.  ``fp8`` runs the FP8 block-scaled
+linear (7168 -> 2048 of one token, else 7168 -> 7168), ``gated`` the gated linear
+7168 -> 2 x 2048 in bf16 and ``resnorm`` the residual norm over 7168 columns, both with
+their gradients above one token.
 """
 
 from __future__ import annotations
@@ -37,7 +43,8 @@ from . import build as B
 
 def main(argv=None):
     p = argparse.ArgumentParser()
-    p.add_argument("case", choices=["moe", "decode", "gemm", "linear", "grouped", "dispatch", "norm", "router", "quant"])
+    p.add_argument("case", choices=["moe", "decode", "gemm", "linear", "grouped", "dispatch", "norm", "router", "quant", "fp8",
+                                "gated", "resnorm"])
     p.add_argument("--T", type=int, default=1)
     p.add_argument("--experts", type=int, default=64)
     p.add_argument("--M", type=int, default=4096)
@@ -114,6 +121,33 @@ def main(argv=None):
         for i in range(a.iters):
             x = workloads.activations(a.M, 7168, seed=80 + i, device=dev)
             ops.quantize_act(x)
+    elif a.case == "fp8":
+        K, N = 7168, 2048 if a.M == 1 else 7168
+        w, ws = ops.fp8_quantize_weight(workloads.weight(N, K, 50, dev).bfloat16())
+        x = workloads.activations(a.M, K, seed=60, device=dev, outliers=True)
+        for _ in range(a.iters):
+            ops.fp8_linear(x, w, ws)
+    elif a.case == "gated":
+        H, I = 7168, 2048
+        wg, wu = (workloads.weight(I, H, s, dev).bfloat16() for s in (51, 52))
+        x = workloads.activations(a.M, H, seed=61, device=dev)
+        dh = workloads.activations(a.M, I, seed=62, device=dev)
+        for _ in range(a.iters):
+            if a.M == 1:
+                ops.gated_linear(x, wg, wu)
+            else:
+                _, gu = ops.gated_linear(x, wg, wu, save=True)
+                ops.gated_linear_backward(dh, x, wg, wu, gu)
+    elif a.case == "resnorm":
+        K = 7168
+        f, r, dr, dy = (workloads.activations(a.M, K, seed=s, device=dev) for s in (63, 64, 65, 66))
+        ga, gb = (workloads.norm_weight(K, seed=s, device=dev) for s in (5, 6))
+        for _ in range(a.iters):
+            if a.M == 1:
+                ops.residual_norm(f, r, ga, gamma_before=gb)
+            else:
+                _, _, st = ops.residual_norm(f, r, ga, gamma_before=gb, save=True)
+                ops.residual_norm_backward(dr, dy, f, r, st, ga, gamma_before=gb)
     elif a.case == "grouped":
         _, G, K, N = workloads.GROUPED_LINEAR.get(a.M, (a.M, 8, 4096, 1024))
         gw = model.make_grouped_weight(G, N, K, seed=90, device=dev)
