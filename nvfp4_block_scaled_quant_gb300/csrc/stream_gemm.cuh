@@ -62,7 +62,7 @@ struct StreamCfg {
   static constexpr uint32_t kTmemCols = kCols <= 32 ? 32 : kCols <= 64 ? 64 : kCols <= 128 ? 128 : 256;
   static constexpr int kRing = kStages * kStageBytes;
   static constexpr int kPartialBytes = kOperands * kTok * 128 * 4;  // over the ring, once it is drained
-  static constexpr size_t kSmem = 1024 + kRing + kStages * kSBytes + 256;
+  static constexpr size_t kSmem = kRing + kStages * kSBytes + 256;
   static_assert(kPartialBytes <= kRing, "the partial sums fit where the ring was");
   static_assert(kCols <= 256, "two CTAs share the SM's 512 tensor-memory columns");
   static_assert(2 * (kSmem + 1024) <= 233472, "two CTAs per SM");
@@ -84,9 +84,7 @@ __global__ void __launch_bounds__(StreamCfg<kFp8, kTok, kQuant>::kThreads, 2)
   constexpr uint32_t kFmt = kFp8 ? 0u : (T::kCode == NVFP4_DT_BF16 ? 1u : 0u);
   constexpr uint32_t kIdesc = mma_idesc(kFmt, false, false, 128, kTok);
 
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                              ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];  // used as declared: its accesses are known to be shared ones
   uint8_t *sW = smem;                                            // stages x operands x 16 KiB
   uint8_t *sX = sW + C::kStages * C::kOperands * C::kWBytes;     // stages x token rows
   float *sS = reinterpret_cast<float *>(sX + C::kStages * C::kXBytes);  // stages x token scales
