@@ -19,6 +19,21 @@ bool dims_ok(int64_t a, int64_t b) { return a < kMaxDim && b < kMaxDim && a * b 
   NV_REQUIRE(dims_ok(a, b), NVFP4_ERR_UNSUPPORTED_SHAPE, "sizes too large: %lld x %lld", (long long)(a), \
              (long long)(b))
 
+// Whether `rows` rows of `cols` elements, `ld` apart, share memory with the same of another tensor, taken
+// as the whole range from the first element to the last.  An output inside an input would be written
+// while other blocks still read it.
+struct Span {
+  const void *p;
+  int64_t rows, ld, cols, bytes;
+};
+bool overlap(const Span &a, const Span &b) {
+  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+  const uintptr_t a1 = a0 + static_cast<uintptr_t>(((a.rows - 1) * a.ld + a.cols) * a.bytes);
+  const uintptr_t b1 = b0 + static_cast<uintptr_t>(((b.rows - 1) * b.ld + b.cols) * b.bytes);
+  return a0 < b1 && b0 < a1;
+}
+
 // Estimated times (in units of 10 ns) that choose between the GEMMs.  The coefficients were fitted to
 // times on a GB300 over M = 16 .. 2048 and five (K, N) between 512 x 512 and 7168 x 7168; they rank
 // the choices, nothing else depends on them.
@@ -213,6 +228,7 @@ nvfp4_status nvfp4_fp8_gemm(const uint8_t *xq, const float *xs, int64_t lds, int
              "lds=%lld must be >= M and a multiple of 4", (long long)lds);
   NV_REQUIRE(aligned(xq, 16) && aligned(xs, 16) && aligned(w, 16) && aligned(w_s, 4) && aligned(y, 16),
              NVFP4_ERR_MISALIGNED, "xq, xs, w and y must be 16-byte aligned");
+  NV_REQUIRE(!overlap({y, M, N, N, 2}, {xq, M, K, K, 1}), NVFP4_ERR_INVALID_ARG, "y overlaps xq");
   DeviceInfo *d;
   nvfp4_status st = device_info(__func__, &d);
   if (st != NVFP4_OK) return st;
@@ -237,6 +253,7 @@ nvfp4_status nvfp4_fp8_linear(const void *x, int dtype, int64_t M, int64_t K, in
              "w and y must be 16-byte aligned");
   const Fp8Ws L = fp8_ws(M, K);
   if ((st = check_ws(__func__, ws, ws_bytes, L.total)) != NVFP4_OK) return st;
+  NV_REQUIRE(!overlap({y, M, N, N, 2}, {x, M, ldx, K, 2}), NVFP4_ERR_INVALID_ARG, "y overlaps x");
   DeviceInfo *d;
   if ((st = device_info(__func__, &d)) != NVFP4_OK) return st;
   if (M == 0) return NVFP4_OK;
@@ -295,6 +312,7 @@ nvfp4_status nvfp4_gated_linear(const void *x, int dtype, int64_t T, int64_t H, 
   if (st != NVFP4_OK) return st;
   NV_REQUIRE(h || T == 0, NVFP4_ERR_INVALID_ARG, "h is NULL");
   NV_REQUIRE(aligned(h, 16) && aligned(gu, 16), NVFP4_ERR_MISALIGNED, "h and gu must be 16-byte aligned");
+  NV_REQUIRE(!overlap({h, T, I, I, 2}, {x, T, ldx, H, 2}), NVFP4_ERR_INVALID_ARG, "h overlaps x");
   DeviceInfo *d;
   if ((st = device_info(__func__, &d)) != NVFP4_OK) return st;
   if (T == 0) return NVFP4_OK;
@@ -447,6 +465,10 @@ nvfp4_status nvfp4_residual_norm(const void *f, int dtype, const void *r, int r_
   NV_REQUIRE(r_out != r || ldr == K, NVFP4_ERR_MISALIGNED, "in place, r must be contiguous");
   NV_REQUIRE(aligned(r_out, 16) && aligned(y, 16) && aligned(stats, 8), NVFP4_ERR_MISALIGNED,
              "r_out and y must be 16-byte aligned");
+  const int64_t r_bytes = r_dtype == NVFP4_DT_FP32 ? 4 : 2;
+  NV_REQUIRE(!overlap({r_out, M, K, K, r_bytes}, {f, M, ldf, K, 2}) &&
+                 (r_out == r || !overlap({r_out, M, K, K, r_bytes}, {r, M, ldr, K, r_bytes})),
+             NVFP4_ERR_INVALID_ARG, "r_out overlaps f, or r at another address than its own");
   DeviceInfo *d;
   if ((st = device_info(__func__, &d)) != NVFP4_OK) return st;
   if (M == 0) return NVFP4_OK;

@@ -46,7 +46,7 @@ def test_fp8_gemm_and_linear(L):
                    (dict(N=1 << 24), 2), (dict(lds=2), 3), (dict(lds=5), 3), (dict(w=P + 8), 3), (dict(y=P + 2), 3)]:
         refuses(L, "nvfp4_fp8_gemm", changed(a, **kw), st)
     need = L.nvfp4_fp8_linear_workspace_bytes(100, 256)
-    assert need >= 100 * 256 + 2 * 100 * 4 and L.nvfp4_fp8_linear_workspace_bytes(32, 256) == 0
+    assert need >= 100 * 256 + 2 * 100 * 4 and L.nvfp4_fp8_linear_workspace_bytes(16, 256) == 0
     assert L.nvfp4_fp8_linear_workspace_bytes(100, 250) == 0 and L.nvfp4_fp8_linear_workspace_bytes(-1, 256) == 0
     b = dict(x=P, dtype=BF, M=100, K=256, ldx=256, N=100, w=P, ws=P, y=P, work=P, bytes=need, stream=None)
     for kw, st in [(dict(bytes=need - 1), 4), (dict(work=None), 1), (dict(work=P + 16), 3), (dict(N=-5), 1), (dict(w=None), 1),
@@ -89,6 +89,17 @@ def test_residual_norm(L):
         refuses(L, "nvfp4_residual_norm_backward", changed(b, **kw), st)
 
 
+def test_an_output_inside_an_input_is_refused(L):
+    """Other blocks may still read what one writes; r_out at r's own address is the exception."""
+    for y in (P, P + 512 * 3, P - 16):
+        refuses(L, "nvfp4_fp8_linear", (P, BF, 4, 256, 256, 8, P, P, y, None, 0, None), 1)
+        refuses(L, "nvfp4_gated_linear", (P, BF, 4, 256, 256, 8, P, P, 0, y, None, None), 1)
+    refuses(L, "nvfp4_fp8_gemm", (P, P, 4, 4, 256, 8, P, P, BF, P + 1008, None), 1)
+    far = 1 << 30
+    for f, r, ro in [(P, far, P), (far, P, P + 128), (far, P, P - 128), (P, far, P + 4 * 128 - 16)]:
+        refuses(L, "nvfp4_residual_norm", (f, BF, r, BF, 4, 64, 64, 64, None, None, 0, 0, 1.0, None, 1e-6, ro, None, None, None), 1)
+
+
 @pytest.mark.parametrize("M,K,groups,kind", [(1, 8, 1, BF), (4096, 7168, 1, BF), (8192, 7168, 8, BF), (1001, 1544, 1, F32), (600, 64, 600, F32),
                                              (3, 16384, 3, F32), (100000, 256, 4, BF)])
 def test_norm_workspace_holds_the_partial_sums(L, M, K, groups, kind):
@@ -104,10 +115,11 @@ def test_valid_calls_without_a_gpu_fail_cleanly(L):
         pytest.skip("a GPU is present")
     buf = ctypes.create_string_buffer(1 << 16)
     p = (ctypes.addressof(buf) + 255) & ~255
+    o = p + (1 << 15)
     calls = [("nvfp4_fp8_quantize_act", (p, BF, 4, 256, 256, p, p, 4, None)),
-             ("nvfp4_fp8_gemm", (p, p, 4, 4, 256, 8, p, p, BF, p, None)),
-             ("nvfp4_gated_linear", (p, BF, 4, 64, 64, 16, p, p, 0, p, None, None)),
-             ("nvfp4_residual_norm", (p, BF, p, BF, 4, 64, 64, 64, None, None, 0, 0, 1.0, None, 1e-6, p, None, None, None))]
+             ("nvfp4_fp8_gemm", (p, p, 4, 4, 256, 8, p, p, BF, o, None)),
+             ("nvfp4_gated_linear", (p, BF, 4, 64, 64, 16, p, p, 0, o, None, None)),
+             ("nvfp4_residual_norm", (p, BF, p, BF, 4, 64, 64, 64, None, None, 0, 0, 1.0, None, 1e-6, o, None, None, None))]
     for name, args in calls:
         assert getattr(L, name)(*args) in (_lib.ERR_CUDA, _lib.ERR_UNSUPPORTED_DEVICE)
 
