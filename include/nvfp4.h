@@ -416,7 +416,8 @@ NVFP4_API nvfp4_status nvfp4_fp8_linear(const void *x, int dtype, int64_t M, int
  * h = act(x Wg^T) * (x Wu^T): both projections, the activation and the product in one kernel.
  * x (T, H), row stride ldx (a multiple of 8); w_gate and w_up (I, H) contiguous; h (T, I)
  * contiguous; all bf16 or all fp16 (`dtype`).  gu, if not NULL, receives the fp32
- * pre-activations (T, 2I), g in columns [0, I) and u in [I, 2I): the input of the backward.
+ * pre-activations (T, 2I), g in columns [0, I) and u in [I, 2I), 32-byte aligned: the input of the
+ * backward.
  * H % 8 == 0, I % 8 == 0. */
 NVFP4_API nvfp4_status nvfp4_gated_linear(const void *x, int dtype, int64_t T, int64_t H, int64_t ldx, int64_t I,
                                           const void *w_gate, const void *w_up, int act, void *h, float *gu,

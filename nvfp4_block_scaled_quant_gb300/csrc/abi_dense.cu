@@ -311,7 +311,7 @@ nvfp4_status nvfp4_gated_linear(const void *x, int dtype, int64_t T, int64_t H, 
   nvfp4_status st = check_gated(__func__, x, dtype, T, H, ldx, I, w_gate, w_up, act);
   if (st != NVFP4_OK) return st;
   NV_REQUIRE(h || T == 0, NVFP4_ERR_INVALID_ARG, "h is NULL");
-  NV_REQUIRE(aligned(h, 16) && aligned(gu, 16), NVFP4_ERR_MISALIGNED, "h and gu must be 16-byte aligned");
+  NV_REQUIRE(aligned(h, 16) && aligned(gu, 32), NVFP4_ERR_MISALIGNED, "h must be 16-byte and gu 32-byte aligned");
   NV_REQUIRE(!overlap({h, T, I, I, 2}, {x, T, ldx, H, 2}), NVFP4_ERR_INVALID_ARG, "h overlaps x");
   DeviceInfo *d;
   if ((st = device_info(__func__, &d)) != NVFP4_OK) return st;

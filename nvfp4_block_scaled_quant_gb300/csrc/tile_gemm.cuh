@@ -402,12 +402,12 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
 #pragma unroll
             for (int i = 0; i < 16; ++i) h[i] = act_fwd<kAct>(__uint_as_float(g[i])) * __uint_as_float(u[i]);
             store16<T>(dst + c * 16, h, left, vec);
-            if (save) {  // N % 8 == 0: whole groups of 4 columns exist or do not
+            if (save) {  // N % 8 == 0: whole groups of 8 columns, a sector each, exist or do not
 #pragma unroll
-              for (int i = 0; i < 16; i += 4)
+              for (int i = 0; i < 16; i += 8)
                 if (i < left) {
-                  *reinterpret_cast<uint4 *>(save + c * 16 + i) = make_uint4(g[i], g[i + 1], g[i + 2], g[i + 3]);
-                  *reinterpret_cast<uint4 *>(save + args.N + c * 16 + i) = make_uint4(u[i], u[i + 1], u[i + 2], u[i + 3]);
+                  st_global_v8(save + c * 16 + i, reinterpret_cast<const uint32_t (&)[8]>(g[i]));
+                  st_global_v8(save + args.N + c * 16 + i, reinterpret_cast<const uint32_t (&)[8]>(u[i]));
                 }
             }
           }
