@@ -23,7 +23,9 @@ constexpr int kFqRows = kFqThreads / kFqGroup;       // rows of a CTA
 constexpr int kFqUnroll = 4;                         // blocks of a row in flight per lane
 
 // One pass over x: a 16-lane group holds one block of one row, 16 rows per CTA, so that the scales
-// of a block column leave as 64 consecutive bytes.  Bound by memory (2 bytes in, 1 out per element).
+// of a block column leave as 64 consecutive bytes.  2 bytes in and 1 out per element; the encoding's
+// instructions take as long as they do (4096 x 7168: 16 us, 5.4 TB/s, issue slots 71% busy; with scalar
+// quotients and a division for the scale 20 us).
 template <class T>
 __global__ void __launch_bounds__(kFqThreads)
     fp8_quantize_act_kernel(const uint16_t *__restrict__ x, int64_t M, int K, int64_t ldx, uint8_t *__restrict__ q,

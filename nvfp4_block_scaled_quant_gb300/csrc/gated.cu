@@ -18,7 +18,8 @@ namespace {
 
 constexpr int kGbThreads = 256;
 
-// [dg | du] of 8 columns per thread: 18 bytes in and 4 out per element of h, bound by memory.
+// [dg | du] of 8 columns per thread: 10 bytes in and 4 out per element of h, bound by memory
+// (4096 x 2048: 16.5 us, 7.1 TB/s, part of it from L2).
 template <class T, int kAct>
 __global__ void __launch_bounds__(kGbThreads)
     gated_grad_kernel(const uint16_t *__restrict__ dh, int64_t lddh, const float *__restrict__ gu, int64_t M, int I,
