@@ -370,7 +370,7 @@ def _scratch(workspace: Optional[torch.Tensor], query: str, like: torch.Tensor, 
     its bytes."""
     if workspace is None:
         n = getattr(lib(), query)(*sizes)
-        return (torch.empty(n, dtype=torch.uint8, device=like.device) if n else None), n
+        return (like.new_empty(n, dtype=torch.uint8) if n else None), n
     n = workspace.numel()
     _whole(workspace, "workspace", (n,), (torch.uint8,))
     return workspace, n
@@ -481,7 +481,7 @@ def gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, acti
     if out is not None:
         _whole(out, "out", (T, I), (x.dtype,))
     h = out if out is not None else x.new_empty((T, I))
-    gu = torch.empty(T, 2 * I, dtype=torch.float32, device=x.device) if save else None
+    gu = x.new_empty((T, 2 * I), dtype=torch.float32) if save else None
     call("nvfp4_gated_linear", x.data_ptr(), kind, T, H, ld, I, gp, up, act, h.data_ptr(), _ptr(gu), st)
     return (h, gu) if save else h
 
@@ -547,7 +547,7 @@ def residual_norm(f: torch.Tensor, r: torch.Tensor, gamma_after: Optional[torch.
         _whole(out, "out", (M, K), (r.dtype,))
     r_out = out if out is not None else r.new_empty((M, K))
     y = f.new_empty((M, K)) if gb is not None else None
-    stats = torch.empty(M, 2, dtype=torch.float32, device=f.device) if save else None
+    stats = f.new_empty((M, 2), dtype=torch.float32) if save else None
     call("nvfp4_residual_norm", f.data_ptr(), kind, r.data_ptr(), rkind, M, K, ldf, ldr, ga, gp, gkind, groups, scale,
          gb, eps, r_out.data_ptr(), _ptr(y), _ptr(stats), st)
     return (r_out, y, stats) if save else (r_out, y)
@@ -579,7 +579,7 @@ def residual_norm_backward(dr_out: Optional[torch.Tensor], dy: Optional[torch.Te
     dr = r.new_empty((M, K))
 
     def grad(p):
-        return None if p is None else torch.empty(p.shape, dtype=torch.float32, device=f.device)
+        return None if p is None else stats.new_empty(p.shape)
 
     dga, dgate, dgb = grad(gamma_after), grad(gate), grad(gamma_before)
     ws, ws_bytes = _scratch(workspace, "nvfp4_residual_norm_backward_workspace_bytes", f, M, K, max(groups, 1), rkind)
