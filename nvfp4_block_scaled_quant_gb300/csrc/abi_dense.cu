@@ -85,6 +85,36 @@ TilePlan tile_plan(int64_t M, int64_t N, int k_blocks, int out_cols, int sms, co
   return cost_n < cost_w ? TilePlan{128, c.start + cost_n} : TilePlan{256, c.start + cost_w};
 }
 
+// The two products of the gradients in one launch: columns of the tiles, and how many rounds of dW's tiles
+// the pairs take that have one tile of dx less than the others (TileOp::kGrad), from the longest pair's time.
+struct GradPlan {
+  int cols, early;
+};
+GradPlan grad_plan(int64_t M, int64_t dw_M, int64_t N, int k_blocks, int dw_k_blocks, int sms, const Cost &c) {
+  GradPlan best = {256, 0};
+  int64_t best_time = -1;
+  for (int cols = 256; cols >= 128; cols /= 2) {
+    const int64_t n = (N + cols - 1) / cols, block = cols == 256 ? c.block256 : c.block128;
+    const int64_t total = (M + kTRows - 1) / kTRows * n, dw_total = (dw_M + kTRows - 1) / kTRows * n;
+    const int64_t time = k_blocks * block + c.tile, dw_time = dw_k_blocks * block + c.tile;
+    const int64_t pairs = total + dw_total < sms / 2 ? total + dw_total : sms / 2;
+    const int64_t behind = total % pairs, rest = pairs - behind;
+    const int64_t fit = behind ? time / dw_time : 0;  // tiles of dW in the time of one of dx
+    for (int64_t early = fit; early <= (behind ? fit + 1 : 0); ++early) {
+      const int64_t base = dw_total < early * rest ? dw_total : early * rest, left = dw_total - base;
+      // the first pair with and the first without a tile in dx's last round (the others take no longer)
+      const int64_t with = (total / pairs + 1) * time + (left > rest ? (left - 1 - rest) / pairs + 1 : 0) * dw_time;
+      const int64_t without = total / pairs * time + ((base + rest - 1) / rest + (left + pairs - 1) / pairs) * dw_time;
+      const int64_t longest = behind && with > without ? with : without;
+      if (best_time < 0 || longest < best_time) {
+        best_time = longest;
+        best = {cols, static_cast<int>(early)};
+      }
+    }
+  }
+  return best;
+}
+
 // The weight-streaming GEMM is considered up to kStreamMaxM rows (its token tiles re-read the weights),
 // and taken up to kStreamMinM whatever the estimates: a pair tile's 128-row boxes of a tensor of 64
 // rows or fewer load at half speed (1536 -> 16384: 22 us for M = 64, 10.5 us for M = 100).
@@ -123,7 +153,6 @@ nvfp4_status fp8_gemm_impl(const char *fn, DeviceInfo *d, const uint8_t *xq, con
   a.M = static_cast<int>(M);
   a.N = static_cast<int>(N);
   a.k_blocks = k_blocks;
-  a.segments = 1;
   a.sa = xs;
   a.ld_sa = lds;
   a.sw = w_s;
@@ -343,7 +372,6 @@ nvfp4_status nvfp4_gated_linear(const void *x, int dtype, int64_t T, int64_t H, 
   a.M = static_cast<int>(T);
   a.N = static_cast<int>(I);
   a.k_blocks = k_blocks;
-  a.segments = 1;
   a.out = h;
   a.ldo = I;
   a.save = gu;
@@ -383,39 +411,34 @@ nvfp4_status nvfp4_gated_linear_backward(const void *dh, int64_t lddh, const voi
   if (!dx && !dw_gate) return NVFP4_OK;
   NV_CUDA(launch_gated_grad(dh, lddh, gu, T, I, dtype, act, ws, d->sms, s), "gated gradient launch");
   uint16_t *dgu = static_cast<uint16_t *>(ws);
+  // an absent product's maps are not used: any valid one stands in
+  CUtensorMap mdg, mdu, mg, mu, ma, mx;
+  TileArgs a = {};
+  a.N = static_cast<int>(H);
+  a.ldo = H;
+  a.err = d->flags;
   if (dx) {
-    CUtensorMap mdg, mdu, mg, mu;
     if ((st = make_map(__func__, &mdg, dgu, I * 2, T, I * 4, kTHalf)) != NVFP4_OK) return st;
     if ((st = make_map(__func__, &mdu, dgu + I, I * 2, T, I * 4, kTHalf)) != NVFP4_OK) return st;
     if ((st = make_map(__func__, &mg, w_gate, H * 2, I, H * 2, 64)) != NVFP4_OK) return st;
     if ((st = make_map(__func__, &mu, w_up, H * 2, I, H * 2, 64)) != NVFP4_OK) return st;
-    TileArgs a = {};
     a.M = static_cast<int>(T);
-    a.N = static_cast<int>(H);
     a.k_blocks = static_cast<int>((I + 63) / 64);
-    a.segments = 2;
     a.out = dx;
-    a.ldo = H;
-    a.err = d->flags;
-    const int cols = tile_plan(T, H, 2 * a.k_blocks, 256, d->sms, kGatedCost).cols;
-    NV_CUDA(launch_gated_dx_gemm(mdg, mdu, mg, mu, a, dtype, cols, s), "input gradient launch");
   }
   if (dw_gate) {
-    CUtensorMap ma, mx;
     if ((st = make_map(__func__, &ma, dgu, I * 4, T, I * 4, 64)) != NVFP4_OK) return st;
     if ((st = make_map(__func__, &mx, x, H * 2, T, ldx * 2, 64)) != NVFP4_OK) return st;
-    TileArgs a = {};
-    a.M = static_cast<int>(2 * I);
-    a.N = static_cast<int>(H);
-    a.k_blocks = static_cast<int>((T + 63) / 64);
-    a.segments = 1;
-    a.out = dw_gate;
-    a.out2 = dw_up;
-    a.ldo = H;
-    a.err = d->flags;
-    const int cols = tile_plan(2 * I, H, a.k_blocks, 256, d->sms, kGatedCost).cols;
-    NV_CUDA(launch_gated_dw_gemm(ma, mx, a, dtype, cols, s), "weight gradient launch");
+    a.dw_M = static_cast<int>(2 * I);
+    a.dw_k_blocks = static_cast<int>((T + 63) / 64);
+    a.dwg = dw_gate;
+    a.dwu = dw_up;
   }
+  if (!dx) mdg = mdu = ma, mg = mu = mx;
+  if (!dw_gate) ma = mdg, mx = mg;
+  const GradPlan p = grad_plan(a.M, a.dw_M, H, 2 * a.k_blocks, a.dw_k_blocks, d->sms, kGatedCost);
+  a.early = p.early;
+  NV_CUDA(launch_gated_grad_gemm(mdg, mdu, mg, mu, ma, mx, a, dtype, p.cols, s), "gradient products launch");
   return NVFP4_OK;
 }
 

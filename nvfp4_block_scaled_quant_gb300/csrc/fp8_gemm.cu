@@ -111,8 +111,8 @@ cudaError_t launch_fp8_quantize_weight(const void *w, int dtype, int64_t N, int6
 
 cudaError_t launch_fp8_tile_gemm(const CUtensorMap &a, const CUtensorMap &b, const TileArgs &args, int dtype, int cols,
                                  cudaStream_t s) {
-  return dtype == NVFP4_DT_BF16 ? launch_tile_gemm_as<TileOp::kFp8, Bf16, 0>(a, a, b, b, args, cols, s)
-                                : launch_tile_gemm_as<TileOp::kFp8, Fp16, 0>(a, a, b, b, args, cols, s);
+  return dtype == NVFP4_DT_BF16 ? launch_tile_gemm_as<TileOp::kFp8, Bf16, 0>(a, a, b, b, a, b, args, cols, s)
+                                : launch_tile_gemm_as<TileOp::kFp8, Fp16, 0>(a, a, b, b, a, b, args, cols, s);
 }
 
 cudaError_t launch_fp8_stream_gemm(const CUtensorMap &w, const CUtensorMap &x, const StreamArgs &args, int dtype,

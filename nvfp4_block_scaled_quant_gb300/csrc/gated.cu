@@ -74,8 +74,8 @@ cudaError_t launch_gated_grad(const void *dh, int64_t lddh, const float *gu, int
 
 cudaError_t launch_gated_tile_gemm(const CUtensorMap &x, const CUtensorMap &wg, const CUtensorMap &wu,
                                    const TileArgs &args, int dtype, int act, int cols, cudaStream_t s) {
-  NVFP4_BY_ACT(return dtype == NVFP4_DT_BF16 ? (launch_tile_gemm_as<TileOp::kGated, Bf16, kAct>(x, x, wg, wu, args, cols, s))
-                                             : (launch_tile_gemm_as<TileOp::kGated, Fp16, kAct>(x, x, wg, wu, args, cols, s)));
+  NVFP4_BY_ACT(return dtype == NVFP4_DT_BF16 ? (launch_tile_gemm_as<TileOp::kGated, Bf16, kAct>(x, x, wg, wu, x, wg, args, cols, s))
+                                             : (launch_tile_gemm_as<TileOp::kGated, Fp16, kAct>(x, x, wg, wu, x, wg, args, cols, s)));
 }
 
 template <int kTok>
@@ -96,16 +96,11 @@ cudaError_t launch_gated_stream_gemm(const CUtensorMap &x, const CUtensorMap &wg
   return cudaErrorInvalidValue;
 }
 
-cudaError_t launch_gated_dx_gemm(const CUtensorMap &dg, const CUtensorMap &du, const CUtensorMap &wg,
-                                 const CUtensorMap &wu, const TileArgs &args, int dtype, int cols, cudaStream_t s) {
-  return dtype == NVFP4_DT_BF16 ? launch_tile_gemm_as<TileOp::kDx, Bf16, 0>(dg, du, wg, wu, args, cols, s)
-                                : launch_tile_gemm_as<TileOp::kDx, Fp16, 0>(dg, du, wg, wu, args, cols, s);
-}
-
-cudaError_t launch_gated_dw_gemm(const CUtensorMap &dgu, const CUtensorMap &x, const TileArgs &args, int dtype, int cols,
-                                 cudaStream_t s) {
-  return dtype == NVFP4_DT_BF16 ? launch_tile_gemm_as<TileOp::kDw, Bf16, 0>(dgu, dgu, x, x, args, cols, s)
-                                : launch_tile_gemm_as<TileOp::kDw, Fp16, 0>(dgu, dgu, x, x, args, cols, s);
+cudaError_t launch_gated_grad_gemm(const CUtensorMap &dg, const CUtensorMap &du, const CUtensorMap &wg,
+                                   const CUtensorMap &wu, const CUtensorMap &dgu, const CUtensorMap &x,
+                                   const TileArgs &args, int dtype, int cols, cudaStream_t s) {
+  return dtype == NVFP4_DT_BF16 ? launch_tile_gemm_as<TileOp::kGrad, Bf16, 0>(dg, du, wg, wu, dgu, x, args, cols, s)
+                                : launch_tile_gemm_as<TileOp::kGrad, Fp16, 0>(dg, du, wg, wu, dgu, x, args, cols, s);
 }
 
 }  // namespace nvfp4

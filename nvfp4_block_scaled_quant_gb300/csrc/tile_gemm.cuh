@@ -7,9 +7,8 @@
 // would stage 48 KB for the same work: the L2 -> SM operand stream is what bounds tiles of this
 // size, so the pair's sharing of B matters.
 //
-// Warps of each CTA: 0 = TMA producer, 1 (and 2 for FP8) = MMA issuer (the even CTA's, for both), 3 = tensor memory,
-// 4..11 =
-// epilogue (two per 32-lane quarter of tensor memory, half of the columns each).
+// Warps of each CTA: 0 = TMA producer, 1 (and 2 for FP8) = MMA issuer (the even CTA's, for both), 3 = tensor
+// memory, 4..11 = epilogue (two per 32-lane quarter of tensor memory, half of the columns each).
 //
 //   Op::kFp8    A = xq (M, K) e4m3, B = wq (N, K) e4m3.  The scales change every 128 K, so every K
 //               block is a product of its own: two issuers take the blocks in turn into an accumulator
@@ -23,10 +22,12 @@
 //               of columns in flight, activation scales through a shared-memory ring.
 //   Op::kGated  A = x (M, K), B = rows of Wg (even CTA) and the matching rows of Wu (odd CTA):
 //               the first half of the accumulator's columns is g, the second u of the same outputs.
-//   Op::kDx     A = [dg | du] in two segments of K = I, B = Wg, then Wu, read along their rows
-//               (MN-major B): dx = dg Wg + du Wu.
-//   Op::kDw     A = [dg | du]^T (MN-major), B = x^T (MN-major), K = tokens: rows 0..I-1 are dWg,
-//               rows I..2I-1 dWu.
+//   Op::kGrad   two products in one launch.  dx = dg Wg + du Wu: A = [dg | du] in two segments of K = I,
+//               B = Wg, then Wu, read along their rows (MN-major B).  [dWg; dWu] = [dg | du]^T x: A and B
+//               MN-major, K = tokens.  Their tiles differ in length, and either alone often leaves SMs idle in its
+//               last wave, so a pair that has one tile of dx less than the others takes `early` tiles of
+//               dW meanwhile.  With the activation's gradient, in one launch / two: 517 x 1536 x 2048 22.4 / 32.4 us,
+//               2048 x 2048 x 4096 94 / 107, 700 x 7168 x 4096 118 / 141, 4096 x 7168 x 2048 274 / 275.
 //
 // Launched in plain stream order, without programmatic dependent launch, and it does not let its
 // successor start early: two pair kernels that overlap that way, one taking over the SMs and tensor memory
@@ -38,22 +39,23 @@
 #pragma once
 
 #include <atomic>
+#include <type_traits>
 
 #include "mma16x8.cuh"
 
 namespace nvfp4 {
 
-enum class TileOp : int { kFp8 = 0, kGated = 1, kDx = 2, kDw = 3 };
+enum class TileOp : int { kFp8 = 0, kGated = 1, kGrad = 2 };
 
 struct TileArgs {
-  int M, N;        // output rows and columns (kGated: N = I; kDw: M = 2I, N = H)
-  int k_blocks;    // 128-byte K blocks of one segment
-  int segments;    // 1, or 2 (kDx)
+  int M, N;        // output rows and columns (kGated: N = I; kGrad: dx's, M = 0 without it)
+  int k_blocks;    // 128-byte K blocks (kGrad: of one of dx's two segments)
+  int dw_M, dw_k_blocks, early;  // kGrad: rows of [dWg; dWu] (0 without them), blocks of tokens, see above
   const float *sa; // kFp8: (K blocks, ld_sa) activation scales
   int64_t ld_sa;
   const float *sw; // kFp8: (ceil(N / 128), K blocks) weight scales
-  void *out;       // 16-bit (M, N), row stride ldo; kDw: dWg
-  void *out2;      // kDw: dWu
+  void *out;       // 16-bit (M, N), row stride ldo
+  void *dwg, *dwu; // kGrad: the weight gradients, (dw_M / 2, N) each, row stride ldo
   int64_t ldo;
   float *save;     // kGated: fp32 (M, 2N) pre-activations [g | u], or null
   uint32_t *err;
@@ -96,15 +98,14 @@ template <TileOp kOp, class T, int kAct, int kTCols>
 __global__ void __launch_bounds__(kTThreads<kOp>, 1)
     tile_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
                      const __grid_constant__ CUtensorMap tmB0, const __grid_constant__ CUtensorMap tmB1,
+                     const __grid_constant__ CUtensorMap tmA2, const __grid_constant__ CUtensorMap tmB2,
                      const TileArgs args) {
   using C = TileCfg<kTCols>;
   constexpr int kBRows = kTCols / 2;  // rows of B staged by a CTA
   constexpr bool kFp8 = kOp == TileOp::kFp8;
-  constexpr bool kAMn = kOp == TileOp::kDw;
-  constexpr bool kBMn = kOp == TileOp::kDw || kOp == TileOp::kDx;
+  constexpr bool kGrad = kOp == TileOp::kGrad;
   constexpr int kOutCols = kOp == TileOp::kGated ? kBRows : kTCols;  // output columns of a tile
   constexpr uint32_t kFmt = kFp8 ? 0u : (T::kCode == NVFP4_DT_BF16 ? 1u : 0u);
-  constexpr uint32_t kIdesc = mma_idesc(kFmt, kAMn, kBMn, kTRows, kTCols);
 
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -149,10 +150,10 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
 
-  const int m_tiles = (args.M + kTRows - 1) / kTRows;
+  const int m_tiles = (args.M + kTRows - 1) / kTRows, dw_m_tiles = kGrad ? (args.dw_M + kTRows - 1) / kTRows : 0;
   const int n_tiles = (args.N + kOutCols - 1) / kOutCols;
-  const int total = m_tiles * n_tiles;
-  const int k_blocks = args.k_blocks * args.segments;
+  const int total = m_tiles * n_tiles, dw_total = dw_m_tiles * n_tiles;
+  const int k_blocks = args.k_blocks * (kGrad ? 2 : 1);
   const int clusters = static_cast<int>(gridDim.x) / 2, cluster_id = static_cast<int>(blockIdx.x) / 2;
   // after a wait that gave up: the time that copies and MMAs in flight need, many times over
   auto settle = [] {
@@ -160,11 +161,46 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
     while (global_timer_ns() - t0 < 10000000ull) {
     }
   };
-  auto tile_at = [&](int idx, int &mt, int &nt) {
+  struct Tile {
+    int mt, nt;
+    bool dw;  // kGrad: a tile of [dWg; dWu]
+  };
+  auto place = [&](int idx, int m_tiles, Tile &t) {
     const int per_group = kTGroupM * n_tiles, g = idx / per_group, in = idx - g * per_group;
     const int rows = min(kTGroupM, m_tiles - g * kTGroupM);
-    nt = in / rows;
-    mt = g * kTGroupM + (in - nt * rows);
+    t.nt = in / rows;
+    t.mt = g * kTGroupM + (in - t.nt * rows);
+  };
+  // The tile at a pair's step of its walk, from `first` in steps of `step`; false past its last.  The pairs take the
+  // tiles in turn.  kGrad: dx's first; the pairs behind the last one of dx's final round then take `early`
+  // rounds of dW's, and the turns go on from them.
+  const int first = kGrad ? 0 : cluster_id, step = kGrad ? 1 : clusters;
+  auto tile_of = [&](int at, Tile &t) {
+    t.dw = false;
+    if constexpr (!kGrad) {
+      if (at >= total) return false;
+      place(at, m_tiles, t);
+      return true;
+    } else {
+      int j = at, idx = cluster_id + j * clusters;
+      if (idx < total) {
+        place(idx, m_tiles, t);
+        return true;
+      }
+      t.dw = true;
+      const int behind = total % clusters, rest = clusters - behind;
+      j -= total / clusters + (cluster_id < behind ? 1 : 0);
+      if (cluster_id >= behind && j < args.early) {
+        idx = cluster_id - behind + j * rest;
+      } else {
+        if (cluster_id >= behind) j -= args.early;
+        const int turn = cluster_id >= behind ? cluster_id - behind : cluster_id + rest;
+        idx = min(dw_total, args.early * rest) + turn + j * clusters;
+      }
+      if (idx >= dw_total) return false;
+      place(idx, dw_m_tiles, t);
+      return true;
+    }
   };
 
   if constexpr (kFp8) {
@@ -174,65 +210,69 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
       asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kTEpiRegs));
   }
   if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ TMA producer
-      const uint64_t pol = policy_evict_normal();
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int idx = cluster_id; ok && idx < total; idx += clusters) {
-        int mt, nt;
-        tile_at(idx, mt, nt);
-        const int a_row = mt * kTRows + static_cast<int>(rank) * kTHalf;
-        const int b_row = kOp == TileOp::kGated ? nt * kBRows : nt * kTCols + static_cast<int>(rank) * kBRows;
-        const CUtensorMap *mapA = &tmA0, *mapB = kOp == TileOp::kGated && rank ? &tmB1 : &tmB0;
-        int kb = 0, seg = 0;
-        for (int it = 0; it < k_blocks; ++it, ++kb) {
-          if (kOp == TileOp::kDx && kb == args.k_blocks) {
-            kb = 0;
-            seg = 1;
-          }
-          if (kOp == TileOp::kDx && seg) {
-            mapA = &tmA1;
-            mapB = &tmB1;
-          }
-          if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, args.err, kPipelineTimeoutNs)) {
-            ok = false;
-            break;
-          }
-          // both CTAs' copies complete on the even CTA's barrier, which expects all of them
-          if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::kStageBytes);
-          const uint32_t bar = cluster_addr(&full[stage], 0);
-          uint8_t *a = sA + stage * C::kABytes, *b = sB + stage * C::kBBytes;
-          if constexpr (kAMn) {  // 64 K rows of 64 elements, two boxes side by side along M
-            tma_load_2d_pair(a, mapA, a_row * 2, kb * 64, bar, pol);
-            tma_load_2d_pair(a + 8192, mapA, a_row * 2 + 128, kb * 64, bar, pol);
-          } else {
-            tma_load_2d_pair(a, mapA, kb * 128, a_row, bar, pol);
-          }
-          if constexpr (kBMn) {
-            tma_load_2d_pair(b, mapB, b_row * 2, kb * 64, bar, pol);
-            if constexpr (kBRows == 128) tma_load_2d_pair(b + 8192, mapB, b_row * 2 + 128, kb * 64, bar, pol);
-          } else {
-            tma_load_2d_pair(b, mapB, kb * 128, b_row, bar, pol);
-          }
-          if (++stage == C::kStages) {
-            stage = 0;
-            phase ^= 1;
-          }
+    // -------------------------------------------------------------- TMA producer (one elected lane copies)
+    const uint64_t pol = policy_evict_normal();
+    const uint32_t full_leader = cluster_addr(full, 0);
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    // K block `kb` of both operands.  The form of A is a constant of each loop: a branch and a choice of the map at
+    // every block made the producer the kernel's limit (dx of 517 x 1536 x 2048 25.7 us instead of 21.3).
+    auto load = [&](const CUtensorMap *mapA, const CUtensorMap *mapB, int kb, int a_row, int b_row, auto dw) {
+      constexpr bool kAMn = decltype(dw)::value;
+      ok = mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, args.err, kPipelineTimeoutNs);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) return;
+      if (elect_one()) {
+        // both CTAs' copies complete on the even CTA's barrier, which expects all of them
+        if (rank == 0) mbar_arrive_expect_tx(&full[stage], 2 * C::kStageBytes);
+        const uint32_t bar = full_leader + stage * 8;
+        uint8_t *a = sA + stage * C::kABytes, *b = sB + stage * C::kBBytes;
+        if constexpr (kAMn) {  // 64 K rows of 64 elements, two boxes side by side along M
+          tma_load_2d_pair(a, mapA, a_row * 2, kb * 64, bar, pol);
+          tma_load_2d_pair(a + 8192, mapA, a_row * 2 + 128, kb * 64, bar, pol);
+        } else {
+          tma_load_2d_pair(a, mapA, kb * 128, a_row, bar, pol);
+        }
+        if constexpr (kGrad) {
+          tma_load_2d_pair(b, mapB, b_row * 2, kb * 64, bar, pol);
+          if constexpr (kBRows == 128) tma_load_2d_pair(b + 8192, mapB, b_row * 2 + 128, kb * 64, bar, pol);
+        } else {
+          tma_load_2d_pair(b, mapB, kb * 128, b_row, bar, pol);
         }
       }
-      // Neither CTA may exit with a commit on its way to one of its barriers (the commits of the even
-      // CTA's issuer arrive on both CTAs'): the ring is followed until every stage is free again.
-      for (int i = 0; ok && i < C::kStages; ++i) {
-        ok = mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, args.err, kPipelineTimeoutNs);
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1;
-        }
+      __syncwarp();
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1;
       }
-      if (!ok) settle();  // copies in flight may complete on the other CTA's barrier
+    };
+    Tile t;
+    for (int at = first; ok && tile_of(at, t); at += step) {
+      const int a_row = t.mt * kTRows + static_cast<int>(rank) * kTHalf;
+      const int b_row = kOp == TileOp::kGated ? t.nt * kBRows : t.nt * kTCols + static_cast<int>(rank) * kBRows;
+      if constexpr (kGrad) {
+        if (t.dw) {
+          for (int kb = 0; ok && kb < args.dw_k_blocks; ++kb) load(&tmA2, &tmB2, kb, a_row, b_row, std::true_type());
+        } else {
+          for (int kb = 0; ok && kb < args.k_blocks; ++kb) load(&tmA0, &tmB0, kb, a_row, b_row, std::false_type());
+          for (int kb = 0; ok && kb < args.k_blocks; ++kb) load(&tmA1, &tmB1, kb, a_row, b_row, std::false_type());
+        }
+      } else {
+        const CUtensorMap *mapB = kOp == TileOp::kGated && rank ? &tmB1 : &tmB0;
+        for (int kb = 0; ok && kb < k_blocks; ++kb) load(&tmA0, mapB, kb, a_row, b_row, std::false_type());
+      }
     }
+    // Neither CTA may exit with a commit on its way to one of its barriers (the commits of the even
+    // CTA's issuer arrive on both CTAs'): the ring is followed until every stage is free again.
+    for (int i = 0; ok && i < C::kStages; ++i) {
+      ok = mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, args.err, kPipelineTimeoutNs);
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    if (!ok) settle();  // copies in flight may complete on the other CTA's barrier
   } else if (warp < kTEpiWarp0) {
     if (rank == 0 && warp <= kTIssuers<kOp>) {
       // ------------------------------------------------------------ MMA issuers
@@ -243,27 +283,26 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
       // K-major rows of 128 bytes: 8-row groups 1024 bytes apart, a K step is 32 bytes on.
       // MN-major boxes (64 elements x 64 K rows): boxes 8192 bytes apart along MN, 8-K groups 1024
       // bytes apart, a K step of 16 rows is 2048 bytes on.
-      constexpr uint32_t kAStep = kAMn ? 2048 / 16 : 32 / 16, kBStep = kBMn ? 2048 / 16 : 32 / 16;
-      // kFp8: the two issuers take the blocks in turn, issuer i into accumulator i
-      const int iss = warp - 1;
       constexpr int kIssuers = kTIssuers<kOp>;
-      const int tiles = cluster_id < total ? (total - 1 - cluster_id) / clusters + 1 : 0;
-      const int64_t blocks = static_cast<int64_t>(tiles) * k_blocks;  // of this launch
-      int stage = iss, it = iss;
+      const int iss = warp - 1;
+      int stage = iss;
       uint32_t phase = 0;
       uint32_t acc = iss;  // the accumulator's turn: the block (kFp8) or the tile
       bool ok = true;
-      for (int64_t g = iss; ok && g < blocks; g += kIssuers) {
+      // block `it` of a tile, its last if `done`
+      auto issue = [&](int it, bool done, auto dw) {
+        constexpr bool kAMn = decltype(dw)::value;
+        constexpr uint32_t kAStep = kAMn ? 2048 / 16 : 32 / 16, kBStep = kGrad ? 2048 / 16 : 32 / 16;
+        constexpr uint32_t kIdesc = mma_idesc(kFmt, kAMn, kGrad, kTRows, kTCols);
         if (kFp8 || it == 0)
           ok = mbar_wait_bounded_cluster(&tempty[acc & 1], ((acc >> 1) & 1) ^ 1, abort_flag, args.err, kPipelineTimeoutNs);
         ok = ok && mbar_wait_bounded_cluster(&full[stage], phase, abort_flag, args.err, kPipelineTimeoutNs);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        if (!ok) return;
         tc_fence_after();
-        const bool done = kFp8 || it == k_blocks - 1;
         if (elect_one()) {
           const uint64_t ad = smem_desc(a0 + stage * C::kABytes, kAMn ? 8192 : 16, 1024, 2);
-          const uint64_t bd = smem_desc(b0 + stage * C::kBBytes, kBMn ? 8192 : 16, 1024, 2);
+          const uint64_t bd = smem_desc(b0 + stage * C::kBBytes, kGrad ? 8192 : 16, 1024, 2);
 #pragma unroll
           for (int j = 0; j < 4; ++j)
             tc_mma<kFp8, true>(tmem_base + (acc & 1) * kTCols, ad + j * kAStep, bd + j * kBStep, kIdesc,
@@ -273,10 +312,26 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
         }
         __syncwarp();
         if (done) acc += kIssuers;
-        it = !kFp8 && done ? 0 : it + 1;
         if ((stage += kIssuers) >= C::kStages) {
           stage -= C::kStages;
           phase ^= 1;
+        }
+      };
+      if constexpr (kFp8) {
+        // the two issuers take the launch's blocks in turn, issuer i into accumulator i
+        const int tiles = cluster_id < total ? (total - 1 - cluster_id) / clusters + 1 : 0;
+        const int64_t blocks = static_cast<int64_t>(tiles) * k_blocks;
+        for (int64_t g = iss; ok && g < blocks; g += kIssuers) issue(0, true, std::false_type());
+      } else {
+        Tile t;
+        for (int at = first; ok && tile_of(at, t); at += step) {
+          if constexpr (kGrad) {
+            if (t.dw) {
+              for (int it = 0; ok && it < args.dw_k_blocks; ++it) issue(it, it == args.dw_k_blocks - 1, std::true_type());
+              continue;
+            }
+          }
+          for (int it = 0; ok && it < k_blocks; ++it) issue(it, it == k_blocks - 1, std::false_type());
         }
       }
       // Every accumulator has come back, so every MMA has completed before the pair frees its tensor
@@ -340,11 +395,11 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
         }
       }
     };
-    for (int idx = cluster_id; ok && idx < total; idx += clusters) {
-      int mt, nt;
-      tile_at(idx, mt, nt);
-      const int row = mt * kTRows + static_cast<int>(rank) * kTHalf + quarter * 32 + lane;
-      const bool row_ok = row < args.M;
+    Tile tile;
+    for (int at = first; ok && tile_of(at, tile); at += step) {
+      const int nt = tile.nt;
+      const int row = tile.mt * kTRows + static_cast<int>(rank) * kTHalf + quarter * 32 + lane;
+      const bool row_ok = row < (kGrad && tile.dw ? args.dw_M : args.M);
       if constexpr (kFp8) {
         const int n0 = nt * kTCols + half * kBRows;  // a warp's columns share one weight scale
         // Scales are fetched ahead: under the operand stream a load takes longer than a block.  The
@@ -356,7 +411,7 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
         float w = ld_early(sw + min(lane, k_blocks - 1)), a[kAhead];
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) a[u] = ld_early(sa + min(u, k_blocks - 1) * args.ld_sa);
-        if (idx != cluster_id) store_tile();  // the previous tile, while this one's first block is made
+        if (at != first) store_tile();  // the previous tile, while this one's first block is made
         out_row = row;
         out_n0 = n0;
 #pragma unroll
@@ -417,11 +472,9 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
         if (!wait_acc()) break;
         const int n0 = nt * kTCols + half * kBRows;
         const uint32_t t = lanes + (acc & 1) * kTCols + half * kBRows;
-        uint16_t *dst = static_cast<uint16_t *>(args.out) + row * args.ldo + n0;
-        if constexpr (kOp == TileOp::kDw) {  // rows I..2I-1 belong to the second output
-          const int split = args.M / 2;
-          if (row >= split) dst = static_cast<uint16_t *>(args.out2) + (row - split) * args.ldo + n0;
-        }
+        const int split = args.dw_M / 2;  // rows of dWg
+        void *out = !tile.dw ? args.out : row < split ? args.dwg : args.dwu;
+        uint16_t *dst = static_cast<uint16_t *>(out) + (tile.dw && row >= split ? row - split : row) * args.ldo + n0;
 #pragma unroll
         for (int c = 0; c < kBRows / 16; ++c) {
           uint32_t r[16];
@@ -471,7 +524,8 @@ int tile_gemm_max_clusters(K kernel, int threads, size_t smem) {
 
 template <TileOp kOp, class T, int kAct, int kTCols>
 cudaError_t launch_tile_gemm_cols(const CUtensorMap &a0, const CUtensorMap &a1, const CUtensorMap &b0,
-                                  const CUtensorMap &b1, const TileArgs &args, cudaStream_t s) {
+                                  const CUtensorMap &b1, const CUtensorMap &a2, const CUtensorMap &b2,
+                                  const TileArgs &args, cudaStream_t s) {
   using C = TileCfg<kTCols>;
   auto kernel = tile_gemm_kernel<kOp, T, kAct, kTCols>;
   static std::atomic<int> fit[64];  // per device; the kernel's shared-memory limit is set with the query
@@ -489,11 +543,12 @@ cudaError_t launch_tile_gemm_cols(const CUtensorMap &a0, const CUtensorMap &a1, 
     fit[dev].store(n);
   }
   const int out_cols = kOp == TileOp::kGated ? kTCols / 2 : kTCols;
-  const int64_t tiles = ((static_cast<int64_t>(args.M) + kTRows - 1) / kTRows) *
-                        ((static_cast<int64_t>(args.N) + out_cols - 1) / out_cols);
-  // a balanced grid: every wave of tiles, the last included, is (nearly) full
+  const int64_t n_tiles = (static_cast<int64_t>(args.N) + out_cols - 1) / out_cols;
+  const int64_t tiles = ((static_cast<int64_t>(args.M) + kTRows - 1) / kTRows +
+                         (kOp == TileOp::kGrad ? (static_cast<int64_t>(args.dw_M) + kTRows - 1) / kTRows : 0)) * n_tiles;
+  // a balanced grid: every wave of equal tiles, the last included, is (nearly) full
   const int64_t waves = (tiles + n - 1) / n;
-  const int clusters = static_cast<int>((tiles + waves - 1) / waves);
+  const int clusters = static_cast<int>(kOp == TileOp::kGrad ? (tiles < n ? tiles : n) : (tiles + waves - 1) / waves);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * clusters);
   cfg.blockDim = dim3(kTThreads<kOp>);
@@ -506,16 +561,17 @@ cudaError_t launch_tile_gemm_cols(const CUtensorMap &a0, const CUtensorMap &a1, 
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a0, a1, b0, b1, args);
+  return cudaLaunchKernelEx(&cfg, kernel, a0, a1, b0, b1, a2, b2, args);
 }
 
 // cols: 256 or 128 accumulator columns per tile; B's tensor maps have boxes of cols / 2 rows
 // (K-major) or 64 columns (MN-major).
 template <TileOp kOp, class T, int kAct>
 cudaError_t launch_tile_gemm_as(const CUtensorMap &a0, const CUtensorMap &a1, const CUtensorMap &b0,
-                                const CUtensorMap &b1, const TileArgs &args, int cols, cudaStream_t s) {
-  return cols == 256 ? launch_tile_gemm_cols<kOp, T, kAct, 256>(a0, a1, b0, b1, args, s)
-                     : launch_tile_gemm_cols<kOp, T, kAct, 128>(a0, a1, b0, b1, args, s);
+                                const CUtensorMap &b1, const CUtensorMap &a2, const CUtensorMap &b2,
+                                const TileArgs &args, int cols, cudaStream_t s) {
+  return cols == 256 ? launch_tile_gemm_cols<kOp, T, kAct, 256>(a0, a1, b0, b1, a2, b2, args, s)
+                     : launch_tile_gemm_cols<kOp, T, kAct, 128>(a0, a1, b0, b1, a2, b2, args, s);
 }
 
 }  // namespace nvfp4
