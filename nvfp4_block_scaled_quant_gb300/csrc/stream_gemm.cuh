@@ -140,40 +140,40 @@ __global__ void __launch_bounds__(StreamCfg<kFp8, kTok, kQuant>::kThreads, 2)
   float acc[kFp8 ? kMaxCols : 1];
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ TMA producer
-      const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
-      // token scales that exist from m0 on, rounded up to whole 16 bytes (a row of scales is padded)
-      const uint32_t s_bytes = kFp8 && !kQuant ? static_cast<uint32_t>(min(kTok, (args.M - m0 + 3) & ~3)) * 4u : 0u;
-      int stage = 0;
-      uint32_t phase = 0;
-      bool ok = true;
-      for (int kb = kb0; kb < kb1; ++kb) {
-        if (!mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, args.err, kPipelineTimeoutNs)) {
-          ok = false;
-          break;
-        }
+    // -------------------------------------------------------------- TMA producer (one elected lane copies)
+    const uint64_t pol_w = policy_evict_first(), pol_x = policy_evict_last();
+    // token scales that exist from m0 on, rounded up to whole 16 bytes (a row of scales is padded)
+    const uint32_t s_bytes = kFp8 && !kQuant ? static_cast<uint32_t>(min(kTok, (args.M - m0 + 3) & ~3)) * 4u : 0u;
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    for (int kb = kb0; kb < kb1; ++kb) {
+      ok = mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, args.err, kPipelineTimeoutNs);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      if (elect_one()) {
         mbar_arrive_expect_tx(&full[stage], C::kStageBytes - (kQuant ? C::kXBytes : 0) + s_bytes);
         uint8_t *w = sW + stage * C::kOperands * C::kWBytes;
         tma_load_2d(w, &tmW0, kb * 128, tile * 128, &full[stage], pol_w);
         if constexpr (!kFp8) tma_load_2d(w + C::kWBytes, &tmW1, kb * 128, tile * 128, &full[stage], pol_w);
         if constexpr (!kQuant) tma_load_2d(sX + stage * C::kXBytes, &tmX, kb * 128, m0, &full[stage], pol_x);
         if constexpr (kFp8 && !kQuant) bulk_load(sS + stage * kTok, args.sa + kb * args.ld_sa + m0, s_bytes, &full[stage], pol_x);
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1;
-        }
       }
-      // no commit is on its way to a barrier of this CTA when it exits
-      for (int i = 0; ok && i < C::kStages; ++i) {
-        ok = mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, args.err, kPipelineTimeoutNs);
-        if (++stage == C::kStages) {
-          stage = 0;
-          phase ^= 1;
-        }
+      __syncwarp();
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1;
       }
-      if (!ok) settle();
     }
+    // no commit is on its way to a barrier of this CTA when it exits
+    for (int i = 0; ok && i < C::kStages; ++i) {
+      ok = mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, args.err, kPipelineTimeoutNs);
+      if (++stage == C::kStages) {
+        stage = 0;
+        phase ^= 1;
+      }
+    }
+    if (!ok) settle();
   } else if (warp == 1) {
     // -------------------------------------------------------------- MMA issuer (one elected lane issues)
     const uint32_t w0 = smem_u32(sW), x0 = smem_u32(sX);
