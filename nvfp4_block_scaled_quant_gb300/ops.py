@@ -370,7 +370,7 @@ def _scratch(workspace: Optional[torch.Tensor], query: str, like: torch.Tensor, 
     its bytes."""
     if workspace is None:
         n = getattr(lib(), query)(*sizes)
-        return (like.new_empty(n, dtype=torch.uint8) if n else None), n
+        return (torch.empty(n, dtype=torch.uint8, device=like.device) if n else None), n
     n = workspace.numel()
     _whole(workspace, "workspace", (n,), (torch.uint8,))
     return workspace, n
@@ -451,7 +451,7 @@ def fp8_linear(x: torch.Tensor, w: torch.Tensor, w_s: torch.Tensor, out: Optiona
     N, wp, wsp = _fp8_weight(w, w_s, K)
     if out is not None:
         _whole(out, "out", (M, N), (x.dtype,))
-    y = out if out is not None else x.new_empty((M, N))
+    y = out if out is not None else torch.empty(M, N, dtype=x.dtype, device=x.device)
     ws, ws_bytes = _scratch(workspace, "nvfp4_fp8_linear_workspace_bytes", x, M, K)
     call("nvfp4_fp8_linear", x.data_ptr(), _kind(x, "x"), M, K, ld, N, wp, wsp, y.data_ptr(), _ptr(ws), ws_bytes, st)
     return y
@@ -480,8 +480,8 @@ def gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, acti
     T, H, I, ld, kind, gp, up, act = _gated_args(x, w_gate, w_up, activation)
     if out is not None:
         _whole(out, "out", (T, I), (x.dtype,))
-    h = out if out is not None else x.new_empty((T, I))
-    gu = x.new_empty((T, 2 * I), dtype=torch.float32) if save else None
+    h = out if out is not None else torch.empty(T, I, dtype=x.dtype, device=x.device)
+    gu = torch.empty(T, 2 * I, dtype=torch.float32, device=x.device) if save else None
     call("nvfp4_gated_linear", x.data_ptr(), kind, T, H, ld, I, gp, up, act, h.data_ptr(), _ptr(gu), st)
     return (h, gu) if save else h
 
@@ -498,9 +498,9 @@ def gated_linear_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tenso
     T, H, I, ld, kind, gp, up, act = _gated_args(x, w_gate, w_up, activation)
     lddh = _ld(dh, "dh", T, I, x.dtype)
     gup = _whole(gu, "gu", (T, 2 * I), (torch.float32,))
-    dx = x.new_empty((T, H)) if need_dx else None
-    dwg = x.new_empty((I, H)) if need_dw else None
-    dwu = x.new_empty((I, H)) if need_dw else None
+    dx = torch.empty(T, H, dtype=x.dtype, device=x.device) if need_dx else None
+    dwg = torch.empty(I, H, dtype=x.dtype, device=x.device) if need_dw else None
+    dwu = torch.empty(I, H, dtype=x.dtype, device=x.device) if need_dw else None
     ws, ws_bytes = _scratch(workspace, "nvfp4_gated_linear_backward_workspace_bytes", x, T, I)
     call("nvfp4_gated_linear_backward", dh.data_ptr(), lddh, x.data_ptr(), ld, kind, T, H, I, gp, up, act, gup,
          _ptr(dx), _ptr(dwg), _ptr(dwu), _ptr(ws), ws_bytes, st)
@@ -545,9 +545,9 @@ def residual_norm(f: torch.Tensor, r: torch.Tensor, gamma_after: Optional[torch.
     M, K, ldf, ldr, kind, rkind, ga, gp, gkind, groups, gb = _norm_args(f, r, gamma_after, gate, gamma_before)
     if out is not None:
         _whole(out, "out", (M, K), (r.dtype,))
-    r_out = out if out is not None else r.new_empty((M, K))
-    y = f.new_empty((M, K)) if gb is not None else None
-    stats = f.new_empty((M, 2), dtype=torch.float32) if save else None
+    r_out = out if out is not None else torch.empty(M, K, dtype=r.dtype, device=r.device)
+    y = torch.empty(M, K, dtype=f.dtype, device=f.device) if gb is not None else None
+    stats = torch.empty(M, 2, dtype=torch.float32, device=f.device) if save else None
     call("nvfp4_residual_norm", f.data_ptr(), kind, r.data_ptr(), rkind, M, K, ldf, ldr, ga, gp, gkind, groups, scale,
          gb, eps, r_out.data_ptr(), _ptr(y), _ptr(stats), st)
     return (r_out, y, stats) if save else (r_out, y)
@@ -575,11 +575,11 @@ def residual_norm_backward(dr_out: Optional[torch.Tensor], dy: Optional[torch.Te
     lddr = K if dr_out is None else _ld(dr_out, "dr_out", M, K, r.dtype)
     lddy = K if dy is None else _ld(dy, "dy", M, K, f.dtype)
     sp = _whole(stats, "stats", (M, 2), (torch.float32,))
-    df = f.new_empty((M, K))
-    dr = r.new_empty((M, K))
+    df = torch.empty(M, K, dtype=f.dtype, device=f.device)
+    dr = torch.empty(M, K, dtype=r.dtype, device=r.device)
 
     def grad(p):
-        return None if p is None else stats.new_empty(p.shape)
+        return None if p is None else torch.empty(p.shape, dtype=torch.float32, device=f.device)
 
     dga, dgate, dgb = grad(gamma_after), grad(gate), grad(gamma_before)
     ws, ws_bytes = _scratch(workspace, "nvfp4_residual_norm_backward_workspace_bytes", f, M, K, max(groups, 1), rkind)
