@@ -29,6 +29,12 @@
  *    token x and its top-k ids and weights).  Those must therefore be final
  *    before the call that opens the chain (nvfp4_linear, nvfp4_moe_forward or
  *    nvfp4_moe_dispatch) is enqueued, which ordinary stream order gives.
+ *  - Kernels on pairs of CTAs (the large products of nvfp4_linear, nvfp4_gemm,
+ *    nvfp4_fp8_linear, nvfp4_fp8_gemm and the gated linear) do not run beside
+ *    one another: across streams, and across the branches of one stream
+ *    capture, each waits for the one enqueued before it.  A captured graph that
+ *    holds such calls is not ordered against other graphs and streams:
+ *    replay it where no other of these calls runs at the same time.
  *  - bf16 tensors are passed as void* to raw bf16 storage (row-major).
  *  - Scale-factor buffers in the "swizzled" tensor-core layout hold
  *    nvfp4_sf_bytes(rows, K) bytes: rows padded to a multiple of 128 and scale

@@ -67,6 +67,33 @@ nvfp4_status device_info(const char *fn, DeviceInfo **out) {
   return NVFP4_OK;
 }
 
+cudaError_t pair_turn_begin(DeviceInfo *d, cudaStream_t s, PairLaunch *now) {
+  cudaStreamCaptureStatus status;
+  cudaError_t e = cudaStreamGetCaptureInfo(s, &status, &now->capture);
+  if (e != cudaSuccess) return e;
+  const bool capturing = status != cudaStreamCaptureStatusNone;
+  if (capturing) {  // no stream of a capture is destroyed during it (and its id cannot be asked for)
+    now->stream = reinterpret_cast<uintptr_t>(s);
+  } else {
+    now->capture = 0;
+    if ((e = cudaStreamGetId(s, &now->stream)) != cudaSuccess) return e;
+  }
+  const PairLaunch &last = d->pair_last[capturing];
+  now->event = last.event;
+  if (!now->event && (e = cudaEventCreateWithFlags(&now->event, cudaEventDisableTiming)) != cudaSuccess) return e;
+  d->pair_last[capturing].event = now->event;
+  // an event of another capture says nothing about this one
+  if (last.made && last.capture == now->capture && last.stream != now->stream) return cudaStreamWaitEvent(s, last.event, 0);
+  return cudaSuccess;
+}
+
+cudaError_t pair_turn_end(DeviceInfo *d, cudaStream_t s, PairLaunch now) {
+  const cudaError_t e = cudaEventRecord(now.event, s);
+  now.made = e == cudaSuccess;
+  d->pair_last[now.capture != 0] = now;
+  return e;
+}
+
 // ---------------------------------------------------------------- TMA descriptors
 
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
@@ -575,7 +602,7 @@ static nvfp4_status gemm_dense(const char *fn, DeviceInfo *d, const uint8_t *xq,
   if (pair_clusters > 0) {
     const int64_t pair_tiles = ((M + 255) / 256) * (N / 256);
     const int clusters = static_cast<int>(pair_tiles < pair_clusters ? pair_tiles : pair_clusters);
-    NV_CUDA(launch_gemm_pair(ta, tb, a, clusters, s), "pair GEMM launch");
+    NV_CUDA(in_pair_turn(d, s, [&] { return launch_gemm_pair(ta, tb, a, clusters, s); }), "pair GEMM launch");
     return NVFP4_OK;
   }
   const int64_t tiles = G * ((M + kBlockM - 1) / kBlockM) * ((N + kBlockN - 1) / kBlockN);

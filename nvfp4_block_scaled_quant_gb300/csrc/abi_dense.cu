@@ -159,7 +159,7 @@ nvfp4_status fp8_gemm_impl(const char *fn, DeviceInfo *d, const uint8_t *xq, con
   a.out = y;
   a.ldo = N;
   a.err = d->flags;
-  NV_CUDA(launch_fp8_tile_gemm(mx, mw, a, dtype, tp.cols, s), "FP8 tile GEMM launch");
+  NV_CUDA(in_pair_turn(d, s, [&] { return launch_fp8_tile_gemm(mx, mw, a, dtype, tp.cols, s); }), "FP8 tile GEMM launch");
   return NVFP4_OK;
 }
 
@@ -376,7 +376,8 @@ nvfp4_status nvfp4_gated_linear(const void *x, int dtype, int64_t T, int64_t H, 
   a.ldo = I;
   a.save = gu;
   a.err = d->flags;
-  NV_CUDA(launch_gated_tile_gemm(mx, mg, mu, a, dtype, act, cols, s), "gated tile GEMM launch");
+  NV_CUDA(in_pair_turn(d, s, [&] { return launch_gated_tile_gemm(mx, mg, mu, a, dtype, act, cols, s); }),
+          "gated tile GEMM launch");
   return NVFP4_OK;
 }
 
@@ -438,7 +439,8 @@ nvfp4_status nvfp4_gated_linear_backward(const void *dh, int64_t lddh, const voi
   if (!dw_gate) ma = mdg, mx = mg;
   const GradPlan p = grad_plan(a.M, a.dw_M, H, 2 * a.k_blocks, a.dw_k_blocks, d->sms, kGatedCost);
   a.early = p.early;
-  NV_CUDA(launch_gated_grad_gemm(mdg, mdu, mg, mu, ma, mx, a, dtype, p.cols, s), "gradient products launch");
+  NV_CUDA(in_pair_turn(d, s, [&] { return launch_gated_grad_gemm(mdg, mdu, mg, mu, ma, mx, a, dtype, p.cols, s); }),
+          "gradient products launch");
   return NVFP4_OK;
 }
 

@@ -7,6 +7,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <mutex>
+
 #include "internal.h"
 
 namespace nvfp4 {
@@ -29,13 +31,39 @@ inline bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintp
 inline size_t align256(size_t v) { return (v + 255) & ~static_cast<size_t>(255); }
 inline int64_t round_up(int64_t v, int64_t a) { return (v + a - 1) / a * a; }
 
+// A CTA-pair launch: its stream, the capture it is part of (0 outside one; ids), and an event behind it.
+struct PairLaunch {
+  cudaEvent_t event = nullptr;
+  unsigned long long stream = 0, capture = 0;
+  bool made = false;
+};
+
 struct DeviceInfo {
   bool ready = false;
   bool supported = false;
   int sms = 0;
   uint32_t *flags = nullptr;
+  std::mutex pair_mutex;
+  PairLaunch pair_last[2];  // the last ones outside and inside a stream capture
 };
 nvfp4_status device_info(const char *fn, DeviceInfo **out);
+
+// Launches of kernels on CTA pairs (tcgen05 cta_group::2) run one after the other on a device, whatever
+// streams they are queued on: two that overlap, one taking over the SMs and tensor memory that the
+// other leaves pair by pair, once stopped making progress (tile_gemm.cuh).  A launch on another stream
+// than the last one's waits for an event behind that one; inside a stream capture the same holds
+// between the branches of the captured graph.  Launches of different graphs, and of a graph and a stream,
+// are not ordered by this: the caller replays them in turn.
+cudaError_t pair_turn_begin(DeviceInfo *d, cudaStream_t s, PairLaunch *now);
+cudaError_t pair_turn_end(DeviceInfo *d, cudaStream_t s, PairLaunch now);
+template <class Launch>
+cudaError_t in_pair_turn(DeviceInfo *d, cudaStream_t s, Launch launch) {
+  std::lock_guard<std::mutex> lock(d->pair_mutex);  // over the launch: the host's order is the device's
+  PairLaunch now;
+  cudaError_t e = pair_turn_begin(d, s, &now);
+  if (e == cudaSuccess) e = launch();
+  return e == cudaSuccess ? pair_turn_end(d, s, now) : e;
+}
 
 // 2-D byte tensor (rows x row_bytes, row stride ld_bytes) read in boxes of
 // 128 bytes x box_rows with the 128-byte swizzle.

@@ -29,13 +29,20 @@
 //               dW meanwhile.  With the activation's gradient, in one launch / two: 517 x 1536 x 2048 22.4 / 32.4 us,
 //               2048 x 2048 x 4096 94 / 107, 700 x 7168 x 4096 118 / 141, 4096 x 7168 x 2048 274 / 275.
 //
-// Launched in plain stream order, without programmatic dependent launch, and it does not let its
-// successor start early: two pair kernels that overlap that way, one taking over the SMs and tensor memory
-// that the other leaves cluster by cluster, stopped making progress once in some thousand launches.
-// It costs about 2 us per launch.
+// Two of these launches never overlap.  On one stream they run in plain stream order, without programmatic
+// dependent launch and without letting a successor start early (about 2 us per launch); on several
+// streams each waits for the one launched before it (in_pair_turn).  An earlier form of the kernel whose launches
+// overlapped, one taking over the SMs and tensor memory that the other leaves cluster by cluster, stopped making
+// progress once in some thousand.  That form left commits and releases on their way to barriers of CTAs
+// that had exited, freed a pair's tensor memory without waiting for the other CTA to have done so, and
+// met at .aligned barriers with warps that might still be diverged; none of this is left, but which of it
+// was the cause is not proven, so the overlap itself is kept out.
 //
-// Every wait is bounded: a role that gives up raises NVFP4_DEVERR_PIPELINE_TIMEOUT, the copies in
-// flight are given time to land, and every thread of the pair meets at the final cluster barrier.
+// Every mbarrier wait is bounded: a role that gives up raises NVFP4_DEVERR_PIPELINE_TIMEOUT, the copies in
+// flight are given time to land, and every thread of the pair meets at the final cluster barrier.  The
+// tensor-memory allocation, the cluster and block barriers and the register reallocation have no limit of their own:
+// the allocation waits for no launch but this one (one CTA per SM by its shared memory), every thread reaches every
+// barrier whatever its waits returned, and the register shares add up to the launch's.
 #pragma once
 
 #include <atomic>

@@ -293,7 +293,9 @@ def moe_finalize(T: int, topk: int, W: MoEWeights, y, workspace, stream=None):
 # 8 elements where a call says "strided rows", everything else contiguous.  They keep no autograd
 # graph: a backward pass is its own call.  An output given as ``out`` overlaps no input
 # (``residual_norm``'s may be r itself).  With ``stream`` given, outputs and scratch are allocated
-# for that stream and the inputs are marked as used on it.
+# for that stream and the inputs are marked as used on it.  Large products of different streams run
+# one after the other; a captured graph that holds some is replayed where no other runs at the
+# same time (on one stream, or on several that wait for one another).
 
 _DT = {torch.bfloat16: _lib.DT_BF16, torch.float16: _lib.DT_FP16}
 _ACT = {"silu": _lib.ACT_SILU, "gelu": _lib.ACT_GELU, "gelu_tanh": _lib.ACT_GELU_TANH}

@@ -1,0 +1,89 @@
+"""Launches of kernels on CTA pairs run one after the other on a device, on whatever streams they are
+queued: a short one queued behind a long one on another stream ends after it, and so do the branches
+of a captured graph.  The results are those of the calls by themselves."""
+
+import pytest
+import torch
+
+from nvfp4_block_scaled_quant_gb300 import model, ops
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+
+
+def fp8(M, K, N, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x = ops.fp8_quantize_act(torch.randn(M, K, generator=g, device=DEV).bfloat16())
+    w = ops.fp8_quantize_weight(torch.randn(N, K, generator=g, device=DEV).bfloat16())
+    return lambda: ops.fp8_gemm(*x, *w)
+
+
+def gated(T, H, I, seed):
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    x, dh = (torch.randn(T, n, generator=g, device=DEV).bfloat16() for n in (H, I))
+    wg, wu = ((torch.randn(I, H, generator=g, device=DEV) * H ** -0.5).bfloat16() for _ in range(2))
+
+    def step():
+        _, gu = ops.gated_linear(x, wg, wu, save=True)
+        return ops.gated_linear_backward(dh, x, wg, wu, gu)[0]
+
+    return step
+
+
+def nvfp4(M, K, N, seed):
+    w = model.make_dense_weight(N, K, seed=seed, device=DEV)
+    x = torch.randn(M, K, generator=torch.Generator(device=DEV).manual_seed(seed), device=DEV).bfloat16()
+    return lambda: ops.linear(x, w.w, w.sf, w.ws2, N)[0]
+
+
+SHORT = {"fp8": lambda: fp8(300, 256, 256, 1), "gated": lambda: gated(300, 128, 128, 2), "nvfp4": lambda: nvfp4(2048, 256, 256, 3)}
+
+
+@pytest.mark.parametrize("kind", list(SHORT))
+def test_a_short_launch_on_another_stream_ends_after_the_long_one(kind):
+    long, short = fp8(4096, 7168, 7168, 4), SHORT[kind]()
+    want_long, want_short = long(), short()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for first, second in ((a, b), (b, a)):
+        ends = [torch.cuda.Event(enable_timing=True) for _ in range(3)]
+        with torch.cuda.stream(first):
+            got = [long()]
+            ends[0].record()
+        with torch.cuda.stream(second):
+            got.append(short())
+            ends[1].record()
+        with torch.cuda.stream(first):
+            got.append(long())
+            ends[2].record()
+        torch.cuda.synchronize()
+        assert ends[0].elapsed_time(ends[1]) > 0 and ends[1].elapsed_time(ends[2]) > 0
+        assert torch.equal(got[0], want_long) and torch.equal(got[1], want_short) and torch.equal(got[2], want_long)
+    assert ops.device_error() == (0, 0)
+
+
+@pytest.mark.parametrize("kind", list(SHORT))
+def test_branches_of_a_captured_graph(kind):
+    long, short = fp8(4096, 7168, 7168, 5), SHORT[kind]()
+    want = long(), short()
+    side, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    ends = [torch.cuda.Event(enable_timing=True, external=True) for _ in range(2)]
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        here = torch.cuda.current_stream()
+        side.wait_stream(here)
+        x = long()
+        ends[0].record()
+        with torch.cuda.stream(side):
+            y = short()
+            ends[1].record()
+        here.wait_stream(side)
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert ends[0].elapsed_time(ends[1]) > 0
+    with torch.cuda.stream(side):  # what a capture recorded orders nothing outside it
+        eager = short()
+    torch.cuda.synchronize()
+    assert torch.equal(x, want[0]) and torch.equal(y, want[1]) and torch.equal(eager, want[1])
+    assert ops.device_error() == (0, 0)
