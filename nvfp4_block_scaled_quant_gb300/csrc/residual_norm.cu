@@ -7,14 +7,16 @@
 // with rstd(v) = 1 / sqrt(mean(v^2) + eps) over a row, all in fp32, and its backward pass.
 //
 // Backward of one row, with w = ga gate (ga alone for a gate per row), ia = rstd(f), ib = rstd(r'),
-// c = scale ia (times the row's gate), t = w f, R = r + c t (which is r'), u = dr' + ib dy gb, and the
-// sums over the row C2 = sum dy gb R, A = sum t u, C = sum t R:
-//   kappa = ib^3 C2 / K,  dR = u - kappa R               the gradient of r' (and of r)
+// g = scale (times the row's gate), t = w f, rh = ib (r + g ia t) (which is ib r'), v = dy gb,
+// u = dr' + ib v, and the sums over the row C2 = sum v rh, A = sum t u, C = sum t rh:
+//   kappa = ib C2 / K,  dR = u - kappa rh                the gradient of r' (and of r)
 //   S     = sum (ia t) dR = ia (A - kappa C)
-//   df    = c w dR - f ia^2 (c / ia) S / K                (the second term is the norm's)
-//   dgate = ga z, dga = gate z with z = sum over rows of c f dR; for a gate per row dgate = scale S
-//   dgb   = sum over rows of ib dy R
-// S is linear in dR, so the three sums come from one sweep and one reduction over the block.
+//   df    = g ia w dR - (ia f) ia g S / K                (the second term is the norm's)
+//   dgate = ga z, dga = gate z with z = sum over rows of g ia dR f; for a gate per row dgate = scale S
+//   dgb   = sum over rows of dy rh
+// S is linear in dR, so the three sums come from one sweep and one reduction over the block.  No
+// power of a statistic is formed: ib^3 and ia^2, gathered out of the sums, leave fp32's range for rows that
+// the formulas still handle (ib^3 is zero past an rms of 1e15).
 // rstd(f) and rstd(r') are kept by the forward (8 bytes per row); everything else is recomputed.
 //
 // Both passes are bound by memory: forward f + r in, r' + y out; backward f, r, dr', dy in, df, dr
@@ -159,8 +161,14 @@ __device__ __forceinline__ uint32_t group_of(int64_t m, int64_t rows_per_group) 
   return static_cast<uint32_t>(m) / static_cast<uint32_t>(rows_per_group);
 }
 
-__device__ __forceinline__ float rstd_of(float sum, int K, float eps) {
-  return __fdiv_rn(1.f, __fsqrt_rn(__fdiv_rn(sum, static_cast<float>(K)) + eps));
+// rstd of a row over the block, from the thread's part of its sum of squares (red as for block_sum).  The parts
+// are scaled by the power of two below 1 / K before they are added, and K alike, so that the sum of a long row
+// stays in fp32's range wherever a thread's part does (an rms of 4e18; the sum of 8192 squares only 2e17);
+// the bits are those of the plain sum.
+__device__ __forceinline__ float row_rstd(float part, float *red, int K, float eps) {
+  const float scale = __int_as_float((127 - (32 - __clz(K - 1))) << 23);
+  const float mean = __fdiv_rn(block_sum(part * scale, red), static_cast<float>(K) * scale);
+  return __fdiv_rn(1.f, __fsqrt_rn(mean + eps));
 }
 
 // ---------------------------------------------------------------- forward
@@ -209,7 +217,7 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const NormArgs a
           s += hi * hi;
         }
       }
-      ia = rstd_of(block_sum(s, red[0]), a.K, a.eps);
+      ia = row_rstd(s, red[0], a.K, a.eps);
     }
     s = 0.f;
 #pragma unroll
@@ -231,7 +239,7 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const NormArgs a
     }
     float ib = 0.f;
     if (a.gb) {
-      ib = rstd_of(block_sum(s, red[1]), a.K, a.eps);
+      ib = row_rstd(s, red[1], a.K, a.eps);
 #pragma unroll
       for (int u = 0; u < kChunks; ++u) {
         const int c = static_cast<int>(threadIdx.x) + u * nt;
@@ -332,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) residual_norm_rows_kernel(con
         for (int i = 0; i < 4; ++i) sum = fma2(v[u][i], v[u][i], sum);
       }
     }
-    const float ia = a.ga ? rstd_of(block_sum(sum2(sum), red[0]), a.K, a.eps) : 1.f;
+    const float ia = a.ga ? row_rstd(sum2(sum), red[0], a.K, a.eps) : 1.f;
     const Two c1 = both(gm * ia);
     sum = both(0.f);
 #pragma unroll
@@ -351,7 +359,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) residual_norm_rows_kernel(con
     }
     float ib = 0.f;
     if (a.gb) {
-      ib = rstd_of(block_sum(sum2(sum), red[1]), a.K, a.eps);  // its barrier: every thread has read the stage
+      ib = row_rstd(sum2(sum), red[1], a.K, a.eps);  // its barrier: every thread has read the stage
     } else {
       __syncthreads();
     }
@@ -391,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, kCtas) residual_norm_rows_kernel(con
 // Half of the time of a 16-bit row is instructions (two sweeps over the row, 16 conversions per four
 // columns), so sums go in packed fp32, a thread takes 16 columns (its fixed work per row, two
 // reductions and a wait, is spread over more than with 8: 375 instructions per eight columns instead
-// of 463), and the warp that is last to finish a row's stage refills it.  8192 x 7168: bf16 133 us, 5.3 TB/s; with an
+// of 463), and the warp that is last to finish a row's stage refills it.  8192 x 7168: bf16 139 us, 5.1 TB/s; with an
 // fp32 residual 143 us, 7.4 TB/s.  Measured and left: sums of the next row taken while this row's are
 // exchanged (147 us: one row fewer is loading), scalar fp32 (144 us).
 constexpr int kNbRedFloats = 4 * 32;  // three sums of up to 32 warps each, and a row of zeros
@@ -469,7 +477,7 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
   const bool row_gate = a.gate_kind == NVFP4_GATE_ROW, channel_gate = a.gate_kind == NVFP4_GATE_CHANNEL;
   const float inv_k = 1.f / static_cast<float>(a.K);
   // Per thread and column: w = ga gate (it changes with the group of rows) and gb; the sums over rows
-  // of dy rh (dgb) and z = scale ia f dR, of which both dga = gate z and dgate = ga z are multiples.
+  // of dy rh (dgb) and z = g ia dR f, of which both dga = gate z and dgate = ga z are multiples.
   Two w[kNormGradGroups][2], gb[kNormGradGroups][2];
   Two acc_a[kNormGradGroups][2], acc_b[kNormGradGroups][2], acc_z[kNormGradGroups][2];
 #pragma unroll
@@ -513,10 +521,8 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
     // barrier below is still met
     mbar_wait_bounded(&full[s], phase, abort_flag, a.err, kPipelineTimeoutNs);
     const uint8_t *d = smem + s * stage_bytes;
-    // With t = w f and R = r + (gm ia) t (so q = ia t and rh = ib R), and u = dr' + ib dy gb:
-    //   C2 = sum dy gb R, A = sum t u, C = sum t R
     const Two c1 = both(gm * ia), ib2 = both(ib);
-    Two fv[2], tv[2], rv[2], dyv[2], uv[2];
+    Two fv[2], tv[2], rv[2], dyv[2], uv[2];  // f, t, rh, dy and dr' of four columns
     auto fetch = [&](int h) {
       load_pairs<T, false, 2>(d, col[h], fv);
       load_pairs<T, kR32, 2>(d + 2 * b16, col[h], rv);
@@ -525,7 +531,7 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         tv[i] = fv[i] * w[h][i];
-        rv[i] = fma2(c1, tv[i], rv[i]);
+        rv[i] = ib2 * fma2(c1, tv[i], rv[i]);
       }
     };
     Two s2 = both(0.f), sA = both(0.f), sC = both(0.f);
@@ -579,10 +585,9 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
         sc += peer_sums[pb][r][2];
       }
     }
-    // dR = u - kappa R, S = sum q dR, df = (gm ia) w dR - lambda f
-    const float kappa = ib * ib * ib * (c2 * inv_k);
+    const float kappa = ib * (c2 * inv_k);
     const float S = ia * (sa - kappa * sc);
-    const Two nk = both(-kappa), nl = both(a.ga ? -ia * ia * (gm * S * inv_k) : 0.f);
+    const Two nk = both(-kappa), nl = both(a.ga ? -ia * (gm * (S * inv_k)) : 0.f), ia2 = both(ia);
     if (row_gate && a.dgate && threadIdx.x == 0 && slice == 0) a.dgate[m] = a.scale * S;
 #pragma unroll
     for (int h = 0; h < kNormGradGroups; ++h) {
@@ -591,11 +596,11 @@ __global__ void __launch_bounds__(kNormGradThreads, 1) residual_norm_backward_ke
         Two df[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          acc_b[h][i] = fma2(ib2 * dyv[i], rv[i], acc_b[h][i]);
+          acc_b[h][i] = fma2(dyv[i], rv[i], acc_b[h][i]);
           uv[i] = fma2(nk, rv[i], fma2(ib2, dyv[i] * gb[h][i], uv[i]));
           const Two sdr = c1 * uv[i];
           acc_z[h][i] = fma2(sdr, fv[i], acc_z[h][i]);
-          df[i] = fma2(nl, fv[i], sdr * w[h][i]);
+          df[i] = fma2(nl, ia2 * fv[i], sdr * w[h][i]);
         }
         store_pairs<T, kR32, 2>(a.dr, m * a.K + k0 + col[h], uv);
         store_pairs<T, false, 2>(a.df, m * a.K + k0 + col[h], df);
