@@ -63,7 +63,7 @@
 extern "C" {
 #endif
 
-#define NVFP4_ABI_VERSION 7
+#define NVFP4_ABI_VERSION 8
 
 /* Exported symbols: the library builds with hidden visibility by default. */
 #if defined(NVFP4_BUILD) && defined(__GNUC__)
@@ -428,12 +428,16 @@ NVFP4_API nvfp4_status nvfp4_fp8_linear(const void *x, int dtype, int64_t M, int
 NVFP4_API nvfp4_status nvfp4_gated_linear(const void *x, int dtype, int64_t T, int64_t H, int64_t ldx, int64_t I,
                                           const void *w_gate, const void *w_up, int act, void *h, float *gu,
                                           void *stream);
-/* Gradients of h: dg = dh u act'(g) and du = dh act(g), rounded to `dtype`, then
+/* Gradients of h: dg = dh u act'(g) and du = dh act(g), rounded to `dtype`'s precision, then
  *   dx = dg Wg + du Wu (T, H),  dw_gate = dg^T x (I, H),  dw_up = du^T x (I, H)
- * with fp32 sums, contiguous, in `dtype`.  dx may be NULL, and dw_gate and dw_up may both be
+ * with fp32 sums, contiguous, in `dtype`.  For fp16 the products take dg and du times a power of two, divided out of
+ * the sums, that puts the largest finite magnitude of both between 2^14 and 2^15: they neither overflow nor lose bits
+ * but where they are below 2^-28 of that one.  dx may be NULL, and dw_gate and dw_up may both be
  * NULL: that product is then left out.  dh (T, I) has row stride lddh (a multiple of 8).
- * With T == 0 the weight gradients are zero.  Workspace: [dg | du]. */
+ * With T == 0 the weight gradients are zero.  Workspace: [dg | du], and 4352 bytes more for fp16 (the size by dtype;
+ * the query without one is bf16's). */
 NVFP4_API size_t nvfp4_gated_linear_backward_workspace_bytes(int64_t T, int64_t I);
+NVFP4_API size_t nvfp4_gated_linear_backward_workspace_bytes_dt(int64_t T, int64_t I, int dtype);
 NVFP4_API nvfp4_status nvfp4_gated_linear_backward(const void *dh, int64_t lddh, const void *x, int64_t ldx,
                                                    int dtype, int64_t T, int64_t H, int64_t I,
                                                    const void *w_gate, const void *w_up, int act, const float *gu,

@@ -46,7 +46,7 @@ GATE_CHANNEL = 1
 GATE_ROW = 2
 
 
-ABI_VERSION = 7  # NVFP4_ABI_VERSION of the header these signatures follow
+ABI_VERSION = 8  # NVFP4_ABI_VERSION of the header these signatures follow
 
 
 class MoeWsLayout(Structure):
@@ -96,6 +96,7 @@ _SIGNATURES = {
     "nvfp4_fp8_linear": (c_int, [P, c_int, I64, I64, I64, I64, P, P, P, P, c_size_t, P]),
     "nvfp4_gated_linear": (c_int, [P, c_int, I64, I64, I64, I64, P, P, c_int, P, P, P]),
     "nvfp4_gated_linear_backward_workspace_bytes": (c_size_t, [I64, I64]),
+    "nvfp4_gated_linear_backward_workspace_bytes_dt": (c_size_t, [I64, I64, c_int]),
     "nvfp4_gated_linear_backward": (c_int, [P, I64, P, I64, c_int, I64, I64, I64, P, P, c_int, P, P, P, P, P, c_size_t,
                                             P]),
     "nvfp4_residual_norm": (c_int, [P, c_int, P, c_int, I64, I64, I64, I64, P, P, c_int, I64, c_float, P, c_float, P, P,

@@ -381,9 +381,14 @@ nvfp4_status nvfp4_gated_linear(const void *x, int dtype, int64_t T, int64_t H, 
   return NVFP4_OK;
 }
 
+size_t nvfp4_gated_linear_backward_workspace_bytes_dt(int64_t T, int64_t I, int dtype) {
+  if (T < 0 || I <= 0 || I % 8 || !dims_ok(T, 2 * I) || !dtype16(dtype)) return 0;
+  const size_t pair = align256(static_cast<size_t>(T) * static_cast<size_t>(I) * 4);
+  return pair + (dtype == NVFP4_DT_FP16 && T > 0 ? align256((kGatedGradParts + 1) * 4) : 0);
+}
+
 size_t nvfp4_gated_linear_backward_workspace_bytes(int64_t T, int64_t I) {
-  if (T < 0 || I <= 0 || I % 8 || !dims_ok(T, 2 * I)) return 0;
-  return align256(static_cast<size_t>(T) * static_cast<size_t>(I) * 4);
+  return nvfp4_gated_linear_backward_workspace_bytes_dt(T, I, NVFP4_DT_BF16);
 }
 
 nvfp4_status nvfp4_gated_linear_backward(const void *dh, int64_t lddh, const void *x, int64_t ldx, int dtype, int64_t T,
@@ -398,7 +403,8 @@ nvfp4_status nvfp4_gated_linear_backward(const void *dh, int64_t lddh, const voi
              "lddh=%lld must be >= I and a multiple of 8", (long long)lddh);
   NV_REQUIRE(aligned(dh, 16) && aligned(gu, 16) && aligned(dx, 16) && aligned(dw_gate, 16) && aligned(dw_up, 16),
              NVFP4_ERR_MISALIGNED, "pointers must be 16-byte aligned");
-  if ((st = check_ws(__func__, ws, ws_bytes, nvfp4_gated_linear_backward_workspace_bytes(T, I))) != NVFP4_OK) return st;
+  st = check_ws(__func__, ws, ws_bytes, nvfp4_gated_linear_backward_workspace_bytes_dt(T, I, dtype));
+  if (st != NVFP4_OK) return st;
   DeviceInfo *d;
   if ((st = device_info(__func__, &d)) != NVFP4_OK) return st;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -410,13 +416,17 @@ nvfp4_status nvfp4_gated_linear_backward(const void *dh, int64_t lddh, const voi
     return NVFP4_OK;
   }
   if (!dx && !dw_gate) return NVFP4_OK;
-  NV_CUDA(launch_gated_grad(dh, lddh, gu, T, I, dtype, act, ws, d->sms, s), "gated gradient launch");
   uint16_t *dgu = static_cast<uint16_t *>(ws);
+  // fp16: the parts of the maximum and, behind them, the factor of the products' sums
+  uint32_t *parts = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(ws) + nvfp4_gated_linear_backward_workspace_bytes(T, I));
+  float *unscale = reinterpret_cast<float *>(parts + kGatedGradParts);
+  NV_CUDA(launch_gated_grad(dh, lddh, gu, T, I, dtype, act, dgu, parts, unscale, d->sms, s), "gated gradient launch");
   // an absent product's maps are not used: any valid one stands in
   CUtensorMap mdg, mdu, mg, mu, ma, mx;
   TileArgs a = {};
   a.N = static_cast<int>(H);
   a.ldo = H;
+  a.unscale = unscale;
   a.err = d->flags;
   if (dx) {
     if ((st = make_map(__func__, &mdg, dgu, I * 2, T, I * 4, kTHalf)) != NVFP4_OK) return st;

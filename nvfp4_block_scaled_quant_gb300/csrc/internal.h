@@ -313,8 +313,10 @@ cudaError_t launch_gated_tile_gemm(const CUtensorMap &x, const CUtensorMap &wg, 
                                    const TileArgs &args, int dtype, int act, int cols, cudaStream_t s);
 cudaError_t launch_gated_stream_gemm(const CUtensorMap &x, const CUtensorMap &wg, const CUtensorMap &wu,
                                      const StreamArgs &args, int dtype, int act, int tok, int splits, cudaStream_t s);
+// [dg | du] into dgu.  fp16: times a power of two whose inverse goes to *unscale; parts: kGatedGradParts words.
+constexpr int kGatedGradParts = 1024;
 cudaError_t launch_gated_grad(const void *dh, int64_t lddh, const float *gu, int64_t M, int64_t I, int dtype, int act,
-                              void *dgu, int sms, cudaStream_t s);
+                              void *dgu, uint32_t *parts, float *unscale, int sms, cudaStream_t s);
 cudaError_t launch_gated_grad_gemm(const CUtensorMap &dg, const CUtensorMap &du, const CUtensorMap &wg,
                                    const CUtensorMap &wu, const CUtensorMap &dgu, const CUtensorMap &x,
                                    const TileArgs &args, int dtype, int cols, cudaStream_t s);

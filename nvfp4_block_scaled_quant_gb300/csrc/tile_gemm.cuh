@@ -63,6 +63,7 @@ struct TileArgs {
   const float *sw; // kFp8: (ceil(N / 128), K blocks) weight scales
   void *out;       // 16-bit (M, N), row stride ldo
   void *dwg, *dwu; // kGrad: the weight gradients, (dw_M / 2, N) each, row stride ldo
+  const float *unscale;  // kGrad, fp16: factor of the sums (the inverse of dg's and du's power of two)
   int64_t ldo;
   float *save;     // kGated: fp32 (M, 2N) pre-activations [g | u], or null
   uint32_t *err;
@@ -369,6 +370,8 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
       ++acc;
     };
     const bool vec = (args.ldo & 7) == 0;
+    constexpr bool kUnscale = kGrad && T::kCode == NVFP4_DT_FP16;
+    const float unscale = kUnscale ? __ldg(args.unscale) : 1.f;
     // kFp8: the sums of this thread's row, kBRows columns from out_n0 on
     float sum[kFp8 ? kBRows : 1];
     int out_row = 0, out_n0 = 0;
@@ -491,7 +494,7 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
           if (c == kBRows / 16 - 1) release();
           float v[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
+          for (int i = 0; i < 16; ++i) v[i] = kUnscale ? __uint_as_float(r[i]) * unscale : __uint_as_float(r[i]);
           if (row_ok) store16<T>(dst + c * 16, v, args.N - n0 - c * 16, vec);
         }
       }

@@ -503,7 +503,7 @@ def gated_linear_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tenso
     dx = torch.empty(T, H, dtype=x.dtype, device=x.device) if need_dx else None
     dwg = torch.empty(I, H, dtype=x.dtype, device=x.device) if need_dw else None
     dwu = torch.empty(I, H, dtype=x.dtype, device=x.device) if need_dw else None
-    ws, ws_bytes = _scratch(workspace, "nvfp4_gated_linear_backward_workspace_bytes", x, T, I)
+    ws, ws_bytes = _scratch(workspace, "nvfp4_gated_linear_backward_workspace_bytes_dt", x, T, I, kind)
     call("nvfp4_gated_linear_backward", dh.data_ptr(), lddh, x.data_ptr(), ld, kind, T, H, I, gp, up, act, gup,
          _ptr(dx), _ptr(dwg), _ptr(dwu), _ptr(ws), ws_bytes, st)
     return dx, dwg, dwu
