@@ -195,7 +195,9 @@ __device__ __forceinline__ void act_bwd(float g, float &a, float &da) {
   } else if constexpr (kAct == NVFP4_ACT_GELU) {
     da = p + g * expf(-0.5f * g * g) * 0.39894228040143268f;
   } else {
-    da = p + g * p * (1.f - p) * 1.59576912160573071f * (1.f + 0.134145f * g * g);
+    // p (1 - p) is 0 long before |g| = 1e4; the square is kept finite, or 0 inf = NaN
+    const float b = fminf(fabsf(g), 1e4f);
+    da = p + g * p * (1.f - p) * 1.59576912160573071f * (1.f + 0.134145f * b * b);
   }
 }
 

@@ -118,6 +118,27 @@ def test_a_non_finite_token_stays_in_its_row(T, bad):
         assert not torch.isfinite(h[2]).any()
 
 
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("size", [50.0, 1e4, 1e10, 1.5e19, 3e19, 1e30])
+def test_huge_pre_activations(kind, size):
+    """act'(g) is 1 or 0 there: no product inside it may leave fp32's range."""
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    T, H, I = 20, 64, 16
+    x, wg, wu, dh, u = (torch.randn(*s, generator=gen, device=DEV).bfloat16() for s in ((T, H), (I, H), (I, H), (T, I), (T, I)))
+    g = size * (torch.randint(0, 2, (T, I), generator=gen, device=DEV) * 2.0 - 1)
+    got = ops.gated_linear_backward(dh, x, wg, wu, torch.cat([g, u.float()], 1), activation=kind)
+    a, da = act64(g.double(), kind)
+    X, G, U, D = x.double(), wg.double(), wu.double(), dh.double()
+    dg, du = D * u.double() * da, D * a
+    want = (dg @ G + du @ U, dg.T @ X, du.T @ X)
+    mags = (dg.abs() @ G.abs() + du.abs() @ U.abs(), dg.abs().T @ X.abs(), du.abs().T @ X.abs())
+    o, e = 2.0 ** -8, 2.0 ** -23
+    for y, w, mag in zip(got, want, mags):
+        assert torch.isfinite(y).all()
+        # half a step of dg or du and of the output; 16 fp32 steps of an activation, 2 I or T of a sum
+        assert ((y.double() - w).abs() <= (1 + o) * (o + (16 + 2 * I + T) * e) * mag + o * w.abs()).all()
+
+
 def test_workspace_by_type():
     from nvfp4_block_scaled_quant_gb300 import _lib
     f = _lib.lib().nvfp4_gated_linear_backward_workspace_bytes_dt
