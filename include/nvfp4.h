@@ -455,8 +455,8 @@ NVFP4_API nvfp4_status nvfp4_gated_linear_backward(const void *dh, int64_t lddh,
  * `r_dtype`: `dtype` or fp32.  gate_kind NVFP4_GATE_CHANNEL: gate (gate_groups, K) contiguous, row
  * m uses gate[m / (M / gate_groups)], M % gate_groups == 0; NVFP4_GATE_ROW: gate (M).
  * y (M, K) contiguous in `dtype`.  stats, if not NULL: fp32 (M, 2) = rstd(f), rstd(r_out) (0 where
- * a norm is absent), the input of the backward.  r_out may be r (same stride K) and else overlaps
- * neither r nor f.
+ * a norm is absent), the input of the backward.  r_out may be r (same stride K) if stats is NULL, since
+ * the backward reads r, and else overlaps neither r nor f.
  * K % 8 == 0, K <= 16384; row strides a multiple of 8. */
 NVFP4_API nvfp4_status nvfp4_residual_norm(const void *f, int dtype, const void *r, int r_dtype, int64_t M,
                                            int64_t K, int64_t ldf, int64_t ldr, const void *gamma_after,

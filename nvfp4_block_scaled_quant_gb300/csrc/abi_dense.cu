@@ -498,6 +498,8 @@ nvfp4_status nvfp4_residual_norm(const void *f, int dtype, const void *r, int r_
   NV_REQUIRE(M == 0 || (y != nullptr) == (gamma_before != nullptr), NVFP4_ERR_INVALID_ARG,
              "y and gamma_before come together");
   NV_REQUIRE(r_out != r || ldr == K, NVFP4_ERR_MISALIGNED, "in place, r must be contiguous");
+  NV_REQUIRE(r_out != r || !stats || M == 0, NVFP4_ERR_INVALID_ARG,
+             "stats in place: the backward needs the r that r_out would overwrite");
   NV_REQUIRE(aligned(r_out, 16) && aligned(y, 16) && aligned(stats, 8), NVFP4_ERR_MISALIGNED,
              "r_out and y must be 16-byte aligned");
   const int64_t r_bytes = r_dtype == NVFP4_DT_FP32 ? 4 : 2;

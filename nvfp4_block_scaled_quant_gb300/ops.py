@@ -538,7 +538,8 @@ def residual_norm(f: torch.Tensor, r: torch.Tensor, gamma_after: Optional[torch.
     n = rmsnorm(f; gamma_after) (f without gamma_after), r_out = r + scale * gate * n, y =
     rmsnorm(r_out; gamma_before) from the unrounded sum (None without gamma_before).  f (M, K) and r
     (M, K; f's type or fp32) strided rows; gate (K,), (groups, K) for M / groups consecutive rows each,
-    or (M, 1).  ``out`` receives r_out and may be r.  K % 8 == 0, K <= 16384.
+    or (M, 1).  ``out`` receives r_out and may be r, but not with ``save``: the backward reads the r that
+    would be overwritten.  K % 8 == 0, K <= 16384.
     """
     st = _here(stream, f, r, gamma_after, gate, gamma_before, out)
     if st < 0:

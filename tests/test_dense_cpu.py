@@ -129,3 +129,11 @@ def test_torch_layer_refuses_cpu_tensors():
     for f in [lambda: ops.fp8_quantize_act(x), lambda: ops.gated_linear(x, w, w), lambda: ops.residual_norm(x, x)]:
         with pytest.raises(ValueError, match="CUDA"):
             f()
+
+
+def test_stats_in_place_are_refused(L):
+    """The backward reads r: a forward that keeps statistics for it may not overwrite r with r_out."""
+    a = dict(f=P, dtype=BF, r=4 * P, rd=BF, M=6, K=64, ldf=64, ldr=64, ga=None, gate=None, kind=0, groups=0, scale=1.0, gb=None, eps=1e-6,
+             ro=4 * P, y=None, stats=8 * P, stream=None)
+    refuses(L, "nvfp4_residual_norm", changed(a), 1)
+    assert b"backward" in L.nvfp4_last_error_string()
