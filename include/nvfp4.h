@@ -387,7 +387,9 @@ NVFP4_API nvfp4_status nvfp4_moe_finalize(int64_t T, int64_t H, int64_t I, int64
  * linear with its gradients, and the norms, gate and residual sum between two blocks with
  * their gradients.  The conventions above hold (device pointers, no allocation, caller's
  * workspace, programmatic dependent launch, 16-byte aligned pointers); element types are
- * given by NVFP4_DT_*.  No input may overlap an output unless a call says so.  M, N, K, T, H
+ * given by NVFP4_DT_*.  What a call writes (outputs, workspace) overlaps neither an input nor anything
+ * else it writes, unless the call says so: refused with NVFP4_ERR_INVALID_ARG (of strided rows the whole
+ * range from the first element to the last counts).  M, N, K, T, H
  * and I are below 2^24, a product of two of them below 2^40.
  * ============================================================================ */
 

@@ -1,6 +1,7 @@
 // Host side of the dense feed-forward operators' C ABI: argument validation, the choice between
 // the weight-streaming and the tile GEMM, tensor maps, workspace layout and launch sequences.
 #include <cstring>
+#include <initializer_list>
 
 #include "abi_util.h"
 #include "stream_gemm.cuh"
@@ -19,19 +20,31 @@ bool dims_ok(int64_t a, int64_t b) { return a < kMaxDim && b < kMaxDim && a * b 
   NV_REQUIRE(dims_ok(a, b), NVFP4_ERR_UNSUPPORTED_SHAPE, "sizes too large: %lld x %lld", (long long)(a), \
              (long long)(b))
 
-// Whether `rows` rows of `cols` elements, `ld` apart, share memory with the same of another tensor, taken
-// as the whole range from the first element to the last.  An output inside an input would be written
-// while other blocks still read it.
+// `rows` rows of `cols` elements of `bytes` bytes, `ld` elements apart, taken as the whole range from the first
+// element to the last.
 struct Span {
   const void *p;
   int64_t rows, ld, cols, bytes;
 };
 bool overlap(const Span &a, const Span &b) {
-  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0) return false;
+  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.cols <= 0 || b.cols <= 0) return false;
   const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
   const uintptr_t a1 = a0 + static_cast<uintptr_t>(((a.rows - 1) * a.ld + a.cols) * a.bytes);
   const uintptr_t b1 = b0 + static_cast<uintptr_t>(((b.rows - 1) * b.ld + b.cols) * b.bytes);
   return a0 < b1 && b0 < a1;
+}
+Span flat(const void *p, int64_t n, int64_t bytes) { return {p, 1, n, n, bytes}; }
+
+// Refuses what is written (outputs, the workspace) inside what is read, which other blocks may still be
+// reading, and inside what else is written.
+nvfp4_status check_disjoint(const char *fn, std::initializer_list<Span> written, std::initializer_list<Span> read) {
+  for (auto w = written.begin(); w != written.end(); ++w) {
+    for (const Span &r : read)
+      if (overlap(*w, r)) return fail(NVFP4_ERR_INVALID_ARG, fn, "an output or the workspace overlaps an input");
+    for (auto o = written.begin(); o != w; ++o)
+      if (overlap(*w, *o)) return fail(NVFP4_ERR_INVALID_ARG, fn, "outputs and workspace overlap one another");
+  }
+  return NVFP4_OK;
 }
 
 // Estimated times (in units of 10 ns) that choose between the GEMMs.  The coefficients were fitted to
@@ -221,6 +234,8 @@ nvfp4_status nvfp4_fp8_quantize_act(const void *x, int dtype, int64_t M, int64_t
   NV_REQUIRE(aligned(q, 16) && aligned(xs, 16), NVFP4_ERR_MISALIGNED, "q and xs must be 16-byte aligned");
   DeviceInfo *d;
   if ((st = device_info(__func__, &d)) != NVFP4_OK) return st;
+  st = check_disjoint(__func__, {{q, M, K, K, 1}, {xs, (K + 127) / 128, lds, M, 4}}, {{x, M, ldx, K, 2}});
+  if (st != NVFP4_OK) return st;
   if (M == 0) return NVFP4_OK;
   NV_CUDA(launch_fp8_quantize_act(x, dtype, M, K, ldx, q, xs, lds, d->sms, static_cast<cudaStream_t>(stream)),
           "FP8 quantise launch");
@@ -235,6 +250,8 @@ nvfp4_status nvfp4_fp8_quantize_weight(const void *w, int dtype, int64_t N, int6
   NV_REQUIRE(N <= 65535 * 128, NVFP4_ERR_UNSUPPORTED_SHAPE, "N=%lld too large", (long long)N);
   NV_REQUIRE(q && w_s, NVFP4_ERR_INVALID_ARG, "NULL pointer argument");
   NV_REQUIRE(aligned(q, 16) && aligned(w_s, 4), NVFP4_ERR_MISALIGNED, "q must be 16-byte aligned");
+  st = check_disjoint(__func__, {{q, N, K, K, 1}, flat(w_s, (N + 127) / 128 * ((K + 127) / 128), 4)}, {{w, N, ldw, K, 2}});
+  if (st != NVFP4_OK) return st;
   DeviceInfo *d;
   if ((st = device_info(__func__, &d)) != NVFP4_OK) return st;
   NV_CUDA(launch_fp8_quantize_weight(w, dtype, N, K, ldw, q, w_s, static_cast<cudaStream_t>(stream)),
@@ -257,10 +274,13 @@ nvfp4_status nvfp4_fp8_gemm(const uint8_t *xq, const float *xs, int64_t lds, int
              "lds=%lld must be >= M and a multiple of 4", (long long)lds);
   NV_REQUIRE(aligned(xq, 16) && aligned(xs, 16) && aligned(w, 16) && aligned(w_s, 4) && aligned(y, 16),
              NVFP4_ERR_MISALIGNED, "xq, xs, w and y must be 16-byte aligned");
-  NV_REQUIRE(!overlap({y, M, N, N, 2}, {xq, M, K, K, 1}), NVFP4_ERR_INVALID_ARG, "y overlaps xq");
-  DeviceInfo *d;
-  nvfp4_status st = device_info(__func__, &d);
+  const int64_t k_blocks = (K + 127) / 128;
+  nvfp4_status st = check_disjoint(__func__, {{y, M, N, N, 2}},
+                                   {{xq, M, K, K, 1}, {xs, k_blocks, lds, M, 4}, flat(w, N * K, 1),
+                                    flat(w_s, (N + 127) / 128 * k_blocks, 4)});
   if (st != NVFP4_OK) return st;
+  DeviceInfo *d;
+  if ((st = device_info(__func__, &d)) != NVFP4_OK) return st;
   if (M == 0) return NVFP4_OK;
   return fp8_gemm_impl(__func__, d, xq, xs, lds, M, K, N, w, w_s, dtype, y, static_cast<cudaStream_t>(stream));
 }
@@ -282,7 +302,9 @@ nvfp4_status nvfp4_fp8_linear(const void *x, int dtype, int64_t M, int64_t K, in
              "w and y must be 16-byte aligned");
   const Fp8Ws L = fp8_ws(M, K);
   if ((st = check_ws(__func__, ws, ws_bytes, L.total)) != NVFP4_OK) return st;
-  NV_REQUIRE(!overlap({y, M, N, N, 2}, {x, M, ldx, K, 2}), NVFP4_ERR_INVALID_ARG, "y overlaps x");
+  st = check_disjoint(__func__, {{y, M, N, N, 2}, flat(ws, static_cast<int64_t>(L.total), 1)},
+                      {{x, M, ldx, K, 2}, flat(w, N * K, 1), flat(w_s, (N + 127) / 128 * ((K + 127) / 128), 4)});
+  if (st != NVFP4_OK) return st;
   DeviceInfo *d;
   if ((st = device_info(__func__, &d)) != NVFP4_OK) return st;
   if (M == 0) return NVFP4_OK;
@@ -341,7 +363,9 @@ nvfp4_status nvfp4_gated_linear(const void *x, int dtype, int64_t T, int64_t H, 
   if (st != NVFP4_OK) return st;
   NV_REQUIRE(h || T == 0, NVFP4_ERR_INVALID_ARG, "h is NULL");
   NV_REQUIRE(aligned(h, 16) && aligned(gu, 32), NVFP4_ERR_MISALIGNED, "h must be 16-byte and gu 32-byte aligned");
-  NV_REQUIRE(!overlap({h, T, I, I, 2}, {x, T, ldx, H, 2}), NVFP4_ERR_INVALID_ARG, "h overlaps x");
+  st = check_disjoint(__func__, {{h, T, I, I, 2}, flat(gu, 2 * T * I, 4)},
+                      {{x, T, ldx, H, 2}, flat(w_gate, I * H, 2), flat(w_up, I * H, 2)});
+  if (st != NVFP4_OK) return st;
   DeviceInfo *d;
   if ((st = device_info(__func__, &d)) != NVFP4_OK) return st;
   if (T == 0) return NVFP4_OK;
@@ -403,7 +427,11 @@ nvfp4_status nvfp4_gated_linear_backward(const void *dh, int64_t lddh, const voi
              "lddh=%lld must be >= I and a multiple of 8", (long long)lddh);
   NV_REQUIRE(aligned(dh, 16) && aligned(gu, 16) && aligned(dx, 16) && aligned(dw_gate, 16) && aligned(dw_up, 16),
              NVFP4_ERR_MISALIGNED, "pointers must be 16-byte aligned");
-  st = check_ws(__func__, ws, ws_bytes, nvfp4_gated_linear_backward_workspace_bytes_dt(T, I, dtype));
+  const size_t need = nvfp4_gated_linear_backward_workspace_bytes_dt(T, I, dtype);
+  if ((st = check_ws(__func__, ws, ws_bytes, need)) != NVFP4_OK) return st;
+  st = check_disjoint(__func__,
+                      {flat(dx, T * H, 2), flat(dw_gate, I * H, 2), flat(dw_up, I * H, 2), flat(ws, static_cast<int64_t>(need), 1)},
+                      {{dh, T, lddh, I, 2}, {x, T, ldx, H, 2}, flat(w_gate, I * H, 2), flat(w_up, I * H, 2), flat(gu, 2 * T * I, 4)});
   if (st != NVFP4_OK) return st;
   DeviceInfo *d;
   if ((st = device_info(__func__, &d)) != NVFP4_OK) return st;
@@ -503,9 +531,11 @@ nvfp4_status nvfp4_residual_norm(const void *f, int dtype, const void *r, int r_
   NV_REQUIRE(aligned(r_out, 16) && aligned(y, 16) && aligned(stats, 8), NVFP4_ERR_MISALIGNED,
              "r_out and y must be 16-byte aligned");
   const int64_t r_bytes = r_dtype == NVFP4_DT_FP32 ? 4 : 2;
-  NV_REQUIRE(!overlap({r_out, M, K, K, r_bytes}, {f, M, ldf, K, 2}) &&
-                 (r_out == r || !overlap({r_out, M, K, K, r_bytes}, {r, M, ldr, K, r_bytes})),
-             NVFP4_ERR_INVALID_ARG, "r_out overlaps f, or r at another address than its own");
+  const int64_t gate_size = gate_kind == NVFP4_GATE_ROW ? M : gate_kind == NVFP4_GATE_CHANNEL ? gate_groups * K : 0;
+  st = check_disjoint(__func__, {flat(r_out, M * K, r_bytes), flat(y, M * K, 2), flat(stats, 2 * M, 4)},
+                      {{f, M, ldf, K, 2}, {r == r_out ? nullptr : r, M, ldr, K, r_bytes}, flat(gamma_after, K, 2),
+                       flat(gamma_before, K, 2), flat(gate, gate_size, 2)});
+  if (st != NVFP4_OK) return st;
   DeviceInfo *d;
   if ((st = device_info(__func__, &d)) != NVFP4_OK) return st;
   if (M == 0) return NVFP4_OK;
@@ -566,7 +596,14 @@ nvfp4_status nvfp4_residual_norm_backward(const void *dr_out, int64_t lddr, cons
   const bool channel = gate_kind == NVFP4_GATE_CHANNEL;
   const int64_t groups = channel ? gate_groups : 1;
   const bool r32 = r_dtype == NVFP4_DT_FP32;
-  st = check_ws(__func__, ws, ws_bytes, nvfp4_residual_norm_backward_workspace_bytes(M, K, groups, r_dtype));
+  const size_t need = nvfp4_residual_norm_backward_workspace_bytes(M, K, groups, r_dtype);
+  if ((st = check_ws(__func__, ws, ws_bytes, need)) != NVFP4_OK) return st;
+  const int64_t r_bytes = r32 ? 4 : 2, gate_size = channel ? groups * K : gate ? M : 0;
+  st = check_disjoint(__func__,
+                      {flat(df, M * K, 2), flat(dr, M * K, r_bytes), flat(dgamma_after, K, 4), flat(dgamma_before, K, 4),
+                       flat(dgate, gate_size, 4), flat(ws, static_cast<int64_t>(need), 1)},
+                      {{dr_out, M, lddr, K, r_bytes}, {dy, M, lddy, K, 2}, {f, M, ldf, K, 2}, {r, M, ldr, K, r_bytes},
+                       flat(stats, 2 * M, 4), flat(gamma_after, K, 2), flat(gamma_before, K, 2), flat(gate, gate_size, 2)});
   if (st != NVFP4_OK) return st;
   DeviceInfo *d;
   if ((st = device_info(__func__, &d)) != NVFP4_OK) return st;

@@ -291,8 +291,8 @@ def moe_finalize(T: int, topk: int, W: MoEWeights, y, workspace, stream=None):
 #
 # The operators around the experts: bf16 or fp16 tensors, rows with any stride that is a multiple of
 # 8 elements where a call says "strided rows", everything else contiguous.  They keep no autograd
-# graph: a backward pass is its own call.  An output given as ``out`` overlaps no input
-# (``residual_norm``'s may be r itself).  With ``stream`` given, outputs and scratch are allocated
+# graph: a backward pass is its own call.  An output given as ``out`` and a ``workspace``
+# overlap no input and not one another (``residual_norm``'s ``out`` may be r itself).  With ``stream`` given, outputs and scratch are allocated
 # for that stream and the inputs are marked as used on it.  Large products of different streams run
 # one after the other; a captured graph that holds some is replayed where no other runs at the
 # same time (on one stream, or on several that wait for one another).

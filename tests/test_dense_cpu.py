@@ -137,3 +137,54 @@ def test_stats_in_place_are_refused(L):
              ro=4 * P, y=None, stats=8 * P, stream=None)
     refuses(L, "nvfp4_residual_norm", changed(a), 1)
     assert b"backward" in L.nvfp4_last_error_string()
+
+
+# every operand of a call in a range of its own: (name, bytes); written ones are moved into each of the others below
+CALLS = {
+    "nvfp4_fp8_quantize_weight": (dict(w=0, dtype=BF, N=200, K=256, ldw=272, q=0, w_s=0, stream=None),
+                                  dict(w=(199 * 272 + 256) * 2, q=200 * 256, w_s=16), ["q", "w_s"]),
+    "nvfp4_fp8_gemm": (dict(xq=0, xs=0, lds=8, M=5, K=256, N=200, w=0, w_s=0, dtype=BF, y=0, stream=None),
+                       dict(xq=5 * 256, xs=(8 + 5) * 4, w=200 * 256, w_s=16, y=5 * 200 * 2), ["y"]),
+    "nvfp4_fp8_linear": (dict(x=0, dtype=HF, M=70, K=256, ldx=264, N=200, w=0, w_s=0, y=0, ws=0, bytes=1 << 15, stream=None),
+                         dict(x=(69 * 264 + 256) * 2, w=200 * 256, w_s=16, y=70 * 200 * 2, ws=70 * 256 + 2 * 72 * 4), ["y", "ws"]),
+    "nvfp4_gated_linear": (dict(x=0, dtype=BF, T=5, H=64, ldx=72, I=16, wg=0, wu=0, act=0, h=0, gu=0, stream=None),
+                           dict(x=(4 * 72 + 64) * 2, wg=16 * 64 * 2, wu=16 * 64 * 2, h=5 * 16 * 2, gu=5 * 32 * 4), ["h", "gu"]),
+    "nvfp4_gated_linear_backward": (
+        dict(dh=0, lddh=24, x=0, ldx=72, dtype=BF, T=5, H=64, I=16, wg=0, wu=0, act=0, gu=0, dx=0, dwg=0, dwu=0, ws=0, bytes=512, stream=None),
+        dict(dh=(4 * 24 + 16) * 2, x=(4 * 72 + 64) * 2, wg=16 * 64 * 2, wu=16 * 64 * 2, gu=5 * 32 * 4, dx=5 * 64 * 2, dwg=16 * 64 * 2,
+             dwu=16 * 64 * 2, ws=512), ["dx", "dwg", "dwu", "ws"]),
+    "nvfp4_residual_norm": (
+        dict(f=0, dtype=BF, r=0, rd=F32, M=6, K=64, ldf=72, ldr=80, ga=0, gate=0, kind=1, groups=3, scale=1.0, gb=0, eps=1e-6, ro=0, y=0,
+             stats=0, stream=None),
+        dict(f=(5 * 72 + 64) * 2, r=(5 * 80 + 64) * 4, ga=128, gate=3 * 128, gb=128, ro=6 * 64 * 4, y=6 * 64 * 2, stats=6 * 8),
+        ["ro", "y", "stats"]),
+    "nvfp4_residual_norm_backward": (
+        dict(dro=0, lddr=72, dy=0, lddy=80, f=0, dtype=BF, r=0, rd=BF, M=6, K=64, ldf=64, ldr=64, stats=0, ga=0, gate=0, kind=2, groups=1,
+             scale=1.0, gb=0, df=0, dr=0, dga=0, dgate=0, dgb=0, ws=0, bytes=1 << 15, stream=None),
+        dict(dro=(5 * 72 + 64) * 2, dy=(5 * 80 + 64) * 2, f=6 * 128, r=6 * 128, stats=6 * 8, ga=128, gate=6 * 2, gb=128, df=6 * 128,
+             dr=6 * 128, dga=256, dgate=6 * 4, dgb=256, ws=1024), ["df", "dr", "dga", "dgate", "dgb", "ws"]),
+}
+
+
+@pytest.mark.parametrize("name", list(CALLS))
+def test_nothing_written_overlaps_another_operand(L, name):
+    """Each output and the workspace at the first and in the last 256 bytes of every other operand, and with its own last
+    byte on the other's first; apart from each other the call gets past its checks."""
+    base, sizes, written = CALLS[name]
+    at = {o: P + (i << 20) for i, o in enumerate(sizes)}
+    base = {**base, **at}
+    if not torch.cuda.is_available():  # the pointers are not real: the call ends at the device
+        assert getattr(L, name)(*changed(base)) in (_lib.ERR_CUDA, _lib.ERR_UNSUPPORTED_DEVICE)
+    for w in written:
+        for o, n in sizes.items():
+            if o == w:
+                continue
+            for p in (at[o], at[o] + (n - 1) // 256 * 256, at[o] - (sizes[w] - 1) // 256 * 256):
+                if (w, o) == ("ro", "r") and p == at["r"]:
+                    continue  # in place: allowed or refused by rules of its own (stride, statistics)
+                refuses(L, name, changed(base, **{w: p}), 1)
+                assert b"overlap" in L.nvfp4_last_error_string(), (w, o)
+    if name == "nvfp4_residual_norm":  # r_out may be r itself (same stride), without statistics
+        same = changed(base, ro=at["r"], ldr=64, stats=None)
+        if not torch.cuda.is_available():
+            assert getattr(L, name)(*same) in (_lib.ERR_CUDA, _lib.ERR_UNSUPPORTED_DEVICE)

@@ -1,0 +1,43 @@
+"""Calls of the dense operators that are refused on a machine with a GPU: nothing is launched, and what the
+call would have written is as it was."""
+
+import pytest
+import torch
+
+from nvfp4_block_scaled_quant_gb300 import _lib, ops
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+BF = _lib.DT_BF16
+
+
+def test_quantising_into_the_activations():
+    buf = torch.arange(1 << 14, device=DEV).to(torch.bfloat16)
+    keep, p = buf.clone(), buf.data_ptr()
+    free = torch.zeros(1 << 14, dtype=torch.uint8, device=DEV).data_ptr()
+    for q, xs in ((p, free), (p + 4 * 256 * 2 - 16, free), (free, p + 1024), (free, free + 4 * 256 - 16)):
+        with pytest.raises(RuntimeError, match="overlap"):
+            _lib.call("nvfp4_fp8_quantize_act", p, BF, 4, 256, 256, q, xs, 4, torch.cuda.current_stream().cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(buf, keep)
+
+
+def test_outputs_and_workspaces_inside_inputs():
+    bf = dict(dtype=torch.bfloat16, device=DEV)
+    x, r = torch.ones(64, 256, **bf), torch.ones(64, 256, **bf)
+    w, ws = ops.fp8_quantize_weight(torch.ones(256, 256, **bf))
+    wg, wu = torch.ones(64, 256, **bf), torch.ones(256, 256, **bf)
+    gate, gb = torch.ones(64, 256, **bf), torch.ones(256, **bf)
+    h, gu = ops.gated_linear(x, wg, wg, save=True)
+    grad_ws = gu.view(torch.uint8).view(-1)
+    keep = [t.clone() for t in (x, r, wg, wu, gate, gu)]
+    for call in [lambda: ops.fp8_linear(x, w, ws, out=wu[:64].view(64, 256), workspace=wu.view(torch.uint8).view(-1)),
+                 lambda: ops.gated_linear(x, wu, wu, out=wu[:64]),
+                 lambda: ops.gated_linear_backward(h, x, wg, wg, gu, workspace=grad_ws),
+                 lambda: ops.residual_norm(x, r, gate=gate, out=gate),
+                 lambda: ops.residual_norm(x, r, gamma_before=x[3], out=x)]:
+        with pytest.raises(RuntimeError, match="overlap"):
+            call()
+    torch.cuda.synchronize()
+    for a, b in zip((x, r, wg, wu, gate, gu), keep):
+        assert torch.equal(a, b)
