@@ -291,7 +291,8 @@ def moe_finalize(T: int, topk: int, W: MoEWeights, y, workspace, stream=None):
 #
 # The operators around the experts: bf16 or fp16 tensors, rows with any stride that is a multiple of
 # 8 elements where a call says "strided rows", everything else contiguous.  They keep no autograd
-# graph: a backward pass is its own call.  An output given as ``out`` and a ``workspace``
+# graph: a backward pass is its own call, and those that have one refuse inputs that require grad while
+# gradients are recorded (the FP8 linear has none and is for inference, like ``linear``).  An output given as ``out`` and a ``workspace``
 # overlap no input and not one another (``residual_norm``'s ``out`` may be r itself).  With ``stream`` given, outputs and scratch are allocated
 # for that stream and the inputs are marked as used on it.  Large products of different streams run
 # one after the other; a captured graph that holds some is replayed where no other runs at the
@@ -314,6 +315,15 @@ def _here(stream, *tensors: Optional[torch.Tensor]) -> int:
     if stream is not None or dev != torch._C._cuda_getDevice():
         return -1
     return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _no_graph(*tensors: Optional[torch.Tensor]) -> None:
+    """Refuses what would silently cut an autograd graph."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError("an input requires grad, but this call records no graph: make it under torch.no_grad() "
+                                 "and take the gradients from the operator's backward call")
 
 
 def _elsewhere(stream, tensors, run):
@@ -477,6 +487,7 @@ def gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor, acti
     fp32 pre-activations [g | u] that ``gated_linear_backward`` takes.  H % 8 == 0, I % 8 == 0.
     """
     st = _here(stream, x, w_gate, w_up, out)
+    _no_graph(x, w_gate, w_up)
     if st < 0:
         return _elsewhere(stream, (x, w_gate, w_up, out), lambda: gated_linear(x, w_gate, w_up, activation, save, out))
     T, H, I, ld, kind, gp, up, act = _gated_args(x, w_gate, w_up, activation)
@@ -494,6 +505,7 @@ def gated_linear_backward(dh: torch.Tensor, x: torch.Tensor, w_gate: torch.Tenso
     """Gradients (dx (T, H), dw_gate (I, H), dw_up (I, H)) of ``gated_linear`` from dh (T, I) strided
     rows and the saved gu; those not asked for are None."""
     st = _here(stream, x, dh, w_gate, w_up, gu, workspace)
+    _no_graph(x, dh, w_gate, w_up)
     if st < 0:
         return _elsewhere(stream, (x, dh, w_gate, w_up, gu, workspace),
                           lambda: gated_linear_backward(dh, x, w_gate, w_up, gu, activation, need_dx, need_dw, workspace))
@@ -542,6 +554,7 @@ def residual_norm(f: torch.Tensor, r: torch.Tensor, gamma_after: Optional[torch.
     would be overwritten.  K % 8 == 0, K <= 16384.
     """
     st = _here(stream, f, r, gamma_after, gate, gamma_before, out)
+    _no_graph(f, r, gamma_after, gate, gamma_before)
     if st < 0:
         return _elsewhere(stream, (f, r, gamma_after, gate, gamma_before, out),
                           lambda: residual_norm(f, r, gamma_after, gate, scale, gamma_before, eps, save, out))
@@ -568,6 +581,7 @@ def residual_norm_backward(dr_out: Optional[torch.Tensor], dy: Optional[torch.Te
     None (zero).  The other arguments are the forward's (eps is already in ``stats``).
     """
     st = _here(stream, f, r, dr_out, dy, stats, gamma_after, gate, gamma_before, workspace)
+    _no_graph(f, r, dr_out, dy, gamma_after, gate, gamma_before)
     if st < 0:
         return _elsewhere(stream, (f, r, dr_out, dy, stats, gamma_after, gate, gamma_before, workspace),
                           lambda: residual_norm_backward(dr_out, dy, f, r, stats, gamma_after, gate, scale, gamma_before,

@@ -41,3 +41,42 @@ def test_outputs_and_workspaces_inside_inputs():
     torch.cuda.synchronize()
     for a, b in zip((x, r, wg, wu, gate, gu), keep):
         assert torch.equal(a, b)
+
+
+def test_inputs_that_require_grad():
+    """A call that records no graph would lose their gradients without a word; under no_grad it is made, and inside an
+    autograd function its forward and backward calls are."""
+    bf = dict(dtype=torch.bfloat16, device=DEV)
+    x, dh, w, g = torch.randn(6, 64, **bf), torch.randn(6, 16, **bf), torch.randn(16, 64, **bf), torch.randn(64, **bf)
+    h, gu = ops.gated_linear(x, w, w, save=True)
+    r_out, y, stats = ops.residual_norm(x, x, g, gate=g, gamma_before=g, save=True)
+    xp, wp, gp, dp = (torch.nn.Parameter(t) for t in (x, w, g, dh))
+    calls = [lambda: ops.gated_linear(xp, w, w), lambda: ops.gated_linear(x, wp, w), lambda: ops.gated_linear(x, w, wp),
+             lambda: ops.gated_linear_backward(dp, x, w, w, gu), lambda: ops.gated_linear_backward(dh, x, wp, w, gu),
+             lambda: ops.residual_norm(xp, x), lambda: ops.residual_norm(x, xp), lambda: ops.residual_norm(x, x, gp),
+             lambda: ops.residual_norm(x, x, gate=gp), lambda: ops.residual_norm(x, x, gamma_before=gp),
+             lambda: ops.residual_norm(xp, x, stream=torch.cuda.current_stream()),
+             lambda: ops.residual_norm_backward(xp, None, x, x, stats, g, gate=g, gamma_before=g),
+             lambda: ops.residual_norm_backward(x, x, x, x, stats, gp, gate=g, gamma_before=g)]
+    for call in calls:
+        with pytest.raises(ValueError, match="grad"):
+            call()
+        with torch.no_grad():
+            call()
+
+    class Gated(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, wg, wu):
+            h, gu = ops.gated_linear(x, wg, wu, save=True)
+            ctx.save_for_backward(x, wg, wu, gu)
+            return h
+
+        @staticmethod
+        def backward(ctx, dh):
+            x, wg, wu, gu = ctx.saved_tensors
+            return ops.gated_linear_backward(dh, x, wg, wu, gu)
+
+    out = Gated.apply(xp, wp, wp)
+    out.backward(dh)
+    dx, dwg, dwu = ops.gated_linear_backward(dh, x, w, w, gu)
+    assert torch.equal(out, h) and torch.equal(xp.grad, dx) and torch.equal(wp.grad, dwg + dwu)
