@@ -437,7 +437,8 @@ def fp8_gemm(xq: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, w_s: torch.Ten
     _size(xs, "xs")
     N, wp, wsp = _fp8_weight(w, w_s, K)
     KB = (K + 127) // 128
-    lds = xs.stride(0) if KB > 1 else max(xs.stride(0), (M + 3) // 4 * 4)
+    # the stride of a single row, or of empty ones, says nothing
+    lds = (M + 3) // 4 * 4 if KB == 1 or M == 0 else xs.stride(0)
     room = xs.untyped_storage().nbytes() // 4 - xs.storage_offset()
     if xs.dtype != torch.float32 or tuple(xs.shape) != (KB, M) or (M > 1 and xs.stride(1) != 1):
         raise ValueError(f"xs must be fp32 ({KB}, {M}) with contiguous rows")

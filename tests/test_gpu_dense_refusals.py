@@ -1,5 +1,5 @@
-"""Calls of the dense operators that are refused on a machine with a GPU: nothing is launched, and what the
-call would have written is as it was."""
+"""Calls of the dense operators that are refused on a machine with a GPU (nothing is launched, and what the
+call would have written is as it was), and calls with no rows, which are not."""
 
 import pytest
 import torch
@@ -80,3 +80,14 @@ def test_inputs_that_require_grad():
     out.backward(dh)
     dx, dwg, dwu = ops.gated_linear_backward(dh, x, w, w, gu)
     assert torch.equal(out, h) and torch.equal(xp.grad, dx) and torch.equal(wp.grad, dwg + dwu)
+
+
+def test_one_row_of_scales_with_any_stride():
+    """A single K block's row of scales is read as it lies, whatever its stride says."""
+    bf = dict(dtype=torch.bfloat16, device=DEV)
+    w, ws = ops.fp8_quantize_weight(torch.randn(24, 64, **bf))
+    q, s = ops.fp8_quantize_act(torch.randn(6, 64, **bf))
+    want = ops.fp8_gemm(q, s, w, ws)
+    wide = torch.zeros(2, 30, device=DEV)  # rows 120 bytes apart, the first one 16-byte aligned
+    wide[0, :6] = s[0]
+    assert torch.equal(ops.fp8_gemm(q, wide[:1, :6], w, ws), want)
