@@ -535,6 +535,8 @@ def _norm_args(f, r, gamma_after, gate, gamma_before):
         return M, K, ldf, ldr, kind, rkind, ga, None, _lib.GATE_NONE, 0, gb
     if gate.dim() == 2 and tuple(gate.shape) == (M, 1):
         return M, K, ldf, ldr, kind, rkind, ga, _whole(gate, "gate", (M, 1), (f.dtype,)), _lib.GATE_ROW, 0, gb
+    if gate.dim() not in (1, 2):
+        raise ValueError(f"gate has shape {tuple(gate.shape)}, expected ({K},), (groups, {K}) or ({M}, 1)")
     groups = 1 if gate.dim() == 1 else gate.shape[0]
     gp = _whole(gate, "gate", (K,) if gate.dim() == 1 else (groups, K), (f.dtype,))
     if groups == 0 or M % groups:

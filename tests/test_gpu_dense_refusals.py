@@ -91,3 +91,10 @@ def test_one_row_of_scales_with_any_stride():
     wide = torch.zeros(2, 30, device=DEV)  # rows 120 bytes apart, the first one 16-byte aligned
     wide[0, :6] = s[0]
     assert torch.equal(ops.fp8_gemm(q, wide[:1, :6], w, ws), want)
+
+
+def test_gates_of_other_ranks():
+    f = torch.zeros(6, 64, dtype=torch.bfloat16, device=DEV)
+    for shape in ((), (1, 6, 64)):
+        with pytest.raises(ValueError, match="gate"):
+            ops.residual_norm(f, f, gate=torch.zeros(shape, dtype=torch.bfloat16, device=DEV))
