@@ -501,7 +501,8 @@ static nvfp4_status check_norm(const char *fn, const void *f, int dtype, const v
                 (long long)ldr);
   if (gate_kind != NVFP4_GATE_NONE && gate_kind != NVFP4_GATE_CHANNEL && gate_kind != NVFP4_GATE_ROW)
     return fail(NVFP4_ERR_INVALID_ARG, fn, "gate kind %d", gate_kind);
-  if ((gate_kind == NVFP4_GATE_NONE) != (gate == nullptr))
+  // a gate of no rows has no address
+  if ((gate_kind == NVFP4_GATE_NONE) != (gate == nullptr) && !(gate_kind == NVFP4_GATE_ROW && M == 0))
     return fail(NVFP4_ERR_INVALID_ARG, fn, "a gate and its kind come together");
   if (gate_kind == NVFP4_GATE_CHANNEL) {
     if (groups <= 0 || M % groups)

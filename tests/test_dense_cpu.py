@@ -188,3 +188,12 @@ def test_nothing_written_overlaps_another_operand(L, name):
         same = changed(base, ro=at["r"], ldr=64, stats=None)
         if not torch.cuda.is_available():
             assert getattr(L, name)(*same) in (_lib.ERR_CUDA, _lib.ERR_UNSUPPORTED_DEVICE)
+
+
+def test_a_gate_of_no_rows_has_no_address(L):
+    if torch.cuda.is_available():
+        pytest.skip("the pointers are not real")
+    a = dict(f=None, dtype=BF, r=None, rd=BF, M=0, K=64, ldf=64, ldr=64, ga=None, gate=None, kind=2, groups=0, scale=1.0, gb=None, eps=1e-6,
+             ro=None, y=None, stats=None, stream=None)
+    assert L.nvfp4_residual_norm(*changed(a)) in (_lib.ERR_CUDA, _lib.ERR_UNSUPPORTED_DEVICE)
+    refuses(L, "nvfp4_residual_norm", changed(a, M=1, f=P, r=2 * P, ro=3 * P), 1)

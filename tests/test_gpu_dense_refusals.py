@@ -82,6 +82,26 @@ def test_inputs_that_require_grad():
     assert torch.equal(out, h) and torch.equal(xp.grad, dx) and torch.equal(wp.grad, dwg + dwu)
 
 
+@pytest.mark.parametrize("K", [64, 256, 400])
+def test_no_rows_through_every_call(K):
+    bf = dict(dtype=torch.bfloat16, device=DEV)
+    x, none = torch.empty(0, K, **bf), torch.empty(0, 1, **bf)
+    w, ws = ops.fp8_quantize_weight(torch.ones(24, K, **bf))
+    q, s = ops.fp8_quantize_act(x)
+    assert q.shape == (0, K) and s.shape == ((K + 127) // 128, 0)
+    assert ops.fp8_gemm(q, s, w, ws).shape == (0, 24) and ops.fp8_linear(x, w, ws).shape == (0, 24)
+    wg = torch.ones(24, K, **bf)
+    h, gu = ops.gated_linear(x, wg, wg, save=True)
+    dx, dwg, dwu = ops.gated_linear_backward(h, x, wg, wg, gu)
+    assert dx.shape == (0, K) and not dwg.any() and not dwu.any()
+    g = torch.ones(K, **bf)
+    for gate in (None, g, torch.ones(3, K, **bf), none):
+        r_out, y, st = ops.residual_norm(x, x, g, gate=gate, gamma_before=g, save=True)
+        df, dr, dga, dgate, dgb = ops.residual_norm_backward(r_out, y, x, x, st, g, gate=gate, gamma_before=g)
+        assert r_out.shape == y.shape == df.shape == dr.shape == (0, K) and not dga.any() and not dgb.any()
+        assert dgate is None if gate is None else dgate.shape == gate.shape and not dgate.any()
+
+
 def test_one_row_of_scales_with_any_stride():
     """A single K block's row of scales is read as it lies, whatever its stride says."""
     bf = dict(dtype=torch.bfloat16, device=DEV)
