@@ -28,6 +28,10 @@
 // NVFP4_DEVERR_PIPELINE_TIMEOUT and leaves its loop; the producer lets its copies in flight
 // land, the issuer drains its MMAs, and every thread of both CTAs then meets at the final
 // cluster barrier before the pair frees its tensor memory.
+//
+// No CTA exits with a commit or a release on its way to one of its barriers, or before the other has freed
+// its share of the tensor memory, and the kernel does not let a successor start early: launches of pair
+// kernels do not overlap (tile_gemm.cuh says why).
 #include "common.cuh"
 
 namespace nvfp4 {
@@ -105,17 +109,20 @@ __global__ void __launch_bounds__(kPThreads, 1)
     prefetch_tensormap(&tmA);
     prefetch_tensormap(&tmB);
   }
+  __syncwarp();
   if (warp == 1) {
     tmem_alloc_pair(tmem_holder, kPTmemCols);
     tmem_relinquish_pair();
   }
   tc_fence_before();
+  __syncwarp();
   __syncthreads();
+  __syncwarp();
   cluster_sync();  // both CTAs' barriers initialised and tensor memory allocated
+  __syncwarp();
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   pdl_wait();
-  pdl_trigger();
 
   const int M = args.dense_M;
   const int n_tiles = args.N / kPN;
@@ -174,6 +181,14 @@ __global__ void __launch_bounds__(kPThreads, 1)
             stage = 0;
             phase ^= 1;
           }
+        }
+      }
+      // the commits of the last stages have arrived: the ring is followed until every stage is free again
+      for (int i = 0; ok && i < kPStages; ++i) {
+        ok = mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, args.err, kPipelineTimeoutNs);
+        if (++stage == kPStages) {
+          stage = 0;
+          phase ^= 1;
         }
       }
       if (!ok) {
@@ -237,10 +252,12 @@ __global__ void __launch_bounds__(kPThreads, 1)
         if (!ok) break;
         tc_commit_pair(tfull, 0x3);  // each issuer: its MMAs of the tile (tfull counts both)
       }
-      // every MMA issued has completed before the pair frees its tensor memory
+      // every MMA issued has completed before the pair frees its tensor memory, and the last tile's
+      // releases, the other CTA's among them, have arrived
       volatile int never = 0;
       tc_commit_pair(drain, 0x1);
       mbar_wait_bounded(drain, 0, &never, nullptr, 100000000ull);
+      if (ok && it > 0) mbar_wait_bounded_cluster(tempty, (it - 1) & 1, abort_flag, args.err, kPipelineTimeoutNs);
     }
   } else if (warp < 2 + kPScaleWarps) {
     // -------------------------------------------------------------- scale staging
@@ -354,10 +371,15 @@ __global__ void __launch_bounds__(kPThreads, 1)
   }
 
   tc_fence_before();
+  __syncwarp();  // the barriers and the deallocation want converged warps; roles leave their waits lane by lane
   __syncthreads();
+  __syncwarp();
   cluster_sync();  // the pair's MMAs have drained and both epilogues have read their accumulators
+  __syncwarp();
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem_base, kPTmemCols);
+  __syncwarp();
+  cluster_sync();  // neither CTA leaves before the other has taken part in it
 }
 
 }  // namespace

@@ -62,6 +62,23 @@ def test_a_short_launch_on_another_stream_ends_after_the_long_one(kind):
     assert ops.device_error() == (0, 0)
 
 
+def test_products_of_different_grids_in_turn():
+    """NVFP4 and FP8 products on CTA pairs with different numbers of pairs, queued without waiting, also in a graph."""
+    calls = [nvfp4(2048, 512, 1024, 7), fp8(900, 384, 520, 8), nvfp4(600, 768, 512, 9), gated(700, 264, 520, 10)]
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    got = [[c() for c in calls] for _ in range(5)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = [c() for _ in range(2) for c in calls]
+    for _ in range(3):
+        graph.replay()
+    torch.cuda.synchronize()
+    for g in [*got, held[:4], held[4:]]:
+        assert all(torch.equal(a, b) for a, b in zip(g, want))
+    assert ops.device_error() == (0, 0)
+
+
 @pytest.mark.parametrize("kind", list(SHORT))
 def test_branches_of_a_captured_graph(kind):
     long, short = fp8(4096, 7168, 7168, 5), SHORT[kind]()
