@@ -398,7 +398,9 @@ NVFP4_API nvfp4_status nvfp4_moe_finalize(int64_t T, int64_t H, int64_t I, int64
  * 128 x 128 block of W (the last block of a row or column may be partial).
  *   s = fl32(max |x| / 448) over the block, q = e4m3_rne_satfinite(fl32(x / s)), q = 0 if s == 0
  *   y[m, n] = sum_b xs[b, m] w_s[n / 128, b] sum_{k in b} q[m, k] w[n, k]       (fp32 sums)
- * A block that holds a NaN or an infinity makes every output of its rows NaN.
+ * A block that holds a NaN or an infinity makes every output of its rows NaN.  xs w_s is formed in
+ * fp32 first: below 2^-126 (activations of 1e-32 or less with weights of about 1) it loses bits, and
+ * above 2^128 it is infinite.
  * x (M, K), row stride ldx (a multiple of 8), bf16 or fp16; q (M, K) codes, contiguous;
  * xs (ceil(K / 128), lds) fp32, xs[b * lds + m], lds >= M a multiple of 4 (every row,
  * the last included, is readable up to M rounded up to 4; entries m >= M are not written and do not
