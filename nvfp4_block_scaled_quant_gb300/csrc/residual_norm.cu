@@ -398,8 +398,8 @@ __global__ void __launch_bounds__(kThreads, kCtas) residual_norm_rows_kernel(con
 //
 // Half of the time of a 16-bit row is instructions (two sweeps over the row, 16 conversions per four
 // columns), so sums go in packed fp32, a thread takes 16 columns (its fixed work per row, two
-// reductions and a wait, is spread over more than with 8: 375 instructions per eight columns instead
-// of 463), and the warp that is last to finish a row's stage refills it.  8192 x 7168: bf16 139 us, 5.1 TB/s; with an
+// reductions and a wait, is spread over more than with 8: 384 instructions per eight columns; about 90
+// more with 8), and the warp that is last to finish a row's stage refills it.  8192 x 7168: bf16 139 us, 5.1 TB/s; with an
 // fp32 residual 143 us, 7.4 TB/s.  Measured and left: sums of the next row taken while this row's are
 // exchanged (147 us: one row fewer is loading), scalar fp32 (144 us).
 constexpr int kNbRedFloats = 4 * 32;  // three sums of up to 32 warps each, and a row of zeros

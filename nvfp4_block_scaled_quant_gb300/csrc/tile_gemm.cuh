@@ -41,8 +41,8 @@
 // Every mbarrier wait is bounded: a role that gives up raises NVFP4_DEVERR_PIPELINE_TIMEOUT, the copies in
 // flight are given time to land, and every thread of the pair meets at the final cluster barrier.  The
 // tensor-memory allocation, the cluster and block barriers and the register reallocation have no limit of their own:
-// the allocation waits for no launch but this one (one CTA per SM by its shared memory), every thread reaches every
-// barrier whatever its waits returned, and the register shares add up to the launch's.
+// the allocation waits at most for CTAs of other kernels to leave the SM (its shared memory holds one of these), every
+// thread reaches every barrier whatever its waits returned, and the register shares add up to the launch's.
 #pragma once
 
 #include <atomic>

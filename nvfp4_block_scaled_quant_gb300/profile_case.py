@@ -27,7 +27,7 @@ the activation quantiser over K = 7168 (M = 1024 .. 16384 are the large-GEMM
 sweep's activations); ``linear`` the dense 1536 -> 16384 linear and ``grouped`` the
 fixed-group 8 x (4096 -> 1024) linear at ``--M`` tokens.  ``fp8`` runs the FP8 block-scaled
 linear (7168 -> 2048 of one token, else 7168 -> 7168), ``gated`` the gated linear
-7168 -> 2 x 2048 in bf16 and ``resnorm`` the residual norm over 7168 columns, both with
+7168 -> 2 x 2048 in bf16 (or fp16) and ``resnorm`` the residual norm over 7168 columns, both with
 their gradients above one token.
 """
 
@@ -49,6 +49,7 @@ def main(argv=None):
     p.add_argument("--experts", type=int, default=64)
     p.add_argument("--M", type=int, default=4096)
     p.add_argument("--iters", type=int, default=3)
+    p.add_argument("--fp16", action="store_true", help="gated: fp16 operands instead of bf16")
     a = p.parse_args(argv)
     B.build()
     from . import model, ops, workloads
@@ -129,9 +130,10 @@ def main(argv=None):
             ops.fp8_linear(x, w, ws)
     elif a.case == "gated":
         H, I = 7168, 2048
-        wg, wu = (workloads.weight(I, H, s, dev).bfloat16() for s in (51, 52))
-        x = workloads.activations(a.M, H, seed=61, device=dev)
-        dh = workloads.activations(a.M, I, seed=62, device=dev)
+        kind = torch.float16 if a.fp16 else torch.bfloat16
+        wg, wu = (workloads.weight(I, H, s, dev).to(kind) for s in (51, 52))
+        x = workloads.activations(a.M, H, seed=61, device=dev).to(kind)
+        dh = workloads.activations(a.M, I, seed=62, device=dev).to(kind)
         for _ in range(a.iters):
             if a.M == 1:
                 ops.gated_linear(x, wg, wu)
