@@ -4,6 +4,7 @@
 #include <initializer_list>
 
 #include "abi_util.h"
+#include "dense.h"
 #include "stream_gemm.cuh"
 #include "tile_gemm.cuh"
 

@@ -9,6 +9,7 @@
 // divides in IEEE fp32.  A NaN in a block gives a NaN scale (the maximum is taken over the bits of
 // |x|, where NaN orders above infinity) and an infinity an infinite one: either way every output of
 // that row is NaN, never a finite number made from a dropped NaN.
+#include "dense.h"
 #include "fp8_encode.cuh"
 #include "stream_gemm.cuh"
 #include "tile_gemm.cuh"

@@ -17,6 +17,7 @@
 // exactly.  An element is then off by half a step or by 2^-39 of the largest one; beside largest gradients of
 // 2^16, where the type ends, that is the order of its smallest step, 2^-24.  The maximum takes a pass of its own
 // (517 x 2048: 4 us, 4096 x 2048: 9 us); bf16 has fp32's range and needs none.
+#include "dense.h"
 #include "stream_gemm.cuh"
 #include "tile_gemm.cuh"
 

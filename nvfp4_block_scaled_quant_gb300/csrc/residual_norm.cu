@@ -25,6 +25,7 @@
 // repeated calls give identical bits.
 #include <atomic>
 
+#include "dense.h"
 #include "mma16x8.cuh"
 
 namespace nvfp4 {

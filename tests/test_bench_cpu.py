@@ -16,3 +16,9 @@ def test_comment_and_layout_edits_keep_the_key_code_edits_change_it():
     assert bench.strip_comments(base) == bench.strip_comments(recommented)
     assert bench.strip_comments(base) != bench.strip_comments(changed)
 
+
+
+def test_the_committed_traffic_belongs_to_the_current_kernel():
+    """Only code that the GEMM kernel is made of is in the key: other operators' declarations stay out of its headers."""
+    for kernel in ("w13", "w2"):
+        assert bench.measured_traffic(kernel, "prefill_moe_32x128_H7168_I2048_E384_k8_zipf1.1") > 0
