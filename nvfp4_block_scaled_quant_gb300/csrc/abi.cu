@@ -67,30 +67,34 @@ nvfp4_status device_info(const char *fn, DeviceInfo **out) {
   return NVFP4_OK;
 }
 
-cudaError_t pair_turn_begin(DeviceInfo *d, cudaStream_t s, PairLaunch *now) {
+cudaError_t pair_turn_begin(DeviceInfo *d, cudaStream_t s, PairLaunch *now, PairLaunch **last) {
   cudaStreamCaptureStatus status;
   cudaError_t e = cudaStreamGetCaptureInfo(s, &status, &now->capture);
   if (e != cudaSuccess) return e;
-  const bool capturing = status != cudaStreamCaptureStatusNone;
-  if (capturing) {  // no stream of a capture is destroyed during it (and its id cannot be asked for)
+  PairLaunch *l = &d->pair_last;
+  if (status != cudaStreamCaptureStatusNone) {
+    // no stream of a capture is destroyed during it (and its id cannot be asked for)
     now->stream = reinterpret_cast<uintptr_t>(s);
+    // this capture's entry, or the oldest one's (ids grow)
+    l = d->pair_captured;
+    for (PairLaunch &c : d->pair_captured)
+      if (c.capture == now->capture || (l->capture != now->capture && c.capture < l->capture)) l = &c;
   } else {
     now->capture = 0;
     if ((e = cudaStreamGetId(s, &now->stream)) != cudaSuccess) return e;
   }
-  const PairLaunch &last = d->pair_last[capturing];
-  now->event = last.event;
-  if (!now->event && (e = cudaEventCreateWithFlags(&now->event, cudaEventDisableTiming)) != cudaSuccess) return e;
-  d->pair_last[capturing].event = now->event;
+  if (!l->event && (e = cudaEventCreateWithFlags(&l->event, cudaEventDisableTiming)) != cudaSuccess) return e;
+  now->event = l->event;
+  *last = l;
   // an event of another capture says nothing about this one
-  if (last.made && last.capture == now->capture && last.stream != now->stream) return cudaStreamWaitEvent(s, last.event, 0);
+  if (l->made && l->capture == now->capture && l->stream != now->stream) return cudaStreamWaitEvent(s, l->event, 0);
   return cudaSuccess;
 }
 
-cudaError_t pair_turn_end(DeviceInfo *d, cudaStream_t s, PairLaunch now) {
+cudaError_t pair_turn_end(cudaStream_t s, const PairLaunch &now, PairLaunch *last) {
   const cudaError_t e = cudaEventRecord(now.event, s);
-  now.made = e == cudaSuccess;
-  d->pair_last[now.capture != 0] = now;
+  *last = now;
+  last->made = e == cudaSuccess;
   return e;
 }
 

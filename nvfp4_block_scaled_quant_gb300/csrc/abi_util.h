@@ -38,13 +38,17 @@ struct PairLaunch {
   bool made = false;
 };
 
+// Stream captures that may go on at once on a device with their branches' pair launches in order.
+constexpr int kMaxPairCaptures = 16;
+
 struct DeviceInfo {
   bool ready = false;
   bool supported = false;
   int sms = 0;
   uint32_t *flags = nullptr;
   std::mutex pair_mutex;
-  PairLaunch pair_last[2];  // the last ones outside and inside a stream capture
+  PairLaunch pair_last;                       // the last one outside captures
+  PairLaunch pair_captured[kMaxPairCaptures];  // and of each of the latest captures
 };
 nvfp4_status device_info(const char *fn, DeviceInfo **out);
 
@@ -54,15 +58,15 @@ nvfp4_status device_info(const char *fn, DeviceInfo **out);
 // than the last one's waits for an event behind that one; inside a stream capture the same holds
 // between the branches of the captured graph.  Launches of different graphs, and of a graph and a stream,
 // are not ordered by this: the caller replays them in turn.
-cudaError_t pair_turn_begin(DeviceInfo *d, cudaStream_t s, PairLaunch *now);
-cudaError_t pair_turn_end(DeviceInfo *d, cudaStream_t s, PairLaunch now);
+cudaError_t pair_turn_begin(DeviceInfo *d, cudaStream_t s, PairLaunch *now, PairLaunch **last);
+cudaError_t pair_turn_end(cudaStream_t s, const PairLaunch &now, PairLaunch *last);
 template <class Launch>
 cudaError_t in_pair_turn(DeviceInfo *d, cudaStream_t s, Launch launch) {
   std::lock_guard<std::mutex> lock(d->pair_mutex);  // over the launch: the host's order is the device's
-  PairLaunch now;
-  cudaError_t e = pair_turn_begin(d, s, &now);
+  PairLaunch now, *last;
+  cudaError_t e = pair_turn_begin(d, s, &now, &last);
   if (e == cudaSuccess) e = launch();
-  return e == cudaSuccess ? pair_turn_end(d, s, now) : e;
+  return e == cudaSuccess ? pair_turn_end(s, now, last) : e;
 }
 
 // 2-D byte tensor (rows x row_bytes, row stride ld_bytes) read in boxes of

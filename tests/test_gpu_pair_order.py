@@ -2,10 +2,12 @@
 queued: a short one queued behind a long one on another stream ends after it, and so do the branches
 of a captured graph.  The results are those of the calls by themselves."""
 
+import ctypes
+
 import pytest
 import torch
 
-from nvfp4_block_scaled_quant_gb300 import model, ops
+from nvfp4_block_scaled_quant_gb300 import _lib, model, ops
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -104,3 +106,42 @@ def test_branches_of_a_captured_graph(kind):
     torch.cuda.synchronize()
     assert torch.equal(x, want[0]) and torch.equal(y, want[1]) and torch.equal(eager, want[1])
     assert ops.device_error() == (0, 0)
+
+
+def test_captures_at_the_same_time_keep_their_own_order():
+    """Two captures go on at once; the second branch of the first one still starts behind its first branch's product,
+    whatever the other capture recorded in between."""
+    rt = ctypes.CDLL("libcudart.so." + torch.version.cuda.split(".")[0])
+    M, K, N = 600, 256, 512
+    x, xs = ops.fp8_quantize_act(torch.ones(M, K, dtype=torch.bfloat16, device=DEV))
+    w, ws = ops.fp8_quantize_weight(torch.ones(N, K, dtype=torch.bfloat16, device=DEV))
+    y = [torch.empty(M, N, dtype=torch.bfloat16, device=DEV) for _ in range(3)]
+
+    def product(out, stream):
+        _lib.call("nvfp4_fp8_gemm", x.data_ptr(), xs.data_ptr(), xs.stride(0), M, K, N, w.data_ptr(), ws.data_ptr(), _lib.DT_BF16,
+                  out.data_ptr(), stream.cuda_stream)
+
+    a, branch, b = (torch.cuda.Stream() for _ in range(3))
+    for s in (a, branch, b):
+        product(y[0], s)
+    torch.cuda.synchronize()
+    handles = [ctypes.c_void_p(s.cuda_stream) for s in (a, b)]
+    for h in handles:
+        assert rt.cudaStreamBeginCapture(h, 2) == 0  # relaxed
+    fork, join = torch.cuda.Event(), torch.cuda.Event()
+    fork.record(a)
+    branch.wait_event(fork)
+    product(y[0], a)
+    product(y[1], b)
+    product(y[2], branch)
+    join.record(branch)
+    a.wait_event(join)
+    roots = []
+    for h in handles:
+        graph, n = ctypes.c_void_p(), ctypes.c_size_t()
+        assert rt.cudaStreamEndCapture(h, ctypes.byref(graph)) == 0
+        assert rt.cudaGraphGetRootNodes(graph, None, ctypes.byref(n)) == 0
+        roots.append(n.value)
+        assert rt.cudaGraphDestroy(graph) == 0
+    assert roots == [1, 1]  # the branch's product is no root of its graph
+    torch.cuda.synchronize()
