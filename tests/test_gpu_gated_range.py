@@ -139,6 +139,34 @@ def test_huge_pre_activations(kind, size):
         assert ((y.double() - w).abs() <= (1 + o) * (o + (16 + 2 * I + T) * e) * mag + o * w.abs()).all()
 
 
+@pytest.mark.parametrize("T", [6, 300])
+def test_captured_gradients_follow_the_size_of_the_data(T):
+    """The power of two is chosen on the device: a replay on much larger or smaller gradients gives the bits of a
+    call on them; also on another stream, with a workspace that both calls share."""
+    gen = torch.Generator(device=DEV).manual_seed(T)
+    x, dh = ((torch.randn(T, n, generator=gen, device=DEV) * 2.0 ** -4).half() for n in (136, 72))
+    wg, wu = ((torch.randn(72, 136, generator=gen, device=DEV) * 2.0 ** -6).half() for _ in range(2))
+    _, gu = ops.gated_linear(x, wg, wu, save=True)
+    gu[:, 72:] += 3.0
+    first = dh.clone()
+    graph = torch.cuda.CUDAGraph()
+    ops.gated_linear_backward(dh, x, wg, wu, gu)
+    with torch.cuda.graph(graph):
+        got = ops.gated_linear_backward(dh, x, wg, wu, gu)
+    from nvfp4_block_scaled_quant_gb300 import _lib
+    work = torch.empty(_lib.lib().nvfp4_gated_linear_backward_workspace_bytes_dt(T, 72, _lib.DT_FP16), dtype=torch.uint8, device=DEV)
+    side = torch.cuda.Stream()
+    for power in (0, 16, -8, 3):
+        dh.copy_((first.double() * 2.0 ** power).half())
+        want = ops.gated_linear_backward(dh, x, wg, wu, gu, workspace=work)
+        graph.replay()
+        side.wait_stream(torch.cuda.current_stream())
+        other = ops.gated_linear_backward(dh, x, wg, wu, gu, workspace=work, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        for a, b, c in zip(got, want, other):
+            assert torch.isfinite(b).all() and b.any() and torch.equal(a, b) and torch.equal(c, b)
+
+
 def test_workspace_by_type():
     from nvfp4_block_scaled_quant_gb300 import _lib
     f = _lib.lib().nvfp4_gated_linear_backward_workspace_bytes_dt

@@ -3,6 +3,7 @@ queued: a short one queued behind a long one on another stream ends after it, an
 of a captured graph.  The results are those of the calls by themselves."""
 
 import ctypes
+import threading
 
 import pytest
 import torch
@@ -145,3 +146,25 @@ def test_captures_at_the_same_time_keep_their_own_order():
         assert rt.cudaGraphDestroy(graph) == 0
     assert roots == [1, 1]  # the branch's product is no root of its graph
     torch.cuda.synchronize()
+
+
+def test_calls_from_several_threads():
+    """Threads with a stream of their own: the launches of each are in its stream's order and in turn with the others'."""
+    calls = [fp8(600, 512, 512, 20), gated(300, 256, 264, 21), nvfp4(1024, 256, 512, 22), fp8(40, 512, 512, 23)]
+    want = [c() for c in calls]
+    torch.cuda.synchronize()
+    got = [None] * len(calls)
+
+    def work(i):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            got[i] = [calls[i]() for _ in range(30)]
+            torch.cuda.current_stream().synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(calls))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for outs, w in zip(got, want):
+        assert outs is not None and all(torch.equal(o, w) for o in outs)
+    assert ops.device_error() == (0, 0)
