@@ -63,7 +63,7 @@
 extern "C" {
 #endif
 
-#define NVFP4_ABI_VERSION 8
+#define NVFP4_ABI_VERSION 9
 
 /* Exported symbols: the library builds with hidden visibility by default. */
 #if defined(NVFP4_BUILD) && defined(__GNUC__)
@@ -467,6 +467,18 @@ NVFP4_API nvfp4_status nvfp4_residual_norm(const void *f, int dtype, const void 
                                            const void *gate, int gate_kind, int64_t gate_groups, float scale,
                                            const void *gamma_before, float eps, void *r_out, void *y,
                                            float *stats, void *stream);
+/* The same with y in 8 bits, as nvfp4_fp8_gemm reads it: e4m3 codes q (M, K), contiguous, and xs (ceil(K / 128), lds)
+ * with xs[b * lds + m] = fl32(max |y| / 448) over columns 128 b .. 128 b + 127 of row m and q = e4m3(y / xs) (0 where xs is
+ * 0), from y in fp32: rounded once, so the codes can differ from those of nvfp4_fp8_quantize_act on the
+ * 16-bit y, which is rounded twice.  The quotient is within two steps of fp32.  A block that holds a NaN or an infinity
+ * has such a scale.  y, if not NULL, also receives the 16-bit output; r_out, y and stats are those of nvfp4_residual_norm
+ * bit for bit (the backward of y is nvfp4_residual_norm_backward's; the rounding to 8 bits has no gradient of its own).
+ * gamma_before is required; K % 16 == 0; lds >= M, a multiple of 4 (entries m >= M are not written). */
+NVFP4_API nvfp4_status nvfp4_residual_norm_fp8(const void *f, int dtype, const void *r, int r_dtype, int64_t M,
+                                               int64_t K, int64_t ldf, int64_t ldr, const void *gamma_after,
+                                               const void *gate, int gate_kind, int64_t gate_groups, float scale,
+                                               const void *gamma_before, float eps, void *r_out, uint8_t *q, float *xs,
+                                               int64_t lds, void *y, float *stats, void *stream);
 /* Gradients, from the gradients dr_out of r_out (r_dtype, row stride lddr) and dy of y (dtype, row
  * stride lddy); either may be NULL (zero).  f, r, the parameters and stats are the forward's.
  * df (M, K) in dtype, dr (M, K) in r_dtype, contiguous; dgamma_after (K), dgamma_before (K) and
@@ -482,6 +494,45 @@ NVFP4_API nvfp4_status nvfp4_residual_norm_backward(const void *dr_out, int64_t 
                                                     const void *gamma_before, void *df, void *dr,
                                                     float *dgamma_after, float *dgate, float *dgamma_before,
                                                     void *ws, size_t ws_bytes, void *stream);
+
+/* ============================================================================
+ * 4-bit integer weights with group scales, and 16-bit activations: for inference.  A checkpoint stores, for each row
+ * of a matrix (N, K), codes c of 4 bits (two per byte, element 2 j in the low half; K / 2 bytes), and for each `group` (32,
+ * 64 or 128) consecutive K elements, the last group of a row may be partial, a scale s in `dtype` and, optionally, a
+ * zero point z (one byte, of which the low four bits count; 8 without zero points).  A weight is (c - z) s.
+ * The conventions of the dense operators hold; x (rows, K) has a row stride ldx (a multiple of 8) and is bf16 or fp16
+ * (`dtype`), the scales' type; K % 8 == 0.  Weights are never rounded: products with c - z are exact, a group's sum is fp32 and
+ * multiplied by its scale in fp32.  A row of x that holds a NaN or an infinity has outputs that are not finite.
+ * ============================================================================ */
+
+/* Lays out G matrices for the products below, once, at load time: codes (G, N, K / 2), scales and zeros (G, N,
+ * ceil(K / group)), contiguous; out nvfp4_w4_prepared_bytes(G, N, K, group, zeros != NULL, gated) bytes (0: sizes that are not
+ * supported).  `gated`: rows [0, N / 2) are a gate projection and [N / 2, N) the up projection of the same outputs (the layout
+ * that the mixture-of-experts layer wants of w13), N even.  dtype: the scales' type, which the products must be given too. */
+NVFP4_API size_t nvfp4_w4_prepared_bytes(int64_t G, int64_t N, int64_t K, int group, int has_zeros, int gated);
+NVFP4_API nvfp4_status nvfp4_w4_prepare(const uint8_t *codes, const void *scales, const uint8_t *zeros, int dtype,
+                                        int64_t G, int64_t N, int64_t K, int group, int gated, uint8_t *out,
+                                        void *stream);
+
+/* y (M, N) = x (M, K) W^T, contiguous in `dtype`, W prepared without `gated`; any N, any M.  The weights are read one
+ * launch early, like those of nvfp4_linear. */
+NVFP4_API nvfp4_status nvfp4_w4_linear(const void *x, int dtype, int64_t M, int64_t K, int64_t ldx, int64_t N,
+                                       const uint8_t *w, int group, int has_zeros, void *y, void *stream);
+
+/* A whole mixture-of-experts layer for a few tokens, in two launches: for every token t
+ *   l = x[t] router^T (fp32), ids = the topk largest of l (the lowest expert first among equals),
+ *   p = softmax of l over the chosen ones (the softmax over all experts, renormalised),
+ *   y[t] = sum_j p_j E_{ids_j}(x[t]) + E_shared(x[t]),  E(x) = W2 h,  h = act(Wg x) * (Wu x) rounded to `dtype`
+ * with fp32 sums; h is the operand of a 16-bit product, as in a layer that stores it.  x (T, H) with row stride ldx;
+ * router (E, H) in `dtype`, contiguous; w13 (E, 2 I, H) prepared with `gated`, w2 (E, H, I) without; sh_w13 and sh_w2 the same for one
+ * expert, both NULL without a shared expert; y (T, H) contiguous; act NVFP4_ACT_*.  Sums have a fixed order: repeated calls give
+ * identical bits.  T <= 64, topk <= 16, topk <= E <= 1024, T topk <= 512; H and I multiples of 8, at most
+ * 16384.  Tokens of one expert share a pass over its weights eight at a time. */
+NVFP4_API size_t nvfp4_w4_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int topk, int has_shared);
+NVFP4_API nvfp4_status nvfp4_w4_moe(const void *x, int dtype, int64_t T, int64_t H, int64_t ldx, int64_t I, int64_t E,
+                                    int topk, const void *router, const uint8_t *w13, const uint8_t *w2,
+                                    const uint8_t *sh_w13, const uint8_t *sh_w2, int group, int has_zeros, int act,
+                                    void *y, void *ws, size_t ws_bytes, void *stream);
 
 /* ------------------------------------------------------------ diagnostics
  * Runs one CTA that waits on a shared-memory barrier nothing arrives at, with

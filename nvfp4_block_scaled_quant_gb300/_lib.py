@@ -46,7 +46,7 @@ GATE_CHANNEL = 1
 GATE_ROW = 2
 
 
-ABI_VERSION = 8  # NVFP4_ABI_VERSION of the header these signatures follow
+ABI_VERSION = 9  # NVFP4_ABI_VERSION of the header these signatures follow
 
 
 class MoeWsLayout(Structure):
@@ -104,6 +104,14 @@ _SIGNATURES = {
     "nvfp4_residual_norm_backward_workspace_bytes": (c_size_t, [I64, I64, I64, c_int]),
     "nvfp4_residual_norm_backward": (c_int, [P, I64, P, I64, P, c_int, P, c_int, I64, I64, I64, I64, P, P, P, c_int,
                                              I64, c_float, P, P, P, P, P, P, P, c_size_t, P]),
+    "nvfp4_residual_norm_fp8": (c_int, [P, c_int, P, c_int, I64, I64, I64, I64, P, P, c_int, I64, c_float, P, c_float, P,
+                                        P, P, I64, P, P, P]),
+    "nvfp4_w4_prepared_bytes": (c_size_t, [I64, I64, I64, c_int, c_int, c_int]),
+    "nvfp4_w4_prepare": (c_int, [P, P, P, c_int, I64, I64, I64, c_int, c_int, P, P]),
+    "nvfp4_w4_linear": (c_int, [P, c_int, I64, I64, I64, I64, P, c_int, c_int, P, P]),
+    "nvfp4_w4_moe_workspace_bytes": (c_size_t, [I64, I64, I64, I64, c_int, c_int]),
+    "nvfp4_w4_moe": (c_int, [P, c_int, I64, I64, I64, I64, I64, c_int, P, P, P, P, P, c_int, c_int, c_int, P, P, c_size_t,
+                             P]),
     "nvfp4_debug_wait_timeout": (c_int, [c_uint32, P]),
 }
 

@@ -11,43 +11,6 @@
 namespace nvfp4 {
 namespace {
 
-constexpr int64_t kMaxDim = int64_t(1) << 24;
-constexpr int64_t kMaxArea = int64_t(1) << 40;
-
-bool dtype16(int d) { return d == NVFP4_DT_BF16 || d == NVFP4_DT_FP16; }
-bool dims_ok(int64_t a, int64_t b) { return a < kMaxDim && b < kMaxDim && a * b < kMaxArea; }
-
-#define NV_DIMS(a, b)                                                                                \
-  NV_REQUIRE(dims_ok(a, b), NVFP4_ERR_UNSUPPORTED_SHAPE, "sizes too large: %lld x %lld", (long long)(a), \
-             (long long)(b))
-
-// `rows` rows of `cols` elements of `bytes` bytes, `ld` elements apart, taken as the whole range from the first
-// element to the last.
-struct Span {
-  const void *p;
-  int64_t rows, ld, cols, bytes;
-};
-bool overlap(const Span &a, const Span &b) {
-  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.cols <= 0 || b.cols <= 0) return false;
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-  const uintptr_t a1 = a0 + static_cast<uintptr_t>(((a.rows - 1) * a.ld + a.cols) * a.bytes);
-  const uintptr_t b1 = b0 + static_cast<uintptr_t>(((b.rows - 1) * b.ld + b.cols) * b.bytes);
-  return a0 < b1 && b0 < a1;
-}
-Span flat(const void *p, int64_t n, int64_t bytes) { return {p, 1, n, n, bytes}; }
-
-// Refuses what is written (outputs, the workspace) inside what is read, which other blocks may still be
-// reading, and inside what else is written.
-nvfp4_status check_disjoint(const char *fn, std::initializer_list<Span> written, std::initializer_list<Span> read) {
-  for (auto w = written.begin(); w != written.end(); ++w) {
-    for (const Span &r : read)
-      if (overlap(*w, r)) return fail(NVFP4_ERR_INVALID_ARG, fn, "an output or the workspace overlaps an input");
-    for (auto o = written.begin(); o != w; ++o)
-      if (overlap(*w, *o)) return fail(NVFP4_ERR_INVALID_ARG, fn, "outputs and workspace overlap one another");
-  }
-  return NVFP4_OK;
-}
-
 // Estimated times (in units of 10 ns) that choose between the GEMMs.  The coefficients were fitted to
 // times on a GB300 over M = 16 .. 2048 and five (K, N) between 512 x 512 and 7168 x 7168; they rank
 // the choices, nothing else depends on them.
@@ -516,30 +479,30 @@ static nvfp4_status check_norm(const char *fn, const void *f, int dtype, const v
   return NVFP4_OK;
 }
 
-nvfp4_status nvfp4_residual_norm(const void *f, int dtype, const void *r, int r_dtype, int64_t M, int64_t K,
-                                 int64_t ldf, int64_t ldr, const void *gamma_after, const void *gate, int gate_kind,
-                                 int64_t gate_groups, float scale, const void *gamma_before, float eps, void *r_out,
-                                 void *y, float *stats, void *stream) {
-  nvfp4_status st = check_norm(__func__, f, dtype, r, r_dtype, M, K, ldf, ldr, gamma_after, gate, gate_kind,
-                               gate_groups, scale, gamma_before);
+// The norm with a 16-bit output (y), an 8-bit one (q, xs) or both.
+static nvfp4_status norm_call(const char *fn, const void *f, int dtype, const void *r, int r_dtype, int64_t M, int64_t K,
+                              int64_t ldf, int64_t ldr, const void *gamma_after, const void *gate, int gate_kind,
+                              int64_t gate_groups, float scale, const void *gamma_before, float eps, void *r_out, void *y,
+                              float *stats, uint8_t *q, float *xs, int64_t lds, void *stream) {
+  nvfp4_status st = check_norm(fn, f, dtype, r, r_dtype, M, K, ldf, ldr, gamma_after, gate, gate_kind, gate_groups, scale,
+                               gamma_before);
   if (st != NVFP4_OK) return st;
-  NV_REQUIRE(eps >= 0.f && eps < 1e30f, NVFP4_ERR_INVALID_ARG, "eps must be finite and >= 0");
-  NV_REQUIRE(r_out || M == 0, NVFP4_ERR_INVALID_ARG, "r_out is NULL");
-  NV_REQUIRE(M == 0 || (y != nullptr) == (gamma_before != nullptr), NVFP4_ERR_INVALID_ARG,
-             "y and gamma_before come together");
-  NV_REQUIRE(r_out != r || ldr == K, NVFP4_ERR_MISALIGNED, "in place, r must be contiguous");
-  NV_REQUIRE(r_out != r || !stats || M == 0, NVFP4_ERR_INVALID_ARG,
-             "stats in place: the backward needs the r that r_out would overwrite");
-  NV_REQUIRE(aligned(r_out, 16) && aligned(y, 16) && aligned(stats, 8), NVFP4_ERR_MISALIGNED,
-             "r_out and y must be 16-byte aligned");
+  if (!(eps >= 0.f && eps < 1e30f)) return fail(NVFP4_ERR_INVALID_ARG, fn, "eps must be finite and >= 0");
+  if (!r_out && M > 0) return fail(NVFP4_ERR_INVALID_ARG, fn, "r_out is NULL");
+  if (r_out == r && ldr != K) return fail(NVFP4_ERR_MISALIGNED, fn, "in place, r must be contiguous");
+  if (r_out == r && stats && M > 0)
+    return fail(NVFP4_ERR_INVALID_ARG, fn, "stats in place: the backward needs the r that r_out would overwrite");
+  if (!aligned(r_out, 16) || !aligned(y, 16) || !aligned(stats, 8))
+    return fail(NVFP4_ERR_MISALIGNED, fn, "r_out and y must be 16-byte aligned");
   const int64_t r_bytes = r_dtype == NVFP4_DT_FP32 ? 4 : 2;
   const int64_t gate_size = gate_kind == NVFP4_GATE_ROW ? M : gate_kind == NVFP4_GATE_CHANNEL ? gate_groups * K : 0;
-  st = check_disjoint(__func__, {flat(r_out, M * K, r_bytes), flat(y, M * K, 2), flat(stats, 2 * M, 4)},
+  st = check_disjoint(fn, {flat(r_out, M * K, r_bytes), flat(y, M * K, 2), flat(stats, 2 * M, 4), flat(q, M * K, 1),
+                           {xs, (K + 127) / 128, lds, M, 4}},
                       {{f, M, ldf, K, 2}, {r == r_out ? nullptr : r, M, ldr, K, r_bytes}, flat(gamma_after, K, 2),
                        flat(gamma_before, K, 2), flat(gate, gate_size, 2)});
   if (st != NVFP4_OK) return st;
   DeviceInfo *d;
-  if ((st = device_info(__func__, &d)) != NVFP4_OK) return st;
+  if ((st = device_info(fn, &d)) != NVFP4_OK) return st;
   if (M == 0) return NVFP4_OK;
   NormArgs a = {};
   a.f = f;
@@ -557,12 +520,37 @@ nvfp4_status nvfp4_residual_norm(const void *f, int dtype, const void *r, int r_
   a.r_out = r_out;
   a.y = y;
   a.stats = stats;
+  a.q = q;
+  a.s = xs;
+  a.lds = lds;
   a.M = M;
   a.K = static_cast<int>(K);
   a.err = d->flags;
-  NV_CUDA(launch_residual_norm(a, dtype, r_dtype == NVFP4_DT_FP32, d->sms, static_cast<cudaStream_t>(stream)),
-          "residual norm launch");
-  return NVFP4_OK;
+  const cudaError_t e = launch_residual_norm(a, dtype, r_dtype == NVFP4_DT_FP32, d->sms, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? NVFP4_OK : cuda_fail(fn, e, "residual norm launch");
+}
+
+nvfp4_status nvfp4_residual_norm(const void *f, int dtype, const void *r, int r_dtype, int64_t M, int64_t K,
+                                 int64_t ldf, int64_t ldr, const void *gamma_after, const void *gate, int gate_kind,
+                                 int64_t gate_groups, float scale, const void *gamma_before, float eps, void *r_out,
+                                 void *y, float *stats, void *stream) {
+  NV_REQUIRE(M <= 0 || (y != nullptr) == (gamma_before != nullptr), NVFP4_ERR_INVALID_ARG, "y and gamma_before come together");
+  return norm_call(__func__, f, dtype, r, r_dtype, M, K, ldf, ldr, gamma_after, gate, gate_kind, gate_groups, scale,
+                   gamma_before, eps, r_out, y, stats, nullptr, nullptr, 0, stream);
+}
+
+nvfp4_status nvfp4_residual_norm_fp8(const void *f, int dtype, const void *r, int r_dtype, int64_t M, int64_t K,
+                                     int64_t ldf, int64_t ldr, const void *gamma_after, const void *gate, int gate_kind,
+                                     int64_t gate_groups, float scale, const void *gamma_before, float eps, void *r_out,
+                                     uint8_t *q, float *xs, int64_t lds, void *y, float *stats, void *stream) {
+  NV_REQUIRE(gamma_before, NVFP4_ERR_INVALID_ARG, "gamma_before is NULL");
+  NV_REQUIRE((q && xs) || M == 0, NVFP4_ERR_INVALID_ARG, "NULL pointer argument");
+  NV_REQUIRE(K % 16 == 0, NVFP4_ERR_UNSUPPORTED_SHAPE, "K=%lld must be a multiple of 16", (long long)K);
+  NV_REQUIRE(lds >= M && lds % 4 == 0 && lds < kMaxDim * 16, NVFP4_ERR_MISALIGNED,
+             "lds=%lld must be >= M and a multiple of 4", (long long)lds);
+  NV_REQUIRE(aligned(q, 16) && aligned(xs, 16), NVFP4_ERR_MISALIGNED, "q and xs must be 16-byte aligned");
+  return norm_call(__func__, f, dtype, r, r_dtype, M, K, ldf, ldr, gamma_after, gate, gate_kind, gate_groups, scale,
+                   gamma_before, eps, r_out, y, stats, q, xs, lds, stream);
 }
 
 size_t nvfp4_residual_norm_backward_workspace_bytes(int64_t M, int64_t K, int64_t gate_groups, int r_dtype) {

@@ -7,6 +7,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <initializer_list>
 #include <mutex>
 
 #include "internal.h"
@@ -76,5 +77,44 @@ nvfp4_status make_map(const char *fn, CUtensorMap *m, const void *base, int64_t 
                       CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_128B);
 
 nvfp4_status check_ws(const char *fn, const void *ws, size_t ws_bytes, size_t need);
+
+// ---------------------------------------------------------------- checks of the operators around the experts
+
+constexpr int64_t kMaxDim = int64_t(1) << 24;
+constexpr int64_t kMaxArea = int64_t(1) << 40;
+
+inline bool dtype16(int d) { return d == NVFP4_DT_BF16 || d == NVFP4_DT_FP16; }
+inline bool dims_ok(int64_t a, int64_t b) { return a < kMaxDim && b < kMaxDim && a * b < kMaxArea; }
+
+#define NV_DIMS(a, b)                                                                                \
+  NV_REQUIRE(dims_ok(a, b), NVFP4_ERR_UNSUPPORTED_SHAPE, "sizes too large: %lld x %lld", (long long)(a), \
+             (long long)(b))
+
+// `rows` rows of `cols` elements of `bytes` bytes, `ld` elements apart, taken as the whole range from the first
+// element to the last.
+struct Span {
+  const void *p;
+  int64_t rows, ld, cols, bytes;
+};
+inline bool overlap(const Span &a, const Span &b) {
+  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0 || a.cols <= 0 || b.cols <= 0) return false;
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
+  const uintptr_t a1 = a0 + static_cast<uintptr_t>(((a.rows - 1) * a.ld + a.cols) * a.bytes);
+  const uintptr_t b1 = b0 + static_cast<uintptr_t>(((b.rows - 1) * b.ld + b.cols) * b.bytes);
+  return a0 < b1 && b0 < a1;
+}
+inline Span flat(const void *p, int64_t n, int64_t bytes) { return {p, 1, n, n, bytes}; }
+
+// Refuses what is written (outputs, the workspace) inside what is read, which other blocks may still be
+// reading, and inside what else is written.
+inline nvfp4_status check_disjoint(const char *fn, std::initializer_list<Span> written, std::initializer_list<Span> read) {
+  for (auto w = written.begin(); w != written.end(); ++w) {
+    for (const Span &r : read)
+      if (overlap(*w, r)) return fail(NVFP4_ERR_INVALID_ARG, fn, "an output or the workspace overlaps an input");
+    for (auto o = written.begin(); o != w; ++o)
+      if (overlap(*w, *o)) return fail(NVFP4_ERR_INVALID_ARG, fn, "outputs and workspace overlap one another");
+  }
+  return NVFP4_OK;
+}
 
 }  // namespace nvfp4

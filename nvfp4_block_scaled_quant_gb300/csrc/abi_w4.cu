@@ -1,0 +1,195 @@
+// Host side of the C ABI of the operators on 4-bit weights with group scales: argument validation, workspace layout and
+// how a product spreads over the GPU.
+#include "abi_util.h"
+#include "w4.h"
+
+namespace nvfp4 {
+namespace {
+
+nvfp4_status check_w4(const char *fn, int dtype, int64_t K, int group) {
+  if (!dtype16(dtype)) return fail(NVFP4_ERR_INVALID_ARG, fn, "dtype %d is neither bf16 nor fp16", dtype);
+  if (group != 32 && group != 64 && group != 128) return fail(NVFP4_ERR_INVALID_ARG, fn, "group size %d, expected 32, 64 or 128", group);
+  if (K % 8) return fail(NVFP4_ERR_UNSUPPORTED_SHAPE, fn, "K=%lld must be a multiple of 8", (long long)K);
+  return NVFP4_OK;
+}
+
+// Bytes of G prepared matrices (N, K); 0 where the sizes are not supported.
+int64_t prepared_bytes(int64_t G, int64_t N, int64_t K, int group, bool zeros, bool gated) {
+  return G * w4_panels(N, gated) * w4_blocks(K) * w4_block_bytes(kW4BlockK / group, zeros);
+}
+
+nvfp4_status check_rows(const char *fn, const void *x, int64_t M, int64_t K, int64_t ldx) {
+  if (!x && M > 0) return fail(NVFP4_ERR_INVALID_ARG, fn, "x is NULL");
+  if (ldx < K || ldx % 8 || ldx >= kMaxDim * 16)
+    return fail(NVFP4_ERR_MISALIGNED, fn, "row stride %lld must be >= %lld and a multiple of 8", (long long)ldx, (long long)K);
+  if (!aligned(x, 16)) return fail(NVFP4_ERR_MISALIGNED, fn, "x must be 16-byte aligned");
+  return NVFP4_OK;
+}
+
+// Clusters along K for `ctas` CTAs per split: waves of two CTAs per SM, each as long as a warp's K blocks and a fixed part
+// (start, sums over the cluster) of about two.
+int stream_splits(int64_t ctas, int blocks, int sms) {
+  int best = 1;
+  int64_t best_time = 0;
+  for (int s = 1; s <= 8 && s <= blocks; ++s) {
+    const int64_t waves = (ctas * s + 2 * sms - 1) / (2 * sms), rank = (blocks + s - 1) / s;
+    const int64_t time = waves * ((rank + 7) / 8 + 2);
+    if (best_time == 0 || time < best_time) best_time = time, best = s;
+  }
+  return best;
+}
+
+struct MoeWs {
+  size_t logits, h, part, counters, total;
+};
+bool moe_sizes_ok(int64_t T, int64_t H, int64_t I, int64_t E, int topk) {
+  return T >= 0 && T <= kW4MoeMaxT && H > 0 && I > 0 && H % 8 == 0 && I % 8 == 0 && H <= kW4MoeMaxDim && I <= kW4MoeMaxDim && E > 0 &&
+         E <= kW4MoeMaxExperts && topk > 0 && topk <= kW4MoeMaxK && topk <= E && T * topk <= kW4MoeMaxEntries;
+}
+MoeWs moe_ws(int64_t T, int64_t H, int64_t I, int64_t E, int topk, bool shared) {
+  MoeWs w;
+  const size_t rows = static_cast<size_t>(T * (topk + (shared ? 1 : 0)));
+  w.logits = 0;
+  w.h = align256(static_cast<size_t>(T * E) * 4);
+  w.part = align256(w.h + rows * static_cast<size_t>(I) * 2);
+  w.counters = align256(w.part + rows * static_cast<size_t>(H) * 4);
+  w.total = align256(w.counters + (kW4MoeCounters + kW4MoeMaxSlots + static_cast<size_t>((H + kW4PanelRows - 1) / kW4PanelRows)) * 4);
+  return w;
+}
+
+}  // namespace
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+extern "C" {
+
+size_t nvfp4_w4_prepared_bytes(int64_t G, int64_t N, int64_t K, int group, int has_zeros, int gated) {
+  if (G <= 0 || N <= 0 || K <= 0 || K % 8 || G >= kMaxDim || !dims_ok(N, K) || (gated && N % 2) ||
+      (group != 32 && group != 64 && group != 128) || G * w4_panels(N, gated != 0) * w4_blocks(K) > INT32_MAX)
+    return 0;
+  return static_cast<size_t>(prepared_bytes(G, N, K, group, has_zeros != 0, gated != 0));
+}
+
+nvfp4_status nvfp4_w4_prepare(const uint8_t *codes, const void *scales, const uint8_t *zeros, int dtype, int64_t G,
+                              int64_t N, int64_t K, int group, int gated, uint8_t *out, void *stream) {
+  NV_REQUIRE(G > 0 && N > 0 && K > 0, NVFP4_ERR_INVALID_ARG, "G=%lld N=%lld K=%lld", (long long)G, (long long)N, (long long)K);
+  nvfp4_status st = check_w4(__func__, dtype, K, group);
+  if (st != NVFP4_OK) return st;
+  NV_REQUIRE(!gated || N % 2 == 0, NVFP4_ERR_UNSUPPORTED_SHAPE, "N=%lld rows do not split into gate and up", (long long)N);
+  NV_REQUIRE(codes && scales && out, NVFP4_ERR_INVALID_ARG, "NULL pointer argument");
+  const size_t bytes = nvfp4_w4_prepared_bytes(G, N, K, group, zeros != nullptr, gated);
+  NV_REQUIRE(bytes > 0, NVFP4_ERR_UNSUPPORTED_SHAPE, "sizes too large: %lld x %lld x %lld", (long long)G, (long long)N, (long long)K);
+  NV_REQUIRE(aligned(codes, 4) && aligned(scales, 2) && aligned(out, 16), NVFP4_ERR_MISALIGNED,
+             "codes must be 4-byte and out 16-byte aligned");
+  const int64_t n_groups = (K + group - 1) / group;
+  st = check_disjoint(__func__, {flat(out, static_cast<int64_t>(bytes), 1)},
+                      {flat(codes, G * N * (K / 2), 1), flat(scales, G * N * n_groups, 2), flat(zeros, G * N * n_groups, 1)});
+  if (st != NVFP4_OK) return st;
+  DeviceInfo *d;
+  if ((st = device_info(__func__, &d)) != NVFP4_OK) return st;
+  NV_CUDA(launch_w4_prepare(codes, static_cast<const uint16_t *>(scales), zeros, dtype, G, N, K, group, gated != 0, out,
+                            static_cast<cudaStream_t>(stream)),
+          "4-bit weight preparation launch");
+  return NVFP4_OK;
+}
+
+nvfp4_status nvfp4_w4_linear(const void *x, int dtype, int64_t M, int64_t K, int64_t ldx, int64_t N, const uint8_t *w,
+                             int group, int has_zeros, void *y, void *stream) {
+  NV_REQUIRE(M >= 0 && K > 0 && N > 0, NVFP4_ERR_INVALID_ARG, "M=%lld K=%lld N=%lld", (long long)M, (long long)K, (long long)N);
+  nvfp4_status st = check_w4(__func__, dtype, K, group);
+  if (st != NVFP4_OK) return st;
+  NV_REQUIRE(dims_ok(M, K) && dims_ok(N, K) && dims_ok(M, N) && w4_panels(N, false) * w4_blocks(K) <= INT32_MAX,
+             NVFP4_ERR_UNSUPPORTED_SHAPE, "sizes too large: M=%lld K=%lld N=%lld", (long long)M, (long long)K, (long long)N);
+  NV_REQUIRE(w && (y || M == 0), NVFP4_ERR_INVALID_ARG, "NULL pointer argument");
+  if ((st = check_rows(__func__, x, M, K, ldx)) != NVFP4_OK) return st;
+  NV_REQUIRE(aligned(w, 16) && aligned(y, 16), NVFP4_ERR_MISALIGNED, "w and y must be 16-byte aligned");
+  const bool zeros = has_zeros != 0;
+  st = check_disjoint(__func__, {{y, M, N, N, 2}}, {{x, M, ldx, K, 2}, flat(w, prepared_bytes(1, N, K, group, zeros, false), 1)});
+  if (st != NVFP4_OK) return st;
+  DeviceInfo *d;
+  if ((st = device_info(__func__, &d)) != NVFP4_OK) return st;
+  if (M == 0) return NVFP4_OK;
+  W4Args a = {};
+  a.x = x;
+  a.ldx = ldx;
+  a.M = static_cast<int>(M);
+  a.N = static_cast<int>(N);
+  a.K = static_cast<int>(K);
+  a.w = w;
+  a.y = y;
+  a.err = d->flags;
+  const int tok8 = M <= 8 ? 1 : 2, blocks = static_cast<int>(w4_blocks(K));
+  const int splits = stream_splits(w4_panels(N, false) * ((M + 8 * tok8 - 1) / (8 * tok8)), blocks, d->sms);
+  const int rank = (blocks + splits - 1) / splits;
+  int depth = (rank + 7) / 8;
+  const int fit = (233472 / 2 - 2048) / (8 * w4_block_bytes(kW4BlockK / group, zeros));
+  if (depth > fit) depth = fit;
+  if (depth > 4) depth = 4;
+  if (depth < tok8) depth = tok8;  // the ring holds a warp's sums at the end
+  NV_CUDA(launch_w4_stream(a, dtype, group, zeros, tok8, splits, depth, static_cast<cudaStream_t>(stream)),
+          "4-bit linear launch");
+  return NVFP4_OK;
+}
+
+size_t nvfp4_w4_moe_workspace_bytes(int64_t T, int64_t H, int64_t I, int64_t E, int topk, int has_shared) {
+  return moe_sizes_ok(T, H, I, E, topk) ? moe_ws(T, H, I, E, topk, has_shared != 0).total : 0;
+}
+
+nvfp4_status nvfp4_w4_moe(const void *x, int dtype, int64_t T, int64_t H, int64_t ldx, int64_t I, int64_t E, int topk,
+                          const void *router, const uint8_t *w13, const uint8_t *w2, const uint8_t *sh_w13,
+                          const uint8_t *sh_w2, int group, int has_zeros, int act, void *y, void *ws, size_t ws_bytes,
+                          void *stream) {
+  NV_REQUIRE(T >= 0 && H > 0 && I > 0 && E > 0 && topk > 0, NVFP4_ERR_INVALID_ARG, "T=%lld H=%lld I=%lld E=%lld topk=%d",
+             (long long)T, (long long)H, (long long)I, (long long)E, topk);
+  nvfp4_status st = check_w4(__func__, dtype, H, group);
+  if (st != NVFP4_OK) return st;
+  NV_REQUIRE(act == NVFP4_ACT_SILU || act == NVFP4_ACT_GELU || act == NVFP4_ACT_GELU_TANH, NVFP4_ERR_INVALID_ARG, "activation %d", act);
+  NV_REQUIRE(moe_sizes_ok(T, H, I, E, topk), NVFP4_ERR_UNSUPPORTED_SHAPE,
+             "T=%lld (at most %d, T topk at most %d), H=%lld and I=%lld (multiples of 8, at most %lld), E=%lld (at most %lld), "
+             "topk=%d (at most %d and E)",
+             (long long)T, kW4MoeMaxT, kW4MoeMaxEntries, (long long)H, (long long)I, (long long)kW4MoeMaxDim, (long long)E,
+             (long long)kW4MoeMaxExperts, topk, kW4MoeMaxK);
+  NV_REQUIRE(router && w13 && w2 && (y || T == 0), NVFP4_ERR_INVALID_ARG, "NULL pointer argument");
+  NV_REQUIRE((sh_w13 == nullptr) == (sh_w2 == nullptr), NVFP4_ERR_INVALID_ARG, "the shared expert's weights come together");
+  if ((st = check_rows(__func__, x, T, H, ldx)) != NVFP4_OK) return st;
+  NV_REQUIRE(aligned(router, 16) && aligned(w13, 16) && aligned(w2, 16) && aligned(sh_w13, 16) && aligned(sh_w2, 16) && aligned(y, 16),
+             NVFP4_ERR_MISALIGNED, "router, weights and y must be 16-byte aligned");
+  const bool zeros = has_zeros != 0, shared = sh_w13 != nullptr;
+  const MoeWs L = moe_ws(T, H, I, E, topk, shared);
+  if ((st = check_ws(__func__, ws, ws_bytes, L.total)) != NVFP4_OK) return st;
+  st = check_disjoint(__func__, {flat(y, T * H, 2), flat(ws, static_cast<int64_t>(L.total), 1)},
+                      {{x, T, ldx, H, 2}, flat(router, E * H, 2), flat(w13, prepared_bytes(E, 2 * I, H, group, zeros, true), 1),
+                       flat(w2, prepared_bytes(E, H, I, group, zeros, false), 1),
+                       flat(sh_w13, prepared_bytes(1, 2 * I, H, group, zeros, true), 1),
+                       flat(sh_w2, prepared_bytes(1, H, I, group, zeros, false), 1)});
+  if (st != NVFP4_OK) return st;
+  DeviceInfo *d;
+  if ((st = device_info(__func__, &d)) != NVFP4_OK) return st;
+  if (T == 0) return NVFP4_OK;
+  uint8_t *p = static_cast<uint8_t *>(ws);
+  W4MoeArgs a = {};
+  a.x = x;
+  a.ldx = ldx;
+  a.T = static_cast<int>(T);
+  a.H = static_cast<int>(H);
+  a.I = static_cast<int>(I);
+  a.E = static_cast<int>(E);
+  a.topk = topk;
+  a.router = router;
+  a.w13 = w13;
+  a.w2 = w2;
+  a.sh13 = sh_w13;
+  a.sh2 = sh_w2;
+  a.act = act;
+  a.y = y;
+  a.logits = reinterpret_cast<float *>(p + L.logits);
+  a.h = reinterpret_cast<uint16_t *>(p + L.h);
+  a.part = reinterpret_cast<float *>(p + L.part);
+  a.counters = reinterpret_cast<int *>(p + L.counters);
+  a.err = d->flags;
+  NV_CUDA(launch_w4_moe(a, dtype, group, zeros, d->sms, static_cast<cudaStream_t>(stream)), "4-bit mixture-of-experts launch");
+  return NVFP4_OK;
+}
+
+}  // extern "C"

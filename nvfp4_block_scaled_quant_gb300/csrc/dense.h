@@ -44,6 +44,9 @@ struct NormArgs {
   float scale, eps;
   void *r_out, *y;            // y (M, K) contiguous
   float *stats;               // (M, 2) rstd(f), rstd(r'), or null
+  uint8_t *q;                 // 8-bit output: e4m3 codes (M, K) of y and (K / 128, lds) scales; y may then be null
+  float *s;
+  int64_t lds;
   int64_t M;
   int K;
   uint32_t *err;
@@ -82,7 +85,7 @@ constexpr int kNormMaxSmem = 225 * 1024;
 constexpr int kNormGradRows = 4;     // rows of a backward CTA aimed at when there are few
 constexpr int kNormSms = 152;        // the plan must not depend on the device: it sizes the workspace
 NormGradPlan norm_grad_plan(int64_t M, int64_t K, int64_t groups, bool r32);
-cudaError_t launch_residual_norm(const NormArgs &a, int dtype, bool r32, int sms, cudaStream_t s);
+cudaError_t launch_residual_norm(const NormArgs &a, int dtype, bool r32, int sms, cudaStream_t s);  // with a.q: the 8-bit output too
 cudaError_t launch_residual_norm_backward(const NormGradArgs &a, const NormGradPlan &p, int dtype, bool r32,
                                           cudaStream_t s);
 

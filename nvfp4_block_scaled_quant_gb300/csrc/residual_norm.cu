@@ -26,7 +26,7 @@
 #include <atomic>
 
 #include "dense.h"
-#include "mma16x8.cuh"
+#include "fp8_encode.cuh"
 
 namespace nvfp4 {
 
@@ -172,11 +172,50 @@ __device__ __forceinline__ float row_rstd(float part, float *red, int K, float e
   return __fdiv_rn(1.f, __fsqrt_rn(mean + eps));
 }
 
+// ---------------------------------------------------------------- 8-bit output
+
+// Eight columns of y in e4m3: the scale is max|y| / 448 over the 128 columns that 16 consecutive lanes hold, from y before
+// its rounding to 16 bits (rounded once, from fp32, the codes are the nearest ones; a quantiser behind the 16-bit output
+// rounds twice).  Lanes without columns pass zeros.  The quotient's error of two steps of fp32 only decides
+// between codes at a midpoint.  NaN orders above infinity in the maximum and makes the scale NaN.
+__device__ __forceinline__ uint2 encode_columns(const Two (&v)[4], float &scale) {
+  float f[8];
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    unpack_f32x2(v[i].v, f[2 * i], f[2 * i + 1]);
+    m = max(m, max(__float_as_uint(f[2 * i]) & 0x7FFFFFFFu, __float_as_uint(f[2 * i + 1]) & 0x7FFFFFFFu));
+  }
+#pragma unroll
+  for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+  scale = __fdiv_rn(__uint_as_float(m), 448.f);
+  if (scale == 0.f) return make_uint2(0u, 0u);
+  uint32_t c[4];
+  if (scale >= kFastScale && scale < __int_as_float(0x7F800000)) {
+    const Two r = both(__frcp_rn(scale));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = e4m3x2((v[i] * r).v);
+  } else {  // tiny, infinite or NaN scales
+#pragma unroll
+    for (int i = 0; i < 4; ++i) c[i] = e4m3x2(pack_f32x2(__fdiv_rn(f[2 * i], scale), __fdiv_rn(f[2 * i + 1], scale)));
+  }
+  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+}
+// The same into the arrays: chunk c (eight columns) of row m.
+__device__ __forceinline__ void store_columns8(const NormArgs &a, int64_t m, int c, bool live, const Two (&v)[4]) {
+  float scale;
+  const uint2 code = encode_columns(v, scale);
+  if (live) {
+    *reinterpret_cast<uint2 *>(a.q + m * a.K + c * 8) = code;
+    if ((c & 15) == 0) a.s[(c >> 4) * a.lds + m] = scale;
+  }
+}
+
 // ---------------------------------------------------------------- forward
 
 // Few rows: one row per CTA, kChunks groups of 8 columns per thread, in registers over both
-// reductions.
-template <class T, bool kR32, int kChunks>
+// reductions.  kOut8: y in 8 bits, and in 16 if a.y is given.
+template <class T, bool kR32, int kChunks, bool kOut8>
 __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const NormArgs a) {
   __shared__ float red[2][32];
   pdl_wait();
@@ -244,12 +283,16 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const NormArgs a
 #pragma unroll
       for (int u = 0; u < kChunks; ++u) {
         const int c = static_cast<int>(threadIdx.x) + u * nt;
-        if (c < chunks) {
+        if (kOut8 || c < chunks) {
           float gb[8], y[8];
-          load_opt<T>(static_cast<const uint16_t *>(a.gb), c * 8, 1.f, gb);
+          load_opt<T>(kOut8 && c >= chunks ? nullptr : static_cast<const uint16_t *>(a.gb), c * 8, 1.f, gb);
 #pragma unroll
           for (int i = 0; i < 8; ++i) y[i] = rv[u][i] * ib * gb[i];
-          Res<T, false>::store(a.y, m * a.K + c * 8, y);
+          if (!kOut8 || (c < chunks && a.y)) Res<T, false>::store(a.y, m * a.K + c * 8, y);
+          if constexpr (kOut8) {
+            const Two v[4] = {two(y[0], y[1]), two(y[2], y[3]), two(y[4], y[5]), two(y[6], y[7])};
+            store_columns8(a, m, c, c < chunks, v);
+          }
         }
       }
     }
@@ -265,7 +308,7 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const NormArgs a
 // parameters of a thread's columns stay in registers (the ring leaves little of the SM's memory to
 // its cache, and re-reading them for every row cost as much as the rows).  8192 x 7168 in bf16: 76 us,
 // 6.2 TB/s.
-template <class T, bool kR32, int kChunks, int kThreads, int kCtas>
+template <class T, bool kR32, int kChunks, int kThreads, int kCtas, bool kOut8>
 __global__ void __launch_bounds__(kThreads, kCtas) residual_norm_rows_kernel(const NormArgs a, int stages) {
   extern __shared__ __align__(128) uint8_t smem[];  // used as declared: its loads are known to be shared ones
   __shared__ float red[2][32];
@@ -376,7 +419,14 @@ __global__ void __launch_bounds__(kThreads, kCtas) residual_norm_rows_kernel(con
         if (c < chunks) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[u][i] = (v[u][i] * both(ib)) * gb[u][i];
-          store_pairs<T, false, 4>(a.y, m * a.K + c * 8, v[u]);
+          if (!kOut8 || a.y) store_pairs<T, false, 4>(a.y, m * a.K + c * 8, v[u]);
+        }
+        if constexpr (kOut8) {
+          if (c >= chunks) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[u][i] = both(0.f);
+          }
+          store_columns8(a, m, c, c < chunks, v[u]);
         }
       }
       // red[1] is written again only after the next row's first barrier, or this one without ga
@@ -704,14 +754,14 @@ __global__ void __launch_bounds__(kSumCols *kSumRows) partial_sum_kernel(const S
   }
 }
 
-template <class T, bool kR32>
+template <class T, bool kR32, bool kOut8>
 cudaError_t norm_forward(const NormArgs &a, int sms, cudaStream_t s) {
   const int chunks = a.K / 8;
   if (a.M <= 2 * sms) {  // few rows: as many threads as the row has chunks, straight from memory (latency)
     const int per = chunks <= 1024 ? 1 : 2;
     const dim3 grid(static_cast<unsigned>(a.M)), block(((chunks + per - 1) / per + 31) / 32 * 32);
-    return per == 1 ? launch_pdl(residual_norm_kernel<T, kR32, 1>, grid, block, 0, s, a)
-                    : launch_pdl(residual_norm_kernel<T, kR32, 2>, grid, block, 0, s, a);
+    return per == 1 ? launch_pdl(residual_norm_kernel<T, kR32, 1, kOut8>, grid, block, 0, s, a)
+                    : launch_pdl(residual_norm_kernel<T, kR32, 2, kOut8>, grid, block, 0, s, a);
   }
   // 16 columns per thread.  Up to 448 threads (K = 7168) two CTAs share an SM with 72 registers a
   // thread; more threads take one CTA per SM.
@@ -727,7 +777,7 @@ cudaError_t norm_forward(const NormArgs &a, int sms, cudaStream_t s) {
   const int smem = stages * stage;
   const int64_t cap = static_cast<int64_t>(sms) * per_sm;
   const dim3 grid(static_cast<unsigned>(a.M < cap ? a.M : cap)), block(threads);
-  auto kernel = wide ? residual_norm_rows_kernel<T, kR32, 2, 1024, 1> : residual_norm_rows_kernel<T, kR32, 2, 448, 2>;
+  auto kernel = wide ? residual_norm_rows_kernel<T, kR32, 2, 1024, 1, kOut8> : residual_norm_rows_kernel<T, kR32, 2, 448, 2, kOut8>;
   static std::atomic<bool> ready[64][2];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -823,9 +873,13 @@ NormGradPlan norm_grad_plan(int64_t M, int64_t K, int64_t groups, bool r32) {
   return p;
 }
 
+template <class T>
+static cudaError_t norm_as(const NormArgs &a, bool r32, int sms, cudaStream_t s) {
+  if (a.q) return r32 ? norm_forward<T, true, true>(a, sms, s) : norm_forward<T, false, true>(a, sms, s);
+  return r32 ? norm_forward<T, true, false>(a, sms, s) : norm_forward<T, false, false>(a, sms, s);
+}
 cudaError_t launch_residual_norm(const NormArgs &a, int dtype, bool r32, int sms, cudaStream_t s) {
-  if (dtype == NVFP4_DT_BF16) return r32 ? norm_forward<Bf16, true>(a, sms, s) : norm_forward<Bf16, false>(a, sms, s);
-  return r32 ? norm_forward<Fp16, true>(a, sms, s) : norm_forward<Fp16, false>(a, sms, s);
+  return dtype == NVFP4_DT_BF16 ? norm_as<Bf16>(a, r32, sms, s) : norm_as<Fp16>(a, r32, sms, s);
 }
 
 cudaError_t launch_residual_norm_backward(const NormGradArgs &a, const NormGradPlan &p, int dtype, bool r32,

@@ -1,0 +1,64 @@
+// Launches of the operators on 4-bit weights with group scales (the linear and the mixture-of-experts layer for a few
+// tokens), as their C entry points call them, and the layout that the weights are prepared into.
+#pragma once
+
+#include "internal.h"
+
+namespace nvfp4 {
+
+// Prepared weights: for each matrix, 64-row panel and 128-wide K block, one contiguous block of
+//   4096 bytes of codes   [chunk of 32 K: 4][pair of 16-row tiles: 2][lane: 32][16 bytes],
+//   scales (16-bit)       [group of the block: 128 / group][g: 8][row tile i: 4][half h: 2], row 16 i + 8 h + g,
+//   zero points (bytes)   in the same order, if the weights have them,
+// so that one bulk copy brings everything a warp needs for 64 x 128 weights, and each lane reads its share of the
+// m16n8k16 A fragments with 16-byte loads.  A lane (g = lane / 4, t = lane % 4) finds four words of eight codes: K
+// elements 32 c + 8 t .. + 7 of rows 32 p + {0, 8, 16, 24} + g.  The order of K inside an MMA is free as long as both
+// operands agree, so a word's eight elements are the lane's share of two MMAs: elements 0..3 of the first, 4..7 of
+// the second, and the activations need no reordering either.  In a word, element 2 j sits in bits 4 j .. 4 j + 3 and element
+// 2 j + 1 in bits 4 j + 16 .., the word rotated left so that j = 0 lies at the top of the 16-bit type's mantissa:
+// (word rotated right by 4 j) & mask | one gives the pair (1 + c / 16) in both halves.
+// Rows and columns that the matrix does not have hold zeros.  A gated matrix (gate rows [0, N / 2), up rows [N / 2, N))
+// has 32 gate rows and the 32 up rows of the same outputs in each panel: tiles 0, 1 and 2, 3.
+constexpr int kW4PanelRows = 64;
+constexpr int kW4BlockK = 128;
+constexpr int kW4CodeBytes = kW4PanelRows * kW4BlockK / 2;
+constexpr int w4_block_bytes(int groups, bool zeros) { return kW4CodeBytes + kW4PanelRows * groups * (zeros ? 3 : 2); }
+inline int64_t w4_panels(int64_t N, bool gated) { return gated ? (N / 2 + 31) / 32 : (N + kW4PanelRows - 1) / kW4PanelRows; }
+inline int64_t w4_blocks(int64_t K) { return (K + kW4BlockK - 1) / kW4BlockK; }
+
+cudaError_t launch_w4_prepare(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int dtype, int64_t G,
+                              int64_t N, int64_t K, int group, bool gated, uint8_t *out, cudaStream_t s);
+
+struct W4Args {
+  const void *x;  // 16-bit (M, K), row stride ldx
+  int64_t ldx;
+  int M, N, K;
+  const uint8_t *w;
+  void *y;  // 16-bit (M, N)
+  uint32_t *err;
+};
+// The weight-streaming product: tokens in tiles of 8 * tok8, K split over a cluster of `splits` CTAs.
+cudaError_t launch_w4_stream(const W4Args &a, int dtype, int group, bool zeros, int tok8, int splits, int depth,
+                             cudaStream_t s);
+
+struct W4MoeArgs {
+  const void *x;  // 16-bit (T, H), row stride ldx
+  int64_t ldx;
+  int T, H, I, E, topk;
+  const void *router;                           // 16-bit (E, H)
+  const uint8_t *w13, *w2, *sh13, *sh2;         // prepared; sh13, sh2 null without a shared expert
+  int act;
+  void *y;                                      // 16-bit (T, H)
+  float *logits;                                // (T, E)
+  uint16_t *h;                                  // (rows, I), row t * topk + j, then the shared expert's T rows
+  float *part;                                  // (rows, H)
+  int *counters;                                // kW4MoeCounters + slots + panels of y, zeroed by the router kernel
+  uint32_t *err;
+};
+constexpr int kW4MoeMaxT = 64, kW4MoeMaxEntries = 512, kW4MoeMaxK = 16;
+constexpr int kW4MoeMaxSlots = kW4MoeMaxEntries + kW4MoeMaxT / 8;
+constexpr int64_t kW4MoeMaxExperts = 1024, kW4MoeMaxDim = 16384;
+constexpr int kW4MoeCounters = 32;  // the item counter, on a cache line of its own
+cudaError_t launch_w4_moe(const W4MoeArgs &a, int dtype, int group, bool zeros, int sms, cudaStream_t s);
+
+}  // namespace nvfp4

@@ -609,6 +609,154 @@ def residual_norm_backward(dr_out: Optional[torch.Tensor], dy: Optional[torch.Te
     return df, dr, dga, dgate, dgb
 
 
+def residual_norm_fp8(f: torch.Tensor, r: torch.Tensor, gamma_before: torch.Tensor,
+                      gamma_after: Optional[torch.Tensor] = None, gate: Optional[torch.Tensor] = None,
+                      scale: float = 1.0, eps: float = 1e-6, want_y: bool = False, save: bool = False,
+                      out: Optional[torch.Tensor] = None, stream=None):
+    """``residual_norm`` with its normed output in 8 bits: returns (r_out, q, s, y), with ``save`` (r_out, q, s, y,
+    stats).
+
+    q (M, K) float8_e4m3fn and s (ceil(K / 128), M) fp32, a view of padded rows, are what ``fp8_gemm`` takes: one
+    scale per 128 columns of a row, max|y| / 448, from y before any rounding.  y is the 16-bit output with ``want_y``, else
+    None.  The other arguments are ``residual_norm``'s; ``residual_norm_backward`` takes ``stats``.  K % 16 == 0.
+    """
+    st = _here(stream, f, r, gamma_before, gamma_after, gate, out)
+    _no_graph(f, r, gamma_before, gamma_after, gate)
+    if st < 0:
+        return _elsewhere(stream, (f, r, gamma_before, gamma_after, gate, out),
+                          lambda: residual_norm_fp8(f, r, gamma_before, gamma_after, gate, scale, eps, want_y, save, out))
+    M, K, ldf, ldr, kind, rkind, ga, gp, gkind, groups, gb = _norm_args(f, r, gamma_after, gate, gamma_before)
+    if out is not None:
+        _whole(out, "out", (M, K), (r.dtype,))
+    r_out = out if out is not None else torch.empty(M, K, dtype=r.dtype, device=r.device)
+    q = torch.empty(M, K, dtype=torch.float8_e4m3fn, device=f.device)
+    lds = (M + 3) // 4 * 4
+    s = torch.empty((K + 127) // 128, lds, dtype=torch.float32, device=f.device)
+    y = torch.empty(M, K, dtype=f.dtype, device=f.device) if want_y else None
+    stats = torch.empty(M, 2, dtype=torch.float32, device=f.device) if save else None
+    call("nvfp4_residual_norm_fp8", f.data_ptr(), kind, r.data_ptr(), rkind, M, K, ldf, ldr, ga, gp, gkind, groups, scale,
+         gb, eps, r_out.data_ptr(), q.data_ptr(), s.data_ptr(), lds, _ptr(y), _ptr(stats), st)
+    s = s[:, :M]
+    return (r_out, q, s, y, stats) if save else (r_out, q, s, y)
+
+
+# --------------------------------------------------------------------------- 4-bit weights with group scales
+#
+# Integer weights of 4 bits with a scale, and optionally a zero point, for each group of consecutive K elements of a row,
+# and 16-bit activations: for inference.  The conventions of the dense operators above hold.
+
+@dataclass(frozen=True)
+class W4Weight:
+    """Prepared 4-bit weights of G matrices (N, K) (see ``w4_prepare``)."""
+    data: torch.Tensor
+    G: int
+    N: int
+    K: int
+    group: int
+    dtype: torch.dtype      # of the scales, and of the activations it goes with
+    has_zeros: bool
+    gated: bool
+
+
+def w4_prepare(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.Tensor] = None, group: int = 128,
+               gated: bool = False, stream=None) -> W4Weight:
+    """Lays out checkpoint weights (c - z) s, once, at load time.
+
+    codes (N, K / 2) uint8 with element 2j in the low half of byte j, or (G, N, K / 2) for G matrices; scales
+    (..., N, ceil(K / group)) bf16 or fp16; zeros uint8 of the same shape, of which the low four bits count (None: 8
+    everywhere); group 32, 64 or 128.  ``gated``: the first N / 2 rows are a gate and the others the up projection of
+    the same outputs (``w4_moe``'s w13).  K % 8 == 0.
+    """
+    st = _here(stream, codes, scales, zeros)
+    if st < 0:
+        return _elsewhere(stream, (codes, scales, zeros), lambda: w4_prepare(codes, scales, zeros, group, gated))
+    if codes.dim() not in (2, 3):
+        raise ValueError(f"codes must be (N, K / 2) or (G, N, K / 2), got {tuple(codes.shape)}")
+    if group not in (32, 64, 128):
+        raise ValueError(f"group {group}, expected 32, 64 or 128")
+    kind = _kind(scales, "scales")
+    G = codes.shape[0] if codes.dim() == 3 else 1
+    N, K = codes.shape[-2], codes.shape[-1] * 2
+    shape = (*codes.shape[:-1], (K + group - 1) // group)
+    cp = _whole(codes, "codes", tuple(codes.shape), (torch.uint8,))
+    sp = _whole(scales, "scales", shape, (scales.dtype,))
+    zp = None if zeros is None else _whole(zeros, "zeros", shape, (torch.uint8,))
+    n = lib().nvfp4_w4_prepared_bytes(G, N, K, group, zeros is not None, gated)
+    data = torch.empty(n, dtype=torch.uint8, device=codes.device)
+    call("nvfp4_w4_prepare", cp, sp, zp, kind, G, N, K, group, gated, data.data_ptr() if n else 16, st)
+    return W4Weight(data, G, N, K, group, scales.dtype, zeros is not None, gated)
+
+
+def _w4(w: W4Weight, what: str, G: int, N: int, K: int, gated: bool, like: Optional[W4Weight] = None) -> int:
+    """Data pointer of a prepared weight of the expected sizes."""
+    if (w.G, w.N, w.K, w.gated) != (G, N, K, gated):
+        raise ValueError(f"{what} holds {w.G} x ({w.N}, {w.K}){' gated' if w.gated else ''}, expected {G} x ({N}, {K})"
+                         f"{' gated' if gated else ''}")
+    if like is not None and (w.dtype, w.group, w.has_zeros) != (like.dtype, like.group, like.has_zeros):
+        raise ValueError(f"{what}: its scales' type, group size and zero points must be those of the other weights")
+    return w.data.data_ptr()
+
+
+def w4_linear(x: torch.Tensor, w: W4Weight, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """y (M, N) = x W^T in x's type: x (M, K) strided rows of the type of the weights' scales."""
+    st = _here(stream, x, w.data, out)
+    _no_graph(x)
+    if st < 0:
+        return _elsewhere(stream, (x, w.data, out), lambda: w4_linear(x, w, out))
+    M, K = _size(x, "x")
+    ld = _ld(x, "x", M, K, w.dtype)
+    wp = _w4(w, "w", 1, w.N, K, False)
+    if out is not None:
+        _whole(out, "out", (M, w.N), (x.dtype,))
+    y = out if out is not None else torch.empty(M, w.N, dtype=x.dtype, device=x.device)
+    call("nvfp4_w4_linear", x.data_ptr(), _DT[w.dtype], M, K, ld, w.N, wp, w.group, w.has_zeros, y.data_ptr(), st)
+    return y
+
+
+def w4_moe_workspace(T: int, H: int, I: int, E: int, topk: int, has_shared: bool, device) -> torch.Tensor:
+    """A workspace for ``w4_moe`` (one call at a time)."""
+    n = int(lib().nvfp4_w4_moe_workspace_bytes(T, H, I, E, topk, int(has_shared)))
+    if n == 0:
+        raise ValueError("unsupported MoE shape")
+    return _u8(n, device=device)
+
+
+def w4_moe(x: torch.Tensor, router: torch.Tensor, w13: W4Weight, w2: W4Weight, topk: int,
+           shared13: Optional[W4Weight] = None, shared2: Optional[W4Weight] = None, activation: str = "silu",
+           out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+    """A whole mixture-of-experts layer for a few tokens: y (T, H) = sum of the top k experts of x (T, H), weighted by
+    the softmax of the router's logits over them, and the shared expert (if given).
+
+    x strided rows; router (E, H); w13 (E, 2I, H) prepared with ``gated``, w2 (E, H, I); shared13 (1, 2I, H) and shared2
+    (1, H, I) alike.  E(x) = W2 (act(Wg x) * (Wu x)), the product rounded to x's type.  T <= 64, topk <= 16, T topk <=
+    512, E <= 1024; H and I multiples of 8, at most 16384.
+    """
+    d13, d2 = None if shared13 is None else shared13.data, None if shared2 is None else shared2.data
+    st = _here(stream, x, router, w13.data, w2.data, d13, d2, out, workspace)
+    _no_graph(x, router)
+    if st < 0:
+        return _elsewhere(stream, (x, router, w13.data, w2.data, d13, d2, out, workspace),
+                          lambda: w4_moe(x, router, w13, w2, topk, shared13, shared2, activation, out, workspace))
+    if activation not in _ACT:
+        raise ValueError(f"activation {activation!r}, expected one of {sorted(_ACT)}")
+    T, H = _size(x, "x")
+    ld = _ld(x, "x", T, H, w13.dtype)
+    E, I = w13.G, w2.K
+    p13, p2 = _w4(w13, "w13", E, 2 * I, H, True), _w4(w2, "w2", E, H, I, False, w13)
+    if (shared13 is None) != (shared2 is None):
+        raise ValueError("the shared expert's weights come together")
+    s13 = None if shared13 is None else _w4(shared13, "shared13", 1, 2 * I, H, True, w13)
+    s2 = None if shared2 is None else _w4(shared2, "shared2", 1, H, I, False, w13)
+    rp = _whole(router, "router", (E, H), (x.dtype,))
+    if out is not None:
+        _whole(out, "out", (T, H), (x.dtype,))
+    y = out if out is not None else torch.empty(T, H, dtype=x.dtype, device=x.device)
+    ws, ws_bytes = _scratch(workspace, "nvfp4_w4_moe_workspace_bytes", x, T, H, I, E, topk, s13 is not None)
+    call("nvfp4_w4_moe", x.data_ptr(), _DT[w13.dtype], T, H, ld, I, E, topk, rp, p13, p2, s13, s2, w13.group, w13.has_zeros,
+         _ACT[activation], y.data_ptr(), _ptr(ws), ws_bytes, st)
+    return y
+
+
 # --------------------------------------------------------------------------- diagnostics
 
 def device_error(stream=None) -> Tuple[int, int]:
