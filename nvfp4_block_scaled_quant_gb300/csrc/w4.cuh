@@ -34,11 +34,11 @@ template <class T>
 __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1, bool add = true) {
   const float c[4] = {add ? d[0] : 0.f, add ? d[1] : 0.f, add ? d[2] : 0.f, add ? d[3] : 0.f};
   if constexpr (T::kCode == NVFP4_DT_BF16)
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
                  : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
   else
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
                  : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
@@ -46,9 +46,12 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 // A word of eight codes -> (1 + c / 16) of its four pairs.
 template <class T>
 __device__ __forceinline__ void w4_unpack(uint32_t w, uint32_t (&p)[4]) {
+  // written as one operation: with both constants as immediates the compiler takes two (the pair of constants stays in registers)
 #pragma unroll
   for (int j = 0; j < 4; ++j)
-    p[j] = (j ? __funnelshift_r(w, w, 4 * j) : w) & W4Bits<T>::kMask | W4Bits<T>::kOne;
+    asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
+        : "=r"(p[j])
+        : "r"(j ? __funnelshift_r(w, w, 4 * j) : w), "r"(W4Bits<T>::kMask), "r"(W4Bits<T>::kOne));
 }
 
 // A lane's activations of one K block: for each chunk of 32 K and tile of 8 tokens the eight elements 32 c + 8 t .. of
@@ -58,9 +61,10 @@ struct W4Frag {
   uint4 v[4][kNT];
 };
 
-// sums += block * x.  sums[i][n] is the C fragment of row tile i and token tile n, without the factor 16.
+// sums += block * x.  sums[i][n] is the C fragment of row tile i and token tile n, two tokens of a row to a pair, without
+// the factor 16.
 template <class T, int kGpb, bool kZeros, int kNT>
-__device__ __forceinline__ void w4_block(const uint8_t *block, const W4Frag<kNT> &x, float (&sums)[4][kNT][4]) {
+__device__ __forceinline__ void w4_block(const uint8_t *block, const W4Frag<kNT> &x, uint64_t (&sums)[4][kNT][2]) {
   const int lane = threadIdx.x & 31, g = lane >> 2;
   constexpr int kChunks = 4 / kGpb;  // of a group
   const uint32_t ones[4] = {W4Bits<T>::kOne, W4Bits<T>::kOne, W4Bits<T>::kOne, W4Bits<T>::kOne};
@@ -110,12 +114,12 @@ __device__ __forceinline__ void w4_block(const uint8_t *block, const W4Frag<kNT>
         z0 = -1.f - 0.0625f * static_cast<float>(zz & 0xFFu);
         z1 = -1.f - 0.0625f * static_cast<float>((zz >> 8) & 0xFFu);
       }
+      const uint64_t s00 = pack_f32x2(s0, s0), s11 = pack_f32x2(s1, s1), z00 = pack_f32x2(z0, z0), z11 = pack_f32x2(z1, z1);
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
-        sums[i][n][0] = fmaf(s0, fmaf(z0, sx[n][0], acc[i][n][0]), sums[i][n][0]);
-        sums[i][n][1] = fmaf(s0, fmaf(z0, sx[n][1], acc[i][n][1]), sums[i][n][1]);
-        sums[i][n][2] = fmaf(s1, fmaf(z1, sx[n][0], acc[i][n][2]), sums[i][n][2]);
-        sums[i][n][3] = fmaf(s1, fmaf(z1, sx[n][1], acc[i][n][3]), sums[i][n][3]);
+        const uint64_t sxx = pack_f32x2(sx[n][0], sx[n][1]);
+        sums[i][n][0] = fma_f32x2(s00, fma_f32x2(z00, sxx, pack_f32x2(acc[i][n][0], acc[i][n][1])), sums[i][n][0]);
+        sums[i][n][1] = fma_f32x2(s11, fma_f32x2(z11, sxx, pack_f32x2(acc[i][n][2], acc[i][n][3])), sums[i][n][1]);
       }
     }
   }
@@ -124,14 +128,17 @@ __device__ __forceinline__ void w4_block(const uint8_t *block, const W4Frag<kNT>
 // A warp's sums in shared memory: token j's 64 rows at j * kW4Pitch (a pitch that spreads the lanes over the banks).
 constexpr int kW4Pitch = 68;
 template <int kNT>
-__device__ __forceinline__ void w4_store_sums(float *at, const float (&sums)[4][kNT][4]) {
+__device__ __forceinline__ void w4_store_sums(float *at, const uint64_t (&sums)[4][kNT][2]) {
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
     for (int n = 0; n < kNT; ++n)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) at[(8 * n + 2 * t + (e & 1)) * kW4Pitch + 16 * i + (e >> 1) * 8 + g] = sums[i][n][e];
+      for (int h = 0; h < 2; ++h) {
+        float *row = at + (8 * n + 2 * t) * kW4Pitch + 16 * i + 8 * h + g;
+        unpack_f32x2(sums[i][n][h], row[0], row[kW4Pitch]);
+      }
 }
 
 }  // namespace nvfp4

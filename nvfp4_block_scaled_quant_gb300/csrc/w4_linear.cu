@@ -84,7 +84,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_stream_kernel(const W4Args 
   pdl_wait();
   pdl_trigger();
 
-  float sums[4][kNT][4] = {};
+  uint64_t sums[4][kNT][2] = {};
   const uint16_t *x = static_cast<const uint16_t *>(a.x) + (m0 + g) * a.ldx + 8 * t;
   auto load_x = [&](int kb, W4Frag<kNT> &f) {
 #pragma unroll

@@ -11,9 +11,12 @@
 //    A slot's down rows go to the workspace in fp32; the CTA that finishes the last slot of a panel adds a token's experts
 //    up in the order of its top k, so repeated calls give identical bits.
 //
-// With few tokens the layer is bound by the bytes of the chosen experts' weights.  Each block of 64 x 128 weights is
-// one bulk copy into a ring of some 90 KB, two CTAs to an SM; eight warps split an item's K blocks and add their
-// sums at its end.
+// With few tokens the layer is bound by the bytes of the chosen experts' weights.  Eight warps of a CTA take an item's
+// K blocks in turn (block b goes to warp b % 8), each through a ring of its own: a block is one bulk copy.  A warp leaves its sums where its
+// last block of the item was and goes on to the next item; a finishing warp adds the eight up and gives the
+// stages back.  Two CTAs share an SM.  (The rings are the warps' own because a warp waits on every phase of its
+// barriers then.  In a common ring, taken block by block, a warp that got a ring's length ahead of a slow copy would take an
+// older phase of the same parity for its own.)
 #include <atomic>
 
 #include "w4.cuh"
@@ -92,10 +95,10 @@ __global__ void __launch_bounds__(kLogitWarps * 32) w4_moe_logits_kernel(const W
 
 // ---------------------------------------------------------------- experts
 
-constexpr int kWarps = 8, kThreads = (kWarps + 1) * 32;  // and a producer warp
-constexpr int kItems = 4;                                // items known ahead
-constexpr int kRedFloats = 8 * kW4Pitch;                 // a warp's sums: eight tokens
-constexpr int kMaxStages = 24;
+constexpr int kWarps = 8;                     // that multiply
+constexpr int kThreads = (kWarps + 2) * 32;   // and a finishing and a producer warp
+constexpr int kItems = 4;                     // items known ahead
+constexpr int kMaxDepth = 3;                  // stages of a warp's ring
 
 struct Plan {
   float weight[kW4MoeMaxEntries];      // of a token's chosen expert, entry t * topk + j
@@ -105,13 +108,11 @@ struct Plan {
   uint16_t slot_count[kW4MoeMaxSlots];
   int slots, shared_slots;
 };
-// While the plan is made, in the room of the sums: the experts' counts, first places and first slots, and the ids.
+// While the plan is made, in the room of the rings: the experts' counts, first places and first slots, and the ids.
 struct PlanScratch {
   int count[kW4MoeMaxExperts], first[kW4MoeMaxExperts], slot0[kW4MoeMaxExperts];
   uint16_t ids[kW4MoeMaxEntries];
 };
-static_assert(sizeof(PlanScratch) <= kWarps * kRedFloats * sizeof(float), "the scratch fits where the sums go");
-
 // Order-preserving bits of a float (NaN above or below everything), never 0: 0 marks an expert that is taken.
 __device__ __forceinline__ uint32_t order_bits(float v) {
   const uint32_t b = __float_as_uint(v);
@@ -225,222 +226,331 @@ __device__ __forceinline__ int load_acquire(const int *p) {
   asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(v) : "l"(p) : "memory");
   return v;
 }
-__device__ __forceinline__ void consumers_meet() {
-  __syncwarp();
-  asm volatile("bar.sync 1, %0;" ::"n"(kWarps * 32) : "memory");
-}
-
 __device__ __forceinline__ float activate(int act, float g) {
   if (act == NVFP4_ACT_SILU) return act_fwd<NVFP4_ACT_SILU>(g);
   if (act == NVFP4_ACT_GELU) return act_fwd<NVFP4_ACT_GELU>(g);
   return act_fwd<NVFP4_ACT_GELU_TANH>(g);
 }
 
+// An item of the list.
+struct Item {
+  int slot;  // -1: no more items
+  int panel, blocks, up;
+};
+
 template <class T, int kGpb, bool kZeros>
-__global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4MoeArgs a, int stages) {
+__global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4MoeArgs a, int depth) {
   constexpr int kBytes = w4_block_bytes(kGpb, kZeros);
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ uint64_t full[kMaxStages], empty[kMaxStages], item_full[kItems], item_empty[kItems];
-  __shared__ int s_item[kItems], s_now, s_finish, s_abort;
+  __shared__ uint64_t full[kWarps][kMaxDepth], empty[kWarps][kMaxDepth], item_full[kItems], item_empty[kItems], sums_full[2], sums_empty[2];
+  __shared__ int4 s_item[kItems];
+  __shared__ int s_sums[2][kWarps], s_finished, s_abort;
+  __shared__ uint16_t s_panels[kW4MoeMaxDim / kW4PanelRows];  // of y, that this CTA finishes
   __shared__ Plan plan;
   volatile int *abort_flag = &s_abort;
-  float *red = reinterpret_cast<float *>(smem + stages * kBytes);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
   if (tid == 0) {
-    for (int s = 0; s < stages; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
-    }
+    for (int w = 0; w < kWarps; ++w)
+      for (int s = 0; s < depth; ++s) {
+        mbar_init(&full[w][s], 1);
+        mbar_init(&empty[w][s], 1);
+      }
     for (int q = 0; q < kItems; ++q) {
       mbar_init(&item_full[q], 1);
-      mbar_init(&item_empty[q], 1);
+      mbar_init(&item_empty[q], kWarps + 1);
+    }
+    for (int u = 0; u < 2; ++u) {
+      mbar_init(&sums_full[u], kWarps);
+      mbar_init(&sums_empty[u], 1);
     }
     s_abort = 0;
-    s_finish = -1;
+    s_finished = 0;
     fence_barrier_init();
   }
   __syncthreads();
   pdl_wait();
   pdl_trigger();
-  make_plan(a, plan, *reinterpret_cast<PlanScratch *>(red));
+  make_plan(a, plan, *reinterpret_cast<PlanScratch *>(smem));
 
   const int slots = plan.slots, shared_slots = plan.shared_slots, entries = a.T * a.topk;
   const int panels13 = (a.I + 31) / 32, panels2 = (a.H + kW4PanelRows - 1) / kW4PanelRows;
-  const int blocks13 = (a.H + kW4BlockK - 1) / kW4BlockK, blocks2 = (a.I + kW4BlockK - 1) / kW4BlockK;
-  const int up_items = slots * panels13, items = up_items + slots * panels2;
   int *counter = a.counters, *slot_done = counter + kW4MoeCounters, *panel_done = slot_done + kW4MoeMaxSlots;
+  // the workspace row of a slot's token j
+  auto row_of = [&](int slot, int j) {
+    const int at = plan.slot_first[slot] + j;
+    return slot < shared_slots ? entries + at : static_cast<int>(plan.sorted[at]);
+  };
 
-  if (warp == kWarps) {
-    // ---------------------------------------------------------------- producer
-    if (lane == 0) {
-      const uint64_t pol = policy_evict_first();
-      int stage = 0, q = 0;
-      uint32_t phase = 0, qphase = 0;
-      bool ok = true;
-      int item = atomicAdd(counter, 1);
-      for (;;) {
+  if (warp == kWarps + 1) {
+    // ---------------------------------------------------------------- producer: lane w fills the ring of warp w
+    const int blocks13 = (a.H + kW4BlockK - 1) / kW4BlockK, blocks2 = (a.I + kW4BlockK - 1) / kW4BlockK;
+    const int up_items = slots * panels13, items = up_items + slots * panels2;
+    const uint64_t pol = policy_evict_first();
+    fence_proxy_async_shared();  // the plan's scratch was where the copies go
+    int stage = 0, q = 0;
+    uint32_t phase = 0, qphase = 0;
+    bool ok = true;
+    int item = lane == 0 ? atomicAdd(counter, 1) : 0;
+    for (;;) {
+      item = __shfl_sync(0xffffffffu, item, 0);
+      const bool up = item < up_items;
+      const int i = up ? item : item - up_items, panels = up ? panels13 : panels2, blocks = up ? blocks13 : blocks2;
+      const int slot = item < items ? i / panels : -1, panel = i % panels;
+      if (lane == 0) {
         ok = mbar_wait_bounded(&item_empty[q], qphase ^ 1, abort_flag, a.err, kPipelineTimeoutNs);
-        if (!ok) break;
-        s_item[q] = item < items ? item : -1;
-        mbar_arrive(&item_full[q]);
-        if (item >= items) break;
-        const int next = atomicAdd(counter, 1);  // on its way while this item's blocks are asked for
-        const bool up = item < up_items;
-        const int i = up ? item : item - up_items, panels = up ? panels13 : panels2, blocks = up ? blocks13 : blocks2;
-        const int slot = i / panels, panel = i - slot * panels;
-        const uint8_t *w = slot < shared_slots ? (up ? a.sh13 : a.sh2) : (up ? a.w13 : a.w2);
-        const int expert = plan.slot_expert[slot];
-        w += (static_cast<int64_t>(expert) * panels + panel) * blocks * kBytes;
-        for (int b = 0; b < blocks; ++b) {
-          ok = mbar_wait_bounded(&empty[stage], phase ^ 1, abort_flag, a.err, kPipelineTimeoutNs);
+        s_item[q] = make_int4(slot, panel, blocks, up);
+        if (ok) mbar_arrive(&item_full[q]);
+      }
+      if (++q == kItems) {
+        q = 0;
+        qphase ^= 1;
+      }
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok || slot < 0) break;
+      if (lane == 0) item = atomicAdd(counter, 1);  // the next one, on its way while this one's blocks are asked for
+      const uint8_t *w = slot < shared_slots ? (up ? a.sh13 : a.sh2) : (up ? a.w13 : a.w2);
+      w += (static_cast<int64_t>(plan.slot_expert[slot]) * panels + panel) * blocks * kBytes;
+      if (lane < kWarps) {
+        for (int b = lane; b < blocks; b += kWarps) {
+          ok = mbar_wait_bounded(&empty[lane][stage], phase ^ 1, abort_flag, a.err, kPipelineTimeoutNs);
           if (!ok) break;
-          mbar_arrive_expect_tx(&full[stage], kBytes);
-          bulk_load(smem + stage * kBytes, w + static_cast<int64_t>(b) * kBytes, kBytes, &full[stage], pol);
-          if (++stage == stages) {
+          mbar_arrive_expect_tx(&full[lane][stage], kBytes);
+          bulk_load(smem + (lane * depth + stage) * kBytes, w + static_cast<int64_t>(b) * kBytes, kBytes, &full[lane][stage], pol);
+          if (++stage == depth) {
             stage = 0;
             phase ^= 1;
           }
         }
-        if (!ok) break;
-        if (++q == kItems) {
-          q = 0;
-          qphase ^= 1;
-        }
-        item = next;
       }
-      if (!ok) {  // copies in flight land before the CTA's memory goes
-        const uint64_t t0 = global_timer_ns();
-        while (global_timer_ns() - t0 < 10000000ull) {
-        }
+      // no lane begins an item before every block of the one before it is asked for
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+    }
+    if (!ok) {  // copies in flight land before the CTA's memory goes
+      const uint64_t t0 = global_timer_ns();
+      while (global_timer_ns() - t0 < 10000000ull) {
       }
     }
     return;
   }
 
-  // ------------------------------------------------------------------ consumers
-  const int g = lane >> 2, t = lane & 3;
+  // the next item of the queue for a whole warp; slot -1 behind the last one or after a wait that gave up
   int q = 0;
   uint32_t qphase = 0;
-  int stage0 = 0;  // stage and phase of the item's first block
-  uint32_t phase0 = 0;
-  for (;;) {
-    if (tid == 0) {
-      int item = -1;
-      if (mbar_wait_bounded(&item_full[q], qphase, abort_flag, a.err, kPipelineTimeoutNs)) {
-        item = s_item[q];
-        mbar_arrive(&item_empty[q]);
-        if (item >= up_items) {  // the slot's h is complete
-          const int *done = slot_done + (item - up_items) / panels2;
-          const uint64_t t0 = global_timer_ns();
-          while (load_acquire(done) < panels13) {
-            if (*abort_flag || global_timer_ns() - t0 > kPipelineTimeoutNs) {
-              if (!*abort_flag) raise_device_error(a.err, NVFP4_DEVERR_PIPELINE_TIMEOUT);
-              *abort_flag = 1;
-              item = -1;
-              break;
-            }
-          }
-        }
-      }
-      s_now = item;
-    }
-    consumers_meet();
-    const int item = s_now, finish = s_finish;
-    if (finish >= 0) {
-      // this CTA was the last to add to a panel of y: a token's experts in the order of its top k, then the shared one
-      for (int e = tid; e < a.T * kW4PanelRows; e += kWarps * 32) {
-        const int row = e >> 6, n = finish * kW4PanelRows + (e & 63);
-        if (n < a.H) {
-          const float *p = a.part + static_cast<int64_t>(row) * a.topk * a.H + n;
-          float v = 0.f;
-          for (int j = 0; j < a.topk; ++j) v = fmaf(plan.weight[row * a.topk + j], __ldcg(p + static_cast<int64_t>(j) * a.H), v);
-          if (shared_slots) v += __ldcg(a.part + static_cast<int64_t>(entries + row) * a.H + n);
-          static_cast<uint16_t *>(a.y)[static_cast<int64_t>(row) * a.H + n] = T::one(v);
-        }
-      }
-    }
-    if (item < 0) break;
+  auto next_item = [&] {
+    const bool ok = mbar_wait_bounded(&item_full[q], qphase, abort_flag, a.err, kPipelineTimeoutNs);
+    const int4 v = s_item[q];
+    const Item item = {__all_sync(0xffffffffu, ok) ? v.x : -1, v.y, v.z, v.w};
+    __syncwarp();
+    if (lane == 0 && ok) mbar_arrive(&item_empty[q]);
     if (++q == kItems) {
       q = 0;
       qphase ^= 1;
     }
-    const bool up = item < up_items;
-    const int i = up ? item : item - up_items, panels = up ? panels13 : panels2, blocks = up ? blocks13 : blocks2;
-    const int slot = i / panels, panel = i - slot * panels, count = plan.slot_count[slot], first = plan.slot_first[slot];
-    const int width = up ? a.H : a.I;
-    // the workspace row of the slot's token j, and this lane's activations
-    auto row_of = [&](int j) { return slot < shared_slots ? entries + first + j : static_cast<int>(plan.sorted[first + j]); };
+    return item;
+  };
+
+  if (warp < kWarps) {
+    // ---------------------------------------------------------------- products
+    const int g = lane >> 2, t = lane & 3;
+    const uint8_t *ring = smem + warp * depth * kBytes;
+    const uint32_t topk_inverse = (65536u + a.topk - 1) / a.topk;  // entries are below 512, topk at most 16: exact
+    int stage = 0, buf = 0;
+    uint32_t phase = 0, bphase = 0;
+    int ready = -1;  // the last slot whose h was seen complete
+    Item item = next_item();
+    // This lane's activations of the item.  Lanes of tokens that the slot does not have take its first one's: their columns
+    // of the sums are left where they are.
     const uint16_t *x = nullptr;
-    if (g < count) {
-      const int row = row_of(g);
-      x = up ? static_cast<const uint16_t *>(a.x) + static_cast<int64_t>(row < entries ? row / a.topk : row - entries) * a.ldx
-             : a.h + static_cast<int64_t>(row) * a.I;
+    int width = 0;
+    auto open = [&](const Item &it) {
+      width = it.up ? a.H : a.I;
+      const int row = row_of(it.slot, g < plan.slot_count[it.slot] ? g : 0);
+      const int token = row < entries ? static_cast<int>((row * topk_inverse) >> 16) : row - entries;
+      x = it.up ? static_cast<const uint16_t *>(a.x) + token * a.ldx : a.h + static_cast<int64_t>(row) * a.I;
       x += 8 * t;
-    }
+    };
     auto load_x = [&](int b, W4Frag<1> &f) {
+      const uint16_t *p = x + b * kW4BlockK;
+      if ((b + 1) * kW4BlockK <= width) {
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        const int k = b * kW4BlockK + 32 * c;
-        f.v[c][0] = x && k + 8 * t < width ? __ldcg(reinterpret_cast<const uint4 *>(x + k)) : make_uint4(0u, 0u, 0u, 0u);
+        for (int c = 0; c < 4; ++c) f.v[c][0] = __ldcg(reinterpret_cast<const uint4 *>(p + 32 * c));
+      } else {
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          f.v[c][0] = b * kW4BlockK + 32 * c + 8 * t < width ? __ldcg(reinterpret_cast<const uint4 *>(p + 32 * c)) : make_uint4(0u, 0u, 0u, 0u);
       }
     };
-    float sums[4][1][4] = {};
-    int stage = stage0 + warp;
-    uint32_t phase = phase0;
-    bool ok = true;
-    for (int b = warp; b < blocks; b += kWarps) {
-      W4Frag<1> f;
-      load_x(b, f);
-      while (stage >= stages) {
-        stage -= stages;
-        phase ^= 1;
+    bool ok = true, have = false;  // have: the item's first activations are loaded
+    W4Frag<1> f, f2;
+    while (item.slot >= 0) {
+      const Item it = item;
+      if (!it.up && ready != it.slot) {  // its h is complete
+        const uint64_t t0 = global_timer_ns();
+        while (load_acquire(slot_done + it.slot) < panels13) {
+          if (*abort_flag || global_timer_ns() - t0 > kPipelineTimeoutNs) {
+            if (!*abort_flag) raise_device_error(a.err, NVFP4_DEVERR_PIPELINE_TIMEOUT);
+            *abort_flag = 1;
+            ok = false;
+            break;
+          }
+        }
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        ready = it.slot;
       }
-      ok = mbar_wait_bounded(&full[stage], phase, abort_flag, a.err, kPipelineTimeoutNs);
+      if (!have && warp < it.blocks) {
+        open(it);
+        load_x(warp, f);
+      }
+      have = false;
+      bool known = false;  // the next item
+      uint64_t sums[4][1][2] = {};
+      // one block with the activations in f, the next one's on their way to `ahead`
+      auto step = [&](int b, const W4Frag<1> &f, W4Frag<1> &ahead) {
+        const bool last = b + kWarps >= it.blocks;
+        if (!last) {
+          load_x(b + kWarps, ahead);
+        } else if (__all_sync(0xffffffffu, mbar_try_wait(&item_full[q], qphase))) {
+          // the next item's activations, if it is known and they are there
+          item = next_item();
+          known = true;
+          if (item.slot >= 0) {
+            if (!item.up && ready != item.slot && __all_sync(0xffffffffu, load_acquire(slot_done + item.slot) >= panels13))
+              ready = item.slot;
+            if (warp < item.blocks && (item.up || ready == item.slot)) {
+              open(item);
+              load_x(warp, ahead);
+              have = true;
+            }
+          }
+        }
+        ok = mbar_wait_bounded(&full[warp][stage], phase, abort_flag, a.err, kPipelineTimeoutNs);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return;
+        w4_block<T, kGpb, kZeros, 1>(ring + stage * kBytes, f, sums);
+        __syncwarp();
+        if (last) return;  // the item's sums go where its last block was
+        if (lane == 0) mbar_arrive(&empty[warp][stage]);
+        if (++stage == depth) {
+          stage = 0;
+          phase ^= 1;
+        }
+      };
+      for (int b = warp; b < it.blocks; b += 2 * kWarps) {
+        step(b, f, f2);
+        if (!ok || b + kWarps >= it.blocks) {
+          f = f2;
+          break;
+        }
+        step(b + kWarps, f2, f);
+        if (!ok) break;
+      }
+      ok = ok && mbar_wait_bounded(&sums_empty[buf], bphase ^ 1, abort_flag, a.err, kPipelineTimeoutNs);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      w4_block<T, kGpb, kZeros, 1>(smem + stage * kBytes, f, sums);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[stage]);
-      stage += kWarps;
-    }
-    stage0 += blocks;
-    while (stage0 >= stages) {
-      stage0 -= stages;
-      phase0 ^= 1;
-    }
-    w4_store_sums<1>(red + warp * kRedFloats, sums);
-    consumers_meet();
-    if (up) {
-      const int j = tid >> 5, c = tid & 31, n = panel * 32 + c;
-      if (j < count && n < a.I) {
-        float gate = 0.f, lift = 0.f;
-#pragma unroll
-        for (int u = 0; u < kWarps; ++u) {
-          gate += red[u * kRedFloats + j * kW4Pitch + c];
-          lift += red[u * kRedFloats + j * kW4Pitch + 32 + c];
+      if (warp < it.blocks) {
+        w4_store_sums<1>(reinterpret_cast<float *>(smem + (warp * depth + stage) * kBytes), sums);
+        fence_proxy_async_shared();  // a copy takes their place later
+        if (lane == 0) s_sums[buf][warp] = stage;
+        if (++stage == depth) {
+          stage = 0;
+          phase ^= 1;
         }
-        a.h[static_cast<int64_t>(row_of(j)) * a.I + n] = T::one(activate(a.act, 16.f * gate) * (16.f * lift));
       }
-    } else {
-      for (int e = tid; e < count * kW4PanelRows; e += kWarps * 32) {
-        const int j = e >> 6, n = panel * kW4PanelRows + (e & 63);
-        float v = 0.f;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sums_full[buf]);
+      if (++buf == 2) {
+        buf = 0;
+        bphase ^= 1;
+      }
+      if (!known) item = next_item();
+    }
+  } else {
+    // ---------------------------------------------------------------- finishing warp: an item's sums over the warps
+    int buf = 0, finished = 0;
+    uint32_t bphase = 0;
+    for (;;) {
+      const Item it = next_item();
+      if (it.slot < 0) break;
+      bool ok = mbar_wait_bounded(&sums_full[buf], bphase, abort_flag, a.err, kPipelineTimeoutNs);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      const int count = plan.slot_count[it.slot], parts = min(it.blocks, kWarps);
+      const float *r[kWarps];
 #pragma unroll
-        for (int u = 0; u < kWarps; ++u) v += red[u * kRedFloats + j * kW4Pitch + (e & 63)];
-        if (n < a.H) a.part[static_cast<int64_t>(row_of(j)) * a.H + n] = 16.f * v;
+      for (int u = 0; u < kWarps; ++u) r[u] = reinterpret_cast<const float *>(smem + (u * depth + (u < parts ? s_sums[buf][u] : 0)) * kBytes);
+      if (it.up) {
+        const int n = it.panel * 32 + lane;
+        for (int j = 0; j < count; ++j) {
+          float gate = 0.f, lift = 0.f;
+#pragma unroll
+          for (int u = 0; u < kWarps; ++u) {
+            if (u < parts) {
+              gate += r[u][j * kW4Pitch + lane];
+              lift += r[u][j * kW4Pitch + 32 + lane];
+            }
+          }
+          if (n < a.I) a.h[static_cast<int64_t>(row_of(it.slot, j)) * a.I + n] = T::one(activate(a.act, 16.f * gate) * (16.f * lift));
+        }
+      } else {
+        const int n = it.panel * kW4PanelRows + 2 * lane;  // H is even
+        for (int j = 0; j < count; ++j) {
+          float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+          for (int u = 0; u < kWarps; ++u) {
+            if (u < parts) {
+              const float2 p = *reinterpret_cast<const float2 *>(r[u] + j * kW4Pitch + 2 * lane);
+              v.x += p.x, v.y += p.y;
+            }
+          }
+          if (n < a.H) *reinterpret_cast<float2 *>(a.part + static_cast<int64_t>(row_of(it.slot, j)) * a.H + n) = make_float2(16.f * v.x, 16.f * v.y);
+        }
+      }
+      // the stages go back to the copies
+      fence_proxy_async_shared();
+      __syncwarp();
+      if (lane < parts) mbar_arrive(&empty[lane][s_sums[buf][lane]]);
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(&sums_empty[buf]);
+        __threadfence();  // the item's results are out
+        if (it.up)
+          atomicAdd(slot_done + it.slot, 1);
+        else if (atomicAdd(panel_done + it.panel, 1) == slots - 1)
+          s_panels[finished++] = static_cast<uint16_t>(it.panel);
+      }
+      if (++buf == 2) {
+        buf = 0;
+        bphase ^= 1;
       }
     }
-    consumers_meet();
-    if (tid == 0) {  // the item's results are out
-      __threadfence();
-      int last = -1;
-      if (up)
-        atomicAdd(slot_done + slot, 1);
-      else if (atomicAdd(panel_done + panel, 1) == slots - 1)
-        last = panel;
-      __threadfence();
-      s_finish = last;
+    if (lane == 0) {
+      __threadfence();  // behind the counts that were seen full
+      s_finished = finished;
+    }
+  }
+  // Panels of y to which this CTA was the last to add: a token's experts in the order of its top k, then the shared one.
+  __syncwarp();
+  asm volatile("bar.sync 1, %0;" ::"n"((kWarps + 1) * 32) : "memory");
+  for (int i = 0; i < s_finished; ++i) {
+    for (int e = tid; e < a.T * (kW4PanelRows / 2); e += (kWarps + 1) * 32) {
+      const int row = e / (kW4PanelRows / 2), n = s_panels[i] * kW4PanelRows + 2 * (e % (kW4PanelRows / 2));
+      if (n >= a.H) continue;
+      const float2 *p = reinterpret_cast<const float2 *>(a.part + static_cast<int64_t>(row) * a.topk * a.H + n);
+      float2 v = make_float2(0.f, 0.f);
+#pragma unroll 4
+      for (int j = 0; j < a.topk; ++j) {
+        const float2 u = __ldcg(p + static_cast<int64_t>(j) * (a.H / 2));
+        const float w = plan.weight[row * a.topk + j];
+        v.x = fmaf(w, u.x, v.x), v.y = fmaf(w, u.y, v.y);
+      }
+      if (shared_slots) {
+        const float2 u = __ldcg(reinterpret_cast<const float2 *>(a.part + static_cast<int64_t>(entries + row) * a.H + n));
+        v.x += u.x, v.y += u.y;
+      }
+      *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.y) + static_cast<int64_t>(row) * a.H + n) = T::pack(v.x, v.y);
     }
   }
 }
@@ -467,11 +577,10 @@ template <class T, int kGpb, bool kZeros>
 cudaError_t experts_as(const W4MoeArgs &a, int sms, cudaStream_t s) {
   constexpr int kBytes = w4_block_bytes(kGpb, kZeros);
   // two CTAs to an SM of 228 KB, of which each CTA's static part and 1 KB of the system's go off
-  constexpr int kRed = kWarps * kRedFloats * 4, kStatic = 8192;
-  constexpr int kFit = (233472 / 2 - 1024 - kStatic - kRed) / kBytes, kStages = kFit < kMaxStages ? kFit : kMaxStages;
-  static_assert(kStages >= kWarps, "a stage for each warp");
-  static_assert(sizeof(Plan) + (2 * kMaxStages + 2 * kItems) * 8 + 64 <= kStatic, "static shared memory");
-  constexpr int kSmem = kStages * kBytes + kRed;
+  constexpr int kStatic = 8192, kFit = (233472 / 2 - 1024 - kStatic) / (kWarps * kBytes), kDepth = kFit < kMaxDepth ? kFit : kMaxDepth;
+  constexpr int kSmem = kDepth * kWarps * kBytes;
+  static_assert(kDepth >= 2 && sizeof(PlanScratch) <= kSmem && kBytes >= 8 * kW4Pitch * 4, "rings, scratch and sums");
+  static_assert(sizeof(Plan) + 2 * kWarps * kMaxDepth * 8 + kItems * 32 + kW4MoeMaxDim / kW4PanelRows * 2 + 256 <= kStatic, "static shared memory");
   auto kernel = w4_moe_experts_kernel<T, kGpb, kZeros>;
   static std::atomic<bool> ready[64];
   int dev = 0;
@@ -487,7 +596,7 @@ cudaError_t experts_as(const W4MoeArgs &a, int sms, cudaStream_t s) {
   const int64_t most = static_cast<int64_t>(a.T * a.topk + (a.sh13 ? (a.T + 7) / 8 : 0)) *
                        ((a.I + 31) / 32 + (a.H + kW4PanelRows - 1) / kW4PanelRows);
   const int64_t ctas = most < 2 * sms ? most : 2 * sms;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), kSmem, s, a, kStages);
+  return launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), kSmem, s, a, kDepth);
 }
 
 template <class T>

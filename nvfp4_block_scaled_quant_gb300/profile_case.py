@@ -12,6 +12,9 @@
     python -m nvfp4_block_scaled_quant_gb300.profile_case fp8 --M 4096 --iters 3
     python -m nvfp4_block_scaled_quant_gb300.profile_case gated --M 4096 --iters 3
     python -m nvfp4_block_scaled_quant_gb300.profile_case resnorm --M 8192 --iters 3
+    python -m nvfp4_block_scaled_quant_gb300.profile_case w4 --M 4096 --iters 3
+    python -m nvfp4_block_scaled_quant_gb300.profile_case w4moe --T 8 --experts 64 --iters 3
+    python -m nvfp4_block_scaled_quant_gb300.profile_case norm8 --M 4096 --iters 3
 
 ``moe`` runs 128-token prefill chunks (hidden 7168, intermediate 2048, top-8
 Zipf(1.1) routing, shared expert; ``--T`` above 1 sets the batch instead, e.g.
@@ -28,7 +31,9 @@ sweep's activations); ``linear`` the dense 1536 -> 16384 linear and ``grouped`` 
 fixed-group 8 x (4096 -> 1024) linear at ``--M`` tokens.  ``fp8`` runs the FP8 block-scaled
 linear (7168 -> 2048 of one token, else 7168 -> 7168), ``gated`` the gated linear
 7168 -> 2 x 2048 in bf16 (or fp16) and ``resnorm`` the residual norm over 7168 columns, both with
-their gradients above one token.
+their gradients above one token.  ``w4`` runs the linear layer on 4-bit weights (7168 -> 2048 of one token, else
+7168 -> 7168; groups of 128), ``w4moe`` the layer of ``--experts`` such experts (hidden 7168, intermediate 2048, top-8,
+shared expert) and ``norm8`` the residual norm with both outputs over 7168 columns.
 """
 
 from __future__ import annotations
@@ -44,7 +49,7 @@ from . import build as B
 def main(argv=None):
     p = argparse.ArgumentParser()
     p.add_argument("case", choices=["moe", "decode", "gemm", "linear", "grouped", "dispatch", "norm", "router", "quant", "fp8",
-                                "gated", "resnorm"])
+                                "gated", "resnorm", "w4", "w4moe", "norm8"])
     p.add_argument("--T", type=int, default=1)
     p.add_argument("--experts", type=int, default=64)
     p.add_argument("--M", type=int, default=4096)
@@ -150,6 +155,31 @@ def main(argv=None):
             else:
                 _, _, st = ops.residual_norm(f, r, ga, gamma_before=gb, save=True)
                 ops.residual_norm_backward(dr, dy, f, r, st, ga, gamma_before=gb)
+    elif a.case in ("w4", "w4moe"):
+        g = torch.Generator(device=dev).manual_seed(71)
+
+        def weights(*shape, gated=False):  # codes at random, scales of trained weights
+            scales = torch.rand(*shape[:-1], shape[-1] // 128, generator=g, device=dev) * 0.005 + 0.001
+            return ops.w4_prepare(torch.randint(256, (*shape[:-1], shape[-1] // 2), generator=g, device=dev, dtype=torch.uint8),
+                                  scales.bfloat16(), gated=gated)
+
+        if a.case == "w4":
+            w = weights(2048 if a.M == 1 else 7168, 7168)
+            x = workloads.activations(a.M, 7168, seed=72, device=dev)
+            for _ in range(a.iters):
+                ops.w4_linear(x, w)
+        else:
+            H, I, E = 7168, 2048, a.experts
+            w13, w2 = weights(E, 2 * I, H, gated=True), weights(E, H, I)
+            s13, s2 = weights(2 * I, H, gated=True), weights(H, I)
+            router = workloads.weight(E, H, 73, dev)
+            for i in range(a.iters):
+                ops.w4_moe(workloads.activations(a.T, H, seed=74 + i, device=dev), router, w13, w2, 8, shared13=s13, shared2=s2)
+    elif a.case == "norm8":
+        f, r = (workloads.activations(a.M, 7168, seed=s, device=dev) for s in (63, 64))
+        ga, gb = (workloads.norm_weight(7168, seed=s, device=dev) for s in (5, 6))
+        for _ in range(a.iters):
+            ops.residual_norm_fp8(f, r, gb, gamma_after=ga, want_y=True)
     elif a.case == "grouped":
         _, G, K, N = workloads.GROUPED_LINEAR.get(a.M, (a.M, 8, 4096, 1024))
         gw = model.make_grouped_weight(G, N, K, seed=90, device=dev)
