@@ -382,8 +382,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
           f.v[c][0] = b * kW4BlockK + 32 * c + 8 * t < width ? __ldcg(reinterpret_cast<const uint4 *>(p + 32 * c)) : make_uint4(0u, 0u, 0u, 0u);
       }
     };
-    bool ok = true, have = false;  // have: the item's first activations are loaded
-    W4Frag<1> f, f2;
+    bool ok = true;
     while (item.slot >= 0) {
       const Item it = item;
       if (!it.up && ready != it.slot) {  // its h is complete
@@ -400,52 +399,22 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
         if (!ok) break;
         ready = it.slot;
       }
-      if (!have && warp < it.blocks) {
-        open(it);
-        load_x(warp, f);
-      }
-      have = false;
-      bool known = false;  // the next item
+      open(it);
       uint64_t sums[4][1][2] = {};
-      // one block with the activations in f, the next one's on their way to `ahead`
-      auto step = [&](int b, const W4Frag<1> &f, W4Frag<1> &ahead) {
-        const bool last = b + kWarps >= it.blocks;
-        if (!last) {
-          load_x(b + kWarps, ahead);
-        } else if (__all_sync(0xffffffffu, mbar_try_wait(&item_full[q], qphase))) {
-          // the next item's activations, if it is known and they are there
-          item = next_item();
-          known = true;
-          if (item.slot >= 0) {
-            if (!item.up && ready != item.slot && __all_sync(0xffffffffu, load_acquire(slot_done + item.slot) >= panels13))
-              ready = item.slot;
-            if (warp < item.blocks && (item.up || ready == item.slot)) {
-              open(item);
-              load_x(warp, ahead);
-              have = true;
-            }
-          }
-        }
+      for (int b = warp; b < it.blocks; b += kWarps) {
+        W4Frag<1> f;
+        load_x(b, f);
         ok = mbar_wait_bounded(&full[warp][stage], phase, abort_flag, a.err, kPipelineTimeoutNs);
         ok = __all_sync(0xffffffffu, ok);
-        if (!ok) return;
+        if (!ok) break;
         w4_block<T, kGpb, kZeros, 1>(ring + stage * kBytes, f, sums);
         __syncwarp();
-        if (last) return;  // the item's sums go where its last block was
+        if (b + kWarps >= it.blocks) break;  // the item's sums go where its last block was
         if (lane == 0) mbar_arrive(&empty[warp][stage]);
         if (++stage == depth) {
           stage = 0;
           phase ^= 1;
         }
-      };
-      for (int b = warp; b < it.blocks; b += 2 * kWarps) {
-        step(b, f, f2);
-        if (!ok || b + kWarps >= it.blocks) {
-          f = f2;
-          break;
-        }
-        step(b + kWarps, f2, f);
-        if (!ok) break;
       }
       ok = ok && mbar_wait_bounded(&sums_empty[buf], bphase ^ 1, abort_flag, a.err, kPipelineTimeoutNs);
       ok = __all_sync(0xffffffffu, ok);
@@ -465,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
         buf = 0;
         bphase ^= 1;
       }
-      if (!known) item = next_item();
+      item = next_item();
     }
   } else {
     // ---------------------------------------------------------------- finishing warp: an item's sums over the warps
