@@ -1,14 +1,19 @@
 // Device code shared by the kernels that stream 4-bit weights through the warp-level tensor instructions: a warp takes
 // prepared blocks of 64 rows x 128 K out of shared memory and adds their products with 8 or 16 tokens to its sums.
 //
-//   y = sum over groups of s (sum over the group of (c - z) x)
-//     = sum over groups of 16 s (sum (1 + c / 16) x - (1 + z / 16) sum x)
+//   y = sum over groups of s (sum (c - z) x) = sum over groups of s (sum c x - z sum x)
 //
-// (1 + c / 16) is exact in bf16 and fp16 and takes one bit operation per pair of codes beside the shift (the code's bits are
-// the top of the mantissa of a number in [1, 2)); taking 8 or z off each weight would cost another one.  sum x of
-// each group and token comes from a fifth row tile whose weights are all one.  Products are exact, sums are fp32; the
-// difference loses at most about three of fp32's 24 bits, where the result is rounded to 8 or 11.  Scales apply to the
-// fp32 sums of their group: no weight is rounded.
+// A code c in the low bits of a bf16 or fp16 number is that number's smallest subnormal times c, and bits 4 to 7 count 16
+// times as much (with bit 7 the exponent of a bf16 becomes 1, whose step is the same): the tensor cores take subnormal operands
+// exactly, so the codes need no conversion at all.  Two masks give the low and high halves of a word's even bytes, one
+// shift and the same masks those of the odd ones: five operations for eight codes, where numbers 1 + c / 16 took
+// seven (these operations bound the product of one token once the weights arrive at the speed of memory: 384 experts, 16
+// tokens 445 -> 405 us).  The step of 2^-133 (bf16) or 2^-24 (fp16) is made up for by the activations: a row
+// is multiplied by a power of two that brings its largest magnitude to 2^60 (2^14) on its way into the MMA, the elements
+// that meet high halves by a sixteenth of it, and the sums by the inverse.  In bf16 nothing is lost by that; in
+// fp16 an element keeps everything down to 2^-36 of its row's largest.
+// sum x of each group and token comes from a fifth row tile whose codes are all one.  Products are exact, sums are
+// fp32, scales apply to the fp32 sums of their group: no weight is rounded.
 #pragma once
 
 #include "mma16x8.cuh"
@@ -16,18 +21,40 @@
 
 namespace nvfp4 {
 
+// The power of two of a row of activations: kTop - exponent of the largest magnitude, at most kMost; kStep: minus the
+// exponent of the smallest subnormal.
 template <class T>
-struct W4Bits;
+struct W4Scale;
 template <>
-struct W4Bits<Bf16> {
-  static constexpr uint32_t kMask = 0x00780078u, kOne = 0x3F803F80u;
-  static constexpr int kRotate = 3;
+struct W4Scale<Bf16> {
+  static constexpr int kTop = 60, kMost = 126, kStep = 133, kMantissa = 7, kBias = 127;
 };
 template <>
-struct W4Bits<Fp16> {
-  static constexpr uint32_t kMask = 0x03C003C0u, kOne = 0x3C003C00u;
-  static constexpr int kRotate = 6;
+struct W4Scale<Fp16> {
+  static constexpr int kTop = 14, kMost = 15, kStep = 24, kMantissa = 10, kBias = 15;
 };
+// ... from the bits of the row's largest magnitude (infinity and NaN included).
+template <class T>
+__device__ __forceinline__ int w4_power(uint32_t max_bits) {
+  using S = W4Scale<T>;
+  return min(S::kTop - (static_cast<int>(max_bits >> S::kMantissa) - S::kBias), S::kMost);
+}
+__device__ __forceinline__ float power_of_two(int e) { return __int_as_float((127 + e) << 23); }
+// A sum of products back in its own size: by 2^(kStep - power) in two steps, which stay in fp32's range.
+template <class T>
+__device__ __forceinline__ float w4_unscale(float sum, int power) {
+  const int e = W4Scale<T>::kStep - power, half = e / 2;
+  return sum * power_of_two(half) * power_of_two(e - half);
+}
+template <class T>
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  if constexpr (T::kCode == NVFP4_DT_BF16)
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  else
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
 
 // D = A B, or D += A B, of 16 x 16 by 16 x 8 with fp32 sums.
 template <class T>
@@ -43,15 +70,19 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
-// A word of eight codes -> (1 + c / 16) of its four pairs.
-template <class T>
+// The largest |element| of eight 16-bit elements, as bits (NaN orders above infinity).
+__device__ __forceinline__ uint32_t w4_max_abs(const uint4 v) {
+  const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
+  return max(m & 0xFFFFu, m >> 16);
+}
+
+// A word of eight codes -> its pairs: low halves of the bytes (elements 0, 1 and 2, 3), high halves (4, 5 and 6, 7).
 __device__ __forceinline__ void w4_unpack(uint32_t w, uint32_t (&p)[4]) {
-  // written as one operation: with both constants as immediates the compiler takes two (the pair of constants stays in registers)
-#pragma unroll
-  for (int j = 0; j < 4; ++j)
-    asm("lop3.b32 %0, %1, %2, %3, 0xEA;"
-        : "=r"(p[j])
-        : "r"(j ? __funnelshift_r(w, w, 4 * j) : w), "r"(W4Bits<T>::kMask), "r"(W4Bits<T>::kOne));
+  const uint32_t v = w >> 8;
+  p[0] = w & 0x000F000Fu;
+  p[1] = v & 0x000F000Fu;
+  p[2] = w & 0x00F000F0u;
+  p[3] = v & 0x00F000F0u;
 }
 
 // A lane's activations of one K block: for each chunk of 32 K and tile of 8 tokens the eight elements 32 c + 8 t .. of
@@ -60,24 +91,41 @@ template <int kNT>
 struct W4Frag {
   uint4 v[4][kNT];
 };
+// The factors of a token's elements, 2^power and a sixteenth of it, in both halves of a word.
+struct W4Factor {
+  uint32_t low, high;
+};
+template <class T>
+__device__ __forceinline__ W4Factor w4_factor(int power) {
+  using S = W4Scale<T>;
+  const uint32_t low = static_cast<uint32_t>(power + S::kBias) << S::kMantissa;
+  return {low * 0x10001u, (low - (4u << S::kMantissa)) * 0x10001u};
+}
+template <class T>
+__device__ __forceinline__ uint4 w4_scaled(const uint4 v, const W4Factor f) {
+  return make_uint4(mul2<T>(v.x, f.low), mul2<T>(v.y, f.low), mul2<T>(v.z, f.high), mul2<T>(v.w, f.high));
+}
 
-// sums += block * x.  sums[i][n] is the C fragment of row tile i and token tile n, two tokens of a row to a pair, without
-// the factor 16.
+// sums += block * x with the rows of x multiplied by their powers of two.  sums[i][n] is the C fragment of row tile i and
+// token tile n, two tokens of a row to a pair.
 template <class T, int kGpb, bool kZeros, int kNT>
-__device__ __forceinline__ void w4_block(const uint8_t *block, const W4Frag<kNT> &x, uint64_t (&sums)[4][kNT][2]) {
+__device__ __forceinline__ void w4_block(const uint8_t *block, const W4Frag<kNT> &raw, const W4Factor (&factor)[kNT], uint64_t (&sums)[4][kNT][2]) {
   const int lane = threadIdx.x & 31, g = lane >> 2;
   constexpr int kChunks = 4 / kGpb;  // of a group
-  const uint32_t ones[4] = {W4Bits<T>::kOne, W4Bits<T>::kOne, W4Bits<T>::kOne, W4Bits<T>::kOne};
+  const uint32_t low1[4] = {0x00010001u, 0x00010001u, 0x00010001u, 0x00010001u};
+  const uint32_t high1[4] = {0x00100010u, 0x00100010u, 0x00100010u, 0x00100010u};
 #pragma unroll
   for (int gi = 0; gi < kGpb; ++gi) {
     float acc[4][kNT][4], sx[kNT][4];  // a group's first MMAs start them
 #pragma unroll
     for (int cc = 0; cc < kChunks; ++cc) {
       const int c = gi * kChunks + cc;
+      uint4 x[kNT];
 #pragma unroll
       for (int n = 0; n < kNT; ++n) {
-        mma16816<T>(sx[n], ones, x.v[c][n].x, x.v[c][n].y, cc != 0);
-        mma16816<T>(sx[n], ones, x.v[c][n].z, x.v[c][n].w);
+        x[n] = w4_scaled<T>(raw.v[c][n], factor[n]);
+        mma16816<T>(sx[n], low1, x[n].x, x[n].y, cc != 0);
+        mma16816<T>(sx[n], high1, x[n].z, x[n].w);
       }
 #pragma unroll
       for (int pair = 0; pair < 2; ++pair) {
@@ -86,14 +134,14 @@ __device__ __forceinline__ void w4_block(const uint8_t *block, const W4Frag<kNT>
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
           uint32_t lo[4], hi[4];
-          w4_unpack<T>(w[2 * s], lo);
-          w4_unpack<T>(w[2 * s + 1], hi);
+          w4_unpack(w[2 * s], lo);
+          w4_unpack(w[2 * s + 1], hi);
           const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
           const int i = 2 * pair + s;
 #pragma unroll
           for (int n = 0; n < kNT; ++n) {
-            mma16816<T>(acc[i][n], a0, x.v[c][n].x, x.v[c][n].y, cc != 0);
-            mma16816<T>(acc[i][n], a1, x.v[c][n].z, x.v[c][n].w);
+            mma16816<T>(acc[i][n], a0, x[n].x, x[n].y, cc != 0);
+            mma16816<T>(acc[i][n], a1, x[n].z, x[n].w);
           }
         }
       }
@@ -108,11 +156,11 @@ __device__ __forceinline__ void w4_block(const uint8_t *block, const W4Frag<kNT>
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float s0 = T::lo(sw[i]), s1 = T::hi(sw[i]);
-      float z0 = -1.5f, z1 = -1.5f;
+      float z0 = -8.f, z1 = -8.f;
       if constexpr (kZeros) {
         const uint32_t zz = zw[i >> 1] >> (16 * (i & 1));
-        z0 = -1.f - 0.0625f * static_cast<float>(zz & 0xFFu);
-        z1 = -1.f - 0.0625f * static_cast<float>((zz >> 8) & 0xFFu);
+        z0 = -static_cast<float>(zz & 0xFFu);
+        z1 = -static_cast<float>((zz >> 8) & 0xFFu);
       }
       const uint64_t s00 = pack_f32x2(s0, s0), s11 = pack_f32x2(s1, s1), z00 = pack_f32x2(z0, z0), z11 = pack_f32x2(z1, z1);
 #pragma unroll

@@ -14,9 +14,8 @@ namespace nvfp4 {
 // m16n8k16 A fragments with 16-byte loads.  A lane (g = lane / 4, t = lane % 4) finds four words of eight codes: K
 // elements 32 c + 8 t .. + 7 of rows 32 p + {0, 8, 16, 24} + g.  The order of K inside an MMA is free as long as both
 // operands agree, so a word's eight elements are the lane's share of two MMAs: elements 0..3 of the first, 4..7 of
-// the second, and the activations need no reordering either.  In a word, element 2 j sits in bits 4 j .. 4 j + 3 and element
-// 2 j + 1 in bits 4 j + 16 .., the word rotated left so that j = 0 lies at the top of the 16-bit type's mantissa:
-// (word rotated right by 4 j) & mask | one gives the pair (1 + c / 16) in both halves.
+// the second, and the activations need no reordering.  In a word, elements 0 to 7 sit in bits 0, 16, 8, 24, 4, 20, 12 and 28:
+// the pairs of the first MMA are the low halves of the bytes, those of the second the high halves.
 // Rows and columns that the matrix does not have hold zeros.  A gated matrix (gate rows [0, N / 2), up rows [N / 2, N))
 // has 32 gate rows and the 32 up rows of the same outputs in each panel: tiles 0, 1 and 2, 3.
 constexpr int kW4PanelRows = 64;
@@ -26,8 +25,8 @@ constexpr int w4_block_bytes(int groups, bool zeros) { return kW4CodeBytes + kW4
 inline int64_t w4_panels(int64_t N, bool gated) { return gated ? (N / 2 + 31) / 32 : (N + kW4PanelRows - 1) / kW4PanelRows; }
 inline int64_t w4_blocks(int64_t K) { return (K + kW4BlockK - 1) / kW4BlockK; }
 
-cudaError_t launch_w4_prepare(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int dtype, int64_t G,
-                              int64_t N, int64_t K, int group, bool gated, uint8_t *out, cudaStream_t s);
+cudaError_t launch_w4_prepare(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int64_t G, int64_t N,
+                              int64_t K, int group, bool gated, uint8_t *out, cudaStream_t s);
 
 struct W4Args {
   const void *x;  // 16-bit (M, K), row stride ldx
@@ -52,13 +51,17 @@ struct W4MoeArgs {
   float *logits;                                // (T, E)
   uint16_t *h;                                  // (rows, I), row t * topk + j, then the shared expert's T rows
   float *part;                                  // (rows, H)
-  int *counters;                                // kW4MoeCounters + slots + panels of y, zeroed by the router kernel
+  int *counters;                                // kW4MoeCounters words and the panels of y, zeroed by the router kernel
+  uint32_t *x_max;                              // (T), the bits of the largest magnitude of each row of x
   uint32_t *err;
 };
 constexpr int kW4MoeMaxT = 64, kW4MoeMaxEntries = 512, kW4MoeMaxK = 16;
 constexpr int kW4MoeMaxSlots = kW4MoeMaxEntries + kW4MoeMaxT / 8;
 constexpr int64_t kW4MoeMaxExperts = 1024, kW4MoeMaxDim = 16384;
-constexpr int kW4MoeCounters = 32;  // the item counter, on a cache line of its own
+// The counters: the item counter on a cache line of its own, the finished panels of h of each slot, the bits of the largest
+// magnitude of each row of h, and behind them the finished slots of each panel of y.
+constexpr int kW4MoeRows = kW4MoeMaxEntries + kW4MoeMaxT;
+constexpr int kW4MoeSlotDone = 32, kW4MoeRowMax = kW4MoeSlotDone + kW4MoeMaxSlots, kW4MoeCounters = kW4MoeRowMax + kW4MoeRows;
 cudaError_t launch_w4_moe(const W4MoeArgs &a, int dtype, int group, bool zeros, int sms, cudaStream_t s);
 
 }  // namespace nvfp4

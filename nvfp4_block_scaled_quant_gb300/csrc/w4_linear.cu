@@ -18,7 +18,7 @@ namespace {
 // One block of prepared weights per CTA of 256 threads, 16 bytes of codes each.  Runs once, at load time.
 __global__ void __launch_bounds__(256) w4_prepare_kernel(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros,
                                                          int64_t N, int64_t K, int64_t panels, int64_t blocks, int group,
-                                                         bool gated, int rotate, uint8_t *out, int block_bytes) {
+                                                         bool gated, uint8_t *out, int block_bytes) {
   pdl_wait();  // no trigger: the next launch may read weights early
   const int64_t id = blockIdx.x, b = id % blocks, p = id / blocks % panels, m = id / blocks / panels;
   const int64_t n_groups = (K + group - 1) / group;
@@ -38,8 +38,8 @@ __global__ void __launch_bounds__(256) w4_prepare_kernel(const uint8_t *codes, c
     const uint32_t v = row >= 0 && k < K ? *reinterpret_cast<const uint32_t *>(codes + ((m * N + row) * K + k) / 2) : 0u;
     uint32_t w = 0;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w |= ((v >> (4 * e)) & 15u) << (4 * (e >> 1) + 16 * (e & 1));
-    word[i] = __funnelshift_l(w, w, rotate);
+    for (int e = 0; e < 8; ++e) w |= ((v >> (4 * e)) & 15u) << (16 * (e & 1) + 8 * ((e >> 1) & 1) + 4 * (e >> 2));
+    word[i] = w;
   }
   reinterpret_cast<uint4 *>(dst)[tid] = make_uint4(word[0], word[1], word[2], word[3]);
   const int groups = kW4BlockK / group;
@@ -61,13 +61,13 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_stream_kernel(const W4Args 
   constexpr int kBytes = w4_block_bytes(kGpb, kZeros), kTok = 8 * kNT;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kWarps][4];
-  __shared__ int s_abort;
+  __shared__ int s_abort, s_power[kTok];
   volatile int *abort_flag = &s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rank = static_cast<int>(blockIdx.x) % splits, panel = static_cast<int>(blockIdx.x) / splits;
   const int m0 = static_cast<int>(blockIdx.y) * kTok, tokens = min(kTok, a.M - m0);
   const int blocks = (a.K + kW4BlockK - 1) / kW4BlockK;
-  const int kb0 = blocks * rank / splits + warp, kb1 = blocks * (rank + 1) / splits;
+  const int first = blocks * rank / splits, kb0 = first + warp, kb1 = blocks * (rank + 1) / splits;
   uint8_t *ring = smem + warp * depth * kBytes;
   const uint8_t *w = a.w + static_cast<int64_t>(panel) * blocks * kBytes;
   const uint64_t pol = policy_evict_normal();
@@ -83,6 +83,23 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_stream_kernel(const W4Args 
   __syncthreads();
   pdl_wait();
   pdl_trigger();
+
+  // the powers of two of the rows' parts that this CTA multiplies
+  for (int j = warp; j < kTok; j += kWarps) {
+    uint32_t m = 0;
+    if (j < tokens) {
+      const uint16_t *row = static_cast<const uint16_t *>(a.x) + (m0 + j) * a.ldx;
+      const int end = min(kb1 * kW4BlockK, a.K);
+#pragma unroll 4
+      for (int k = first * kW4BlockK + 8 * lane; k < end; k += 256) m = max(m, w4_max_abs(__ldg(reinterpret_cast<const uint4 *>(row + k))));
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (lane == 0) s_power[j] = w4_power<T>(m);
+  }
+  __syncthreads();
+  W4Factor factor[kNT];
+#pragma unroll
+  for (int n = 0; n < kNT; ++n) factor[n] = w4_factor<T>(s_power[8 * n + g]);
 
   uint64_t sums[4][kNT][2] = {};
   const uint16_t *x = static_cast<const uint16_t *>(a.x) + (m0 + g) * a.ldx + 8 * t;
@@ -106,7 +123,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_stream_kernel(const W4Args 
     ok = mbar_wait_bounded(&full[warp][stage], phase, abort_flag, a.err, kPipelineTimeoutNs);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
-    w4_block<T, kGpb, kZeros, kNT>(ring + stage * kBytes, f, sums);
+    w4_block<T, kGpb, kZeros, kNT>(ring + stage * kBytes, f, factor, sums);
     __syncwarp();
     if (lane == 0 && kb + depth * kWarps < kb1) {
       mbar_arrive_expect_tx(&full[warp][stage], kBytes);
@@ -132,7 +149,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_stream_kernel(const W4Args 
     float v = part[at];
 #pragma unroll
     for (int u = 1; u < kWarps; ++u) v += part[u * pitch + at];
-    part[at] = v;
+    part[at] = w4_unscale<T>(v, s_power[e >> 6]);
   }
   block_meet();
   if (splits > 1) cluster_meet();
@@ -155,7 +172,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_stream_kernel(const W4Args 
 #pragma unroll
       for (int r = 1; r < 8; ++r)
         if (r < splits) s += v[r];
-      if (n < a.N) static_cast<uint16_t *>(a.y)[static_cast<int64_t>(m0 + (e >> 6)) * a.N + n] = T::one(16.f * s);
+      if (n < a.N) static_cast<uint16_t *>(a.y)[static_cast<int64_t>(m0 + (e >> 6)) * a.N + n] = T::one(s);
     }
   }
   if (splits > 1) cluster_meet();  // no CTA leaves while another reads its sums
@@ -209,12 +226,11 @@ cudaError_t stream_group(const W4Args &a, int group, bool zeros, int tok8, int s
 
 }  // namespace
 
-cudaError_t launch_w4_prepare(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int dtype, int64_t G,
-                              int64_t N, int64_t K, int group, bool gated, uint8_t *out, cudaStream_t s) {
+cudaError_t launch_w4_prepare(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int64_t G, int64_t N,
+                              int64_t K, int group, bool gated, uint8_t *out, cudaStream_t s) {
   const int64_t panels = w4_panels(N, gated), blocks = w4_blocks(K);
-  const int rotate = dtype == NVFP4_DT_BF16 ? W4Bits<Bf16>::kRotate : W4Bits<Fp16>::kRotate;
   return launch_pdl(w4_prepare_kernel, dim3(static_cast<unsigned>(G * panels * blocks)), dim3(256), 0, s, codes, scales, zeros,
-                    N, K, panels, blocks, group, gated, rotate, out, w4_block_bytes(kW4BlockK / group, zeros != nullptr));
+                    N, K, panels, blocks, group, gated, out, w4_block_bytes(kW4BlockK / group, zeros != nullptr));
 }
 
 cudaError_t launch_w4_stream(const W4Args &a, int dtype, int group, bool zeros, int tok8, int splits, int depth,

@@ -33,6 +33,9 @@ constexpr int kLogitMaxSplit = 8;
 template <class T, int kNT>
 __global__ void __launch_bounds__(kLogitWarps * 32) w4_moe_logits_kernel(const W4MoeArgs a, int splits, int n_counters) {
   __shared__ float part[kLogitWarps][16 * 8 * kNT];
+  __shared__ uint32_t s_max[8 * kNT];
+  if (threadIdx.x < 8 * kNT) s_max[threadIdx.x] = 0u;
+  __syncthreads();
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -43,6 +46,7 @@ __global__ void __launch_bounds__(kLogitWarps * 32) w4_moe_logits_kernel(const W
   const uint16_t *x = static_cast<const uint16_t *>(a.x) + g * a.ldx + 8 * t;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   float acc[kNT][4] = {};
+  uint32_t top[kNT] = {};  // of the tokens' elements, needed once: the first 16 experts' cluster keeps it
 #pragma unroll(kNT == 1 ? 4 : 2)
   for (int c = c0 + warp; c < c1; c += kLogitWarps) {
     const int k = 32 * c;
@@ -53,6 +57,7 @@ __global__ void __launch_bounds__(kLogitWarps * 32) w4_moe_logits_kernel(const W
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
       const uint4 b = in && 8 * n + g < a.T ? __ldg(reinterpret_cast<const uint4 *>(x + 8 * n * a.ldx + k)) : zero;
+      if (tile == 0) top[n] = max(top[n], w4_max_abs(b));
       mma16816<T>(acc[n], a0, b.x, b.y);
       mma16816<T>(acc[n], a1, b.z, b.w);
     }
@@ -61,6 +66,10 @@ __global__ void __launch_bounds__(kLogitWarps * 32) w4_moe_logits_kernel(const W
   for (int n = 0; n < kNT; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) part[warp][(8 * n + 2 * t + (e & 1)) * 16 + 8 * (e >> 1) + g] = acc[n][e];
+  if (tile == 0) {
+#pragma unroll
+    for (int n = 0; n < kNT; ++n) atomicMax(&s_max[8 * n + g], top[n]);
+  }
   __syncthreads();
   const int live = 16 * min(a.T, 8 * kNT);
   for (int e = threadIdx.x; e < live; e += kLogitWarps * 32) {
@@ -90,6 +99,16 @@ __global__ void __launch_bounds__(kLogitWarps * 32) w4_moe_logits_kernel(const W
     const int expert = tile * 16 + (e & 15);
     if (expert < a.E) a.logits[static_cast<int64_t>(e >> 4) * a.E + expert] = s;
   }
+  if (tile == 0 && rank == 0 && threadIdx.x < a.T) {
+    uint32_t m = 0;
+    for (int r = 0; r < splits; ++r) {
+      uint32_t addr, v;
+      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(s_max) + threadIdx.x * 4), "r"(r));
+      asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+      m = max(m, v);
+    }
+    a.x_max[threadIdx.x] = m;
+  }
   if (splits > 1) cluster_meet();
 }
 
@@ -106,6 +125,7 @@ struct Plan {
   uint16_t slot_expert[kW4MoeMaxSlots];
   uint16_t slot_first[kW4MoeMaxSlots]; // place of its first entry in `sorted` (shared expert: its first token)
   uint16_t slot_count[kW4MoeMaxSlots];
+  int power[kW4MoeMaxT];               // of two, that the tokens' activations are multiplied by
   int slots, shared_slots;
 };
 // While the plan is made, in the room of the rings: the experts' counts, first places and first slots, and the ids.
@@ -164,9 +184,11 @@ __device__ __forceinline__ void top_k(const float *logits, int E, int topk, uint
 }
 
 // The table of slots: the same in every CTA.
+template <class T>
 __device__ void make_plan(const W4MoeArgs &a, Plan &plan, PlanScratch &s) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, entries = a.T * a.topk;
   for (int e = tid; e < a.E; e += kThreads) s.count[e] = 0;
+  if (tid < a.T) plan.power[tid] = w4_power<T>(__ldcg(a.x_max + tid));
   for (int t = warp; t < a.T; t += kThreads / 32) {
     const float *l = a.logits + static_cast<int64_t>(t) * a.E;
     uint16_t *ids = s.ids + t * a.topk;
@@ -271,11 +293,12 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
   __syncthreads();
   pdl_wait();
   pdl_trigger();
-  make_plan(a, plan, *reinterpret_cast<PlanScratch *>(smem));
+  make_plan<T>(a, plan, *reinterpret_cast<PlanScratch *>(smem));
 
   const int slots = plan.slots, shared_slots = plan.shared_slots, entries = a.T * a.topk;
   const int panels13 = (a.I + 31) / 32, panels2 = (a.H + kW4PanelRows - 1) / kW4PanelRows;
-  int *counter = a.counters, *slot_done = counter + kW4MoeCounters, *panel_done = slot_done + kW4MoeMaxSlots;
+  int *counter = a.counters, *slot_done = counter + kW4MoeSlotDone, *panel_done = counter + kW4MoeCounters;
+  uint32_t *row_max = reinterpret_cast<uint32_t *>(counter + kW4MoeRowMax);
   // the workspace row of a slot's token j
   auto row_of = [&](int slot, int j) {
     const int at = plan.slot_first[slot] + j;
@@ -364,12 +387,14 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
     // of the sums are left where they are.
     const uint16_t *x = nullptr;
     int width = 0;
+    W4Factor factor[1];
     auto open = [&](const Item &it) {
       width = it.up ? a.H : a.I;
       const int row = row_of(it.slot, g < plan.slot_count[it.slot] ? g : 0);
       const int token = row < entries ? static_cast<int>((row * topk_inverse) >> 16) : row - entries;
       x = it.up ? static_cast<const uint16_t *>(a.x) + token * a.ldx : a.h + static_cast<int64_t>(row) * a.I;
       x += 8 * t;
+      factor[0] = w4_factor<T>(it.up ? plan.power[token] : w4_power<T>(__ldcg(row_max + row)));
     };
     auto load_x = [&](int b, W4Frag<1> &f) {
       const uint16_t *p = x + b * kW4BlockK;
@@ -407,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
         ok = mbar_wait_bounded(&full[warp][stage], phase, abort_flag, a.err, kPipelineTimeoutNs);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        w4_block<T, kGpb, kZeros, 1>(ring + stage * kBytes, f, sums);
+        w4_block<T, kGpb, kZeros, 1>(ring + stage * kBytes, f, factor, sums);
         __syncwarp();
         if (b + kWarps >= it.blocks) break;  // the item's sums go where its last block was
         if (lane == 0) mbar_arrive(&empty[warp][stage]);
@@ -461,7 +486,11 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
               lift += r[u][j * kW4Pitch + 32 + lane];
             }
           }
-          if (n < a.I) a.h[static_cast<int64_t>(row_of(it.slot, j)) * a.I + n] = T::one(activate(a.act, 16.f * gate) * (16.f * lift));
+          const int row = row_of(it.slot, j), power = plan.power[row < entries ? row / a.topk : row - entries];
+          const uint16_t h = T::one(activate(a.act, w4_unscale<T>(gate, power)) * w4_unscale<T>(lift, power));
+          if (n < a.I) a.h[static_cast<int64_t>(row) * a.I + n] = h;
+          const uint32_t top = __reduce_max_sync(0xffffffffu, n < a.I ? h & 0x7FFFu : 0u);
+          if (lane == 0) atomicMax(row_max + row, top);
         }
       } else {
         const int n = it.panel * kW4PanelRows + 2 * lane;  // H is even
@@ -474,7 +503,9 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
               v.x += p.x, v.y += p.y;
             }
           }
-          if (n < a.H) *reinterpret_cast<float2 *>(a.part + static_cast<int64_t>(row_of(it.slot, j)) * a.H + n) = make_float2(16.f * v.x, 16.f * v.y);
+          const int row = row_of(it.slot, j), power = w4_power<T>(__ldcg(row_max + row));
+          if (n < a.H)
+            *reinterpret_cast<float2 *>(a.part + static_cast<int64_t>(row) * a.H + n) = make_float2(w4_unscale<T>(v.x, power), w4_unscale<T>(v.y, power));
         }
       }
       // the stages go back to the copies
@@ -575,7 +606,7 @@ cudaError_t moe_as(const W4MoeArgs &a, int group, bool zeros, int sms, cudaStrea
   if (splits > chunks / kLogitWarps) splits = chunks / kLogitWarps;
   if (splits > kLogitMaxSplit) splits = kLogitMaxSplit;
   if (splits < 1) splits = 1;
-  const int n = kW4MoeCounters + kW4MoeMaxSlots + (a.H + kW4PanelRows - 1) / kW4PanelRows;
+  const int n = kW4MoeCounters + (a.H + kW4PanelRows - 1) / kW4PanelRows;
   cudaError_t e = a.T <= 8 ? logits_as<T, 1>(a, splits, n, s) : a.T <= 16 ? logits_as<T, 2>(a, splits, n, s) : logits_as<T, 8>(a, splits, n, s);
   if (e != cudaSuccess) return e;
   if (group == 128) return zeros ? experts_as<T, 1, true>(a, sms, s) : experts_as<T, 1, false>(a, sms, s);

@@ -25,23 +25,25 @@ def checkpoint(gen, shape, group, zeros, dt, device):
 
 
 def weight(ck, group):
-    """(W, B) of one checkpoint matrix: the real numbers it stands for, and s (32 + c + z), the size of the terms that
+    """(W, B) of one checkpoint matrix: the real numbers it stands for, and s (c + z), the size of the terms that
     the kernels add up for an element."""
     codes, scales, zeros = ck
     N, half = codes.shape
     c = torch.stack([codes & 15, codes >> 4], dim=-1).reshape(N, 2 * half).to(F64)
     s = scales.to(F64).repeat_interleave(group, dim=1)[:, :2 * half]
     z = torch.full_like(c, 8.0) if zeros is None else zeros.to(F64).repeat_interleave(group, dim=1)[:, :2 * half]
-    return (c - z) * s, (32 + c + z) * s
+    return (c - z) * s, (c + z) * s
 
 
 def product(x, ck, group):
     """(y, e) of x W^T: the product and a bound of the fp32 sums' error.  An element passes at most 8 MMAs of
     its group's sum, the difference and the product with the scale, one addition per group, and 16 over warps and
-    CTAs; each is off by at most 2^-23 (the MMA may cut instead of rounding) of the sum of the terms' sizes."""
+    CTAs; each is off by at most 2^-23 (the MMA may cut instead of rounding) of the sum of the terms' sizes.
+    Activations lose what is below 2^-36 of their row's largest."""
     w, b = weight(ck, group)
     steps = 8 + 2 + -(-x.shape[1] // group) + 16
-    return x @ w.T, steps * 2.0 ** -23 * (x.abs() @ b.T)
+    size = x.abs() + 2.0 ** -13 * x.abs().amax(dim=1, keepdim=True) / steps if x.shape[0] else x
+    return x @ w.T, steps * 2.0 ** -23 * (size @ b.T)
 
 
 def act(kind, g):
