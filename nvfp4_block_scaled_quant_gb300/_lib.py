@@ -108,7 +108,8 @@ _SIGNATURES = {
                                         P, P, I64, P, P, P]),
     "nvfp4_w4_prepared_bytes": (c_size_t, [I64, I64, I64, c_int, c_int, c_int]),
     "nvfp4_w4_prepare": (c_int, [P, P, P, c_int, I64, I64, I64, c_int, c_int, P, P]),
-    "nvfp4_w4_linear": (c_int, [P, c_int, I64, I64, I64, I64, P, c_int, c_int, P, P]),
+    "nvfp4_w4_linear_workspace_bytes": (c_size_t, [I64, I64, I64, c_int]),
+    "nvfp4_w4_linear": (c_int, [P, c_int, I64, I64, I64, I64, P, c_int, c_int, P, P, c_size_t, P]),
     "nvfp4_w4_moe_workspace_bytes": (c_size_t, [I64, I64, I64, I64, c_int, c_int]),
     "nvfp4_w4_moe": (c_int, [P, c_int, I64, I64, I64, I64, I64, c_int, P, P, P, P, P, c_int, c_int, c_int, P, P, c_size_t,
                              P]),

@@ -1,6 +1,7 @@
 // Host side of the C ABI of the operators on 4-bit weights with group scales: argument validation, workspace layout and
 // how a product spreads over the GPU.
 #include "abi_util.h"
+#include "tile_gemm.cuh"
 #include "w4.h"
 
 namespace nvfp4 {
@@ -37,6 +38,21 @@ int stream_splits(int64_t ctas, int blocks, int sms) {
     if (best_time == 0 || time < best_time) best_time = time, best = s;
   }
   return best;
+}
+
+// Many tokens: where the written-out weights and their scales are in the workspace.
+constexpr int64_t kStreamMaxTokens = 64;
+struct LinearWs {
+  size_t w, scales, total;
+  int64_t lds;
+};
+LinearWs linear_ws(int64_t M, int64_t N, int64_t K, int group) {
+  LinearWs w = {};
+  if (M <= kStreamMaxTokens) return w;
+  w.lds = round_up(N, 4);
+  w.scales = align256(static_cast<size_t>(N) * static_cast<size_t>(K) * 2);
+  w.total = align256(w.scales + static_cast<size_t>(w.lds) * static_cast<size_t>((K + group - 1) / group) * 4);
+  return w;
 }
 
 struct MoeWs {
@@ -95,8 +111,14 @@ nvfp4_status nvfp4_w4_prepare(const uint8_t *codes, const void *scales, const ui
   return NVFP4_OK;
 }
 
+size_t nvfp4_w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int group) {
+  if (M < 0 || N <= 0 || K <= 0 || K % 8 || !dims_ok(M, K) || !dims_ok(N, K) || !dims_ok(M, N) || (group != 32 && group != 64 && group != 128))
+    return 0;
+  return linear_ws(M, N, K, group).total;
+}
+
 nvfp4_status nvfp4_w4_linear(const void *x, int dtype, int64_t M, int64_t K, int64_t ldx, int64_t N, const uint8_t *w,
-                             int group, int has_zeros, void *y, void *stream) {
+                             int group, int has_zeros, void *y, void *ws, size_t ws_bytes, void *stream) {
   NV_REQUIRE(M >= 0 && K > 0 && N > 0, NVFP4_ERR_INVALID_ARG, "M=%lld K=%lld N=%lld", (long long)M, (long long)K, (long long)N);
   nvfp4_status st = check_w4(__func__, dtype, K, group);
   if (st != NVFP4_OK) return st;
@@ -106,11 +128,15 @@ nvfp4_status nvfp4_w4_linear(const void *x, int dtype, int64_t M, int64_t K, int
   if ((st = check_rows(__func__, x, M, K, ldx)) != NVFP4_OK) return st;
   NV_REQUIRE(aligned(w, 16) && aligned(y, 16), NVFP4_ERR_MISALIGNED, "w and y must be 16-byte aligned");
   const bool zeros = has_zeros != 0;
-  st = check_disjoint(__func__, {{y, M, N, N, 2}}, {{x, M, ldx, K, 2}, flat(w, prepared_bytes(1, N, K, group, zeros, false), 1)});
+  const LinearWs L = linear_ws(M, N, K, group);
+  if ((st = check_ws(__func__, ws, ws_bytes, L.total)) != NVFP4_OK) return st;
+  st = check_disjoint(__func__, {{y, M, N, N, 2}, flat(ws, static_cast<int64_t>(L.total), 1)},
+                      {{x, M, ldx, K, 2}, flat(w, prepared_bytes(1, N, K, group, zeros, false), 1)});
   if (st != NVFP4_OK) return st;
   DeviceInfo *d;
   if ((st = device_info(__func__, &d)) != NVFP4_OK) return st;
   if (M == 0) return NVFP4_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
   W4Args a = {};
   a.x = x;
   a.ldx = ldx;
@@ -120,16 +146,36 @@ nvfp4_status nvfp4_w4_linear(const void *x, int dtype, int64_t M, int64_t K, int
   a.w = w;
   a.y = y;
   a.err = d->flags;
-  const int tok8 = M <= 8 ? 1 : 2, blocks = static_cast<int>(w4_blocks(K));
-  const int splits = stream_splits(w4_panels(N, false) * ((M + 8 * tok8 - 1) / (8 * tok8)), blocks, d->sms);
-  const int rank = (blocks + splits - 1) / splits;
-  int depth = (rank + 7) / 8;
-  const int fit = (233472 / 2 - 2048) / (8 * w4_block_bytes(kW4BlockK / group, zeros));
-  if (depth > fit) depth = fit;
-  if (depth > 4) depth = 4;
-  if (depth < tok8) depth = tok8;  // the ring holds a warp's sums at the end
-  NV_CUDA(launch_w4_stream(a, dtype, group, zeros, tok8, splits, depth, static_cast<cudaStream_t>(stream)),
-          "4-bit linear launch");
+  if (M <= kStreamMaxTokens) {
+    const int tok8 = M <= 8 ? 1 : 2, blocks = static_cast<int>(w4_blocks(K));
+    const int splits = stream_splits(w4_panels(N, false) * ((M + 8 * tok8 - 1) / (8 * tok8)), blocks, d->sms);
+    const int rank = (blocks + splits - 1) / splits;
+    int depth = (rank + 7) / 8;
+    const int fit = (233472 / 2 - 2048) / (8 * w4_block_bytes(kW4BlockK / group, zeros));
+    if (depth > fit) depth = fit;
+    if (depth > 4) depth = 4;
+    if (depth < tok8) depth = tok8;  // the ring holds a warp's sums at the end
+    NV_CUDA(launch_w4_stream(a, dtype, group, zeros, tok8, splits, depth, s), "4-bit linear launch");
+    return NVFP4_OK;
+  }
+  uint16_t *ints = static_cast<uint16_t *>(ws);
+  float *scales = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + L.scales);
+  const int cols = 256;
+  CUtensorMap mw, mx;
+  if ((st = make_map(__func__, &mw, ints, K * 2, N, K * 2, kTHalf)) != NVFP4_OK) return st;
+  if ((st = make_map(__func__, &mx, x, K * 2, M, ldx * 2, cols / 2)) != NVFP4_OK) return st;
+  TileArgs t = {};
+  t.M = a.N;
+  t.N = a.M;
+  t.k_blocks = static_cast<int>((K + 63) / 64);
+  t.groups = static_cast<int>((K + group - 1) / group);
+  t.sa = scales;
+  t.ld_sa = L.lds;
+  t.out = y;
+  t.ldo = N;
+  t.err = d->flags;
+  NV_CUDA(launch_w4_expand(a, dtype, group, zeros, ints, scales, L.lds, s), "4-bit weight expansion launch");
+  NV_CUDA(in_pair_turn(d, s, [&] { return launch_w4_tile_gemm(mw, mx, t, dtype, group, cols, s); }), "4-bit tile GEMM launch");
   return NVFP4_OK;
 }
 

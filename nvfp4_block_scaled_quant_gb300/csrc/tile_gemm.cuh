@@ -20,6 +20,10 @@
 //               longer than the other's MMAs.  Measured and left: four accumulators of 128 columns (two
 //               issuers; 8 warps 200 us, 16 warps 175 us), 16 epilogue warps on 256 columns, two batches
 //               of columns in flight, activation scales through a shared-memory ring.
+//   Op::kW4     A = the codes less their zero points (N, K) as 16-bit integers, B = x (M, K): the same promotion, of
+//               every group of 32, 64 or 128 K with its scale (kAct holds the group's size; one scale per row of A, which the
+//               operands are swapped for: a thread's columns share it).  A group of 128 is two K blocks, one of 32 half a block, which the
+//               two issuers share.  The output is written across: a lane's row is an output column.
 //   Op::kGated  A = x (M, K), B = rows of Wg (even CTA) and the matching rows of Wu (odd CTA):
 //               the first half of the accumulator's columns is g, the second u of the same outputs.
 //   Op::kGrad   two products in one launch.  dx = dg Wg + du Wu: A = [dg | du] in two segments of K = I,
@@ -52,16 +56,17 @@
 
 namespace nvfp4 {
 
-enum class TileOp : int { kFp8 = 0, kGated = 1, kGrad = 2 };
+enum class TileOp : int { kFp8 = 0, kGated = 1, kGrad = 2, kW4 = 3 };
 
 struct TileArgs {
   int M, N;        // output rows and columns (kGated: N = I; kGrad: dx's, M = 0 without it)
   int k_blocks;    // 128-byte K blocks (kGrad: of one of dx's two segments)
   int dw_M, dw_k_blocks, early;  // kGrad: rows of [dWg; dWu] (0 without them), blocks of tokens, see above
-  const float *sa; // kFp8: (K blocks, ld_sa) activation scales
+  const float *sa; // kFp8: (K blocks, ld_sa) activation scales; kW4: (groups, ld_sa) scales of A's rows
   int64_t ld_sa;
   const float *sw; // kFp8: (ceil(N / 128), K blocks) weight scales
-  void *out;       // 16-bit (M, N), row stride ldo
+  void *out;       // 16-bit (M, N), row stride ldo; kW4: (N, M)
+  int groups;      // kW4: of a row
   void *dwg, *dwu; // kGrad: the weight gradients, (dw_M / 2, N) each, row stride ldo
   const float *unscale;  // kGrad, fp16: factor of the sums (the inverse of dg's and du's power of two)
   int64_t ldo;
@@ -92,8 +97,10 @@ constexpr int kTEpiWarps = 8;
 template <TileOp kOp>
 constexpr int kTThreads = (kTEpiWarp0 + kTEpiWarps<kOp>)*32;
 template <TileOp kOp>
-constexpr int kTIssuers = kOp == TileOp::kFp8 ? 2 : 1;
-// kFp8: registers per thread.  The launch gives every warp 168 (three warps on each quarter of an
+constexpr bool kTScaled = kOp == TileOp::kFp8 || kOp == TileOp::kW4;
+template <TileOp kOp>
+constexpr int kTIssuers = kTScaled<kOp> ? 2 : 1;
+// kTScaled: registers per thread.  The launch gives every warp 168 (three warps on each quarter of an
 // SM); the epilogue's 128 sums, scales and accumulator columns in flight take more, which the first four
 // warps give up.
 constexpr int kTLaunchRegs = 168, kTLightRegs = 56, kTEpiRegs = 224;
@@ -110,7 +117,8 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
                      const TileArgs args) {
   using C = TileCfg<kTCols>;
   constexpr int kBRows = kTCols / 2;  // rows of B staged by a CTA
-  constexpr bool kFp8 = kOp == TileOp::kFp8;
+  constexpr bool kFp8 = kOp == TileOp::kFp8, kW4 = kOp == TileOp::kW4, kScaled = kTScaled<kOp>;
+  constexpr bool kHalves = kW4 && kAct == 32;  // a K block holds two groups, one for each issuer
   constexpr bool kGrad = kOp == TileOp::kGrad;
   constexpr int kOutCols = kOp == TileOp::kGated ? kBRows : kTCols;  // output columns of a tile
   constexpr uint32_t kFmt = kFp8 ? 0u : (T::kCode == NVFP4_DT_BF16 ? 1u : 0u);
@@ -134,7 +142,7 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
   if (threadIdx.x == 0) {
     for (int s = 0; s < C::kStages; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 1);
+      mbar_init(&empty[s], kHalves ? 2 : 1);
     }
     for (int b = 0; b < 2; ++b) {
       mbar_init(&tfull[b], 1);
@@ -211,7 +219,7 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
     }
   };
 
-  if constexpr (kFp8) {
+  if constexpr (kScaled) {
     if (warp < kTEpiWarp0)
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kTLightRegs));
     else
@@ -325,7 +333,64 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
           phase ^= 1;
         }
       };
-      if constexpr (kFp8) {
+      if constexpr (kW4) {
+        // The two issuers take the launch's groups in turn, issuer i into accumulator i.  Both follow the ring over
+        // every block.
+        constexpr uint32_t kIdesc = mma_idesc(kFmt, false, false, kTRows, kTCols);
+        constexpr int kSteps = kHalves ? 2 : 4;                   // MMAs of a block and group
+        constexpr int kBlocks = kAct == 128 ? 2 : 1;              // K blocks of a group
+        uint32_t turn = 0, mine = 0;                              // groups seen, and taken by this issuer
+        stage = 0;
+        auto advance = [&] {
+          if (++stage == C::kStages) {
+            stage = 0;
+            phase ^= 1;
+          }
+        };
+        Tile t;
+        for (int at = first; ok && tile_of(at, t); at += step) {
+          for (int g = 0; ok && g < args.groups; ++g, ++turn) {
+            const int n_blocks = kHalves ? ((g & 1) || g + 1 == args.groups) : min(kBlocks, k_blocks - g * kBlocks);
+            if (static_cast<int>(turn & 1) != iss) {
+              if (kHalves && !(g & 1) && g + 1 == args.groups) {
+                // a row's last block holds one group: the other issuer's release of it
+                ok = mbar_wait_bounded_cluster(&full[stage], phase, abort_flag, args.err, kPipelineTimeoutNs);
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok && elect_one()) tc_commit_pair(&empty[stage], 0x3);
+                __syncwarp();
+              }
+              for (int b = 0; b < n_blocks; ++b) advance();
+              continue;
+            }
+            ok = mbar_wait_bounded_cluster(&tempty[iss], (mine & 1) ^ 1, abort_flag, args.err, kPipelineTimeoutNs);
+            ok = __all_sync(0xffffffffu, ok);
+            for (int b = 0; ok && b < (kHalves ? 1 : n_blocks); ++b) {
+              ok = mbar_wait_bounded_cluster(&full[stage], phase, abort_flag, args.err, kPipelineTimeoutNs);
+              ok = __all_sync(0xffffffffu, ok);
+              if (!ok) break;
+              tc_fence_after();
+              if (elect_one()) {
+                const uint64_t ad = smem_desc(a0 + stage * C::kABytes, 16, 1024, 2);
+                const uint64_t bd = smem_desc(b0 + stage * C::kBBytes, 16, 1024, 2);
+                const int j0 = kHalves ? 2 * (g & 1) : 0;
+#pragma unroll
+                for (int j = 0; j < kSteps; ++j)
+                  tc_mma<false, true>(tmem_base + iss * kTCols, ad + (j0 + j) * 2, bd + (j0 + j) * 2, kIdesc, (b | j) != 0);
+                tc_commit_pair(&empty[stage], 0x3);
+                if (b == (kHalves ? 1 : n_blocks) - 1) tc_commit_pair(&tfull[iss], 0x3);
+              }
+              __syncwarp();
+              if (!kHalves) advance();
+            }
+            if (kHalves && n_blocks) advance();
+            ++mine;
+          }
+        }
+        if (ok && mine) {  // as below
+          ok = mbar_wait_bounded_cluster(&tempty[iss], (mine - 1) & 1, abort_flag, args.err, kPipelineTimeoutNs);
+        }
+        acc = 0;
+      } else if constexpr (kFp8) {
         // the two issuers take the launch's blocks in turn, issuer i into accumulator i
         const int tiles = cluster_id < total ? (total - 1 - cluster_id) / clusters + 1 : 0;
         const int64_t blocks = static_cast<int64_t>(tiles) * k_blocks;
@@ -344,7 +409,7 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
       }
       // Every accumulator has come back, so every MMA has completed before the pair frees its tensor
       // memory, and no release of the other CTA's epilogue is on its way to this CTA's barriers.
-      for (int64_t turn = static_cast<int64_t>(acc) - 2; ok && turn < acc; ++turn)
+      for (int64_t turn = static_cast<int64_t>(acc) - 2; !kW4 && ok && turn < acc; ++turn)
         if (turn >= 0 && (!kFp8 || (turn & 1) == iss))
           ok = mbar_wait_bounded_cluster(&tempty[turn & 1], static_cast<uint32_t>(turn >> 1) & 1, abort_flag, args.err,
                                          kPipelineTimeoutNs);
@@ -372,11 +437,20 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
     const bool vec = (args.ldo & 7) == 0;
     constexpr bool kUnscale = kGrad && T::kCode == NVFP4_DT_FP16;
     const float unscale = kUnscale ? __ldg(args.unscale) : 1.f;
-    // kFp8: the sums of this thread's row, kBRows columns from out_n0 on
-    float sum[kFp8 ? kBRows : 1];
+    // kTScaled: the sums of this thread's row, kBRows columns from out_n0 on
+    float sum[kScaled ? kBRows : 1];
     int out_row = 0, out_n0 = 0;
     auto store_tile = [&]() {
-      if constexpr (kFp8) {
+      if constexpr (kW4) {
+        // 32 consecutive elements of an output row per store
+        if (out_row < args.M) {
+          uint16_t *dst = static_cast<uint16_t *>(args.out) + out_n0 * args.ldo + out_row;
+          const int left = args.N - out_n0;
+#pragma unroll
+          for (int i = 0; i < kBRows; ++i)
+            if (i < left) dst[i * args.ldo] = T::one(sum[i]);
+        }
+      } else if constexpr (kFp8) {
 #pragma unroll
         for (int c = 0; c < kBRows / 16; ++c) {
           float v[16];
@@ -410,7 +484,38 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
       const int nt = tile.nt;
       const int row = tile.mt * kTRows + static_cast<int>(rank) * kTHalf + quarter * 32 + lane;
       const bool row_ok = row < (kGrad && tile.dw ? args.dw_M : args.M);
-      if constexpr (kFp8) {
+      if constexpr (kW4) {
+        const float *sa = args.sa + min(row, args.M - 1);
+        const int n_groups = args.groups;
+        float a[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) a[u] = ld_early(sa + min(u, n_groups - 1) * args.ld_sa);
+        if (at != first) store_tile();  // the previous tile, while this one's first group is made
+        out_row = row;
+        out_n0 = nt * kTCols + half * kBRows;
+#pragma unroll
+        for (int i = 0; i < kBRows; ++i) sum[i] = 0.f;
+        for (int g0 = 0; ok && g0 < n_groups; g0 += kAhead) {
+#pragma unroll
+          for (int u = 0; u < kAhead; ++u) {
+            if (g0 + u >= n_groups) break;
+            const float f = a[u];
+            a[u] = ld_early(sa + min(g0 + u + kAhead, n_groups - 1) * args.ld_sa);
+            if (!wait_acc()) break;
+            const uint32_t t = lanes + (acc & 1) * kTCols + half * kBRows;
+#pragma unroll
+            for (int c = 0; c < kBRows / 16; ++c) {
+              uint32_t r[16];
+              tmem_ld16(t + c * 16, r);
+              tmem_ld_wait();
+              if (c == kBRows / 16 - 1) release();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) sum[c * 16 + i] = fmaf(__uint_as_float(r[i]), f, sum[c * 16 + i]);
+            }
+          }
+        }
+        if (!ok) break;
+      } else if constexpr (kFp8) {
         const int n0 = nt * kTCols + half * kBRows;  // a warp's columns share one weight scale
         // Scales are fetched ahead: under the operand stream a load takes longer than a block.  The
         // thread's row's activation scales kAhead blocks ahead (the loop is unrolled, so that no

@@ -40,6 +40,14 @@ struct W4Args {
 cudaError_t launch_w4_stream(const W4Args &a, int dtype, int group, bool zeros, int tok8, int splits, int depth,
                              cudaStream_t s);
 
+// Many tokens: the integers c - z of the prepared weights as a 16-bit matrix (N, K), the scales as (groups, lds) fp32, and
+// the product of that matrix and x on CTA pairs.
+struct TileArgs;
+cudaError_t launch_w4_expand(const W4Args &a, int dtype, int group, bool zeros, uint16_t *out, float *scales, int64_t lds,
+                             cudaStream_t s);
+cudaError_t launch_w4_tile_gemm(const CUtensorMap &w, const CUtensorMap &x, const TileArgs &args, int dtype, int group, int cols,
+                                cudaStream_t s);
+
 struct W4MoeArgs {
   const void *x;  // 16-bit (T, H), row stride ldx
   int64_t ldx;

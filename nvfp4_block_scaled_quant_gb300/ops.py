@@ -697,19 +697,22 @@ def _w4(w: W4Weight, what: str, G: int, N: int, K: int, gated: bool, like: Optio
     return w.data.data_ptr()
 
 
-def w4_linear(x: torch.Tensor, w: W4Weight, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+def w4_linear(x: torch.Tensor, w: W4Weight, out: Optional[torch.Tensor] = None,
+              workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y (M, N) = x W^T in x's type: x (M, K) strided rows of the type of the weights' scales."""
-    st = _here(stream, x, w.data, out)
+    st = _here(stream, x, w.data, out, workspace)
     _no_graph(x)
     if st < 0:
-        return _elsewhere(stream, (x, w.data, out), lambda: w4_linear(x, w, out))
+        return _elsewhere(stream, (x, w.data, out, workspace), lambda: w4_linear(x, w, out, workspace))
     M, K = _size(x, "x")
     ld = _ld(x, "x", M, K, w.dtype)
     wp = _w4(w, "w", 1, w.N, K, False)
     if out is not None:
         _whole(out, "out", (M, w.N), (x.dtype,))
     y = out if out is not None else torch.empty(M, w.N, dtype=x.dtype, device=x.device)
-    call("nvfp4_w4_linear", x.data_ptr(), _DT[w.dtype], M, K, ld, w.N, wp, w.group, w.has_zeros, y.data_ptr(), st)
+    ws, ws_bytes = _scratch(workspace, "nvfp4_w4_linear_workspace_bytes", x, M, w.N, K, w.group)
+    call("nvfp4_w4_linear", x.data_ptr(), _DT[w.dtype], M, K, ld, w.N, wp, w.group, w.has_zeros, y.data_ptr(), _ptr(ws),
+         ws_bytes, st)
     return y
 
 
