@@ -20,8 +20,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libnvfp4_gb300.so")
 SOURCES = ["abi.cu", "quant.cu", "route.cu", "gemm.cu", "gemm_pair.cu", "norm.cu", "router.cu",
-           "abi_dense.cu", "fp8_gemm.cu", "gated.cu", "residual_norm.cu", "abi_w4.cu", "w4_linear.cu", "w4_gemm.cu",
-           "w4_moe.cu"]
+           "abi_dense.cu", "fp8_gemm.cu", "gated.cu", "residual_norm.cu", "abi_w4.cu", "w4_linear.cu", "w4_tc.cu",
+           "w4_gemm.cu", "w4_moe.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",
          "--expt-relaxed-constexpr", f"-I{os.path.join(ROOT, 'include')}", "-DNVFP4_BUILD"]

@@ -40,15 +40,31 @@ int stream_splits(int64_t ctas, int blocks, int sms) {
   return best;
 }
 
+// How w4_tc_kernel covers M tokens: tiles of `tok`, clusters of `splits` CTAs along K; one CTA to an SM.
+struct TcPlan {
+  int tok, splits;
+};
+TcPlan tc_plan(int64_t M, int64_t N, int blocks, int sms) {
+  TcPlan p = {16, 1};
+  while (p.tok < 128 && p.tok < M) p.tok *= 2;
+  const int64_t tiles = (N + 127) / 128 * ((M + p.tok - 1) / p.tok);
+  int64_t best = 0;
+  for (int s = 1; s <= 4 && s <= blocks; ++s) {
+    const int64_t time = (tiles * s + sms - 1) / sms * ((blocks + s - 1) / s + 6);
+    if (best == 0 || time < best) best = time, p.splits = s;
+  }
+  return p;
+}
+
 // Many tokens: where the written-out weights and their scales are in the workspace.
-constexpr int64_t kStreamMaxTokens = 64;
+constexpr int64_t kStreamMaxTokens = 8, kTcMaxTokens = 512;
 struct LinearWs {
   size_t w, scales, total;
   int64_t lds;
 };
 LinearWs linear_ws(int64_t M, int64_t N, int64_t K, int group) {
   LinearWs w = {};
-  if (M <= kStreamMaxTokens) return w;
+  if (M <= kTcMaxTokens) return w;
   w.lds = round_up(N, 4);
   w.scales = align256(static_cast<size_t>(N) * static_cast<size_t>(K) * 2);
   w.total = align256(w.scales + static_cast<size_t>(w.lds) * static_cast<size_t>((K + group - 1) / group) * 4);
@@ -156,6 +172,13 @@ nvfp4_status nvfp4_w4_linear(const void *x, int dtype, int64_t M, int64_t K, int
     if (depth > 4) depth = 4;
     if (depth < tok8) depth = tok8;  // the ring holds a warp's sums at the end
     NV_CUDA(launch_w4_stream(a, dtype, group, zeros, tok8, splits, depth, s), "4-bit linear launch");
+    return NVFP4_OK;
+  }
+  if (M <= kTcMaxTokens) {
+    const TcPlan p = tc_plan(M, N, static_cast<int>(w4_blocks(K)), d->sms);
+    CUtensorMap mx;
+    if ((st = make_map(__func__, &mx, x, K * 2, M, ldx * 2, p.tok)) != NVFP4_OK) return st;
+    NV_CUDA(launch_w4_tc(mx, a, dtype, group, zeros, p.tok, p.splits, s), "4-bit linear launch");
     return NVFP4_OK;
   }
   uint16_t *ints = static_cast<uint16_t *>(ws);
