@@ -128,66 +128,75 @@ struct Plan {
   int power[kW4MoeMaxT];               // of two, that the tokens' activations are multiplied by
   int slots, shared_slots;
 };
-// While the plan is made, in the room of the rings: the experts' counts, first places and first slots, and the ids.
+// While the plan is made, in the room of the rings: each expert's tokens as a bit mask, the place of its first entry and its first
+// slot (16 bits each), and the ids.
 struct PlanScratch {
-  int count[kW4MoeMaxExperts], first[kW4MoeMaxExperts], slot0[kW4MoeMaxExperts];
+  uint32_t tokens[2][kW4MoeMaxExperts], first[kW4MoeMaxExperts], chunk[32];
   uint16_t ids[kW4MoeMaxEntries];
 };
+static_assert(kW4MoeMaxT <= 64, "a token is a bit of two words");
 // Order-preserving bits of a float (NaN above or below everything), never 0: 0 marks an expert that is taken.
 __device__ __forceinline__ uint32_t order_bits(float v) {
   const uint32_t b = __float_as_uint(v);
   const uint32_t k = b ^ ((b >> 31) ? 0xFFFFFFFFu : 0x80000000u);
   return k ? k : 1u;
 }
+__device__ __forceinline__ float order_value(uint32_t k) { return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xFFFFFFFFu)); }
 
 // The top k of one token's logits by a warp, the lowest expert first among equals; the weights are the softmax
-// over all experts renormalised over the chosen ones, which is the softmax over the chosen ones.
+// over all experts renormalised over the chosen ones, which is the softmax over the chosen ones.  A lane holds every 32nd
+// logit and knows its best two.  The rounds are one after the other: each takes the best of all, whose lane goes on to its
+// second, or looks for the next one in the rare case that it has given that up too (looking every time took 400 cycles a
+// round at 384 experts).
 template <int kPer>
 __device__ __forceinline__ void top_k(const float *logits, int E, int topk, uint16_t *ids, float *weight) {
   const int lane = threadIdx.x & 31;
-  uint32_t key[kPer];
-  uint32_t mine = 0;
+  uint32_t key[kPer], best = 0, second = 0;
+  int at = 0, at2 = 0;  // their places, the first among equals
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) key[i] = lane + 32 * i < E ? order_bits(__ldcg(logits + lane + 32 * i)) : 0u;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
-    const int e = lane + 32 * i;
-    key[i] = e < E ? order_bits(__ldcg(logits + e)) : 0u;
-    mine = max(mine, key[i]);
+    if (key[i] > best)
+      second = best, at2 = at, best = key[i], at = i;
+    else if (key[i] > second)
+      second = key[i], at2 = i;
   }
-  float first = 0.f, sum = 0.f, w = 0.f;
+  float mine = -INFINITY;  // lane j: the logit of the j-th choice
   for (int j = 0; j < topk; ++j) {
-    const uint32_t best = __reduce_max_sync(0xffffffffu, mine);
-    int at = 0x7fffffff;
-    if (mine == best) {
-#pragma unroll
-      for (int i = kPer - 1; i >= 0; --i)
-        if (key[i] == best) at = lane + 32 * i;
-    }
-    const int e = __reduce_min_sync(0xffffffffu, at);
-    if (at == e) {  // taken: this lane's next best
-      mine = 0;
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        if (lane + 32 * i == e) key[i] = 0u;
-        mine = max(mine, key[i]);
-      }
-    }
-    const float v = __uint_as_float(best ^ ((best >> 31) ? 0x80000000u : 0xFFFFFFFFu));
-    if (j == 0) first = v;
-    const float p = expf(v - first);
-    sum += p;
+    const uint32_t top = __reduce_max_sync(0xffffffffu, best);
+    const int e = __reduce_min_sync(0xffffffffu, best == top ? lane + 32 * at : 0x7fffffff);
     if (lane == j) {
-      w = p;
+      mine = order_value(top);
       ids[j] = static_cast<uint16_t>(e);
     }
+    if ((e & 31) == lane) {
+      if (second) {
+        best = second, at = at2, second = 0;
+      } else {  // the next behind this one
+        uint32_t next = 0;
+        int next_at = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i)
+          if ((key[i] < best || (key[i] == best && i > at)) && key[i] > next) next = key[i], next_at = i;
+        best = next, at = next_at;
+      }
+    }
   }
-  if (lane < topk) weight[lane] = __fdiv_rn(w, sum);
+  const float first = __shfl_sync(0xffffffffu, mine, 0);
+  const float p = lane < topk ? expf(mine - first) : 0.f;
+  float sum = p;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  if (lane < topk) weight[lane] = __fdiv_rn(p, sum);
 }
 
-// The table of slots: the same in every CTA.
+// The table of slots, the same in every CTA: experts in their order, tokens in theirs.
 template <class T>
 __device__ void make_plan(const W4MoeArgs &a, Plan &plan, PlanScratch &s) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, entries = a.T * a.topk;
-  for (int e = tid; e < a.E; e += kThreads) s.count[e] = 0;
+  if (entries > 32)
+    for (int e = tid; e < a.E; e += kThreads) s.tokens[0][e] = s.tokens[1][e] = 0u;
   if (tid < a.T) plan.power[tid] = w4_power<T>(__ldcg(a.x_max + tid));
   for (int t = warp; t < a.T; t += kThreads / 32) {
     const float *l = a.logits + static_cast<int64_t>(t) * a.E;
@@ -200,44 +209,82 @@ __device__ void make_plan(const W4MoeArgs &a, Plan &plan, PlanScratch &s) {
     else
       top_k<32>(l, a.E, a.topk, ids, w);
   }
-  __syncthreads();
-  for (int f = tid; f < entries; f += kThreads) atomicAdd(&s.count[s.ids[f]], 1);
-  __syncthreads();
   const int shared_slots = a.sh13 ? (a.T + 7) / 8 : 0;
-  if (warp == 0) {  // exclusive sums over the experts
-    const int per = (a.E + 31) / 32, e0 = min(lane * per, a.E), e1 = min(e0 + per, a.E);
-    int n = 0, slots = 0;
-    for (int e = e0; e < e1; ++e) n += s.count[e], slots += (s.count[e] + 7) / 8;
-    int n_at = n, slots_at = slots;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const int u = __shfl_up_sync(0xffffffffu, n_at, o), v = __shfl_up_sync(0xffffffffu, slots_at, o);
-      if (lane >= o) n_at += u, slots_at += v;
-    }
-    if (lane == 31) plan.slots = shared_slots + slots_at, plan.shared_slots = shared_slots;
-    n_at -= n;
-    slots_at += shared_slots - slots;
-    for (int e = e0; e < e1; ++e) {
-      s.first[e] = n_at, s.slot0[e] = slots_at;
-      n_at += s.count[e], slots_at += (s.count[e] + 7) / 8;
-    }
-  }
   for (int i = tid; i < shared_slots; i += kThreads) {
     plan.slot_expert[i] = 0;
     plan.slot_first[i] = static_cast<uint16_t>(8 * i);
     plan.slot_count[i] = static_cast<uint16_t>(min(8, a.T - 8 * i));
   }
   __syncthreads();
+  if (entries <= 32) {
+    // few entries: a warp counts the ones of smaller experts and the earlier ones of the same expert
+    if (warp == 0) {
+      const int e = lane < entries ? s.ids[lane] : 0x7fff;
+      int rank = 0, same = 0, less = 0, slot = shared_slots;
+      for (int o = 0; o < entries; ++o) {
+        const int u = __shfl_sync(0xffffffffu, e, o);
+        rank += u == e && o < lane, same += u == e, less += u < e;
+      }
+      const uint32_t heads = __ballot_sync(0xffffffffu, lane < entries && rank % 8 == 0);
+      for (int o = 0; o < entries; ++o) slot += __shfl_sync(0xffffffffu, e, o) < e && (heads >> o & 1);
+      if (lane < entries) {
+        plan.sorted[less + rank] = static_cast<uint16_t>(lane);
+        if (rank % 8 == 0) {
+          plan.slot_expert[slot + rank / 8] = static_cast<uint16_t>(e);
+          plan.slot_first[slot + rank / 8] = static_cast<uint16_t>(less + rank);
+          plan.slot_count[slot + rank / 8] = static_cast<uint16_t>(min(8, same - rank));
+        }
+      }
+      if (lane == 0) plan.slots = shared_slots + __popc(heads), plan.shared_slots = shared_slots;
+    }
+    __syncthreads();
+    return;
+  }
   for (int f = tid; f < entries; f += kThreads) {
-    const int e = s.ids[f];
-    int rank = 0;  // entries of the same expert before this one
-    for (int o = 0; o < f; ++o) rank += s.ids[o] == e;
-    plan.sorted[s.first[e] + rank] = static_cast<uint16_t>(f);
+    const int t = f / a.topk;
+    atomicOr(&s.tokens[t >> 5][s.ids[f]], 1u << (t & 31));
+  }
+  __syncthreads();
+  // exclusive sums over the experts, entries in the low and slots in the high half: of each 32 experts by a warp, then
+  // over those
+  const int chunks = (a.E + 31) / 32;
+  for (int c = warp; c < chunks; c += kThreads / 32) {
+    const int e = 32 * c + lane;
+    const uint32_t n = e < a.E ? __popc(s.tokens[0][e]) + __popc(s.tokens[1][e]) : 0u, own = n | ((n + 7) / 8 << 16);
+    uint32_t sum = own;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += u;
+    }
+    if (e < a.E) s.first[e] = sum - own;
+    if (lane == 31) s.chunk[c] = sum;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    uint32_t sum = lane < chunks ? s.chunk[lane] : 0u;
+    const uint32_t own = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+      const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += u;
+    }
+    s.chunk[lane] = sum - own + (static_cast<uint32_t>(shared_slots) << 16);
+    if (lane == 31) plan.slots = shared_slots + static_cast<int>(sum >> 16), plan.shared_slots = shared_slots;
+  }
+  __syncthreads();
+  for (int f = tid; f < entries; f += kThreads) {
+    const int e = s.ids[f], t = f / a.topk;
+    const uint32_t m0 = s.tokens[0][e], m1 = s.tokens[1][e], below = (1u << (t & 31)) - 1u;
+    const int n = __popc(m0) + __popc(m1), rank = t < 32 ? __popc(m0 & below) : __popc(m0) + __popc(m1 & below);
+    const uint32_t start = s.first[e] + s.chunk[e >> 5];
+    const int first = static_cast<int>(start & 0xFFFFu) + rank;
+    plan.sorted[first] = static_cast<uint16_t>(f);
     if (rank % 8 == 0) {
-      const int slot = s.slot0[e] + rank / 8;
+      const int slot = static_cast<int>(start >> 16) + rank / 8;
       plan.slot_expert[slot] = static_cast<uint16_t>(e);
-      plan.slot_first[slot] = static_cast<uint16_t>(s.first[e] + rank);
-      plan.slot_count[slot] = static_cast<uint16_t>(min(8, s.count[e] - rank));
+      plan.slot_first[slot] = static_cast<uint16_t>(first);
+      plan.slot_count[slot] = static_cast<uint16_t>(min(8, n - rank));
     }
   }
   __syncthreads();
@@ -293,6 +340,9 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
   __syncthreads();
   pdl_wait();
   pdl_trigger();
+  // the first item, on its way while the plan is made
+  int first_item = 0;
+  if (tid == (kWarps + 1) * 32) first_item = atomicAdd(a.counters, 1);
   make_plan<T>(a, plan, *reinterpret_cast<PlanScratch *>(smem));
 
   const int slots = plan.slots, shared_slots = plan.shared_slots, entries = a.T * a.topk;
@@ -314,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
     int stage = 0, q = 0;
     uint32_t phase = 0, qphase = 0;
     bool ok = true;
-    int item = lane == 0 ? atomicAdd(counter, 1) : 0;
+    int item = first_item;
     for (;;) {
       item = __shfl_sync(0xffffffffu, item, 0);
       const bool up = item < up_items;
@@ -534,24 +584,26 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
   // Panels of y to which this CTA was the last to add: a token's experts in the order of its top k, then the shared one.
   __syncwarp();
   asm volatile("bar.sync 1, %0;" ::"n"((kWarps + 1) * 32) : "memory");
-  for (int i = 0; i < s_finished; ++i) {
-    for (int e = tid; e < a.T * (kW4PanelRows / 2); e += (kWarps + 1) * 32) {
-      const int row = e / (kW4PanelRows / 2), n = s_panels[i] * kW4PanelRows + 2 * (e % (kW4PanelRows / 2));
-      if (n >= a.H) continue;
-      const float2 *p = reinterpret_cast<const float2 *>(a.part + static_cast<int64_t>(row) * a.topk * a.H + n);
-      float2 v = make_float2(0.f, 0.f);
-#pragma unroll 4
-      for (int j = 0; j < a.topk; ++j) {
-        const float2 u = __ldcg(p + static_cast<int64_t>(j) * (a.H / 2));
-        const float w = plan.weight[row * a.topk + j];
-        v.x = fmaf(w, u.x, v.x), v.y = fmaf(w, u.y, v.y);
-      }
-      if (shared_slots) {
-        const float2 u = __ldcg(reinterpret_cast<const float2 *>(a.part + static_cast<int64_t>(entries + row) * a.H + n));
-        v.x += u.x, v.y += u.y;
-      }
-      *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.y) + static_cast<int64_t>(row) * a.H + n) = T::pack(v.x, v.y);
+  constexpr int kPairs = kW4PanelRows / 2;
+  for (int e = tid; e < s_finished * a.T * kPairs; e += (kWarps + 1) * 32) {
+    const int at = e / kPairs, row = at % a.T, n = s_panels[at / a.T] * kW4PanelRows + 2 * (e % kPairs);
+    if (n >= a.H) continue;
+    const float2 *p = reinterpret_cast<const float2 *>(a.part + static_cast<int64_t>(row) * a.topk * a.H + n);
+    float2 v = make_float2(0.f, 0.f), u[9];
+    for (int j0 = 0; j0 < a.topk; j0 += 8) {  // eight loads and the shared expert's in flight
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j0 + j < a.topk) u[j] = __ldcg(p + static_cast<int64_t>(j0 + j) * (a.H / 2));
+      if (shared_slots && j0 + 8 >= a.topk) u[8] = __ldcg(reinterpret_cast<const float2 *>(a.part + static_cast<int64_t>(entries + row) * a.H + n));
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j0 + j < a.topk) {
+          const float w = plan.weight[row * a.topk + j0 + j];
+          v.x = fmaf(w, u[j].x, v.x), v.y = fmaf(w, u[j].y, v.y);
+        }
     }
+    if (shared_slots) v.x += u[8].x, v.y += u[8].y;
+    *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.y) + static_cast<int64_t>(row) * a.H + n) = T::pack(v.x, v.y);
   }
 }
 

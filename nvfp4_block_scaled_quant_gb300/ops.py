@@ -631,12 +631,12 @@ def residual_norm_fp8(f: torch.Tensor, r: torch.Tensor, gamma_before: torch.Tens
     r_out = out if out is not None else torch.empty(M, K, dtype=r.dtype, device=r.device)
     q = torch.empty(M, K, dtype=torch.float8_e4m3fn, device=f.device)
     lds = (M + 3) // 4 * 4
-    s = torch.empty((K + 127) // 128, lds, dtype=torch.float32, device=f.device)
+    s = torch.empty((K + 127) // 128 * lds, dtype=torch.float32, device=f.device)
     y = torch.empty(M, K, dtype=f.dtype, device=f.device) if want_y else None
     stats = torch.empty(M, 2, dtype=torch.float32, device=f.device) if save else None
     call("nvfp4_residual_norm_fp8", f.data_ptr(), kind, r.data_ptr(), rkind, M, K, ldf, ldr, ga, gp, gkind, groups, scale,
          gb, eps, r_out.data_ptr(), q.data_ptr(), s.data_ptr(), lds, _ptr(y), _ptr(stats), st)
-    s = s[:, :M]
+    s = s.as_strided(((K + 127) // 128, M), (lds, 1))
     return (r_out, q, s, y, stats) if save else (r_out, q, s, y)
 
 
