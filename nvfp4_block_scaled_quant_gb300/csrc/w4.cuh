@@ -167,10 +167,9 @@ __device__ __forceinline__ void w4_block(const uint8_t *block, const W4Frag<kNT>
     for (int i = 0; i < 4; ++i) {
       const float s0 = T::lo(sw[i]), s1 = T::hi(sw[i]);
       float z0 = -8.f, z1 = -8.f;
-      if constexpr (kZeros) {
-        const uint32_t zz = zw[i >> 1] >> (16 * (i & 1));
-        z0 = -static_cast<float>(zz & 0xFFu);
-        z1 = -static_cast<float>((zz >> 8) & 0xFFu);
+      if constexpr (kZeros) {  // a byte under the exponent of 2^23 is 2^23 + z
+        z0 = 8388608.f - __uint_as_float(__byte_perm(zw[i >> 1], 0x4B000000u, 0x7540u + 2 * (i & 1)));
+        z1 = 8388608.f - __uint_as_float(__byte_perm(zw[i >> 1], 0x4B000000u, 0x7541u + 2 * (i & 1)));
       }
       const uint64_t s00 = pack_f32x2(s0, s0), s11 = pack_f32x2(s1, s1), z00 = pack_f32x2(z0, z0), z11 = pack_f32x2(z1, z1);
 #pragma unroll
