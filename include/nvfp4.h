@@ -470,7 +470,7 @@ NVFP4_API nvfp4_status nvfp4_residual_norm(const void *f, int dtype, const void 
 /* The same with y in 8 bits, as nvfp4_fp8_gemm reads it: e4m3 codes q (M, K), contiguous, and xs (ceil(K / 128), lds)
  * with xs[b * lds + m] = fl32(max |y| / 448) over columns 128 b .. 128 b + 127 of row m and q = e4m3(y / xs) (0 where xs is
  * 0), from y in fp32: rounded once, so the codes can differ from those of nvfp4_fp8_quantize_act on the
- * 16-bit y, which is rounded twice.  The quotient is within two steps of fp32.  A block that holds a NaN or an infinity
+ * 16-bit y, which is rounded twice.  The quotient is within a step of fp32.  A block that holds a NaN or an infinity
  * has such a scale.  y, if not NULL, also receives the 16-bit output; r_out, y and stats are those of nvfp4_residual_norm
  * bit for bit (the backward of y is nvfp4_residual_norm_backward's; the rounding to 8 bits has no gradient of its own).
  * gamma_before is required; K % 16 == 0; lds >= M, a multiple of 4 (entries m >= M are not written). */

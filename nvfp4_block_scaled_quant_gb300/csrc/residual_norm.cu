@@ -174,28 +174,38 @@ __device__ __forceinline__ float row_rstd(float part, float *red, int K, float e
 
 // ---------------------------------------------------------------- 8-bit output
 
+constexpr float kFastMax = 448.f * kFastScale;
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // Eight columns of y in e4m3: the scale is max|y| / 448 over the 128 columns that 16 consecutive lanes hold, from y before
 // its rounding to 16 bits (rounded once, from fp32, the codes are the nearest ones; a quantiser behind the 16-bit output
-// rounds twice).  Lanes without columns pass zeros.  The quotient's error of two steps of fp32 only decides
-// between codes at a midpoint.  NaN orders above infinity in the maximum and makes the scale NaN.
+// rounds twice).  Lanes without columns pass zeros.  The corrected quotient is within a step of fp32, which can only decide
+// between codes at a midpoint.  A NaN stays in the maximum and makes the scale NaN.
 __device__ __forceinline__ uint2 encode_columns(const Two (&v)[4], float &scale) {
-  float f[8];
-  uint32_t m = 0;
+  float f[8], m = 0.f;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     unpack_f32x2(v[i].v, f[2 * i], f[2 * i + 1]);
-    m = max(m, max(__float_as_uint(f[2 * i]) & 0x7FFFFFFFu, __float_as_uint(f[2 * i + 1]) & 0x7FFFFFFFu));
+    m = max_nan(m, max_nan(fabsf(f[2 * i]), fabsf(f[2 * i + 1])));
   }
 #pragma unroll
-  for (int o = 8; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-  scale = __fdiv_rn(__uint_as_float(m), 448.f);
-  if (scale == 0.f) return make_uint2(0u, 0u);
+  for (int o = 8; o; o >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, o));
   uint32_t c[4];
-  if (scale >= kFastScale && scale < __int_as_float(0x7F800000)) {
-    const Two r = both(__frcp_rn(scale));
+  if (m >= kFastMax && m < __int_as_float(0x7F800000)) {
+    // fl32(m / 448) by the corrected product: right for every mantissa (all of them in the tests)
+    scale = quotient(m, 448.f, 1.f / 448.f);
+    float rcp;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(rcp) : "f"(scale));
+    const Two r = both(rcp), minus = both(-scale);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = e4m3x2((v[i] * r).v);
-  } else {  // tiny, infinite or NaN scales
+    for (int i = 0; i < 4; ++i) c[i] = e4m3x2(quotients(v[i].v, minus.v, r.v));
+  } else {  // zero, tiny, infinite or NaN maxima
+    scale = __fdiv_rn(m, 448.f);
+    if (scale == 0.f) return make_uint2(0u, 0u);
 #pragma unroll
     for (int i = 0; i < 4; ++i) c[i] = e4m3x2(pack_f32x2(__fdiv_rn(f[2 * i], scale), __fdiv_rn(f[2 * i + 1], scale)));
   }
