@@ -89,7 +89,9 @@ PairPlan pair_plan(int64_t M, int64_t N, int64_t K, int group, int sms) {
 // also size the workspace.
 constexpr int64_t kStreamMaxTokens = 16;
 constexpr int kPlanSms = 152;
+constexpr int64_t kTcMaxTokens = int64_t(65535) * 128;  // the grid's second dimension
 bool takes_pairs(int64_t M, int64_t N, int64_t K, int group) {
+  if (M > kTcMaxTokens) return true;
   return M > kStreamMaxTokens && pair_plan(M, N, K, group, kPlanSms).time < tc_plan(M, N, K, group, kPlanSms).time;
 }
 
