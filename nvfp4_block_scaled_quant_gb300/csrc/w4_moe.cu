@@ -4,15 +4,15 @@
 // 2. Everything else.  Every CTA takes the top k of each token's logits itself and builds the same table of slots (an expert and
 //    up to eight of its tokens); that costs less than a launch or a grid-wide exchange.  The work is a list of items in a
 //    fixed order: first, slot by slot, panels of 32 gate and 32 up rows (h = act(g) u), then panels of 64 rows of
-//    the down projection.  CTAs claim items one by one from a counter.  A down item waits until its slot's h
+//    the down projection, up to four panels to an item.  CTAs claim items one by one from a counter.  A down item waits until its slot's h
 //    is complete; those items have lower numbers, so running CTAs hold them already, and however few CTAs run at
 //    once, some claimed item can always go on.  While a CTA waits its producer warp goes on: the weights of the
 //    next items stream into the ring regardless of h.
 //    A slot's down rows go to the workspace in fp32; the CTA that finishes the last slot of a panel adds a token's experts
 //    up in the order of its top k, so repeated calls give identical bits.
 //
-// With few tokens the layer is bound by the bytes of the chosen experts' weights.  Eight warps of a CTA take an item's
-// K blocks in turn (block b goes to warp b % 8), each through a ring of its own: a block is one bulk copy.  A warp leaves its sums where its
+// With few tokens the layer is bound by the bytes of the chosen experts' weights.  Eight warps of a CTA share an item's
+// panels and take a panel's K blocks in turn, each through a ring of its own: a block is one bulk copy.  A warp leaves its sums where its
 // last block of the item was and goes on to the next item; a finishing warp adds the eight up and gives the
 // stages back.  Two CTAs share an SM.  (The rings are the warps' own because a warp waits on every phase of its
 // barriers then.  In a common ring, taken block by block, a warp that got a ring's length ahead of a slow copy would take an
@@ -191,6 +191,15 @@ __device__ __forceinline__ void top_k(const float *logits, int E, int topk, uint
   if (lane < topk) weight[lane] = __fdiv_rn(p, sum);
 }
 
+// How many panels (log2) an item holds, shared out to the warps, so that a warp has more K blocks in a row and the items' own
+// cost (the first load of its activations, its sums, its signals) is spread over more of them.  That pays where a CTA takes many items; where it
+// takes few, smaller ones spread better.  Two panels / one: 59 tokens, 80 experts of 5280 x 352 (22 items of the down projection to a
+// CTA) 97 / 110 us, 32 tokens, 180 of 1256 x 1808 (26 and 9) 119 / 132; 1 token, 384 of 7168 x 2048 (2 and 3) 58 / 50.
+__device__ __forceinline__ int item_split(int slots, int panels, int ctas) {
+  const int rounds = slots * panels / ctas;
+  return rounds < 8 ? 0 : rounds < 32 ? 1 : 2;
+}
+
 // The table of slots, the same in every CTA: experts in their order, tokens in theirs.
 template <class T>
 __device__ void make_plan(const W4MoeArgs &a, Plan &plan, PlanScratch &s) {
@@ -304,7 +313,7 @@ __device__ __forceinline__ float activate(int act, float g) {
 // An item of the list.
 struct Item {
   int slot;  // -1: no more items
-  int panel, blocks, up;
+  int panel, blocks, up;  // its first panel
 };
 
 template <class T, int kGpb, bool kZeros>
@@ -347,6 +356,9 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
 
   const int slots = plan.slots, shared_slots = plan.shared_slots, entries = a.T * a.topk;
   const int panels13 = (a.I + 31) / 32, panels2 = (a.H + kW4PanelRows - 1) / kW4PanelRows;
+  const int blocks13 = (a.H + kW4BlockK - 1) / kW4BlockK, blocks2 = (a.I + kW4BlockK - 1) / kW4BlockK;
+  const int split13 = item_split(slots, panels13, gridDim.x), split2 = item_split(slots, panels2, gridDim.x);
+  const int items13 = (panels13 + (1 << split13) - 1) >> split13, items2 = (panels2 + (1 << split2) - 1) >> split2;  // of a slot
   int *counter = a.counters, *slot_done = counter + kW4MoeSlotDone, *panel_done = counter + kW4MoeCounters;
   uint32_t *row_max = reinterpret_cast<uint32_t *>(counter + kW4MoeRowMax);
   // the workspace row of a slot's token j
@@ -357,8 +369,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
 
   if (warp == kWarps + 1) {
     // ---------------------------------------------------------------- producer: lane w fills the ring of warp w
-    const int blocks13 = (a.H + kW4BlockK - 1) / kW4BlockK, blocks2 = (a.I + kW4BlockK - 1) / kW4BlockK;
-    const int up_items = slots * panels13, items = up_items + slots * panels2;
+    const int up_items = slots * items13, items = up_items + slots * items2;
     const uint64_t pol = policy_evict_first();
     fence_proxy_async_shared();  // the plan's scratch was where the copies go
     int stage = 0, q = 0;
@@ -368,11 +379,11 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
     for (;;) {
       item = __shfl_sync(0xffffffffu, item, 0);
       const bool up = item < up_items;
-      const int i = up ? item : item - up_items, panels = up ? panels13 : panels2, blocks = up ? blocks13 : blocks2;
-      const int slot = item < items ? i / panels : -1, panel = i % panels;
+      const int i = up ? item : item - up_items, n = up ? items13 : items2, blocks = up ? blocks13 : blocks2;
+      const int slot = item < items ? i / n : -1, panel0 = i % n << (up ? split13 : split2);
       if (lane == 0) {
         ok = mbar_wait_bounded(&item_empty[q], qphase ^ 1, abort_flag, a.err, kPipelineTimeoutNs);
-        s_item[q] = make_int4(slot, panel, blocks, up);
+        s_item[q] = make_int4(slot, panel0, blocks, up);
         if (ok) mbar_arrive(&item_full[q]);
       }
       if (++q == kItems) {
@@ -383,9 +394,10 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
       if (!ok || slot < 0) break;
       if (lane == 0) item = atomicAdd(counter, 1);  // the next one, on its way while this one's blocks are asked for
       const uint8_t *w = slot < shared_slots ? (up ? a.sh13 : a.sh2) : (up ? a.w13 : a.w2);
+      const int warps = kWarps >> (up ? split13 : split2), panels = up ? panels13 : panels2, panel = panel0 + lane / warps;
       w += (static_cast<int64_t>(plan.slot_expert[slot]) * panels + panel) * blocks * kBytes;
-      if (lane < kWarps) {
-        for (int b = lane; b < blocks; b += kWarps) {
+      if (lane < kWarps && panel < panels) {
+        for (int b = lane % warps; b < blocks; b += warps) {
           ok = mbar_wait_bounded(&empty[lane][stage], phase ^ 1, abort_flag, a.err, kPipelineTimeoutNs);
           if (!ok) break;
           mbar_arrive_expect_tx(&full[lane][stage], kBytes);
@@ -462,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
       const Item it = item;
       if (!it.up && ready != it.slot) {  // its h is complete
         const uint64_t t0 = global_timer_ns();
-        while (load_acquire(slot_done + it.slot) < panels13) {
+        while (load_acquire(slot_done + it.slot) < items13) {
           if (*abort_flag || global_timer_ns() - t0 > kPipelineTimeoutNs) {
             if (!*abort_flag) raise_device_error(a.err, NVFP4_DEVERR_PIPELINE_TIMEOUT);
             *abort_flag = 1;
@@ -475,8 +487,11 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
         ready = it.slot;
       }
       open(it);
+      // this warp's panel of the item, and its K blocks: every `warps`-th from the first
+      const int shift = it.up ? split13 : split2, warps = kWarps >> shift, first = warp & (warps - 1);
+      const bool some = it.panel + (warp >> (3 - shift)) < (it.up ? panels13 : panels2) && first < it.blocks;
       uint64_t sums[4][1][2] = {};
-      for (int b = warp; b < it.blocks; b += kWarps) {
+      for (int b = first; some && b < it.blocks; b += warps) {
         W4Frag<1> f;
         load_x(b, f);
         ok = mbar_wait_bounded(&full[warp][stage], phase, abort_flag, a.err, kPipelineTimeoutNs);
@@ -484,7 +499,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
         if (!ok) break;
         w4_block<T, kGpb, kZeros, 1>(ring + stage * kBytes, f, factor, sums);
         __syncwarp();
-        if (b + kWarps >= it.blocks) break;  // the item's sums go where its last block was
+        if (b + warps >= it.blocks) break;  // the item's sums go where its last block was
         if (lane == 0) mbar_arrive(&empty[warp][stage]);
         if (++stage == depth) {
           stage = 0;
@@ -494,7 +509,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
       ok = ok && mbar_wait_bounded(&sums_empty[buf], bphase ^ 1, abort_flag, a.err, kPipelineTimeoutNs);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      if (warp < it.blocks) {
+      if (some) {
         w4_store_sums<1>(reinterpret_cast<float *>(smem + (warp * depth + stage) * kBytes), sums);
         fence_proxy_async_shared();  // a copy takes their place later
         if (lane == 0) s_sums[buf][warp] = stage;
@@ -513,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
     }
   } else {
     // ---------------------------------------------------------------- finishing warp: an item's sums over the warps
-    int buf = 0, finished = 0;
+    int buf = 0, finished = 0, rows_slot = -1, rows_up = 0, row = 0, power = 0;
     uint32_t bphase = 0;
     for (;;) {
       const Item it = next_item();
@@ -521,65 +536,83 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
       bool ok = mbar_wait_bounded(&sums_full[buf], bphase, abort_flag, a.err, kPipelineTimeoutNs);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
-      const int count = plan.slot_count[it.slot], parts = min(it.blocks, kWarps);
+      const int count = plan.slot_count[it.slot], shift = it.up ? split13 : split2, warps = kWarps >> shift;
+      const int parts = min(it.blocks, warps), panels = min(1 << shift, (it.up ? panels13 : panels2) - it.panel);
+      if (it.slot != rows_slot || it.up != rows_up) {  // lane j: the workspace row of token j, and the power of its activations
+        rows_slot = it.slot, rows_up = it.up;
+        row = row_of(it.slot, min(lane & 7, count - 1));
+        power = it.up ? plan.power[row < entries ? row / a.topk : row - entries] : w4_power<T>(__ldcg(row_max + row));
+      }
       const float *r[kWarps];
 #pragma unroll
-      for (int u = 0; u < kWarps; ++u) r[u] = reinterpret_cast<const float *>(smem + (u * depth + (u < parts ? s_sums[buf][u] : 0)) * kBytes);
-      if (it.up) {
-        const int n = it.panel * 32 + lane;
-        for (int j = 0; j < count; ++j) {
-          float gate = 0.f, lift = 0.f;
+      for (int u = 0; u < kWarps; ++u) r[u] = reinterpret_cast<const float *>(smem + (u * depth + s_sums[buf][u]) * kBytes);
+      auto sum4 = [&](uint32_t in, int at) {  // over the warps of `in`, in their order
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-          for (int u = 0; u < kWarps; ++u) {
-            if (u < parts) {
-              gate += r[u][j * kW4Pitch + lane];
-              lift += r[u][j * kW4Pitch + 32 + lane];
+        for (int u = 0; u < kWarps; ++u)
+          if (in >> u & 1) {
+            const float4 p = *reinterpret_cast<const float4 *>(r[u] + at);
+            v.x += p.x, v.y += p.y, v.z += p.z, v.w += p.w;
+          }
+        return v;
+      };
+      for (int sub = 0; sub < panels; ++sub) {
+        const uint32_t in = ((1u << parts) - 1u) << (sub * warps);  // the warps that hold its sums
+        if (it.up) {
+          // four tokens at a time, four outputs to a lane
+          const int c = 4 * (lane & 7), n = (it.panel + sub) * 32 + c;
+          for (int j0 = 0; j0 < count; j0 += 4) {
+            const int j = j0 + (lane >> 3), to = __shfl_sync(0xffffffffu, row, j & 7), e = __shfl_sync(0xffffffffu, power, j & 7);
+            const bool live = j < count && n < a.I;
+            uint32_t top = 0;
+            if (live) {
+              const float4 gate = sum4(in, j * kW4Pitch + c), lift = sum4(in, j * kW4Pitch + 32 + c);
+              auto out = [&](float gv, float lv) { return activate(a.act, w4_unscale<T>(gv, e)) * w4_unscale<T>(lv, e); };
+              const uint32_t lo = T::pack(out(gate.x, lift.x), out(gate.y, lift.y)), hi = T::pack(out(gate.z, lift.z), out(gate.w, lift.w));
+              *reinterpret_cast<uint2 *>(a.h + static_cast<int64_t>(to) * a.I + n) = make_uint2(lo, hi);
+              const uint32_t m = __vmaxu2(lo & 0x7FFF7FFFu, hi & 0x7FFF7FFFu);
+              top = max(m & 0xFFFFu, m >> 16);
+            }
+#pragma unroll
+            for (int o = 4; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            if (live && c == 0) atomicMax(row_max + to, top);
+          }
+        } else {
+          // two tokens at a time, four outputs to a lane
+          const int c = 4 * (lane & 15), n = (it.panel + sub) * kW4PanelRows + c;
+          for (int j0 = 0; j0 < count; j0 += 2) {
+            const int j = j0 + (lane >> 4), to = __shfl_sync(0xffffffffu, row, j & 7), e = __shfl_sync(0xffffffffu, power, j & 7);
+            if (j < count && n < a.H) {
+              const float4 v = sum4(in, j * kW4Pitch + c);
+              *reinterpret_cast<float4 *>(a.part + static_cast<int64_t>(to) * a.H + n) =
+                  make_float4(w4_unscale<T>(v.x, e), w4_unscale<T>(v.y, e), w4_unscale<T>(v.z, e), w4_unscale<T>(v.w, e));
             }
           }
-          const int row = row_of(it.slot, j), power = plan.power[row < entries ? row / a.topk : row - entries];
-          const uint16_t h = T::one(activate(a.act, w4_unscale<T>(gate, power)) * w4_unscale<T>(lift, power));
-          if (n < a.I) a.h[static_cast<int64_t>(row) * a.I + n] = h;
-          const uint32_t top = __reduce_max_sync(0xffffffffu, n < a.I ? h & 0x7FFFu : 0u);
-          if (lane == 0) atomicMax(row_max + row, top);
-        }
-      } else {
-        const int n = it.panel * kW4PanelRows + 2 * lane;  // H is even
-        for (int j = 0; j < count; ++j) {
-          float2 v = make_float2(0.f, 0.f);
-#pragma unroll
-          for (int u = 0; u < kWarps; ++u) {
-            if (u < parts) {
-              const float2 p = *reinterpret_cast<const float2 *>(r[u] + j * kW4Pitch + 2 * lane);
-              v.x += p.x, v.y += p.y;
-            }
-          }
-          const int row = row_of(it.slot, j), power = w4_power<T>(__ldcg(row_max + row));
-          if (n < a.H)
-            *reinterpret_cast<float2 *>(a.part + static_cast<int64_t>(row) * a.H + n) = make_float2(w4_unscale<T>(v.x, power), w4_unscale<T>(v.y, power));
         }
       }
       // the stages go back to the copies
       fence_proxy_async_shared();
       __syncwarp();
-      if (lane < parts) mbar_arrive(&empty[lane][s_sums[buf][lane]]);
+      if (lane < panels * warps && (lane & (warps - 1)) < parts) mbar_arrive(&empty[lane][s_sums[buf][lane]]);
       __syncwarp();
-      if (lane == 0) {
-        mbar_arrive(&sums_empty[buf]);
-        __threadfence();  // the item's results are out
-        if (it.up)
-          atomicAdd(slot_done + it.slot, 1);
-        else if (atomicAdd(panel_done + it.panel, 1) == slots - 1)
-          s_panels[finished++] = static_cast<uint16_t>(it.panel);
+      if (lane == 0) mbar_arrive(&sums_empty[buf]);
+      __threadfence();  // the item's results are out
+      __syncwarp();
+      if (it.up) {
+        if (lane == 0) atomicAdd(slot_done + it.slot, 1);
+      } else {
+        const bool last = lane < panels && atomicAdd(panel_done + it.panel + lane, 1) == slots - 1;
+        const uint32_t ends = __ballot_sync(0xffffffffu, last);
+        if (last) s_panels[finished + __popc(ends & ((1u << lane) - 1u))] = static_cast<uint16_t>(it.panel + lane);
+        finished += __popc(ends);
       }
       if (++buf == 2) {
         buf = 0;
         bphase ^= 1;
       }
     }
-    if (lane == 0) {
-      __threadfence();  // behind the counts that were seen full
-      s_finished = finished;
-    }
+    __threadfence();  // behind the counts that were seen full
+    if (lane == 0) s_finished = finished;
   }
   // Panels of y to which this CTA was the last to add: a token's experts in the order of its top k, then the shared one.
   __syncwarp();
@@ -644,7 +677,7 @@ cudaError_t experts_as(const W4MoeArgs &a, int sms, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     ready[dev].store(true);
   }
-  // no more CTAs than items
+  // no more CTAs than panels
   const int64_t most = static_cast<int64_t>(a.T * a.topk + (a.sh13 ? (a.T + 7) / 8 : 0)) *
                        ((a.I + 31) / 32 + (a.H + kW4PanelRows - 1) / kW4PanelRows);
   const int64_t ctas = most < 2 * sms ? most : 2 * sms;
