@@ -24,14 +24,15 @@
  *    except nvfp4_get_device_error.  Kernels use programmatic dependent launch:
  *    a kernel may start while the previous kernel on the stream finishes, and
  *    reads its inputs only after that kernel completed.  The one exception is
- *    that the GEMMs of nvfp4_linear and of the MoE stages read the weights and
- *    the routing arrays one launch early (the one-token MoE forward also the
- *    token x and its top-k ids and weights).  Those must therefore be final
- *    before the call that opens the chain (nvfp4_linear, nvfp4_moe_forward or
- *    nvfp4_moe_dispatch) is enqueued, which ordinary stream order gives.
+ *    that the GEMMs of nvfp4_linear and of the MoE stages and nvfp4_w4_linear read
+ *    the weights and the routing arrays one launch early (the one-token MoE
+ *    forward also the token x and its top-k ids and weights).  Those must
+ *    therefore be final before the call that opens the chain (nvfp4_linear,
+ *    nvfp4_w4_linear, nvfp4_moe_forward or nvfp4_moe_dispatch) is enqueued, which
+ *    ordinary stream order gives.
  *  - Kernels on pairs of CTAs (the large products of nvfp4_linear, nvfp4_gemm,
- *    nvfp4_fp8_linear, nvfp4_fp8_gemm and the gated linear) do not run beside
- *    one another: across streams, and across the branches of one stream
+ *    nvfp4_fp8_linear, nvfp4_fp8_gemm, the gated linear and nvfp4_w4_linear of
+ *    many tokens) do not run beside one another: across streams, and across the branches of one stream
  *    capture, each waits for the one enqueued before it.  A captured graph that
  *    holds such calls is not ordered against other graphs and streams:
  *    replay it where no other of these calls runs at the same time.

@@ -14,7 +14,7 @@ nvfp4_status check_w4(const char *fn, int dtype, int64_t K, int group) {
   return NVFP4_OK;
 }
 
-// Bytes of G prepared matrices (N, K); 0 where the sizes are not supported.
+// Bytes of G prepared matrices (N, K).
 int64_t prepared_bytes(int64_t G, int64_t N, int64_t K, int group, bool zeros, bool gated) {
   return G * w4_panels(N, gated) * w4_blocks(K) * w4_block_bytes(kW4BlockK / group, zeros);
 }
@@ -202,7 +202,7 @@ nvfp4_status nvfp4_w4_linear(const void *x, int dtype, int64_t M, int64_t K, int
   a.err = d->flags;
   if (M <= kStreamMaxTokens) {
     const int tok8 = M <= 8 ? 1 : 2, blocks = static_cast<int>(w4_blocks(K));
-    const int splits = stream_splits(w4_panels(N, false) * ((M + 8 * tok8 - 1) / (8 * tok8)), blocks, d->sms);
+    const int splits = stream_splits(w4_panels(N, false), blocks, d->sms);
     const int rank = (blocks + splits - 1) / splits;
     int depth = (rank + 7) / 8;
     const int fit = (233472 / 2 - 2048) / (8 * w4_block_bytes(kW4BlockK / group, zeros));

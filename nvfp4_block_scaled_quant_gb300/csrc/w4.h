@@ -36,7 +36,7 @@ struct W4Args {
   void *y;  // 16-bit (M, N)
   uint32_t *err;
 };
-// The weight-streaming product: tokens in tiles of 8 * tok8, K split over a cluster of `splits` CTAs.
+// The weight-streaming product of at most 8 * tok8 (16) tokens, K split over a cluster of `splits` CTAs.
 cudaError_t launch_w4_stream(const W4Args &a, int dtype, int group, bool zeros, int tok8, int splits, int depth,
                              cudaStream_t s);
 

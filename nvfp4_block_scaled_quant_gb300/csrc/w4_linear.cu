@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_stream_kernel(const W4Args 
   volatile int *abort_flag = &s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rank = static_cast<int>(blockIdx.x) % splits, panel = static_cast<int>(blockIdx.x) / splits;
-  const int m0 = static_cast<int>(blockIdx.y) * kTok, tokens = min(kTok, a.M - m0);
+  const int tokens = a.M;  // at most kTok
   const int blocks = (a.K + kW4BlockK - 1) / kW4BlockK;
   const int first = blocks * rank / splits, kb0 = first + warp, kb1 = blocks * (rank + 1) / splits;
   uint8_t *ring = smem + warp * depth * kBytes;
@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_stream_kernel(const W4Args 
   for (int j = warp; j < kTok; j += kWarps) {
     uint32_t m = 0;
     if (j < tokens) {
-      const uint16_t *row = static_cast<const uint16_t *>(a.x) + (m0 + j) * a.ldx;
+      const uint16_t *row = static_cast<const uint16_t *>(a.x) + j * a.ldx;
       const int end = min(kb1 * kW4BlockK, a.K);
 #pragma unroll 4
       for (int k = first * kW4BlockK + 8 * lane; k < end; k += 256) m = max(m, w4_max_abs(__ldg(reinterpret_cast<const uint4 *>(row + k))));
@@ -102,7 +102,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_stream_kernel(const W4Args 
   for (int n = 0; n < kNT; ++n) factor[n] = w4_factor<T>(s_power[8 * n + g]);
 
   uint64_t sums[4][kNT][2] = {};
-  const uint16_t *x = static_cast<const uint16_t *>(a.x) + (m0 + g) * a.ldx + 8 * t;
+  const uint16_t *x = static_cast<const uint16_t *>(a.x) + g * a.ldx + 8 * t;
   auto load_x = [&](int kb, W4Frag<kNT> &f) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_stream_kernel(const W4Args 
 #pragma unroll
       for (int r = 1; r < 8; ++r)
         if (r < splits) s += v[r];
-      if (n < a.N) static_cast<uint16_t *>(a.y)[static_cast<int64_t>(m0 + (e >> 6)) * a.N + n] = T::one(s);
+      if (n < a.N) static_cast<uint16_t *>(a.y)[static_cast<int64_t>(e >> 6) * a.N + n] = T::one(s);
     }
   }
   if (splits > 1) cluster_meet();  // no CTA leaves while another reads its sums
@@ -193,7 +193,7 @@ cudaError_t stream_as(const W4Args &a, int splits, int depth, cudaStream_t s) {
     ready[dev].store(true);
   }
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(w4_panels(a.N, false) * splits), static_cast<unsigned>((a.M + 8 * kNT - 1) / (8 * kNT)));
+  cfg.gridDim = dim3(static_cast<unsigned>(w4_panels(a.N, false) * splits));
   cfg.blockDim = dim3(kWarps * 32);
   cfg.dynamicSmemBytes = static_cast<size_t>(kWarps) * depth * kBytes;
   cfg.stream = s;

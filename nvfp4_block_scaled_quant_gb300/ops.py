@@ -8,6 +8,7 @@ path.
 
 from __future__ import annotations
 
+import functools
 from dataclasses import dataclass
 from typing import Optional, Tuple
 
@@ -687,6 +688,11 @@ def w4_prepare(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.
     return W4Weight(data, G, N, K, group, scales.dtype, zeros is not None, gated)
 
 
+@functools.lru_cache(None)
+def _w4_bytes(G: int, N: int, K: int, group: int, has_zeros: bool, gated: bool) -> int:
+    return int(lib().nvfp4_w4_prepared_bytes(G, N, K, group, has_zeros, gated))
+
+
 def _w4(w: W4Weight, what: str, G: int, N: int, K: int, gated: bool, like: Optional[W4Weight] = None) -> int:
     """Data pointer of a prepared weight of the expected sizes."""
     if (w.G, w.N, w.K, w.gated) != (G, N, K, gated):
@@ -695,6 +701,14 @@ def _w4(w: W4Weight, what: str, G: int, N: int, K: int, gated: bool, like: Optio
     if like is not None and (w.dtype, w.group, w.has_zeros) != (like.dtype, like.group, like.has_zeros):
         raise ValueError(f"{what}: its scales' type, group size and zero points must be those of the other weights")
     return w.data.data_ptr()
+
+
+def _w4_whole(w: W4Weight, what: str, *sizes) -> int:
+    """The same of a weight whose data must have their bytes (a W4Weight may come from a file instead of ``w4_prepare``)."""
+    p = _w4(w, what, *sizes)
+    if w.data.dtype != torch.uint8 or w.data.numel() != _w4_bytes(w.G, w.N, w.K, w.group, w.has_zeros, w.gated) or not w.data.is_contiguous():
+        raise ValueError(f"{what}: {w.data.numel()} elements of {w.data.dtype} are not the data of {w.G} x ({w.N}, {w.K})")
+    return p
 
 
 def w4_linear(x: torch.Tensor, w: W4Weight, out: Optional[torch.Tensor] = None,
@@ -706,7 +720,7 @@ def w4_linear(x: torch.Tensor, w: W4Weight, out: Optional[torch.Tensor] = None,
         return _elsewhere(stream, (x, w.data, out, workspace), lambda: w4_linear(x, w, out, workspace))
     M, K = _size(x, "x")
     ld = _ld(x, "x", M, K, w.dtype)
-    wp = _w4(w, "w", 1, w.N, K, False)
+    wp = _w4_whole(w, "w", 1, w.N, K, False)
     if out is not None:
         _whole(out, "out", (M, w.N), (x.dtype,))
     y = out if out is not None else torch.empty(M, w.N, dtype=x.dtype, device=x.device)
@@ -745,11 +759,11 @@ def w4_moe(x: torch.Tensor, router: torch.Tensor, w13: W4Weight, w2: W4Weight, t
     T, H = _size(x, "x")
     ld = _ld(x, "x", T, H, w13.dtype)
     E, I = w13.G, w2.K
-    p13, p2 = _w4(w13, "w13", E, 2 * I, H, True), _w4(w2, "w2", E, H, I, False, w13)
+    p13, p2 = _w4_whole(w13, "w13", E, 2 * I, H, True), _w4_whole(w2, "w2", E, H, I, False, w13)
     if (shared13 is None) != (shared2 is None):
         raise ValueError("the shared expert's weights come together")
-    s13 = None if shared13 is None else _w4(shared13, "shared13", 1, 2 * I, H, True, w13)
-    s2 = None if shared2 is None else _w4(shared2, "shared2", 1, H, I, False, w13)
+    s13 = None if shared13 is None else _w4_whole(shared13, "shared13", 1, 2 * I, H, True, w13)
+    s2 = None if shared2 is None else _w4_whole(shared2, "shared2", 1, H, I, False, w13)
     rp = _whole(router, "router", (E, H), (x.dtype,))
     if out is not None:
         _whole(out, "out", (T, H), (x.dtype,))

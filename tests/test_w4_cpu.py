@@ -177,6 +177,16 @@ def test_weights_of_other_kinds(other):
         ops._w4(w, "w", 1, 64, 64, False, fake(1, 64, 64))
 
 
+def test_weights_whose_data_do_not_fit(L):
+    """A weight built by hand: too few bytes, too many, another type, every other byte."""
+    n = L.nvfp4_w4_prepared_bytes(1, 64, 64, 128, 0, 0)
+    for data in (torch.zeros(n - 1, dtype=torch.uint8), torch.zeros(n + 1, dtype=torch.uint8), torch.zeros(n, dtype=torch.int8),
+                 torch.zeros(2 * n, dtype=torch.uint8)[::2], torch.zeros(0, dtype=torch.uint8)):
+        with pytest.raises(ValueError, match="are not the data of"):
+            ops._w4_whole(dataclasses.replace(fake(1, 64, 64), data=data), "w", 1, 64, 64, False)
+    ops._w4_whole(dataclasses.replace(fake(1, 64, 64), data=torch.zeros(n, dtype=torch.uint8)), "w", 1, 64, 64, False)
+
+
 def test_workspace_of_unsupported_sizes():
     with pytest.raises(ValueError, match="unsupported"):
         ops.w4_moe_workspace(65, 64, 64, 8, 2, False, "cpu")
