@@ -131,9 +131,11 @@ struct Plan {
 // While the plan is made, in the room of the rings: each expert's tokens as a bit mask, the place of its first entry and its first
 // slot (16 bits each), and the ids.
 struct PlanScratch {
-  uint32_t tokens[2][kW4MoeMaxExperts], first[kW4MoeMaxExperts], chunk[32];
+  uint32_t tokens[2][kW4MoeMaxExperts + 32], first[kW4MoeMaxExperts + 32];
   uint16_t ids[kW4MoeMaxEntries];
 };
+// An expert's place there, such that lanes that read 32 experts apart meet different banks.
+__device__ __forceinline__ int spread(int e) { return e + (e >> 5); }
 static_assert(kW4MoeMaxT <= 64, "a token is a bit of two words");
 // Order-preserving bits of a float (NaN above or below everything), never 0: 0 marks an expert that is taken.
 __device__ __forceinline__ uint32_t order_bits(float v) {
@@ -149,12 +151,10 @@ __device__ __forceinline__ float order_value(uint32_t k) { return __uint_as_floa
 // second, or looks for the next one in the rare case that it has given that up too (looking every time took 400 cycles a
 // round at 384 experts).
 template <int kPer>
-__device__ __forceinline__ void top_k(const float *logits, int E, int topk, uint16_t *ids, float *weight) {
+__device__ __forceinline__ void top_k(const uint32_t (&key)[kPer], int topk, uint16_t *ids, float *weight) {
   const int lane = threadIdx.x & 31;
-  uint32_t key[kPer], best = 0, second = 0;
+  uint32_t best = 0, second = 0;
   int at = 0, at2 = 0;  // their places, the first among equals
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) key[i] = lane + 32 * i < E ? order_bits(__ldcg(logits + lane + 32 * i)) : 0u;
 #pragma unroll
   for (int i = 0; i < kPer; ++i) {
     if (key[i] > best)
@@ -165,12 +165,15 @@ __device__ __forceinline__ void top_k(const float *logits, int E, int topk, uint
   float mine = -INFINITY;  // lane j: the logit of the j-th choice
   for (int j = 0; j < topk; ++j) {
     const uint32_t top = __reduce_max_sync(0xffffffffu, best);
-    const int e = __reduce_min_sync(0xffffffffu, best == top ? lane + 32 * at : 0x7fffffff);
-    if (lane == j) {
-      mine = order_value(top);
-      ids[j] = static_cast<uint16_t>(e);
+    const uint32_t holders = __ballot_sync(0xffffffffu, best == top);
+    bool taken = best == top;
+    if (holders & (holders - 1)) {  // several lanes: the lowest expert's
+      const int e = __reduce_min_sync(0xffffffffu, taken ? lane + 32 * at : 0x7fffffff);
+      taken = (e & 31) == lane;
     }
-    if ((e & 31) == lane) {
+    if (lane == j) mine = order_value(top);
+    if (taken) {
+      ids[j] = static_cast<uint16_t>(lane + 32 * at);
       if (second) {
         best = second, at = at2, second = 0;
       } else {  // the next behind this one
@@ -191,6 +194,25 @@ __device__ __forceinline__ void top_k(const float *logits, int E, int topk, uint
   if (lane < topk) weight[lane] = __fdiv_rn(p, sum);
 }
 
+// ... of this warp's tokens, the next one's logits on their way meanwhile.
+template <int kPer>
+__device__ __forceinline__ void choose(const W4MoeArgs &a, uint16_t *ids, float *weight) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint32_t next[kPer];
+  auto load = [&](int t) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) next[i] = lane + 32 * i < a.E ? __float_as_uint(__ldcg(a.logits + t * a.E + lane + 32 * i)) : 0u;
+  };
+  if (warp < a.T) load(warp);
+  for (int t = warp; t < a.T; t += kThreads / 32) {
+    uint32_t key[kPer];
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) key[i] = lane + 32 * i < a.E ? order_bits(__uint_as_float(next[i])) : 0u;
+    if (t + kThreads / 32 < a.T) load(t + kThreads / 32);
+    top_k<kPer>(key, a.topk, ids + t * a.topk, weight + t * a.topk);
+  }
+}
+
 // How many panels (log2) an item holds, shared out to the warps, so that a warp has more K blocks in a row and the items' own
 // cost (the first load of its activations, its sums, its signals) is spread over more of them.  That pays where a CTA takes many items; where it
 // takes few, smaller ones spread better.  Two panels / one: 59 tokens, 80 experts of 5280 x 352 (22 items of the down projection to a
@@ -205,19 +227,14 @@ template <class T>
 __device__ void make_plan(const W4MoeArgs &a, Plan &plan, PlanScratch &s) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, entries = a.T * a.topk;
   if (entries > 32)
-    for (int e = tid; e < a.E; e += kThreads) s.tokens[0][e] = s.tokens[1][e] = 0u;
+    for (int e = tid; e < a.E; e += kThreads) s.tokens[0][spread(e)] = s.tokens[1][spread(e)] = 0u;
   if (tid < a.T) plan.power[tid] = w4_power<T>(__ldcg(a.x_max + tid));
-  for (int t = warp; t < a.T; t += kThreads / 32) {
-    const float *l = a.logits + static_cast<int64_t>(t) * a.E;
-    uint16_t *ids = s.ids + t * a.topk;
-    float *w = plan.weight + t * a.topk;
-    if (a.E <= 128)
-      top_k<4>(l, a.E, a.topk, ids, w);
-    else if (a.E <= 384)
-      top_k<12>(l, a.E, a.topk, ids, w);
-    else
-      top_k<32>(l, a.E, a.topk, ids, w);
-  }
+  if (a.E <= 128)
+    choose<4>(a, s.ids, plan.weight);
+  else if (a.E <= 384)
+    choose<12>(a, s.ids, plan.weight);
+  else
+    choose<32>(a, s.ids, plan.weight);
   const int shared_slots = a.sh13 ? (a.T + 7) / 8 : 0;
   for (int i = tid; i < shared_slots; i += kThreads) {
     plan.slot_expert[i] = 0;
@@ -251,42 +268,38 @@ __device__ void make_plan(const W4MoeArgs &a, Plan &plan, PlanScratch &s) {
   }
   for (int f = tid; f < entries; f += kThreads) {
     const int t = f / a.topk;
-    atomicOr(&s.tokens[t >> 5][s.ids[f]], 1u << (t & 31));
+    atomicOr(&s.tokens[t >> 5][spread(s.ids[f])], 1u << (t & 31));
   }
   __syncthreads();
-  // exclusive sums over the experts, entries in the low and slots in the high half: of each 32 experts by a warp, then
-  // over those
-  const int chunks = (a.E + 31) / 32;
-  for (int c = warp; c < chunks; c += kThreads / 32) {
-    const int e = 32 * c + lane;
-    const uint32_t n = e < a.E ? __popc(s.tokens[0][e]) + __popc(s.tokens[1][e]) : 0u, own = n | ((n + 7) / 8 << 16);
+  // exclusive sums over the experts, entries in the low and slots in the high half: each lane of a warp those of `per`
+  // experts in a row, twice
+  if (warp == 0) {
+    const int per = (a.E + 31) / 32, e0 = lane * per, e1 = min(e0 + per, a.E);
+    uint32_t own = 0;
+    auto both = [&](int e) {
+      const uint32_t n = __popc(s.tokens[0][spread(e)]) + __popc(s.tokens[1][spread(e)]);
+      return n | ((n + 7) / 8 << 16);
+    };
+    for (int e = e0; e < e1; ++e) own += both(e);
     uint32_t sum = own;
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
       const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
       if (lane >= o) sum += u;
     }
-    if (e < a.E) s.first[e] = sum - own;
-    if (lane == 31) s.chunk[c] = sum;
-  }
-  __syncthreads();
-  if (warp == 0) {
-    uint32_t sum = lane < chunks ? s.chunk[lane] : 0u;
-    const uint32_t own = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o *= 2) {
-      const uint32_t u = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += u;
-    }
-    s.chunk[lane] = sum - own + (static_cast<uint32_t>(shared_slots) << 16);
     if (lane == 31) plan.slots = shared_slots + static_cast<int>(sum >> 16), plan.shared_slots = shared_slots;
+    sum += (static_cast<uint32_t>(shared_slots) << 16) - own;
+    for (int e = e0; e < e1; ++e) {
+      s.first[spread(e)] = sum;
+      sum += both(e);
+    }
   }
   __syncthreads();
   for (int f = tid; f < entries; f += kThreads) {
     const int e = s.ids[f], t = f / a.topk;
-    const uint32_t m0 = s.tokens[0][e], m1 = s.tokens[1][e], below = (1u << (t & 31)) - 1u;
+    const uint32_t m0 = s.tokens[0][spread(e)], m1 = s.tokens[1][spread(e)], below = (1u << (t & 31)) - 1u;
     const int n = __popc(m0) + __popc(m1), rank = t < 32 ? __popc(m0 & below) : __popc(m0) + __popc(m1 & below);
-    const uint32_t start = s.first[e] + s.chunk[e >> 5];
+    const uint32_t start = s.first[spread(e)];
     const int first = static_cast<int>(start & 0xFFFFu) + rank;
     plan.sorted[first] = static_cast<uint16_t>(f);
     if (rank % 8 == 0) {
