@@ -40,27 +40,28 @@ int stream_splits(int64_t ctas, int blocks, int sms) {
   return best;
 }
 
-// Estimated times, in units of 10 ns, that choose between the kernels and their tiles.  The coefficients were fitted to times on a
-// GB300 over 32 to 1024 tokens and six (K, N) between 512 x 512 and 7168 x 7168; they rank the choices, nothing else depends on
-// them.  Groups of 64 and 32 take longer where each group's sums pass through registers.
-constexpr int64_t kTcStart[4] = {460, 600, 910, 1010}, kTcBlock[4] = {54, 52, 50, 66};  // by tokens of a tile: 16, 32, 64, 128
-constexpr int64_t kTileStart = 700, kTileEnd[2] = {300, 200}, kTileBlock[2] = {30, 23};  // 256 and 128 columns; 64 K
+// Estimated times in ns that choose between the kernels, their tiles and splits.  The coefficients were fitted to times on a
+// GB300 over 32 to 1024 tokens and six (K, N) between 512 x 512 and 7168 x 7168, every choice of each measured (the chosen one is
+// 0.1% slower than the best on average); they rank the choices, nothing else depends on them.  Groups of 64 and 32 take longer
+// where each group's sums pass through registers.
+constexpr int64_t kTcStart[4] = {4600, 5200, 6100, 7900}, kTcBlock[4] = {540, 470, 620, 720};  // by tokens of a tile: 16, 32, 64, 128
+constexpr int64_t kTileStart = 5400, kTileEnd[2] = {2200, 1500}, kTileBlock[2] = {272, 205};   // 256 and 128 columns; 64 K
 
-// How w4_tc_kernel covers M tokens: tiles of `tok`, clusters of `splits` CTAs along K.  One CTA to an SM: a cluster takes
-// `splits` of the 19 SMs of a GPC.
+// How w4_tc_kernel covers M tokens: tiles of `tok`, clusters of `splits` CTAs along K, one CTA to an SM.
+constexpr int kTcClusters[4] = {152, 76, 46, 36};  // of 1 to 4 CTAs that a GB300 holds at once
 struct TcPlan {
   int tok, splits;
   int64_t time;
 };
-TcPlan tc_plan(int64_t M, int64_t N, int64_t K, int group, int sms) {
+TcPlan tc_plan(int64_t M, int64_t N, int64_t K, int group) {
   TcPlan p = {16, 1, 0};
   int size = 0;
   while (p.tok < 128 && p.tok < M) p.tok *= 2, ++size;
   const int64_t tiles = (N + 127) / 128 * ((M + p.tok - 1) / p.tok), blocks = w4_blocks(K);
-  const int64_t block = kTcBlock[size] * (group == 32 ? 16 : group == 64 ? 11 : 10) / 10;
+  const int64_t block = kTcBlock[size] * (group == 32 ? 174 : group == 64 ? 110 : 100) / 100;
   for (int s = 1; s <= 4 && s <= blocks; ++s) {
-    const int64_t fit = sms >= 8 * s ? sms / 8 / s * 8 : 1;  // clusters at once
-    const int64_t time = (tiles + fit - 1) / fit * ((blocks + s - 1) / s * block + kTcStart[size]);
+    const int64_t waves = (tiles + kTcClusters[s - 1] - 1) / kTcClusters[s - 1];
+    const int64_t time = waves * ((blocks + s - 1) / s * block + kTcStart[size]);
     if (p.time == 0 || time < p.time) p.time = time, p.splits = s;
   }
   return p;
@@ -73,11 +74,11 @@ struct PairPlan {
 };
 PairPlan pair_plan(int64_t M, int64_t N, int64_t K, int group, int sms) {
   PairPlan p = {256, 0};
-  const int64_t expand = N * K / 27000;  // 2.5 bytes a weight
+  const int64_t expand = N * K / 2640;  // 2.5 bytes a weight
   for (int i = 0; i < 2; ++i) {
     const int cols = i ? 128 : 256;
     const int64_t tiles = (N + kTRows - 1) / kTRows * ((M + cols - 1) / cols), waves = (tiles + sms / 2 - 1) / (sms / 2);
-    const int64_t block = kTileBlock[i] * (group == 32 ? 26 : group == 64 ? 14 : 10) / 10;
+    const int64_t block = kTileBlock[i] * (group == 32 ? 27 : group == 64 ? 14 : 10) / 10;
     const int64_t time = kTileStart + expand + waves * ((K + 63) / 64 * block + kTileEnd[i]);
     if (p.time == 0 || time < p.time) p = {cols, time};
   }
@@ -92,7 +93,7 @@ constexpr int kPlanSms = 152;
 constexpr int64_t kTcMaxTokens = int64_t(65535) * 128;  // the grid's second dimension
 bool takes_pairs(int64_t M, int64_t N, int64_t K, int group) {
   if (M > kTcMaxTokens) return true;
-  return M > kStreamMaxTokens && pair_plan(M, N, K, group, kPlanSms).time < tc_plan(M, N, K, group, kPlanSms).time;
+  return M > kStreamMaxTokens && pair_plan(M, N, K, group, kPlanSms).time < tc_plan(M, N, K, group).time;
 }
 
 // For the pair GEMM: where the written-out weights and their scales are in the workspace.
@@ -213,7 +214,7 @@ nvfp4_status nvfp4_w4_linear(const void *x, int dtype, int64_t M, int64_t K, int
     return NVFP4_OK;
   }
   if (L.total == 0) {
-    const TcPlan p = tc_plan(M, N, K, group, kPlanSms);
+    const TcPlan p = tc_plan(M, N, K, group);
     CUtensorMap mx;
     if ((st = make_map(__func__, &mx, x, K * 2, M, ldx * 2, p.tok)) != NVFP4_OK) return st;
     NV_CUDA(launch_w4_tc(mx, a, dtype, group, zeros, p.tok, p.splits, s), "4-bit linear launch");
@@ -222,9 +223,10 @@ nvfp4_status nvfp4_w4_linear(const void *x, int dtype, int64_t M, int64_t K, int
   uint16_t *ints = static_cast<uint16_t *>(ws);
   float *scales = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + L.scales);
   const int cols = pair_plan(M, N, K, group, kPlanSms).cols;
-  CUtensorMap mw, mx;
+  CUtensorMap mw, mx, my = {};
   if ((st = make_map(__func__, &mw, ints, K * 2, N, K * 2, kTHalf)) != NVFP4_OK) return st;
   if ((st = make_map(__func__, &mx, x, K * 2, M, ldx * 2, cols / 2)) != NVFP4_OK) return st;
+  if (N % 8 == 0 && (st = make_map(__func__, &my, y, N * 2, M, N * 2, 32, 64, CU_TENSOR_MAP_SWIZZLE_NONE)) != NVFP4_OK) return st;
   TileArgs t = {};
   t.M = a.N;
   t.N = a.M;
@@ -236,7 +238,7 @@ nvfp4_status nvfp4_w4_linear(const void *x, int dtype, int64_t M, int64_t K, int
   t.ldo = N;
   t.err = d->flags;
   NV_CUDA(launch_w4_expand(a, dtype, group, zeros, ints, scales, L.lds, s), "4-bit weight expansion launch");
-  NV_CUDA(in_pair_turn(d, s, [&] { return launch_w4_tile_gemm(mw, mx, t, dtype, group, cols, s); }), "4-bit tile GEMM launch");
+  NV_CUDA(in_pair_turn(d, s, [&] { return launch_w4_tile_gemm(mw, mx, my, t, dtype, group, cols, s); }), "4-bit tile GEMM launch");
   return NVFP4_OK;
 }
 

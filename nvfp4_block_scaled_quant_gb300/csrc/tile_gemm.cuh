@@ -85,11 +85,14 @@ struct TileCfg {
   static constexpr int kStageBytes = kABytes + kBBytes;
   static constexpr int kRing = kStages * kStageBytes;
   static constexpr uint32_t kTmemCols = 2 * kCols;  // two accumulators
-  static constexpr int kStoreBytes = 8 * 32 * 36;   // kFp8: a warp's 32 rows of 16 columns on their way out
-  static constexpr size_t kSmem = 1024 + kRing + 256 + kStoreBytes;
-  static_assert(kSmem <= 232448, "per-block shared memory limit");
   static_assert((2 * kStages + 4) * 8 + 8 <= 256, "barrier region");
 };
+// Outputs on their way out.  kFp8: a warp's 32 rows of 16 columns; kW4: two places of 32 rows of 32 columns.
+template <TileOp kOp>
+constexpr int kTStoreBytes = kOp == TileOp::kW4 ? 8 * 2 * 2048 : 8 * 32 * 36;
+template <TileOp kOp, int kCols>
+constexpr size_t kTSmem = 1024 + TileCfg<kCols>::kRing + 256 + kTStoreBytes<kOp>;
+static_assert(kTSmem<TileOp::kW4, 256> <= 232448 && kTSmem<TileOp::kW4, 128> <= 232448, "per-block shared memory limit");
 constexpr int kTAllocWarp = 3;  // owns the tensor memory; it has no other role, so it is never diverged
 constexpr int kTEpiWarp0 = 4;  // epilogue warps start on a multiple of four: a warp reads lane quarter warp % 4
 template <TileOp kOp>
@@ -109,6 +112,16 @@ static_assert(kTEpiWarp0 * kTLightRegs + kTEpiWarps<TileOp::kFp8> * kTEpiRegs <=
               "register split within what the block was launched with");
 constexpr int kAhead = 4;             // kFp8: K blocks that a thread's scales are fetched ahead
 constexpr int kTGroupM = 8;           // m tiles walked together, so that a wave shares rows of B in L2
+// kW4: a box of shared memory to the output, and the wait until the thread's copies but the last kLeft have been read.
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, int x, int y, const void *from) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.bulk_group [%0, {%1, %2}], [%3];" ::"l"(map), "r"(x), "r"(y), "r"(smem_u32(from))
+               : "memory");
+  asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+template <int kLeft>
+__device__ __forceinline__ void bulk_store_wait_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kLeft) : "memory");
+}
 template <TileOp kOp, class T, int kAct, int kTCols>
 __global__ void __launch_bounds__(kTThreads<kOp>, 1)
     tile_gemm_kernel(const __grid_constant__ CUtensorMap tmA0, const __grid_constant__ CUtensorMap tmA1,
@@ -439,36 +452,32 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
     const float unscale = kUnscale ? __ldg(args.unscale) : 1.f;
     // kTScaled: the sums of this thread's row, kBRows columns from out_n0 on
     float sum[kScaled ? kBRows : 1];
-    int out_row = 0, out_n0 = 0;
+    int out_row = 0, out_n0 = 0, store_turn = 0;
     auto store_tile = [&]() {
       if constexpr (kW4) {
-        // Eight lanes exchange 8 rows x 8 columns, so that each stores 16 bytes of an output row: lane l gets column l % 8
-        // of every eight, rows of its group of eight lanes (2-byte stores of 32 lanes cost 5 us more per tile).
+        // A lane's row is an output column.  32 output rows of a warp's 32 columns at a time go through one of its two places in
+        // shared memory, from where TMA takes them: a warp is free of them once they are in shared memory.  (Eight lanes that
+        // exchanged 8 x 8 through shuffles and stored 16 bytes each took 4 us of a tile: 4096 tokens 1536 -> 16384 177 us instead of 143.)
         uint16_t *dst = static_cast<uint16_t *>(args.out);
         const int left = args.N - out_n0;
         if (vec) {
-          const bool b0 = lane & 1, b1 = lane & 2, b2 = lane & 4;
-          dst += (out_n0 + (lane & 7)) * args.ldo + (out_row & ~7);
 #pragma unroll
-          for (int i = 0; i < kBRows; i += 8) {
-            uint32_t q[4], u[2][2], v[4];
+          for (int c = 0; c < kBRows / 32; ++c) {
+            if (32 * c < left && (out_row & ~31) < args.M) {
+              uint16_t *place = s_store + (warp - kTEpiWarp0) * 2048 + store_turn * 1024;
+              bulk_store_wait_read<1>();  // of the place's last copy
+              __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t a = T::pack(sum[i + 2 * j], sum[i + 2 * j + 1]), o = __shfl_xor_sync(0xffffffffu, a, 1);
-              q[j] = b0 ? __byte_perm(o, a, 0x7632) : __byte_perm(a, o, 0x5410);
+              for (int j = 0; j < 32; j += 2) {
+                const uint32_t v = T::pack(sum[32 * c + j], sum[32 * c + j + 1]);
+                place[j * 32 + lane] = static_cast<uint16_t>(v);
+                place[j * 32 + 32 + lane] = static_cast<uint16_t>(v >> 16);
+              }
+              fence_proxy_async_shared();
+              __syncwarp();
+              if (lane == 0) tma_store_2d(&tmA2, (out_row & ~31) * 2, out_n0 + 32 * c, place);
+              store_turn ^= 1;
             }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t keep = b1 ? q[2 * j + 1] : q[2 * j], got = __shfl_xor_sync(0xffffffffu, b1 ? q[2 * j] : q[2 * j + 1], 2);
-              u[j][0] = b1 ? got : keep, u[j][1] = b1 ? keep : got;
-            }
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const uint32_t keep = b2 ? u[1][j] : u[0][j], got = __shfl_xor_sync(0xffffffffu, b2 ? u[0][j] : u[1][j], 4);
-              v[j] = b2 ? got : keep, v[2 + j] = b2 ? keep : got;
-            }
-            if (i + (lane & 7) < left && (out_row & ~7) < args.M)
-              *reinterpret_cast<uint4 *>(dst + i * args.ldo) = make_uint4(v[0], v[1], v[2], v[3]);
           }
         } else if (out_row < args.M) {
           dst += out_n0 * args.ldo + out_row;
@@ -631,6 +640,7 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
       }
     }
     if (ok && cluster_id < total) store_tile();
+    if constexpr (kW4) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
 
   tc_fence_before();
@@ -667,7 +677,7 @@ template <TileOp kOp, class T, int kAct, int kTCols>
 cudaError_t launch_tile_gemm_cols(const CUtensorMap &a0, const CUtensorMap &a1, const CUtensorMap &b0,
                                   const CUtensorMap &b1, const CUtensorMap &a2, const CUtensorMap &b2,
                                   const TileArgs &args, cudaStream_t s) {
-  using C = TileCfg<kTCols>;
+  constexpr size_t kSmem = kTSmem<kOp, kTCols>;
   auto kernel = tile_gemm_kernel<kOp, T, kAct, kTCols>;
   static std::atomic<int> fit[64];  // per device; the kernel's shared-memory limit is set with the query
   int dev = 0;
@@ -676,7 +686,7 @@ cudaError_t launch_tile_gemm_cols(const CUtensorMap &a0, const CUtensorMap &a1, 
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   int n = fit[dev].load();
   if (n <= 0) {
-    n = tile_gemm_max_clusters(kernel, kTThreads<kOp>, C::kSmem);
+    n = tile_gemm_max_clusters(kernel, kTThreads<kOp>, kSmem);
     if (n <= 0) {
       const cudaError_t last = cudaGetLastError();
       return last != cudaSuccess ? last : cudaErrorLaunchOutOfResources;
@@ -693,7 +703,7 @@ cudaError_t launch_tile_gemm_cols(const CUtensorMap &a0, const CUtensorMap &a1, 
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * clusters);
   cfg.blockDim = dim3(kTThreads<kOp>);
-  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.dynamicSmemBytes = kSmem;
   cfg.stream = s;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;

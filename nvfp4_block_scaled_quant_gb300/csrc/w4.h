@@ -50,8 +50,9 @@ cudaError_t launch_w4_tc(const CUtensorMap &x, const W4Args &a, int dtype, int g
 struct TileArgs;
 cudaError_t launch_w4_expand(const W4Args &a, int dtype, int group, bool zeros, uint16_t *out, float *scales, int64_t lds,
                              cudaStream_t s);
-cudaError_t launch_w4_tile_gemm(const CUtensorMap &w, const CUtensorMap &x, const TileArgs &args, int dtype, int group, int cols,
-                                cudaStream_t s);
+// y: a map of the output with boxes of 32 x 32, used where N % 8 == 0 (else any map).
+cudaError_t launch_w4_tile_gemm(const CUtensorMap &w, const CUtensorMap &x, const CUtensorMap &y, const TileArgs &args, int dtype,
+                                int group, int cols, cudaStream_t s);
 
 struct W4MoeArgs {
   const void *x;  // 16-bit (T, H), row stride ldx

@@ -53,10 +53,10 @@ cudaError_t expand_as(const W4Args &a, int group, bool zeros, uint16_t *out, flo
 }
 
 template <class T>
-cudaError_t gemm_as(const CUtensorMap &w, const CUtensorMap &x, const TileArgs &args, int group, int cols, cudaStream_t s) {
-  if (group == 128) return launch_tile_gemm_as<TileOp::kW4, T, 128>(w, w, x, x, w, x, args, cols, s);
-  if (group == 64) return launch_tile_gemm_as<TileOp::kW4, T, 64>(w, w, x, x, w, x, args, cols, s);
-  return launch_tile_gemm_as<TileOp::kW4, T, 32>(w, w, x, x, w, x, args, cols, s);
+cudaError_t gemm_as(const CUtensorMap &w, const CUtensorMap &x, const CUtensorMap &y, const TileArgs &args, int group, int cols, cudaStream_t s) {
+  if (group == 128) return launch_tile_gemm_as<TileOp::kW4, T, 128>(w, w, x, x, y, x, args, cols, s);
+  if (group == 64) return launch_tile_gemm_as<TileOp::kW4, T, 64>(w, w, x, x, y, x, args, cols, s);
+  return launch_tile_gemm_as<TileOp::kW4, T, 32>(w, w, x, x, y, x, args, cols, s);
 }
 
 }  // namespace
@@ -66,9 +66,9 @@ cudaError_t launch_w4_expand(const W4Args &a, int dtype, int group, bool zeros, 
   return dtype == NVFP4_DT_BF16 ? expand_as<Bf16>(a, group, zeros, out, scales, lds, s) : expand_as<Fp16>(a, group, zeros, out, scales, lds, s);
 }
 
-cudaError_t launch_w4_tile_gemm(const CUtensorMap &w, const CUtensorMap &x, const TileArgs &args, int dtype, int group, int cols,
-                                cudaStream_t s) {
-  return dtype == NVFP4_DT_BF16 ? gemm_as<Bf16>(w, x, args, group, cols, s) : gemm_as<Fp16>(w, x, args, group, cols, s);
+cudaError_t launch_w4_tile_gemm(const CUtensorMap &w, const CUtensorMap &x, const CUtensorMap &y, const TileArgs &args, int dtype,
+                                int group, int cols, cudaStream_t s) {
+  return dtype == NVFP4_DT_BF16 ? gemm_as<Bf16>(w, x, y, args, group, cols, s) : gemm_as<Fp16>(w, x, y, args, group, cols, s);
 }
 
 }  // namespace nvfp4
