@@ -224,7 +224,7 @@ __device__ __forceinline__ void store_columns8(const NormArgs &a, int64_t m, int
 // ---------------------------------------------------------------- forward
 
 // Few rows: one row per CTA, kChunks groups of 8 columns per thread, in registers over both
-// reductions.  kOut8: y in 8 bits, and in 16 if a.y is given.
+// reductions.  kOut8: y in 8 bits, and in 16 if a.y is given (one row of 7168 3.3 us).
 template <class T, bool kR32, int kChunks, bool kOut8>
 __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const NormArgs a) {
   __shared__ float red[2][32];
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(1024, 1) residual_norm_kernel(const NormArgs a
 // kThreads, kCtas: most threads of a CTA and CTAs per SM, which set the registers per thread: the
 // parameters of a thread's columns stay in registers (the ring leaves little of the SM's memory to
 // its cache, and re-reading them for every row cost as much as the rows).  8192 x 7168 in bf16: 76 us,
-// 6.2 TB/s.
+// 6.2 TB/s; 4096 x 7168 with both outputs (kOut8) 47.7 us, 5.6 TB/s, 70% of the issue slots.
 template <class T, bool kR32, int kChunks, int kThreads, int kCtas, bool kOut8>
 __global__ void __launch_bounds__(kThreads, kCtas) residual_norm_rows_kernel(const NormArgs a, int stages) {
   extern __shared__ __align__(128) uint8_t smem[];  // used as declared: its loads are known to be shared ones

@@ -20,10 +20,11 @@
 //               longer than the other's MMAs.  Measured and left: four accumulators of 128 columns (two
 //               issuers; 8 warps 200 us, 16 warps 175 us), 16 epilogue warps on 256 columns, two batches
 //               of columns in flight, activation scales through a shared-memory ring.
-//   Op::kW4     A = the codes less their zero points (N, K) as 16-bit integers, B = x (M, K): the same promotion, of
-//               every group of 32, 64 or 128 K with its scale (kAct holds the group's size; one scale per row of A, which the
-//               operands are swapped for: a thread's columns share it).  A group of 128 is two K blocks, one of 32 half a block, which the
-//               two issuers share.  The output is written across: a lane's row is an output column.
+//   Op::kW4     A = the codes less their zero points (N, K) as 16-bit integers, B = x (M, K): the same promotion,
+//               of every group of 32, 64 or 128 K (kAct) with its scale.  The operands are swapped, so that
+//               a thread's columns share the one scale of its row of A.  A group of 128 is two K blocks, one of
+//               32 half a block, which the two issuers share.  The output is written across: a lane's row is an
+//               output column.  4096 x 7168 x 7168, groups of 128: 234 us, 1.80 PF/s, tensor pipe 86% busy.
 //   Op::kGated  A = x (M, K), B = rows of Wg (even CTA) and the matching rows of Wu (odd CTA):
 //               the first half of the accumulator's columns is g, the second u of the same outputs.
 //   Op::kGrad   two products in one launch.  dx = dg Wg + du Wu: A = [dg | du] in two segments of K = I,
