@@ -108,3 +108,28 @@ def test_stream_and_graph(M):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, torch.roll(want, k, 0)) and torch.equal(z, y)
+
+
+@pytest.mark.parametrize("group,zeros,kind", [(128, False, "bf16"), (128, True, "fp16"), (64, True, "bf16"), (32, False, "fp16"), (32, True, "bf16")])
+@pytest.mark.parametrize("M,K,N", [(1100, 136, 1160), (900, 264, 2056), (2100, 776, 1137), (1281, 200, 4104), (600, 520, 4100), (3001, 264, 1048),
+                                   (513, 64, 16392), (700, 72, 8200)])
+def test_many_rows(M, K, N, group, zeros, kind):
+    """Sizes that go through written-out weights: edges inside tiles of either direction, outputs of whole 16-byte rows and others, groups
+    and K blocks that end early; nothing is written outside of y."""
+    x, ck, w = make(M, K, N, group, zeros, kind, 8)
+    pad = 4096
+    flat = torch.full((M * N + 2 * pad,), 7.0, device="cuda", dtype=x.dtype)
+    y = ops.w4_linear(x, w, out=flat[pad:pad + M * N].view(M, N))
+    verify(x, ck, group, y)
+    assert (flat[:pad] == 7).all() and (flat[pad + M * N:] == 7).all()
+    assert torch.equal(ops.w4_linear(x, w), y)
+
+
+def test_many_rows_do_not_mix():
+    x, _, w = make(1500, 264, 1048, 128, False, "bf16", 9)
+    y = ops.w4_linear(x, w)
+    bad = x.clone()
+    bad[700, 5] = float("nan")
+    z = ops.w4_linear(bad, w)
+    assert torch.equal(torch.cat([z[:700], z[701:]]), torch.cat([y[:700], y[701:]]))
+    assert not torch.isfinite(z[700]).any()
