@@ -639,27 +639,46 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
   // Panels of y to which this CTA was the last to add: a token's experts in the order of its top k, then the shared one.
   __syncwarp();
   asm volatile("bar.sync 1, %0;" ::"n"((kWarps + 1) * 32) : "memory");
-  constexpr int kPairs = kW4PanelRows / 2;
-  for (int e = tid; e < s_finished * a.T * kPairs; e += (kWarps + 1) * 32) {
-    const int at = e / kPairs, row = at % a.T, n = s_panels[at / a.T] * kW4PanelRows + 2 * (e % kPairs);
-    if (n >= a.H) continue;
-    const float2 *p = reinterpret_cast<const float2 *>(a.part + static_cast<int64_t>(row) * a.topk * a.H + n);
-    float2 v = make_float2(0.f, 0.f), u[9];
-    for (int j0 = 0; j0 < a.topk; j0 += 8) {  // eight loads and the shared expert's in flight
+  // Two or four columns to a thread: four are fewer turns where a panel has more than a pair for each thread (51 tokens, 116
+  // experts of 1384 x 184 55.6 -> 52.0 us), two 1% less time where it has not.
+  const int finished_rows = s_finished * a.T;
+  auto add_up = [&](auto pair) {
+    using V = decltype(pair);
+    constexpr int kCols = sizeof(V) / 4, kChunks = kW4PanelRows / kCols;
+    for (int e = tid; e < finished_rows * kChunks; e += (kWarps + 1) * 32) {
+      const int at = e / kChunks, row = at % a.T, n = s_panels[at / a.T] * kW4PanelRows + kCols * (e % kChunks);
+      if (n >= a.H) continue;
+      const float *p = a.part + static_cast<int64_t>(row) * a.topk * a.H + n;
+      V u[9];
+      float v[kCols] = {};
+      for (int j0 = 0; j0 < a.topk; j0 += 8) {  // eight loads and the shared expert's in flight
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j0 + j < a.topk) u[j] = __ldcg(p + static_cast<int64_t>(j0 + j) * (a.H / 2));
-      if (shared_slots && j0 + 8 >= a.topk) u[8] = __ldcg(reinterpret_cast<const float2 *>(a.part + static_cast<int64_t>(entries + row) * a.H + n));
+        for (int j = 0; j < 8; ++j)
+          if (j0 + j < a.topk) u[j] = __ldcg(reinterpret_cast<const V *>(p + static_cast<int64_t>(j0 + j) * a.H));
+        if (shared_slots && j0 + 8 >= a.topk) u[8] = __ldcg(reinterpret_cast<const V *>(a.part + static_cast<int64_t>(entries + row) * a.H + n));
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (j0 + j < a.topk) {
-          const float w = plan.weight[row * a.topk + j0 + j];
-          v.x = fmaf(w, u[j].x, v.x), v.y = fmaf(w, u[j].y, v.y);
-        }
+        for (int j = 0; j < 8; ++j)
+          if (j0 + j < a.topk) {
+            const float w = plan.weight[row * a.topk + j0 + j];
+#pragma unroll
+            for (int c = 0; c < kCols; ++c) v[c] = fmaf(w, reinterpret_cast<const float *>(&u[j])[c], v[c]);
+          }
+      }
+      if (shared_slots) {
+#pragma unroll
+        for (int c = 0; c < kCols; ++c) v[c] += reinterpret_cast<const float *>(&u[8])[c];
+      }
+      uint32_t *y = reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.y) + static_cast<int64_t>(row) * a.H + n);
+      if constexpr (kCols == 4)
+        *reinterpret_cast<uint2 *>(y) = make_uint2(T::pack(v[0], v[1]), T::pack(v[2], v[3]));
+      else
+        *y = T::pack(v[0], v[1]);
     }
-    if (shared_slots) v.x += u[8].x, v.y += u[8].y;
-    *reinterpret_cast<uint32_t *>(static_cast<uint16_t *>(a.y) + static_cast<int64_t>(row) * a.H + n) = T::pack(v.x, v.y);
-  }
+  };
+  if (a.T * (kW4PanelRows / 2) <= (kWarps + 1) * 32)
+    add_up(float2{});
+  else
+    add_up(float4{});
 }
 
 template <class T, int kNT>
