@@ -111,7 +111,7 @@ LinearWs linear_ws(int64_t M, int64_t N, int64_t K, int group) {
 }
 
 struct MoeWs {
-  size_t logits, h, part, counters, x_max, total;
+  size_t logits, h, part, counters, total;
 };
 bool moe_sizes_ok(int64_t T, int64_t H, int64_t I, int64_t E, int topk) {
   return T >= 0 && T <= kW4MoeMaxT && H > 0 && I > 0 && H % 8 == 0 && I % 8 == 0 && H <= kW4MoeMaxDim && I <= kW4MoeMaxDim && E > 0 &&
@@ -124,8 +124,7 @@ MoeWs moe_ws(int64_t T, int64_t H, int64_t I, int64_t E, int topk, bool shared) 
   w.h = align256(static_cast<size_t>(T * E) * 4);
   w.part = align256(w.h + rows * static_cast<size_t>(I) * 2);
   w.counters = align256(w.part + rows * static_cast<size_t>(H) * 4);
-  w.x_max = align256(w.counters + (kW4MoeCounters + static_cast<size_t>((H + kW4PanelRows - 1) / kW4PanelRows)) * 4);
-  w.total = align256(w.x_max + kW4MoeMaxT * 4);
+  w.total = align256(w.counters + (kW4MoeCounters + static_cast<size_t>((H + kW4PanelRows - 1) / kW4PanelRows)) * 4);
   return w;
 }
 
@@ -297,7 +296,6 @@ nvfp4_status nvfp4_w4_moe(const void *x, int dtype, int64_t T, int64_t H, int64_
   a.h = reinterpret_cast<uint16_t *>(p + L.h);
   a.part = reinterpret_cast<float *>(p + L.part);
   a.counters = reinterpret_cast<int *>(p + L.counters);
-  a.x_max = reinterpret_cast<uint32_t *>(p + L.x_max);
   a.err = d->flags;
   NV_CUDA(launch_w4_moe(a, dtype, group, zeros, d->sms, static_cast<cudaStream_t>(stream)), "4-bit mixture-of-experts launch");
   return NVFP4_OK;

@@ -1,20 +1,16 @@
 // Device code shared by the kernels that stream 4-bit weights through the warp-level tensor instructions: a warp takes
 // prepared blocks of 64 rows x 128 K out of shared memory and adds their products with 8 or 16 tokens to its sums.
 //
-//   y = sum over groups of s (sum (c - z) x) = sum over groups of s (sum c x - z sum x)
+//   y = sum over groups of s sum (c - z) x
 //
 // A code c in the low bits of a bf16 or fp16 number is that number's smallest subnormal times c, and bits 4 to 7 count 16
-// times as much (with bit 7 the exponent of a bf16 becomes 1, whose step is the same): the tensor cores take subnormal operands
-// exactly, so the codes need no conversion at all.  Two masks give the low and high halves of a word's even bytes, one
-// shift and the same masks those of the odd ones: five operations for eight codes, where numbers 1 + c / 16 took
-// seven (these operations bound the product of one token once the weights arrive at the speed of memory: 384 experts, 16
-// tokens 445 -> 405 us).  The step of 2^-133 (bf16) or 2^-24 (fp16) is made up for by the activations: a row
-// is multiplied by a power of two that brings its largest magnitude to 2^120 (2^14) on its way into the MMA, the elements
-// that meet high halves by a sixteenth of it, and the sums by the inverse.  In bf16 nothing is lost by that; in
-// fp16 an element keeps everything down to 2^-36 of its row's largest.
-// sum x of each group and token comes from a fifth row tile whose codes are all one.  Products are exact, sums are
-// fp32, scales apply to the fp32 sums of their group: no weight is rounded.  (A group's sum is 2^-13 of its size in bf16, so that it
-// keeps its bits under the smallest scales; brought to 2^60, rows under scales of 2^-76 were 4% off and under 2^-90 zero.)
+// times as much (with bit 7 the exponent of a bf16 becomes 1, whose step is the same).  Two masks give the low and high halves
+// of a word's even bytes, one shift and the same masks those of the odd ones, and one multiplication and addition of
+// each pair takes the zero points off: nine operations for eight codes.  The result (c - z) 2^-kRest is exact in either type and
+// normal, so that activations go into the MMA as they are and the sums are multiplied by 2^kRest at the end.  Products are exact,
+// sums are fp32, scales apply to the fp32 sums of their group: no weight is rounded.
+// (Codes as they are, their sums less z sum x, are five operations, but c x and z x round apart where c = z: under an
+// activation of 10^9 times its neighbours, which meets weights of zero, nothing of the neighbours was left.)
 #pragma once
 
 #include "mma16x8.cuh"
@@ -22,30 +18,22 @@
 
 namespace nvfp4 {
 
-// The power of two of a row of activations: kTop - exponent of the largest magnitude, at most kMost; kStep: minus the
-// exponent of the smallest subnormal.
+// kStep: minus the exponent of the type's smallest subnormal; 2^kUp, a number of the type, brings a code to 2^-kRest of its size.
 template <class T>
 struct W4Scale;
 template <>
 struct W4Scale<Bf16> {
-  static constexpr int kTop = 120, kMost = 126, kStep = 133, kMantissa = 7, kBias = 127;
+  static constexpr int kStep = 133, kUp = 126, kRest = kStep - kUp, kMantissa = 7, kBias = 127;
 };
 template <>
 struct W4Scale<Fp16> {
-  static constexpr int kTop = 14, kMost = 15, kStep = 24, kMantissa = 10, kBias = 15;
+  static constexpr int kStep = 24, kUp = 14, kRest = kStep - kUp, kMantissa = 10, kBias = 15;
 };
-// ... from the bits of the row's largest magnitude (infinity and NaN included).
-template <class T>
-__device__ __forceinline__ int w4_power(uint32_t max_bits) {
-  using S = W4Scale<T>;
-  return min(S::kTop - (static_cast<int>(max_bits >> S::kMantissa) - S::kBias), S::kMost);
-}
 __device__ __forceinline__ float power_of_two(int e) { return __int_as_float((127 + e) << 23); }
-// A sum of products back in its own size: by 2^(kStep - power) in two steps, which stay in fp32's range.
+// 2^e in both halves of a word.
 template <class T>
-__device__ __forceinline__ float w4_unscale(float sum, int power) {
-  const int e = W4Scale<T>::kStep - power, half = e / 2;
-  return sum * power_of_two(half) * power_of_two(e - half);
+__device__ __forceinline__ uint32_t power_of_two2(int e) {
+  return static_cast<uint32_t>((e + W4Scale<T>::kBias) << W4Scale<T>::kMantissa) * 0x10001u;
 }
 template <class T>
 __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
@@ -81,19 +69,23 @@ __device__ __forceinline__ uint32_t fma2_16(uint32_t a, uint32_t b, uint32_t c) 
   return d;
 }
 
-// The largest |element| of eight 16-bit elements, as bits (NaN orders above infinity).
-__device__ __forceinline__ uint32_t w4_max_abs(const uint4 v) {
-  const uint32_t m = __vmaxu2(__vmaxu2(v.x & 0x7FFF7FFFu, v.y & 0x7FFF7FFFu), __vmaxu2(v.z & 0x7FFF7FFFu, v.w & 0x7FFF7FFFu));
-  return max(m & 0xFFFFu, m >> 16);
+// -z 2^-kRest in both halves of a word: of zero point z, or of byte j of four of them (at most 15).
+template <class T>
+__device__ __forceinline__ uint32_t w4_zero(int z) {
+  return T::pack(static_cast<float>(-z) * power_of_two(-W4Scale<T>::kRest), static_cast<float>(-z) * power_of_two(-W4Scale<T>::kRest));
 }
-
-// A word of eight codes -> its pairs: low halves of the bytes (elements 0, 1 and 2, 3), high halves (4, 5 and 6, 7).
-__device__ __forceinline__ void w4_unpack(uint32_t w, uint32_t (&p)[4]) {
-  const uint32_t v = w >> 8;
-  p[0] = w & 0x000F000Fu;
-  p[1] = v & 0x000F000Fu;
-  p[2] = w & 0x00F000F0u;
-  p[3] = v & 0x00F000F0u;
+template <class T>
+__device__ __forceinline__ uint32_t w4_zero(uint32_t bytes, int j) {  // under a sign bit a byte is minus its number of subnormal steps
+  return mul2<T>(__byte_perm(bytes, 0x80u, 0x4040u + 0x0101u * j), power_of_two2<T>(W4Scale<T>::kUp));
+}
+// A word of eight codes -> the pairs (c - z) 2^-kRest: low halves of the bytes (elements 0, 1 and 2, 3), high halves (4, 5 and 6, 7).
+template <class T>
+__device__ __forceinline__ void w4_unpack(uint32_t w, uint32_t zero, uint32_t (&p)[4]) {
+  const uint32_t v = w >> 8, low = power_of_two2<T>(W4Scale<T>::kUp), high = power_of_two2<T>(W4Scale<T>::kUp - 4);
+  p[0] = fma2_16<T>(w & 0x000F000Fu, low, zero);
+  p[1] = fma2_16<T>(v & 0x000F000Fu, low, zero);
+  p[2] = fma2_16<T>(w & 0x00F000F0u, high, zero);
+  p[3] = fma2_16<T>(v & 0x00F000F0u, high, zero);
 }
 
 // A lane's activations of one K block: for each chunk of 32 K and tile of 8 tokens the eight elements 32 c + 8 t .. of
@@ -102,82 +94,56 @@ template <int kNT>
 struct W4Frag {
   uint4 v[4][kNT];
 };
-// The factors of a token's elements, 2^power and a sixteenth of it, in both halves of a word.
-struct W4Factor {
-  uint32_t low, high;
-};
-template <class T>
-__device__ __forceinline__ W4Factor w4_factor(int power) {
-  using S = W4Scale<T>;
-  const uint32_t low = static_cast<uint32_t>(power + S::kBias) << S::kMantissa;
-  return {low * 0x10001u, (low - (4u << S::kMantissa)) * 0x10001u};
-}
-template <class T>
-__device__ __forceinline__ uint4 w4_scaled(const uint4 v, const W4Factor f) {
-  return make_uint4(mul2<T>(v.x, f.low), mul2<T>(v.y, f.low), mul2<T>(v.z, f.high), mul2<T>(v.w, f.high));
-}
 
-// sums += block * x with the rows of x multiplied by their powers of two.  sums[i][n] is the C fragment of row tile i and
-// token tile n, two tokens of a row to a pair.
+// sums += block * x 2^-kRest.  sums[i][n] is the C fragment of row tile i and token tile n, two tokens of a row to a pair.
 template <class T, int kGpb, bool kZeros, int kNT>
-__device__ __forceinline__ void w4_block(const uint8_t *block, const W4Frag<kNT> &raw, const W4Factor (&factor)[kNT], uint64_t (&sums)[4][kNT][2]) {
+__device__ __forceinline__ void w4_block(const uint8_t *block, const W4Frag<kNT> &x, uint64_t (&sums)[4][kNT][2]) {
   const int lane = threadIdx.x & 31, g = lane >> 2;
   constexpr int kChunks = 4 / kGpb;  // of a group
-  const uint32_t low1[4] = {0x00010001u, 0x00010001u, 0x00010001u, 0x00010001u};
-  const uint32_t high1[4] = {0x00100010u, 0x00100010u, 0x00100010u, 0x00100010u};
 #pragma unroll
   for (int gi = 0; gi < kGpb; ++gi) {
-    float acc[4][kNT][4], sx[kNT][4];  // a group's first MMAs start them
 #pragma unroll
-    for (int cc = 0; cc < kChunks; ++cc) {
-      const int c = gi * kChunks + cc;
-      uint4 x[kNT];
+    for (int pair = 0; pair < 2; ++pair) {  // of row tiles: half as many sums and zero points to hold as with the chunks outside
+      float acc[2][kNT][4];  // a group's first MMAs start them
+      uint32_t zero[4];      // of rows 32 pair + 8 j + g
+      if constexpr (kZeros) {
+        const uint32_t zq = *reinterpret_cast<const uint32_t *>(block + kW4CodeBytes + kGpb * 128 + (gi * 8 + g) * 8 + 4 * pair);
 #pragma unroll
-      for (int n = 0; n < kNT; ++n) {
-        x[n] = w4_scaled<T>(raw.v[c][n], factor[n]);
-        mma16816<T>(sx[n], low1, x[n].x, x[n].y, cc != 0);
-        mma16816<T>(sx[n], high1, x[n].z, x[n].w);
+        for (int j = 0; j < 4; ++j) zero[j] = w4_zero<T>(zq, j);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) zero[j] = w4_zero<T>(8);
       }
 #pragma unroll
-      for (int pair = 0; pair < 2; ++pair) {
+      for (int cc = 0; cc < kChunks; ++cc) {
+        const int c = gi * kChunks + cc;
         const uint4 q = *reinterpret_cast<const uint4 *>(block + ((c * 2 + pair) * 32 + lane) * 16);
         const uint32_t w[4] = {q.x, q.y, q.z, q.w};
 #pragma unroll
-        for (int s = 0; s < 2; ++s) {
+        for (int i = 0; i < 2; ++i) {
           uint32_t lo[4], hi[4];
-          w4_unpack(w[2 * s], lo);
-          w4_unpack(w[2 * s + 1], hi);
+          w4_unpack<T>(w[2 * i], zero[2 * i], lo);
+          w4_unpack<T>(w[2 * i + 1], zero[2 * i + 1], hi);
           const uint32_t a0[4] = {lo[0], hi[0], lo[1], hi[1]}, a1[4] = {lo[2], hi[2], lo[3], hi[3]};
-          const int i = 2 * pair + s;
 #pragma unroll
           for (int n = 0; n < kNT; ++n) {
-            mma16816<T>(acc[i][n], a0, x[n].x, x[n].y, cc != 0);
-            mma16816<T>(acc[i][n], a1, x[n].z, x[n].w);
+            mma16816<T>(acc[i][n], a0, x.v[c][n].x, x.v[c][n].y, cc != 0);
+            mma16816<T>(acc[i][n], a1, x.v[c][n].z, x.v[c][n].w);
           }
         }
       }
-    }
-    const uint4 sq = *reinterpret_cast<const uint4 *>(block + kW4CodeBytes + (gi * 8 + g) * 16);
-    const uint32_t sw[4] = {sq.x, sq.y, sq.z, sq.w};
-    uint32_t zw[2] = {0u, 0u};
-    if constexpr (kZeros) {
-      const uint2 zq = *reinterpret_cast<const uint2 *>(block + kW4CodeBytes + kGpb * 128 + (gi * 8 + g) * 8);
-      zw[0] = zq.x, zw[1] = zq.y;
-    }
+      const uint2 sq = *reinterpret_cast<const uint2 *>(block + kW4CodeBytes + (gi * 8 + g) * 16 + 8 * pair);
+      const uint32_t sw[2] = {sq.x, sq.y};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float s0 = T::lo(sw[i]), s1 = T::hi(sw[i]);
-      float z0 = -8.f, z1 = -8.f;
-      if constexpr (kZeros) {  // a byte under the exponent of 2^23 is 2^23 + z
-        z0 = 8388608.f - __uint_as_float(__byte_perm(zw[i >> 1], 0x4B000000u, 0x7540u + 2 * (i & 1)));
-        z1 = 8388608.f - __uint_as_float(__byte_perm(zw[i >> 1], 0x4B000000u, 0x7541u + 2 * (i & 1)));
-      }
-      const uint64_t s00 = pack_f32x2(s0, s0), s11 = pack_f32x2(s1, s1), z00 = pack_f32x2(z0, z0), z11 = pack_f32x2(z1, z1);
+      for (int i = 0; i < 2; ++i) {
+        const float s0 = T::lo(sw[i]), s1 = T::hi(sw[i]);
+        const uint64_t s00 = pack_f32x2(s0, s0), s11 = pack_f32x2(s1, s1);
 #pragma unroll
-      for (int n = 0; n < kNT; ++n) {
-        const uint64_t sxx = pack_f32x2(sx[n][0], sx[n][1]);
-        sums[i][n][0] = fma_f32x2(s00, fma_f32x2(z00, sxx, pack_f32x2(acc[i][n][0], acc[i][n][1])), sums[i][n][0]);
-        sums[i][n][1] = fma_f32x2(s11, fma_f32x2(z11, sxx, pack_f32x2(acc[i][n][2], acc[i][n][3])), sums[i][n][1]);
+        for (int n = 0; n < kNT; ++n) {
+          uint64_t(&sum)[2] = sums[2 * pair + i][n];
+          sum[0] = fma_f32x2(s00, pack_f32x2(acc[i][n][0], acc[i][n][1]), sum[0]);
+          sum[1] = fma_f32x2(s11, pack_f32x2(acc[i][n][2], acc[i][n][3]), sum[1]);
+        }
       }
     }
   }

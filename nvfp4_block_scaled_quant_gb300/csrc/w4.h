@@ -66,16 +66,14 @@ struct W4MoeArgs {
   uint16_t *h;                                  // (rows, I), row t * topk + j, then the shared expert's T rows
   float *part;                                  // (rows, H)
   int *counters;                                // kW4MoeCounters words and the panels of y, zeroed by the router kernel
-  uint32_t *x_max;                              // (T), the bits of the largest magnitude of each row of x
   uint32_t *err;
 };
 constexpr int kW4MoeMaxT = 64, kW4MoeMaxEntries = 512, kW4MoeMaxK = 16;
 constexpr int kW4MoeMaxSlots = kW4MoeMaxEntries + kW4MoeMaxT / 8;
 constexpr int64_t kW4MoeMaxExperts = 1024, kW4MoeMaxDim = 16384;
-// The counters: the item counter on a cache line of its own, the finished panels of h of each slot, the bits of the largest
-// magnitude of each row of h, and behind them the finished slots of each panel of y.
-constexpr int kW4MoeRows = kW4MoeMaxEntries + kW4MoeMaxT;
-constexpr int kW4MoeSlotDone = 32, kW4MoeRowMax = kW4MoeSlotDone + kW4MoeMaxSlots, kW4MoeCounters = kW4MoeRowMax + kW4MoeRows;
+// The counters: the item counter on a cache line of its own, the finished panels of h of each slot, and behind them the
+// finished slots of each panel of y.
+constexpr int kW4MoeSlotDone = 32, kW4MoeCounters = kW4MoeSlotDone + kW4MoeMaxSlots;
 cudaError_t launch_w4_moe(const W4MoeArgs &a, int dtype, int group, bool zeros, int sms, cudaStream_t s);
 
 }  // namespace nvfp4

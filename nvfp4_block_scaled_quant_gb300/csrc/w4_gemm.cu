@@ -19,20 +19,14 @@ __global__ void __launch_bounds__(256) w4_expand_kernel(const uint8_t *w, int N,
   const uint4 v = __ldg(reinterpret_cast<const uint4 *>(src) + tid);
   const uint32_t word[4] = {v.x, v.y, v.z, v.w};
   const int gi = c * kGpb / 4;
-  // c 2^-kStep -> (c - z) 2^-e -> c - z: multiplying by the whole 2^kStep is out of the type's range
-  using S = W4Scale<T>;
-  constexpr int kUp = S::kMantissa == 7 ? 126 : 14, kRest = S::kStep - kUp;
-  auto power = [](int e) { return static_cast<uint32_t>((e + S::kBias) << S::kMantissa) * 0x10001u; };
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int row = panel * kW4PanelRows + 32 * pair + 8 * i + g;
-    float z = 8.f;
-    if constexpr (kZeros) z = static_cast<float>(__ldg(src + kW4CodeBytes + 128 * kGpb + (gi * 8 + g) * 8 + 4 * pair + i));
-    const uint32_t zz = T::pack(-z * power_of_two(-kRest), -z * power_of_two(-kRest));
-    uint32_t p[4];
-    w4_unpack(word[i], p);
+    uint32_t zero = w4_zero<T>(8), p[4];
+    if constexpr (kZeros) zero = w4_zero<T>(__ldg(src + kW4CodeBytes + 128 * kGpb + (gi * 8 + g) * 8 + 4 * pair + i), 0);
+    w4_unpack<T>(word[i], zero, p);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) p[j] = mul2<T>(fma2_16<T>(p[j], power(j < 2 ? kUp : kUp - 4), zz), power(kRest));
+    for (int j = 0; j < 4; ++j) p[j] = mul2<T>(p[j], power_of_two2<T>(W4Scale<T>::kRest));  // in two steps: 2^kStep is out of the type's range
     if (row < N && k < K) *reinterpret_cast<uint4 *>(out + static_cast<int64_t>(row) * K + k) = make_uint4(p[0], p[1], p[2], p[3]);
   }
   if (tid < 64 * kGpb) {

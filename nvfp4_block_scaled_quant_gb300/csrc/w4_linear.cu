@@ -60,14 +60,14 @@ constexpr int kWarps = 8;
 
 template <class T, int kGpb, bool kZeros, int kNT>
 __global__ void __launch_bounds__(kWarps * 32, 2) w4_stream_kernel(const W4Args a, int splits, int depth) {
-  constexpr int kBytes = w4_block_bytes(kGpb, kZeros), kTok = 8 * kNT;
+  constexpr int kBytes = w4_block_bytes(kGpb, kZeros);
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ uint64_t full[kWarps][4];
-  __shared__ int s_abort, s_power[kTok];
+  __shared__ int s_abort;
   volatile int *abort_flag = &s_abort;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int rank = static_cast<int>(blockIdx.x) % splits, panel = static_cast<int>(blockIdx.x) / splits;
-  const int tokens = a.M;  // at most kTok
+  const int tokens = a.M;  // at most 8 kNT
   const int blocks = (a.K + kW4BlockK - 1) / kW4BlockK;
   const int first = blocks * rank / splits, kb0 = first + warp, kb1 = blocks * (rank + 1) / splits;
   uint8_t *ring = smem + warp * depth * kBytes;
@@ -85,23 +85,6 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_stream_kernel(const W4Args 
   __syncthreads();
   pdl_wait();
   pdl_trigger();
-
-  // the powers of two of the rows' parts that this CTA multiplies
-  for (int j = warp; j < kTok; j += kWarps) {
-    uint32_t m = 0;
-    if (j < tokens) {
-      const uint16_t *row = static_cast<const uint16_t *>(a.x) + j * a.ldx;
-      const int end = min(kb1 * kW4BlockK, a.K);
-#pragma unroll 4
-      for (int k = first * kW4BlockK + 8 * lane; k < end; k += 256) m = max(m, w4_max_abs(__ldg(reinterpret_cast<const uint4 *>(row + k))));
-    }
-    m = __reduce_max_sync(0xffffffffu, m);
-    if (lane == 0) s_power[j] = w4_power<T>(m);
-  }
-  __syncthreads();
-  W4Factor factor[kNT];
-#pragma unroll
-  for (int n = 0; n < kNT; ++n) factor[n] = w4_factor<T>(s_power[8 * n + g]);
 
   uint64_t sums[4][kNT][2] = {};
   const uint16_t *x = static_cast<const uint16_t *>(a.x) + g * a.ldx + 8 * t;
@@ -125,7 +108,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_stream_kernel(const W4Args 
     ok = mbar_wait_bounded(&full[warp][stage], phase, abort_flag, a.err, kPipelineTimeoutNs);
     ok = __all_sync(0xffffffffu, ok);
     if (!ok) break;
-    w4_block<T, kGpb, kZeros, kNT>(ring + stage * kBytes, f, factor, sums);
+    w4_block<T, kGpb, kZeros, kNT>(ring + stage * kBytes, f, sums);
     __syncwarp();
     if (lane == 0 && kb + depth * kWarps < kb1) {
       mbar_arrive_expect_tx(&full[warp][stage], kBytes);
@@ -151,7 +134,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_stream_kernel(const W4Args 
     float v = part[at];
 #pragma unroll
     for (int u = 1; u < kWarps; ++u) v += part[u * pitch + at];
-    part[at] = w4_unscale<T>(v, s_power[e >> 6]);
+    part[at] = v * power_of_two(W4Scale<T>::kRest);
   }
   block_meet();
   if (splits > 1) cluster_meet();

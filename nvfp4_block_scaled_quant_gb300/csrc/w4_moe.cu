@@ -35,9 +35,6 @@ constexpr int kLogitMaxSplit = 8;
 template <class T, int kNT>
 __global__ void __launch_bounds__(kLogitWarps * 32) w4_moe_logits_kernel(const W4MoeArgs a, int splits, int n_counters) {
   __shared__ float part[kLogitWarps][16 * 8 * kNT];
-  __shared__ uint32_t s_max[8 * kNT];
-  if (threadIdx.x < 8 * kNT) s_max[threadIdx.x] = 0u;
-  __syncthreads();
   pdl_wait();
   pdl_trigger();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -48,7 +45,6 @@ __global__ void __launch_bounds__(kLogitWarps * 32) w4_moe_logits_kernel(const W
   const uint16_t *x = static_cast<const uint16_t *>(a.x) + g * a.ldx + 8 * t;
   const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
   float acc[kNT][4] = {};
-  uint32_t top[kNT] = {};  // of the tokens' elements, needed once: the first 16 experts' cluster keeps it
 #pragma unroll(kNT == 1 ? 4 : 2)
   for (int c = c0 + warp; c < c1; c += kLogitWarps) {
     const int k = 32 * c;
@@ -59,7 +55,6 @@ __global__ void __launch_bounds__(kLogitWarps * 32) w4_moe_logits_kernel(const W
 #pragma unroll
     for (int n = 0; n < kNT; ++n) {
       const uint4 b = in && 8 * n + g < a.T ? __ldg(reinterpret_cast<const uint4 *>(x + 8 * n * a.ldx + k)) : zero;
-      if (tile == 0) top[n] = max(top[n], w4_max_abs(b));
       mma16816<T>(acc[n], a0, b.x, b.y);
       mma16816<T>(acc[n], a1, b.z, b.w);
     }
@@ -68,10 +63,6 @@ __global__ void __launch_bounds__(kLogitWarps * 32) w4_moe_logits_kernel(const W
   for (int n = 0; n < kNT; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) part[warp][(8 * n + 2 * t + (e & 1)) * 16 + 8 * (e >> 1) + g] = acc[n][e];
-  if (tile == 0) {
-#pragma unroll
-    for (int n = 0; n < kNT; ++n) atomicMax(&s_max[8 * n + g], top[n]);
-  }
   __syncthreads();
   const int live = 16 * min(a.T, 8 * kNT);
   for (int e = threadIdx.x; e < live; e += kLogitWarps * 32) {
@@ -101,16 +92,6 @@ __global__ void __launch_bounds__(kLogitWarps * 32) w4_moe_logits_kernel(const W
     const int expert = tile * 16 + (e & 15);
     if (expert < a.E) a.logits[static_cast<int64_t>(e >> 4) * a.E + expert] = s;
   }
-  if (tile == 0 && rank == 0 && threadIdx.x < a.T) {
-    uint32_t m = 0;
-    for (int r = 0; r < splits; ++r) {
-      uint32_t addr, v;
-      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(smem_u32(s_max) + threadIdx.x * 4), "r"(r));
-      asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
-      m = max(m, v);
-    }
-    a.x_max[threadIdx.x] = m;
-  }
   if (splits > 1) cluster_meet();
 }
 
@@ -127,7 +108,6 @@ struct Plan {
   uint16_t slot_expert[kW4MoeMaxSlots];
   uint16_t slot_first[kW4MoeMaxSlots]; // place of its first entry in `sorted` (shared expert: its first token)
   uint16_t slot_count[kW4MoeMaxSlots];
-  int power[kW4MoeMaxT];               // of two, that the tokens' activations are multiplied by
   int slots, shared_slots;
 };
 // While the plan is made, in the room of the rings: each expert's tokens as a bit mask, the place of its first entry and its first
@@ -225,12 +205,10 @@ __device__ __forceinline__ int item_split(int slots, int panels, int ctas) {
 }
 
 // The table of slots, the same in every CTA: experts in their order, tokens in theirs.
-template <class T>
 __device__ void make_plan(const W4MoeArgs &a, Plan &plan, PlanScratch &s) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, entries = a.T * a.topk;
   if (entries > 32)
     for (int e = tid; e < a.E; e += kThreads) s.tokens[0][spread(e)] = s.tokens[1][spread(e)] = 0u;
-  if (tid < a.T) plan.power[tid] = w4_power<T>(__ldcg(a.x_max + tid));
   // (with four places to a lane, where it has one expert, each choice ends in a search: 53 tokens, 28 experts, top 8 40 us instead of 34)
   if (a.E <= 32)
     choose<1>(a, s.ids, plan.weight);
@@ -370,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
   // the first item, on its way while the plan is made
   int first_item = 0;
   if (tid == (kWarps + 1) * 32) first_item = atomicAdd(a.counters, 1);
-  make_plan<T>(a, plan, *reinterpret_cast<PlanScratch *>(smem));
+  make_plan(a, plan, *reinterpret_cast<PlanScratch *>(smem));
 
   const int slots = plan.slots, shared_slots = plan.shared_slots, entries = a.T * a.topk;
   const int panels13 = (a.I + 31) / 32, panels2 = (a.H + kW4PanelRows - 1) / kW4PanelRows;
@@ -382,7 +360,6 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
   // 50.0 us, 13 tokens, 24 experts of 1544 x 1000 38 / 36, 16 tokens, 384 of 7168 x 2048 399 / 409.
   const int depth = split2 == 0 ? 2 : most;
   int *counter = a.counters, *slot_done = counter + kW4MoeSlotDone, *panel_done = counter + kW4MoeCounters;
-  uint32_t *row_max = reinterpret_cast<uint32_t *>(counter + kW4MoeRowMax);
   // the workspace row of a slot's token j
   auto row_of = [&](int slot, int j) {
     const int at = plan.slot_first[slot] + j;
@@ -471,14 +448,12 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
     // of the sums are left where they are.
     const uint16_t *x = nullptr;
     int width = 0;
-    W4Factor factor[1];
     auto open = [&](const Item &it) {
       width = it.up ? a.H : a.I;
       const int row = row_of(it.slot, g < plan.slot_count[it.slot] ? g : 0);
       const int token = row < entries ? static_cast<int>((row * topk_inverse) >> 16) : row - entries;
       x = it.up ? static_cast<const uint16_t *>(a.x) + token * a.ldx : a.h + static_cast<int64_t>(row) * a.I;
       x += 8 * t;
-      factor[0] = w4_factor<T>(it.up ? plan.power[token] : w4_power<T>(__ldcg(row_max + row)));
     };
     auto load_x = [&](int b, W4Frag<1> &f) {
       const uint16_t *p = x + b * kW4BlockK;
@@ -519,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
         ok = mbar_wait_bounded(&full[warp][stage], phase, abort_flag, a.err, kPipelineTimeoutNs);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        w4_block<T, kGpb, kZeros, 1>(ring + stage * kBytes, f, factor, sums);
+        w4_block<T, kGpb, kZeros, 1>(ring + stage * kBytes, f, sums);
         __syncwarp();
         if (b + warps >= it.blocks) break;  // the item's sums go where its last block was
         if (lane == 0) mbar_arrive(&empty[warp][stage]);
@@ -550,7 +525,8 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
     }
   } else {
     // ---------------------------------------------------------------- finishing warp: an item's sums over the warps
-    int buf = 0, finished = 0, rows_slot = -1, rows_up = 0, row = 0, power = 0;
+    const float kUnscale = power_of_two(W4Scale<T>::kRest);
+    int buf = 0, finished = 0, rows_slot = -1, row = 0;
     uint32_t bphase = 0;
     for (;;) {
       const Item it = next_item();
@@ -560,10 +536,9 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
       if (!ok) break;
       const int count = plan.slot_count[it.slot], shift = it.up ? split13 : split2, warps = kWarps >> shift;
       const int parts = min(it.blocks, warps), panels = min(1 << shift, (it.up ? panels13 : panels2) - it.panel);
-      if (it.slot != rows_slot || it.up != rows_up) {  // lane j: the workspace row of token j, and the power of its activations
-        rows_slot = it.slot, rows_up = it.up;
+      if (it.slot != rows_slot) {  // lane j: the workspace row of token j
+        rows_slot = it.slot;
         row = row_of(it.slot, min(lane & 7, count - 1));
-        power = it.up ? plan.power[row < entries ? row / a.topk : row - entries] : w4_power<T>(__ldcg(row_max + row));
       }
       const float *r[kWarps];
 #pragma unroll
@@ -584,30 +559,23 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
           // four tokens at a time, four outputs to a lane
           const int c = 4 * (lane & 7), n = (it.panel + sub) * 32 + c;
           for (int j0 = 0; j0 < count; j0 += 4) {
-            const int j = j0 + (lane >> 3), to = __shfl_sync(0xffffffffu, row, j & 7), e = __shfl_sync(0xffffffffu, power, j & 7);
-            const bool live = j < count && n < a.I;
-            uint32_t top = 0;
-            if (live) {
+            const int j = j0 + (lane >> 3), to = __shfl_sync(0xffffffffu, row, j & 7);
+            if (j < count && n < a.I) {
               const float4 gate = sum4(in, j * kW4Pitch + c), lift = sum4(in, j * kW4Pitch + 32 + c);
-              auto out = [&](float gv, float lv) { return activate(a.act, w4_unscale<T>(gv, e)) * w4_unscale<T>(lv, e); };
+              auto out = [&](float gv, float lv) { return activate(a.act, gv * kUnscale) * (lv * kUnscale); };
               const uint32_t lo = T::pack(out(gate.x, lift.x), out(gate.y, lift.y)), hi = T::pack(out(gate.z, lift.z), out(gate.w, lift.w));
               *reinterpret_cast<uint2 *>(a.h + static_cast<int64_t>(to) * a.I + n) = make_uint2(lo, hi);
-              const uint32_t m = __vmaxu2(lo & 0x7FFF7FFFu, hi & 0x7FFF7FFFu);
-              top = max(m & 0xFFFFu, m >> 16);
             }
-#pragma unroll
-            for (int o = 4; o; o >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            if (live && c == 0) atomicMax(row_max + to, top);
           }
         } else {
           // two tokens at a time, four outputs to a lane
           const int c = 4 * (lane & 15), n = (it.panel + sub) * kW4PanelRows + c;
           for (int j0 = 0; j0 < count; j0 += 2) {
-            const int j = j0 + (lane >> 4), to = __shfl_sync(0xffffffffu, row, j & 7), e = __shfl_sync(0xffffffffu, power, j & 7);
+            const int j = j0 + (lane >> 4), to = __shfl_sync(0xffffffffu, row, j & 7);
             if (j < count && n < a.H) {
               const float4 v = sum4(in, j * kW4Pitch + c);
               *reinterpret_cast<float4 *>(a.part + static_cast<int64_t>(to) * a.H + n) =
-                  make_float4(w4_unscale<T>(v.x, e), w4_unscale<T>(v.y, e), w4_unscale<T>(v.z, e), w4_unscale<T>(v.w, e));
+                  make_float4(v.x * kUnscale, v.y * kUnscale, v.z * kUnscale, v.w * kUnscale);
             }
           }
         }

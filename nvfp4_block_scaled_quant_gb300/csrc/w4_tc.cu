@@ -51,9 +51,7 @@ struct TcCfg {
 template <class T, int kGpb, bool kZeros, int kTok>
 __global__ void __launch_bounds__(512, 1) w4_tc_kernel(const __grid_constant__ CUtensorMap tmX, const W4Args args, const int splits) {
   using C = TcCfg<kGpb, kZeros, kTok>;
-  using S = W4Scale<T>;
   constexpr uint32_t kIdesc = mma_idesc(T::kCode == NVFP4_DT_BF16 ? 1u : 0u, false, false, 128, kTok);
-  constexpr int kUp = S::kMantissa == 7 ? 126 : 14, kRest = S::kStep - kUp;  // the operand is (c - z) 2^-kRest
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t *sA = smem, *sX = sA + C::kStages * C::kABytes, *sC = smem + C::kRing;
@@ -191,7 +189,6 @@ __global__ void __launch_bounds__(512, 1) w4_tc_kernel(const __grid_constant__ C
     constexpr int kShare = C::kDeq / C::kStages, kUnits = 8 / kShare;
     const int w = warp - 4 - C::kEpi, stage = w % C::kStages, unit0 = w / C::kStages * kUnits;
     const int t = lane & 3, cb = (lane >> 2) & 1, steps = 2 * (kb1 - kb0);
-    auto power = [](int e) { return static_cast<uint32_t>((e + S::kBias) << S::kMantissa) * 0x10001u; };
     for (int s = stage; s < steps; s += C::kStages) {
       const int cs = (s >> 1) % C::kCodes;
       ok = wait(&full_c[cs], (s >> 1) / C::kCodes & 1);
@@ -212,19 +209,14 @@ __global__ void __launch_bounds__(512, 1) w4_tc_kernel(const __grid_constant__ C
         // a panel that does not exist gives rows of the product that are not written
         const int unit = unit0 + q, panel = unit >> 2, pair = (unit >> 1) & 1, g = (lane >> 3) + 4 * (unit & 1);
         const uint32_t word[4] = {v[q].x, v[q].y, v[q].z, v[q].w};
-        uint32_t zeros = 0x08080808u;
+        uint32_t zeros = 0u;
         if constexpr (kZeros)
           zeros = *reinterpret_cast<const uint32_t *>(sC + (cs * 2 + panel) * C::kBlock + kW4CodeBytes + 128 * kGpb + (gi * 8 + g) * 8 + 4 * pair);
         uint8_t *dst = sA + stage * C::kABytes + (64 * panel + 32 * pair + g) * 128 + (((4 * cb + t) ^ g) << 4);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          float z = -8.f * power_of_two(-kRest);
-          if constexpr (kZeros) z = -static_cast<float>((zeros >> (8 * i)) & 0xFFu) * power_of_two(-kRest);
-          const uint32_t zz = T::pack(z, z);
           uint32_t p[4];
-          w4_unpack(word[i], p);
-#pragma unroll
-          for (int j = 0; j < 4; ++j) p[j] = fma2_16<T>(p[j], power(j < 2 ? kUp : kUp - 4), zz);
+          w4_unpack<T>(word[i], kZeros ? w4_zero<T>(zeros, i) : w4_zero<T>(8), p);
           *reinterpret_cast<uint4 *>(dst + i * 1024) = make_uint4(p[0], p[1], p[2], p[3]);
         }
       }
@@ -315,7 +307,7 @@ __global__ void __launch_bounds__(512, 1) w4_tc_kernel(const __grid_constant__ C
 #pragma unroll
       for (int r = 1; r < 8; ++r)
         if (r < splits) s += v[r];
-      if (f < args.N) static_cast<uint16_t *>(args.y)[static_cast<int64_t>(m0 + (e >> 7)) * args.N + f] = T::one(s * power_of_two(kRest));
+      if (f < args.N) static_cast<uint16_t *>(args.y)[static_cast<int64_t>(m0 + (e >> 7)) * args.N + f] = T::one(s * power_of_two(W4Scale<T>::kRest));
     }
   }
   if (splits > 1) cluster_meet();  // no CTA leaves while another reads its sums

@@ -45,3 +45,53 @@ def test_small_bf16_scales_of_experts(T, up, down):
     want, err, _, sure = moe(x.to(F64), router, cks[0], cks[1], topk, 64, "silu", BF, (cks[2], cks[3]))
     assert sure
     check(y, want, err, BF)
+
+
+def without_column(ck, group, col):
+    """The checkpoint with weights of zero (c = z) in one column."""
+    codes, scales, zeros = (None if v is None else v.clone() for v in ck)
+    z = torch.full_like(codes[..., col // 2], 8) if zeros is None else zeros[..., col // group]
+    codes[..., col // 2] = codes[..., col // 2] & (0x0F if col % 2 else 0xF0) | z << (4 if col % 2 else 0)
+    return codes, scales, zeros
+
+
+OUTLIERS = [("bf16", 1e4, 1.0), ("bf16", 1e9, 1.0), ("bf16", 1e36, 1.0), ("fp16", 6e4, 1.0), ("fp16", 6e4, 2.0 ** -14), ("fp16", 6e4, 2.0 ** -20)]
+
+
+@pytest.mark.parametrize("kind,outlier,size", OUTLIERS)
+@pytest.mark.parametrize("group,zeros", [(32, False), (64, True), (128, False), (128, True)])
+@pytest.mark.parametrize("M", [1, 7, 16, 40, 1100])
+def test_outlier_that_meets_zero_weights(M, group, zeros, kind, outlier, size):
+    """An activation that only meets weights of zero adds nothing: the bound is that of the row without it."""
+    g = torch.Generator(device=DEV).manual_seed(M + group)
+    dt, K, N, col = {"bf16": BF, "fp16": torch.float16}[kind], 392, 200, 131 if zeros else 134
+    ck = without_column(checkpoint(g, (N, K), group, zeros, dt, DEV), group, col)
+    # scales that bring the outputs of small rows into fp16's normal range
+    ck = (ck[0], (ck[1].float() / max(size, 2.0 ** -14)).to(dt), ck[2])
+    x = (torch.randn(M, K, generator=g, device=DEV) * size).to(dt)
+    x[:, col] = 0
+    want, err = product(x.to(F64), ck, group)
+    x[:, col] = outlier
+    check(ops.w4_linear(x, ops.w4_prepare(*ck, group=group)), want, err, dt)
+
+
+@pytest.mark.parametrize("kind,outlier,size", OUTLIERS)
+@pytest.mark.parametrize("group,zeros", [(32, True), (128, False)])
+@pytest.mark.parametrize("T", [1, 13])
+def test_outlier_that_meets_zero_weights_of_experts(T, group, zeros, kind, outlier, size):
+    """The same in the experts' up projections, the router blind to the column too."""
+    g = torch.Generator(device=DEV).manual_seed(T + group)
+    dt, H, I, E, topk, col = {"bf16": BF, "fp16": torch.float16}[kind], 392, 136, 12, 3, 134
+    cks = [checkpoint(g, s, group, zeros, dt, DEV) for s in ((E, 2 * I, H), (E, H, I), (2 * I, H), (H, I))]
+    for i in (0, 2):
+        codes, scales, z = without_column(cks[i], group, col)
+        cks[i] = (codes, (scales.float() / max(size, 2.0 ** -14)).to(dt), z)
+    x = (torch.randn(T, H, generator=g, device=DEV) * size).to(dt)
+    router = (torch.randn(E, H, generator=g, device=DEV) * H ** -0.5).to(dt)
+    router[:, col] = 0
+    x[:, col] = 0
+    want, err, _, sure = moe(x.to(F64), router, cks[0], cks[1], topk, group, "silu", dt, (cks[2], cks[3]))
+    assert sure
+    x[:, col] = outlier
+    w13, w2, s13, s2 = (ops.w4_prepare(*c, group=group, gated=i % 2 == 0) for i, c in enumerate(cks))
+    check(ops.w4_moe(x, router, w13, w2, topk, shared13=s13, shared2=s2), want, err, dt)
