@@ -527,7 +527,8 @@ NVFP4_API nvfp4_status nvfp4_w4_linear(const void *x, int dtype, int64_t M, int6
  *   l = x[t] router^T (fp32), ids = the topk largest of l (the lowest expert first among equals),
  *   p = softmax of l over the chosen ones (the softmax over all experts, renormalised),
  *   y[t] = sum_j p_j E_{ids_j}(x[t]) + E_shared(x[t]),  E(x) = W2 h,  h = act(Wg x) * (Wu x) rounded to `dtype`
- * with fp32 sums; h is the operand of a 16-bit product, as in a layer that stores it.  x (T, H) with row stride ldx;
+ * with fp32 sums; h is the operand of a 16-bit product, as in a layer that stores it.  In fp16 a row of h that passes 65504 is
+ * held times a power of two: it does not overflow (elements under 2^-28 of its largest lose bits).  x (T, H) with row stride ldx;
  * router (E, H) in `dtype`, contiguous; w13 (E, 2 I, H) prepared with `gated`, w2 (E, H, I) without; sh_w13 and sh_w2 the same for one
  * expert, both NULL without a shared expert; y (T, H) contiguous; act NVFP4_ACT_*.  Sums have a fixed order: repeated calls give
  * identical bits.  T <= 64, topk <= 16, topk <= E <= 1024, T topk <= 512; H and I multiples of 8, at most

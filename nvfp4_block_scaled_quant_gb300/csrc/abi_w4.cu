@@ -111,7 +111,8 @@ LinearWs linear_ws(int64_t M, int64_t N, int64_t K, int group) {
 }
 
 struct MoeWs {
-  size_t logits, h, part, counters, total;
+  size_t logits, h, part, powers, counters, total;
+  int64_t ld_powers;
 };
 bool moe_sizes_ok(int64_t T, int64_t H, int64_t I, int64_t E, int topk) {
   return T >= 0 && T <= kW4MoeMaxT && H > 0 && I > 0 && H % 8 == 0 && I % 8 == 0 && H <= kW4MoeMaxDim && I <= kW4MoeMaxDim && E > 0 &&
@@ -123,7 +124,14 @@ MoeWs moe_ws(int64_t T, int64_t H, int64_t I, int64_t E, int topk, bool shared) 
   w.logits = 0;
   w.h = align256(static_cast<size_t>(T * E) * 4);
   w.part = align256(w.h + rows * static_cast<size_t>(I) * 2);
-  w.counters = align256(w.part + rows * static_cast<size_t>(H) * 4);
+  // A slot's powers are done with when the first of its sums goes to `part`: they share its rows where a row holds a byte for each
+  // panel of h.
+  const int64_t panels = (I + 31) / 32;
+  const size_t end = w.part + rows * static_cast<size_t>(H) * 4;
+  const bool share = panels <= 4 * H;
+  w.powers = share ? w.part : end;
+  w.ld_powers = share ? 4 * H : panels;
+  w.counters = align256(share ? end : end + rows * static_cast<size_t>(panels));
   w.total = align256(w.counters + (kW4MoeCounters + static_cast<size_t>((H + kW4PanelRows - 1) / kW4PanelRows)) * 4);
   return w;
 }
@@ -295,6 +303,8 @@ nvfp4_status nvfp4_w4_moe(const void *x, int dtype, int64_t T, int64_t H, int64_
   a.logits = reinterpret_cast<float *>(p + L.logits);
   a.h = reinterpret_cast<uint16_t *>(p + L.h);
   a.part = reinterpret_cast<float *>(p + L.part);
+  a.powers = p + L.powers;
+  a.ld_powers = L.ld_powers;
   a.counters = reinterpret_cast<int *>(p + L.counters);
   a.err = d->flags;
   NV_CUDA(launch_w4_moe(a, dtype, group, zeros, d->sms, static_cast<cudaStream_t>(stream)), "4-bit mixture-of-experts launch");

@@ -65,15 +65,18 @@ struct W4MoeArgs {
   float *logits;                                // (T, E)
   uint16_t *h;                                  // (rows, I), row t * topk + j, then the shared expert's T rows
   float *part;                                  // (rows, H)
+  uint8_t *powers;                              // (rows, panels of h) with row stride ld_powers, fp16: what each panel of h is stored times, as -log2
+  int64_t ld_powers;
   int *counters;                                // kW4MoeCounters words and the panels of y, zeroed by the router kernel
   uint32_t *err;
 };
 constexpr int kW4MoeMaxT = 64, kW4MoeMaxEntries = 512, kW4MoeMaxK = 16;
 constexpr int kW4MoeMaxSlots = kW4MoeMaxEntries + kW4MoeMaxT / 8;
 constexpr int64_t kW4MoeMaxExperts = 1024, kW4MoeMaxDim = 16384;
-// The counters: the item counter on a cache line of its own, the finished panels of h of each slot, and behind them the
-// finished slots of each panel of y.
-constexpr int kW4MoeSlotDone = 32, kW4MoeCounters = kW4MoeSlotDone + kW4MoeMaxSlots;
+// The counters: the item counter on a cache line of its own, the finished panels of h of each slot, the largest power of each row of
+// h, and behind them the finished slots of each panel of y.
+constexpr int kW4MoeRows = kW4MoeMaxEntries + kW4MoeMaxT;
+constexpr int kW4MoeSlotDone = 32, kW4MoeRowPower = kW4MoeSlotDone + kW4MoeMaxSlots, kW4MoeCounters = kW4MoeRowPower + kW4MoeRows;
 cudaError_t launch_w4_moe(const W4MoeArgs &a, int dtype, int group, bool zeros, int sms, cudaStream_t s);
 
 }  // namespace nvfp4

@@ -11,6 +11,11 @@
 //    A slot's down rows go to the workspace in fp32; the CTA that finishes the last slot of a panel adds a token's experts
 //    up in the order of its top k, so repeated calls give identical bits.
 //
+// h is held in 16 bits, the operand of the down product: one rounding of half a step, as in a layer that stores it; in 32 bits the
+// product would take two operands.  In fp16 an h past 65504 would be an infinity where the layer's output need not be: a
+// panel of such a row is stored times a power of two that brings its largest to 2^14, and the first warp that finds such a slot
+// complete brings the other panels of the row to the same power.  Rows within the range are stored as they are.
+//
 // With few tokens the layer is bound by the bytes of the chosen experts' weights: 16 tokens, 384 experts of 7168 x 2048 396 us, 94% of
 // the copy bandwidth; one token 50 us, of which 8 pass before weights stream.  Eight warps of a CTA share an item's
 // panels and take a panel's K blocks in turn, each through a ring of its own: a block is one bulk copy.  A warp leaves its sums where its
@@ -306,6 +311,54 @@ __device__ __forceinline__ float activate(int act, float g) {
   return act_fwd<NVFP4_ACT_GELU_TANH>(g);
 }
 
+// The workspace row of a slot's token j.
+__device__ __forceinline__ int slot_row(const Plan &plan, int entries, int slot, int j) {
+  const int at = plan.slot_first[slot] + j;
+  return slot < plan.shared_slots ? entries + at : static_cast<int>(plan.sorted[at]);
+}
+
+// fp16: a slot's count has its finished items in the low bits and counts those with panels past the type's range from kSlotWide on.
+// A warp that finds the count complete and such panels in it comes here: the first brings every panel of such a row to the row's
+// largest power, the others wait.
+constexpr int kSlotWide = 1 << 10, kSlotClaimed = 1 << 28, kSlotSettled = 1 << 29;
+static_assert(kW4MoeMaxDim / 32 < kSlotWide && kW4MoeMaxDim / 32 * kSlotWide < kSlotClaimed, "items of a slot");
+__device__ __noinline__ bool settle(uint16_t *h, int I, const uint8_t *powers, int64_t ld_powers, const int *row_power, const Plan &plan, int entries,
+                                    int slot, int *done, volatile int *abort_flag, uint32_t *err) {
+  const int lane = threadIdx.x & 31;
+  __syncwarp();
+  int before = 0;
+  if (lane == 0) before = atomicOr(done, kSlotClaimed);
+  before = __shfl_sync(0xffffffffu, before, 0);
+  if (before & kSlotClaimed) {
+    bool ok = true;
+    const uint64_t t0 = global_timer_ns();
+    while (!(load_acquire(done) & kSlotSettled)) {
+      if (*abort_flag || global_timer_ns() - t0 > kPipelineTimeoutNs) {
+        if (!*abort_flag) raise_device_error(err, NVFP4_DEVERR_PIPELINE_TIMEOUT);
+        *abort_flag = 1;
+        ok = false;
+        break;
+      }
+    }
+    return __all_sync(0xffffffffu, ok) != 0;
+  }
+  __threadfence();  // behind the panels, whose counts were seen
+  for (int j = 0; j < plan.slot_count[slot]; ++j) {
+    const int row = slot_row(plan, entries, slot, j), most = __ldcg(row_power + row);
+    if (most == 0) continue;
+    uint32_t *pairs = reinterpret_cast<uint32_t *>(h + static_cast<int64_t>(row) * I);
+    for (int i = lane; i < I / 2; i += 32) {
+      const float f = power_of_two(__ldcg(powers + row * ld_powers + i / 16) - most);
+      const uint32_t v = __ldcg(pairs + i);
+      pairs[i] = Fp16::pack(Fp16::lo(v) * f, Fp16::hi(v) * f);
+    }
+  }
+  __threadfence();
+  __syncwarp();
+  if (lane == 0) atomicOr(done, kSlotSettled);
+  return true;
+}
+
 // An item of the list.
 struct Item {
   int slot;  // -1: no more items
@@ -359,12 +412,9 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
   // is behind while others run out: two stages where items are few and small, else three.  Three / two: one token 51.2 /
   // 50.0 us, 13 tokens, 24 experts of 1544 x 1000 38 / 36, 16 tokens, 384 of 7168 x 2048 399 / 409.
   const int depth = split2 == 0 ? 2 : most;
-  int *counter = a.counters, *slot_done = counter + kW4MoeSlotDone, *panel_done = counter + kW4MoeCounters;
-  // the workspace row of a slot's token j
-  auto row_of = [&](int slot, int j) {
-    const int at = plan.slot_first[slot] + j;
-    return slot < shared_slots ? entries + at : static_cast<int>(plan.sorted[at]);
-  };
+  int *counter = a.counters, *slot_done = counter + kW4MoeSlotDone, *row_power = counter + kW4MoeRowPower, *panel_done = counter + kW4MoeCounters;
+  constexpr bool kPowers = T::kCode == NVFP4_DT_FP16;  // h may pass the type's range
+  auto row_of = [&](int slot, int j) { return slot_row(plan, entries, slot, j); };
 
   if (warp == kWarps + 1) {
     // ---------------------------------------------------------------- producer: lane w fills the ring of warp w
@@ -471,7 +521,8 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
       const Item it = item;
       if (!it.up && ready != it.slot) {  // its h is complete
         const uint64_t t0 = global_timer_ns();
-        while (load_acquire(slot_done + it.slot) < items13) {
+        int seen;
+        while (((seen = load_acquire(slot_done + it.slot)) & (kSlotWide - 1)) < items13) {
           if (*abort_flag || global_timer_ns() - t0 > kPipelineTimeoutNs) {
             if (!*abort_flag) raise_device_error(a.err, NVFP4_DEVERR_PIPELINE_TIMEOUT);
             *abort_flag = 1;
@@ -480,6 +531,8 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
           }
         }
         ok = __all_sync(0xffffffffu, ok);
+        if (kPowers && ok && __any_sync(0xffffffffu, seen >= kSlotWide))
+          ok = settle(a.h, a.I, a.powers, a.ld_powers, row_power, plan, entries, it.slot, slot_done + it.slot, abort_flag, a.err);
         if (!ok) break;
         ready = it.slot;
       }
@@ -526,7 +579,8 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
   } else {
     // ---------------------------------------------------------------- finishing warp: an item's sums over the warps
     const float kUnscale = power_of_two(W4Scale<T>::kRest);
-    int buf = 0, finished = 0, rows_slot = -1, row = 0;
+    int buf = 0, finished = 0, rows_slot = -1, rows_up = 0, row = 0;
+    float unscale = 0.f;
     uint32_t bphase = 0;
     for (;;) {
       const Item it = next_item();
@@ -536,9 +590,10 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
       if (!ok) break;
       const int count = plan.slot_count[it.slot], shift = it.up ? split13 : split2, warps = kWarps >> shift;
       const int parts = min(it.blocks, warps), panels = min(1 << shift, (it.up ? panels13 : panels2) - it.panel);
-      if (it.slot != rows_slot) {  // lane j: the workspace row of token j
-        rows_slot = it.slot;
+      if (it.slot != rows_slot || it.up != rows_up) {  // lane j: the workspace row of token j, and the factor of its sums of the down product
+        rows_slot = it.slot, rows_up = it.up;
         row = row_of(it.slot, min(lane & 7, count - 1));
+        if (kPowers && !it.up) unscale = power_of_two(W4Scale<T>::kRest + __ldcg(row_power + row));
       }
       const float *r[kWarps];
 #pragma unroll
@@ -553,6 +608,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
           }
         return v;
       };
+      bool wide = false;  // a row's panel passed the type's range
       for (int sub = 0; sub < panels; ++sub) {
         const uint32_t in = ((1u << parts) - 1u) << (sub * warps);  // the warps that hold its sums
         if (it.up) {
@@ -560,22 +616,41 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
           const int c = 4 * (lane & 7), n = (it.panel + sub) * 32 + c;
           for (int j0 = 0; j0 < count; j0 += 4) {
             const int j = j0 + (lane >> 3), to = __shfl_sync(0xffffffffu, row, j & 7);
-            if (j < count && n < a.I) {
+            const bool live = j < count && n < a.I;
+            float v[4] = {}, largest = 0.f;
+            if (live) {
               const float4 gate = sum4(in, j * kW4Pitch + c), lift = sum4(in, j * kW4Pitch + 32 + c);
               auto out = [&](float gv, float lv) { return activate(a.act, gv * kUnscale) * (lv * kUnscale); };
-              const uint32_t lo = T::pack(out(gate.x, lift.x), out(gate.y, lift.y)), hi = T::pack(out(gate.z, lift.z), out(gate.w, lift.w));
-              *reinterpret_cast<uint2 *>(a.h + static_cast<int64_t>(to) * a.I + n) = make_uint2(lo, hi);
+              v[0] = out(gate.x, lift.x), v[1] = out(gate.y, lift.y), v[2] = out(gate.z, lift.z), v[3] = out(gate.w, lift.w);
             }
+            if constexpr (kPowers) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) largest = fmaxf(largest, fabsf(v[i]));
+#pragma unroll
+              for (int o = 4; o; o >>= 1) largest = fmaxf(largest, __shfl_xor_sync(0xffffffffu, largest, o));
+              const int bits = __float_as_int(largest), power = largest > 65504.f && bits < 0x7F800000 ? (bits >> 23) - 127 - 14 : 0;
+              wide |= __any_sync(0xffffffffu, power) != 0;
+              if (power) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) v[i] *= power_of_two(-power);
+              }
+              if (live && c == 0) {
+                a.powers[to * a.ld_powers + it.panel + sub] = static_cast<uint8_t>(power);
+                if (power) atomicMax(row_power + to, power);
+              }
+            }
+            if (live)
+              *reinterpret_cast<uint2 *>(a.h + static_cast<int64_t>(to) * a.I + n) = make_uint2(T::pack(v[0], v[1]), T::pack(v[2], v[3]));
           }
         } else {
           // two tokens at a time, four outputs to a lane
           const int c = 4 * (lane & 15), n = (it.panel + sub) * kW4PanelRows + c;
           for (int j0 = 0; j0 < count; j0 += 2) {
             const int j = j0 + (lane >> 4), to = __shfl_sync(0xffffffffu, row, j & 7);
+            const float u = kPowers ? __shfl_sync(0xffffffffu, unscale, j & 7) : kUnscale;
             if (j < count && n < a.H) {
               const float4 v = sum4(in, j * kW4Pitch + c);
-              *reinterpret_cast<float4 *>(a.part + static_cast<int64_t>(to) * a.H + n) =
-                  make_float4(v.x * kUnscale, v.y * kUnscale, v.z * kUnscale, v.w * kUnscale);
+              *reinterpret_cast<float4 *>(a.part + static_cast<int64_t>(to) * a.H + n) = make_float4(v.x * u, v.y * u, v.z * u, v.w * u);
             }
           }
         }
@@ -589,7 +664,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
       __threadfence();  // the item's results are out
       __syncwarp();
       if (it.up) {
-        if (lane == 0) atomicAdd(slot_done + it.slot, 1);
+        if (lane == 0) atomicAdd(slot_done + it.slot, wide ? kSlotWide + 1 : 1);
       } else {
         const bool last = lane < panels && atomicAdd(panel_done + it.panel + lane, 1) == slots - 1;
         const uint32_t ends = __ballot_sync(0xffffffffu, last);

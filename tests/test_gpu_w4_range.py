@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from nvfp4_block_scaled_quant_gb300 import ops
-from w4_reference import F64, check, checkpoint, moe, product
+from w4_reference import F64, check, checkpoint, moe, product, weight
 
 pytestmark = pytest.mark.gpu
 DEV = "cuda"
@@ -95,3 +95,43 @@ def test_outlier_that_meets_zero_weights_of_experts(T, group, zeros, kind, outli
     x[:, col] = outlier
     w13, w2, s13, s2 = (ops.w4_prepare(*c, group=group, gated=i % 2 == 0) for i, c in enumerate(cks))
     check(ops.w4_moe(x, router, w13, w2, topk, shared13=s13, shared2=s2), want, err, dt)
+
+
+SIZES = (1.0, 300.0, 1e-2, 3000.0, 30.0, 1e4)
+
+
+def wide_layer(T, H, I, E, topk, group, zeros, seed):
+    """An fp16 layer whose hidden rows pass 65504 for some tokens while its outputs do not."""
+    g = torch.Generator(device=DEV).manual_seed(seed)
+    dt = torch.float16
+    cks = [checkpoint(g, s, group, zeros, dt, DEV) for s in ((E, 2 * I, H), (E, H, I), (2 * I, H), (H, I))]
+    for i in (1, 3):
+        cks[i] = (cks[i][0], (cks[i][1].float() * 2.0 ** -10).to(dt), cks[i][2])
+    x = torch.randn(T, H, generator=g, device=DEV) * torch.tensor(SIZES, device=DEV)[(torch.arange(T, device=DEV) + (T == 1)) % len(SIZES)][:, None]
+    router = (torch.randn(E, H, generator=g, device=DEV) * H ** -0.5).to(dt)
+    packed = [ops.w4_prepare(*c, group=group, gated=i % 2 == 0) for i, c in enumerate(cks)]
+
+    def run(x):
+        return ops.w4_moe(x, router, packed[0], packed[1], topk, shared13=packed[2], shared2=packed[3])
+
+    return x.clamp(-6e4, 6e4).to(dt), router, cks, run
+
+
+@pytest.mark.parametrize("group,zeros", [(32, True), (64, False), (128, True)])
+@pytest.mark.parametrize("T,H,I,E,topk", [(1, 264, 136, 8, 2), (6, 392, 40, 12, 3), (13, 64, 1000, 6, 2), (40, 136, 264, 5, 2), (64, 264, 72, 40, 8),
+                                          (7, 8, 2056, 4, 2)])
+def test_fp16_hidden_rows_past_the_range(T, H, I, E, topk, group, zeros):
+    x, router, cks, run = wide_layer(T, H, I, E, topk, group, zeros, T + I)
+    want, err, _, _ = moe(x.to(F64), router, cks[0], cks[1], topk, group, "silu", x.dtype, (cks[2], cks[3]))
+    gu = x.to(F64) @ weight((cks[2][0], cks[2][1], cks[2][2]), group)[0].T
+    assert (torch.nn.functional.silu(gu[:, :I]) * gu[:, I:]).abs().max() > 65504  # of the shared expert
+    fits = want.abs() + err < 65504
+    assert fits.float().mean() > 0.5
+    y = run(x)
+    check(torch.where(fits, y, 0), torch.where(fits, want, 0), err, x.dtype)
+    assert torch.equal(y, run(x))
+    # the others' outputs do not hang on the large tokens
+    keep = torch.arange(T, device=DEV) % len(SIZES) % 2 == 0
+    if T > 1:
+        calm = torch.where(keep[:, None], x, x.clamp(-1, 1))
+        assert torch.equal(run(calm)[keep], y[keep])
