@@ -516,8 +516,8 @@ NVFP4_API nvfp4_status nvfp4_w4_prepare(const uint8_t *codes, const void *scales
                                         void *stream);
 
 /* y (M, N) = x (M, K) W^T, contiguous in `dtype`, W prepared without `gated`; any N, any M.  For few tokens the weights are read one
- * launch early, like those of nvfp4_linear, and the workspace's size is 0; for many it holds the weights as 16-bit integers
- * and the scales in fp32 (about 2 N K bytes). */
+ * launch early, like those of nvfp4_linear, and no workspace is needed; for many it holds the weights as 16-bit integers
+ * and the scales in fp32 (about 2 N K bytes).  The size returned for M rows is enough for every smaller number of rows too. */
 NVFP4_API size_t nvfp4_w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int group);
 NVFP4_API nvfp4_status nvfp4_w4_linear(const void *x, int dtype, int64_t M, int64_t K, int64_t ldx, int64_t N,
                                        const uint8_t *w, int group, int has_zeros, void *y, void *ws, size_t ws_bytes,

@@ -96,14 +96,26 @@ bool takes_pairs(int64_t M, int64_t N, int64_t K, int group) {
   return M > kStreamMaxTokens && pair_plan(M, N, K, group, kPlanSms).time < tc_plan(M, N, K, group).time;
 }
 
+// ... of any number of rows up to M.  The estimates are steps of M, so that the choice can go back and forth as M grows (12288 x 4096
+// in groups of 32: pairs for 129 to 256 rows, not up to 384, again beyond); a step ends at each of the numbers tried.  From
+// 8192 rows on, where x and y outweigh the weights of any product that has not taken pairs by then, the answer is yes.
+bool may_take_pairs(int64_t M, int64_t N, int64_t K, int group) {
+  if (M <= kStreamMaxTokens) return false;
+  for (int64_t m = 32; m < 8192; m += m < 128 ? m : 128) {
+    if (takes_pairs(m, N, K, group)) return true;
+    if (m >= M) return false;
+  }
+  return true;
+}
+
 // For the pair GEMM: where the written-out weights and their scales are in the workspace.
 struct LinearWs {
-  size_t w, scales, total;
+  size_t scales, total;
   int64_t lds;
 };
-LinearWs linear_ws(int64_t M, int64_t N, int64_t K, int group) {
+LinearWs linear_ws(int64_t N, int64_t K, int group, bool pairs) {
   LinearWs w = {};
-  if (!takes_pairs(M, N, K, group)) return w;
+  if (!pairs) return w;
   w.lds = round_up(N, 4);
   w.scales = align256(static_cast<size_t>(N) * static_cast<size_t>(K) * 2);
   w.total = align256(w.scales + static_cast<size_t>(w.lds) * static_cast<size_t>((K + group - 1) / group) * 4);
@@ -176,7 +188,7 @@ nvfp4_status nvfp4_w4_prepare(const uint8_t *codes, const void *scales, const ui
 size_t nvfp4_w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int group) {
   if (M < 0 || N <= 0 || K <= 0 || K % 8 || !dims_ok(M, K) || !dims_ok(N, K) || !dims_ok(M, N) || (group != 32 && group != 64 && group != 128))
     return 0;
-  return linear_ws(M, N, K, group).total;
+  return linear_ws(N, K, group, may_take_pairs(M, N, K, group)).total;
 }
 
 nvfp4_status nvfp4_w4_linear(const void *x, int dtype, int64_t M, int64_t K, int64_t ldx, int64_t N, const uint8_t *w,
@@ -190,7 +202,7 @@ nvfp4_status nvfp4_w4_linear(const void *x, int dtype, int64_t M, int64_t K, int
   if ((st = check_rows(__func__, x, M, K, ldx)) != NVFP4_OK) return st;
   NV_REQUIRE(aligned(w, 16) && aligned(y, 16), NVFP4_ERR_MISALIGNED, "w and y must be 16-byte aligned");
   const bool zeros = has_zeros != 0;
-  const LinearWs L = linear_ws(M, N, K, group);
+  const LinearWs L = linear_ws(N, K, group, takes_pairs(M, N, K, group));
   if ((st = check_ws(__func__, ws, ws_bytes, L.total)) != NVFP4_OK) return st;
   st = check_disjoint(__func__, {{y, M, N, N, 2}, flat(ws, static_cast<int64_t>(L.total), 1)},
                       {{x, M, ldx, K, 2}, flat(w, prepared_bytes(1, N, K, group, zeros, false), 1)});

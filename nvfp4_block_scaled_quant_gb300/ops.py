@@ -711,6 +711,11 @@ def _w4_whole(w: W4Weight, what: str, *sizes) -> int:
     return p
 
 
+def w4_linear_workspace(M: int, w: W4Weight) -> torch.Tensor:
+    """A workspace for ``w4_linear`` of up to M rows (one call at a time); empty where none is needed."""
+    return _u8(int(lib().nvfp4_w4_linear_workspace_bytes(M, w.N, w.K, w.group)), device=w.data.device)
+
+
 def w4_linear(x: torch.Tensor, w: W4Weight, out: Optional[torch.Tensor] = None,
               workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """y (M, N) = x W^T in x's type: x (M, K) strided rows of the type of the weights' scales."""
