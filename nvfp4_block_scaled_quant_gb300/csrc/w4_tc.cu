@@ -11,7 +11,7 @@
 // weights), 128 rows 28.3 (465 TF/s).
 // Warps: 0 = codes, 1 and 3 = MMA (3 also tensor memory), 2 = tokens, then the epilogue (four warps for each 64 tokens, one
 // 32-row quarter of tensor memory each) and the dequantising warps.  Every wait is bounded, as in the other
-// kernels.
+// kernels; what hangs on the tokens waits for the previous launch first, whose time does not count.
 #include <atomic>
 
 #include "w4.cuh"
@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(512, 1) w4_tc_kernel(const __grid_constant__ C
     int stage = 0;
     uint32_t phase = 0;
     for (int kb = kb0; kb < kb1; ++kb) {
+      if (kb == kb0 + C::kCodes) pdl_wait();  // the ring is full: the next place hangs on the tokens
       ok = wait(&empty_c[stage], phase ^ 1);
       if (!ok) break;
       if (lane == 0) {
@@ -150,6 +151,7 @@ __global__ void __launch_bounds__(512, 1) w4_tc_kernel(const __grid_constant__ C
     // A commit takes its issuer some 200 cycles, waits and the rest of a stage about as much: one commit per stage, whose barrier everyone
     // follows (with one for the stage, one for the tokens and one for the accumulator, and one issuer: 16 tokens
     // 7168 -> 7168 30 us instead of 20), and two issuers that take the groups (of 32: the stages) in turn.
+    pdl_wait();
     const int iss = warp >> 1;  // warps 1 and 3
     const uint32_t a0 = smem_u32(sA), x0 = smem_u32(sX);
     constexpr int kSteps = kGpb == 4 ? 2 : 4;       // MMAs of a group in a stage
@@ -193,6 +195,7 @@ __global__ void __launch_bounds__(512, 1) w4_tc_kernel(const __grid_constant__ C
       const int cs = (s >> 1) % C::kCodes;
       ok = wait(&full_c[cs], (s >> 1) / C::kCodes & 1);
       if (s >= C::kStages) {  // the stage's last product, which also was its tokens' last use
+        if (s < 2 * C::kStages) pdl_wait();  // the warp's first stage was written meanwhile
         ok = ok && wait(&done[stage], (s / C::kStages & 1) ^ 1);
         if (ok && lane == 0) mbar_arrive(&empty_x[C::x_stage(s - C::kStages)]);
       }
@@ -229,6 +232,7 @@ __global__ void __launch_bounds__(512, 1) w4_tc_kernel(const __grid_constant__ C
     }
   } else if (warp >= 4) {
     // -------------------------------------------------------------- epilogue: this CTA's sums of a row and 64 (kTok) tokens
+    pdl_wait();
     constexpr int kCols = kTok > 64 ? 64 : kTok;
     const int quarter = warp & 3, col0 = (warp - 4) / 4 * kCols, row = quarter * 32 + lane, r = row & 63;
     const uint32_t lanes = tmem_base + (static_cast<uint32_t>(quarter * 32) << 16) + col0;
