@@ -44,17 +44,18 @@ int stream_splits(int64_t ctas, int blocks, int sms) {
 // GB300 over 32 to 1024 tokens and six (K, N) between 512 x 512 and 7168 x 7168, every choice of each measured (the chosen one is
 // 0.1% slower than the best on average); they rank the choices, nothing else depends on them.  Groups of 64 and 32 take longer
 // where each group's sums pass through registers.
-constexpr int64_t kTcStart[4] = {4600, 5200, 6100, 7900}, kTcBlock[4] = {540, 470, 620, 720};  // by tokens of a tile: 16, 32, 64, 128
+constexpr int64_t kTcStart[3] = {5200, 6100, 7900}, kTcBlock[3] = {470, 620, 720};  // by tokens of a tile: 32, 64, 128
 constexpr int64_t kTileStart = 5400, kTileEnd[2] = {2200, 1500}, kTileBlock[2] = {272, 205};   // 256 and 128 columns; 64 K
 
 // How w4_tc_kernel covers M tokens: tiles of `tok`, clusters of `splits` CTAs along K, one CTA to an SM.
 constexpr int kTcClusters[4] = {152, 76, 46, 36};  // of 1 to 4 CTAs that a GB300 holds at once
+constexpr int kPlanPairs = 76;                     // of CTAs
 struct TcPlan {
   int tok, splits;
   int64_t time;
 };
 TcPlan tc_plan(int64_t M, int64_t N, int64_t K, int group) {
-  TcPlan p = {16, 1, 0};
+  TcPlan p = {32, 1, 0};
   int size = 0;
   while (p.tok < 128 && p.tok < M) p.tok *= 2, ++size;
   const int64_t tiles = (N + 127) / 128 * ((M + p.tok - 1) / p.tok), blocks = w4_blocks(K);
@@ -72,12 +73,12 @@ struct PairPlan {
   int cols;
   int64_t time;
 };
-PairPlan pair_plan(int64_t M, int64_t N, int64_t K, int group, int sms) {
+PairPlan pair_plan(int64_t M, int64_t N, int64_t K, int group) {
   PairPlan p = {256, 0};
   const int64_t expand = N * K / 2640;  // 2.5 bytes a weight
   for (int i = 0; i < 2; ++i) {
     const int cols = i ? 128 : 256;
-    const int64_t tiles = (N + kTRows - 1) / kTRows * ((M + cols - 1) / cols), waves = (tiles + sms / 2 - 1) / (sms / 2);
+    const int64_t tiles = (N + kTRows - 1) / kTRows * ((M + cols - 1) / cols), waves = (tiles + kPlanPairs - 1) / kPlanPairs;
     const int64_t block = kTileBlock[i] * (group == 32 ? 27 : group == 64 ? 14 : 10) / 10;
     const int64_t time = kTileStart + expand + waves * ((K + 63) / 64 * block + kTileEnd[i]);
     if (p.time == 0 || time < p.time) p = {cols, time};
@@ -87,13 +88,12 @@ PairPlan pair_plan(int64_t M, int64_t N, int64_t K, int group, int sms) {
 
 // Which kernel takes M tokens.  Up to 16 the weight-streaming one is faster whatever the sizes (16 tokens of 7168 -> 7168 15.6
 // against 20 us, 1536 -> 16384 9.0 against 11).  Above, the estimates decide, from sizes alone for the full GPU, since they
-// also size the workspace.
+// also size the workspace, which is asked for without a device; a choice made for 152 SMs is right on fewer, if not the fastest.
 constexpr int64_t kStreamMaxTokens = 16;
-constexpr int kPlanSms = 152;
 constexpr int64_t kTcMaxTokens = int64_t(65535) * 128;  // the grid's second dimension
 bool takes_pairs(int64_t M, int64_t N, int64_t K, int group) {
   if (M > kTcMaxTokens) return true;
-  return M > kStreamMaxTokens && pair_plan(M, N, K, group, kPlanSms).time < tc_plan(M, N, K, group).time;
+  return M > kStreamMaxTokens && pair_plan(M, N, K, group).time < tc_plan(M, N, K, group).time;
 }
 
 // ... of any number of rows up to M.  The estimates are steps of M, so that the choice can go back and forth as M grows (12288 x 4096
@@ -241,7 +241,7 @@ nvfp4_status nvfp4_w4_linear(const void *x, int dtype, int64_t M, int64_t K, int
   }
   uint16_t *ints = static_cast<uint16_t *>(ws);
   float *scales = reinterpret_cast<float *>(static_cast<uint8_t *>(ws) + L.scales);
-  const int cols = pair_plan(M, N, K, group, kPlanSms).cols;
+  const int cols = pair_plan(M, N, K, group).cols;
   CUtensorMap mw, mx, my = {};
   if ((st = make_map(__func__, &mw, ints, K * 2, N, K * 2, kTHalf)) != NVFP4_OK) return st;
   if ((st = make_map(__func__, &mx, x, K * 2, M, ldx * 2, cols / 2)) != NVFP4_OK) return st;

@@ -40,7 +40,7 @@ struct W4Args {
 cudaError_t launch_w4_stream(const W4Args &a, int dtype, int group, bool zeros, int tok8, int splits, int depth,
                              cudaStream_t s);
 
-// Some ten to some hundred tokens: tokens in tiles of tok (16, 32, 64 or 128), K split over a cluster of `splits` CTAs; x: a map
+// Some ten to some hundred tokens: tokens in tiles of tok (32, 64 or 128), K split over a cluster of `splits` CTAs; x: a map
 // of x with boxes of tok rows.
 cudaError_t launch_w4_tc(const CUtensorMap &x, const W4Args &a, int dtype, int group, bool zeros, int tok, int splits,
                          cudaStream_t s);

@@ -32,14 +32,14 @@ struct TcCfg {
   // Accumulators.  The epilogue follows the stages' barriers, so the MMAs may not get four stages ahead of it: two for
   // groups of two stages.  Each belongs to one issuer: four where a stage holds two groups.
   static constexpr int kBufs = kGpb == 1 ? 2 : kGpb == 4 || kTok <= 64 ? 4 : 2;
-  static constexpr uint32_t kTmemCols = kBufs * kTok < 32 ? 32 : kBufs * kTok;
+  static constexpr uint32_t kTmemCols = kBufs * kTok;
   static constexpr int kEpi = kTok > 64 ? 8 : 4, kDeq = 12 - kEpi;
   static constexpr int kThreads = 512;
   static constexpr size_t kSmem = kRing + kCodes * 2 * kBlock + 1024;
   static_assert(kSmem <= 232448 - 1024, "per-block shared memory limit");
   static_assert(kTok * 128 * 4 <= kRing, "the sums fit where the ring was");
   static_assert(kDeq % kStages == 0 && kCodes % 2 == 0, "a warp sees every phase of the barriers it waits on");
-  static_assert(kTok % 16 == 0 && kTmemCols <= 512, "MMA N, tensor memory");
+  static_assert(kTok % 32 == 0 && kTmemCols <= 512, "MMA N, tensor memory");
   // The issuer of a 64-wide step (they take the groups of 128, else the steps, in turn), and its tokens' stage: each issuer has
   // half of the ring, of which it sees every phase.
   static __device__ __forceinline__ int issuer(int step) { return kGpb == 1 ? (step >> 1) & 1 : step & 1; }
@@ -149,8 +149,8 @@ __global__ void __launch_bounds__(512, 1) w4_tc_kernel(const __grid_constant__ C
   } else if (warp < 4) {
     // -------------------------------------------------------------- MMA issuers (one elected lane issues)
     // A commit takes its issuer some 200 cycles, waits and the rest of a stage about as much: one commit per stage, whose barrier everyone
-    // follows (with one for the stage, one for the tokens and one for the accumulator, and one issuer: 16 tokens
-    // 7168 -> 7168 30 us instead of 20), and two issuers that take the groups (of 32: the stages) in turn.
+    // follows (with one for the stage, one for the tokens and one for the accumulator, and one issuer, a tile of 16 tokens
+    // 7168 -> 7168 took 30 us instead of 20), and two issuers that take the groups (of 32: the stages) in turn.
     pdl_wait();
     const int iss = warp >> 1;  // warps 1 and 3
     const uint32_t a0 = smem_u32(sA), x0 = smem_u32(sX);
@@ -351,7 +351,6 @@ cudaError_t tc_as(const CUtensorMap &x, const W4Args &a, int splits, cudaStream_
 template <class T, int kGpb, bool kZeros>
 cudaError_t tc_tok(const CUtensorMap &x, const W4Args &a, int tok, int splits, cudaStream_t s) {
   switch (tok) {
-    case 16: return tc_as<T, kGpb, kZeros, 16>(x, a, splits, s);
     case 32: return tc_as<T, kGpb, kZeros, 32>(x, a, splits, s);
     case 64: return tc_as<T, kGpb, kZeros, 64>(x, a, splits, s);
     case 128: return tc_as<T, kGpb, kZeros, 128>(x, a, splits, s);
