@@ -13,6 +13,8 @@
 // activation of 10^9 times its neighbours, which meets weights of zero, nothing of the neighbours was left.)
 #pragma once
 
+#include <atomic>
+
 #include "mma16x8.cuh"
 #include "w4.h"
 
@@ -163,6 +165,61 @@ __device__ __forceinline__ void w4_store_sums(float *at, const uint64_t (&sums)[
         float *row = at + (8 * n + 2 * t) * kW4Pitch + 16 * i + 8 * h + g;
         unpack_f32x2(sums[i][n][h], row[0], row[kW4Pitch]);
       }
+}
+
+// The sum over a cluster's CTAs, in their order, of the float at one shared-memory address; every load is in flight before the
+// sums.
+constexpr int kW4MaxRanks = 8;
+__device__ __forceinline__ float cluster_sum(uint32_t at, int ranks) {
+  float v[kW4MaxRanks];
+#pragma unroll
+  for (int r = 0; r < kW4MaxRanks; ++r) {
+    v[r] = 0.f;
+    if (r < ranks) {
+      uint32_t addr;
+      asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(at), "r"(r));
+      asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[r]) : "r"(addr) : "memory");
+    }
+  }
+  float sum = v[0];
+#pragma unroll
+  for (int r = 1; r < kW4MaxRanks; ++r)
+    if (r < ranks) sum += v[r];
+  return sum;
+}
+
+// Lets a kernel have `bytes` of dynamic shared memory, once per device.
+template <auto kKernel>
+cudaError_t allow_smem(int bytes) {
+  static std::atomic<bool> ready[64];
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (ready[dev].load()) return cudaSuccess;
+  const cudaError_t set = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (set == cudaSuccess) ready[dev].store(true);
+  return set;
+}
+
+// A launch in clusters of `ranks` CTAs along x that may start while the one before ends.
+template <class... KArgs, class... Args>
+cudaError_t launch_clusters(void (*kernel)(KArgs...), dim3 grid, int threads, size_t smem, int ranks, cudaStream_t s, Args &&...args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = static_cast<unsigned>(ranks);
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<KArgs>(args)...);
 }
 
 }  // namespace nvfp4

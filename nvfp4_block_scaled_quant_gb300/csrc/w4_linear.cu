@@ -8,8 +8,6 @@
 // The first blocks are asked for before the wait for the previous launch: prepared weights are final by then.
 // One row with many outputs streams at 6.0 TB/s; small products are bound by the wait for the launch before, the first blocks'
 // latency and the cluster's sums: 1 x 7168 -> 2048 4.5 us, 13 x 1536 -> 16384 9.4, 16 x 7168 -> 7168 15.6.
-#include <atomic>
-
 #include "w4.cuh"
 
 namespace nvfp4 {
@@ -143,20 +141,7 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_stream_kernel(const W4Args 
     const uint32_t base = smem_u32(smem);
     for (int e = e0 + static_cast<int>(threadIdx.x); e < e1; e += kWarps * 32) {
       const int at = (e >> 6) * kW4Pitch + (e & 63), n = panel * kW4PanelRows + (e & 63);
-      float v[8];  // every rank's load is in flight before the sums
-#pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        v[r] = 0.f;
-        if (r < splits) {
-          uint32_t addr;
-          asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(base + at * 4), "r"(r));
-          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[r]) : "r"(addr) : "memory");
-        }
-      }
-      float s = v[0];
-#pragma unroll
-      for (int r = 1; r < 8; ++r)
-        if (r < splits) s += v[r];
+      const float s = cluster_sum(base + at * 4, splits);
       if (n < a.N) static_cast<uint16_t *>(a.y)[static_cast<int64_t>(e >> 6) * a.N + n] = T::one(s);
     }
   }
@@ -166,32 +151,10 @@ __global__ void __launch_bounds__(kWarps * 32, 2) w4_stream_kernel(const W4Args 
 template <class T, int kGpb, bool kZeros, int kNT>
 cudaError_t stream_as(const W4Args &a, int splits, int depth, cudaStream_t s) {
   constexpr int kBytes = w4_block_bytes(kGpb, kZeros);
-  auto kernel = w4_stream_kernel<T, kGpb, kZeros, kNT>;
-  static std::atomic<bool> ready[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = allow_smem<w4_stream_kernel<T, kGpb, kZeros, kNT>>(kWarps * 4 * kBytes);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!ready[dev].load()) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWarps * 4 * kBytes);
-    if (e != cudaSuccess) return e;
-    ready[dev].store(true);
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(w4_panels(a.N, false) * splits));
-  cfg.blockDim = dim3(kWarps * 32);
-  cfg.dynamicSmemBytes = static_cast<size_t>(kWarps) * depth * kBytes;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, a, splits, depth);
+  return launch_clusters(w4_stream_kernel<T, kGpb, kZeros, kNT>, dim3(static_cast<unsigned>(w4_panels(a.N, false) * splits)), kWarps * 32,
+                         static_cast<size_t>(kWarps) * depth * kBytes, splits, s, a, splits, depth);
 }
 
 template <class T, int kGpb, bool kZeros>

@@ -23,8 +23,6 @@
 // stages back.  Two CTAs share an SM.  (The rings are the warps' own because a warp waits on every phase of its
 // barriers then.  In a common ring, taken block by block, a warp that got a ring's length ahead of a slow copy would take an
 // older phase of the same parity for its own.)
-#include <atomic>
-
 #include "w4.cuh"
 
 namespace nvfp4 {
@@ -33,7 +31,6 @@ namespace {
 // ---------------------------------------------------------------- router logits
 
 constexpr int kLogitWarps = 8;
-constexpr int kLogitMaxSplit = 8;
 
 // 16 experts per cluster, K split over its CTAs and their warps; kNT tiles of eight tokens.  A chain of latencies (loads, sums over
 // warps and cluster): 384 experts of 7168 and one token take about 5 us, 5.5 MB.
@@ -80,20 +77,7 @@ __global__ void __launch_bounds__(kLogitWarps * 32) w4_moe_logits_kernel(const W
   if (splits > 1) cluster_meet();
   const uint32_t base = smem_u32(part);
   for (int e = live * rank / splits + static_cast<int>(threadIdx.x); e < live * (rank + 1) / splits; e += kLogitWarps * 32) {
-    float v[kLogitMaxSplit];
-#pragma unroll
-    for (int r = 0; r < kLogitMaxSplit; ++r) {
-      v[r] = 0.f;
-      if (r < splits) {
-        uint32_t addr;
-        asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(base + e * 4), "r"(r));
-        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[r]) : "r"(addr) : "memory");
-      }
-    }
-    float s = v[0];
-#pragma unroll
-    for (int r = 1; r < kLogitMaxSplit; ++r)
-      if (r < splits) s += v[r];
+    const float s = cluster_sum(base + e * 4, splits);
     const int expert = tile * 16 + (e & 15);
     if (expert < a.E) a.logits[static_cast<int64_t>(e >> 4) * a.E + expert] = s;
   }
@@ -726,20 +710,8 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
 
 template <class T, int kNT>
 cudaError_t logits_as(const W4MoeArgs &a, int splits, int n_counters, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.E + 15) / 16 * splits));
-  cfg.blockDim = dim3(kLogitWarps * 32);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, w4_moe_logits_kernel<T, kNT>, a, splits, n_counters);
+  return launch_clusters(w4_moe_logits_kernel<T, kNT>, dim3(static_cast<unsigned>((a.E + 15) / 16 * splits)), kLogitWarps * 32, 0, splits, s, a, splits,
+                         n_counters);
 }
 
 template <class T, int kGpb, bool kZeros>
@@ -750,22 +722,13 @@ cudaError_t experts_as(const W4MoeArgs &a, int sms, cudaStream_t s) {
   constexpr int kSmem = kDepth * kWarps * kBytes;
   static_assert(kDepth >= 2 && sizeof(PlanScratch) <= kSmem && kBytes >= 8 * kW4Pitch * 4, "rings, scratch and sums");
   static_assert(sizeof(Plan) + 2 * kWarps * kMaxDepth * 8 + kItems * 32 + kW4MoeMaxDim / kW4PanelRows * 2 + 256 <= kStatic, "static shared memory");
-  auto kernel = w4_moe_experts_kernel<T, kGpb, kZeros>;
-  static std::atomic<bool> ready[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = allow_smem<w4_moe_experts_kernel<T, kGpb, kZeros>>(kSmem);
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!ready[dev].load()) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (e != cudaSuccess) return e;
-    ready[dev].store(true);
-  }
   // no more CTAs than panels
   const int64_t most = static_cast<int64_t>(a.T * a.topk + (a.sh13 ? (a.T + 7) / 8 : 0)) *
                        ((a.I + 31) / 32 + (a.H + kW4PanelRows - 1) / kW4PanelRows);
   const int64_t ctas = most < 2 * sms ? most : 2 * sms;
-  return launch_pdl(kernel, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), kSmem, s, a, kDepth);
+  return launch_pdl(w4_moe_experts_kernel<T, kGpb, kZeros>, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), kSmem, s, a, kDepth);
 }
 
 template <class T>
@@ -773,7 +736,7 @@ cudaError_t moe_as(const W4MoeArgs &a, int group, bool zeros, int sms, cudaStrea
   const int tiles = (a.E + 15) / 16, chunks = (a.H + 31) / 32;
   int splits = sms / tiles;
   if (splits > chunks / kLogitWarps) splits = chunks / kLogitWarps;
-  if (splits > kLogitMaxSplit) splits = kLogitMaxSplit;
+  if (splits > kW4MaxRanks) splits = kW4MaxRanks;
   if (splits < 1) splits = 1;
   const int n = kW4MoeCounters + (a.H + kW4PanelRows - 1) / kW4PanelRows;
   cudaError_t e = a.T <= 8 ? logits_as<T, 1>(a, splits, n, s) : a.T <= 16 ? logits_as<T, 2>(a, splits, n, s) : logits_as<T, 8>(a, splits, n, s);

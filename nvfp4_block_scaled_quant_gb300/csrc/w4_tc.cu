@@ -12,8 +12,6 @@
 // Warps: 0 = codes, 1 and 3 = MMA (3 also tensor memory), 2 = tokens, then the epilogue (four warps for each 64 tokens, one
 // 32-row quarter of tensor memory each) and the dequantising warps.  Every wait is bounded, as in the other
 // kernels; what hangs on the tokens waits for the previous launch first, whose time does not count.
-#include <atomic>
-
 #include "w4.cuh"
 
 namespace nvfp4 {
@@ -297,20 +295,7 @@ __global__ void __launch_bounds__(512, 1) w4_tc_kernel(const __grid_constant__ C
     const uint32_t base = smem_u32(smem);
     for (int e = live * rank / splits * 128 + static_cast<int>(threadIdx.x); e < live * (rank + 1) / splits * 128; e += C::kThreads) {
       const int f = tile * 128 + (e & 127);
-      float v[8];  // every rank's load is in flight before the sums
-#pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        v[r] = 0.f;
-        if (r < splits) {
-          uint32_t addr;
-          asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(base + e * 4), "r"(r));
-          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v[r]) : "r"(addr) : "memory");
-        }
-      }
-      float s = v[0];
-#pragma unroll
-      for (int r = 1; r < 8; ++r)
-        if (r < splits) s += v[r];
+      const float s = cluster_sum(base + e * 4, splits);
       if (f < args.N) static_cast<uint16_t *>(args.y)[static_cast<int64_t>(m0 + (e >> 7)) * args.N + f] = T::one(s * power_of_two(W4Scale<T>::kRest));
     }
   }
@@ -320,32 +305,10 @@ __global__ void __launch_bounds__(512, 1) w4_tc_kernel(const __grid_constant__ C
 template <class T, int kGpb, bool kZeros, int kTok>
 cudaError_t tc_as(const CUtensorMap &x, const W4Args &a, int splits, cudaStream_t s) {
   using C = TcCfg<kGpb, kZeros, kTok>;
-  auto kernel = w4_tc_kernel<T, kGpb, kZeros, kTok>;
-  static std::atomic<bool> ready[64];
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  const cudaError_t e = allow_smem<w4_tc_kernel<T, kGpb, kZeros, kTok>>(static_cast<int>(C::kSmem));
   if (e != cudaSuccess) return e;
-  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-  if (!ready[dev].load()) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(C::kSmem));
-    if (e != cudaSuccess) return e;
-    ready[dev].store(true);
-  }
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((a.N + 127) / 128 * splits), static_cast<unsigned>((a.M + kTok - 1) / kTok));
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = static_cast<unsigned>(splits);
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, kernel, x, a, splits);
+  return launch_clusters(w4_tc_kernel<T, kGpb, kZeros, kTok>, dim3(static_cast<unsigned>((a.N + 127) / 128 * splits), static_cast<unsigned>((a.M + kTok - 1) / kTok)),
+                         C::kThreads, C::kSmem, splits, s, x, a, splits);
 }
 
 template <class T, int kGpb, bool kZeros>
