@@ -86,8 +86,8 @@ PairPlan pair_plan(int64_t M, int64_t N, int64_t K, int group) {
   return p;
 }
 
-// Which kernel takes M tokens.  Up to 16 the weight-streaming one is faster whatever the sizes (16 tokens of 7168 -> 7168 15.6
-// against 20 us, 1536 -> 16384 9.0 against 11).  Above, the estimates decide, from sizes alone for the full GPU, since they
+// Which kernel takes M tokens.  Up to 16 the weight-streaming one is faster whatever the sizes (16 tokens of 7168 -> 7168 13.6
+// against 20 us, 1536 -> 16384 7.2 against 11).  Above, the estimates decide, from sizes alone for the full GPU, since they
 // also size the workspace, which is asked for without a device; a choice made for 152 SMs is right on fewer, if not the fastest.
 constexpr int64_t kStreamMaxTokens = 16;
 constexpr int64_t kTcMaxTokens = int64_t(65535) * 128;  // the grid's second dimension

@@ -6,8 +6,8 @@
 // as soon as the warp is done with the one in its place, so no warp waits for another until the sums are
 // added up, over the warps and then over the cluster, in a fixed order (repeated calls give identical bits).
 // The first blocks are asked for before the wait for the previous launch: prepared weights are final by then.
-// One row with many outputs streams at 6.0 TB/s; small products are bound by the wait for the launch before, the first blocks'
-// latency and the cluster's sums: 1 x 7168 -> 2048 4.5 us, 13 x 1536 -> 16384 9.4, 16 x 7168 -> 7168 15.6.
+// One row with many outputs streams at 6.1 TB/s; small products are bound by the wait for the launch before, the first blocks'
+// latency and the cluster's sums: 1 x 7168 -> 2048 4.6 us, 13 x 1536 -> 16384 7.3, 16 x 7168 -> 7168 13.6.
 #include "w4.cuh"
 
 namespace nvfp4 {

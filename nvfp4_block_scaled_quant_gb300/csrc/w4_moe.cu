@@ -16,7 +16,7 @@
 // panel of such a row is stored times a power of two that brings its largest to 2^14, and the first warp that finds such a slot
 // complete brings the other panels of the row to the same power.  Rows within the range are stored as they are.
 //
-// With few tokens the layer is bound by the bytes of the chosen experts' weights: 16 tokens, 384 experts of 7168 x 2048 396 us, 94% of
+// With few tokens the layer is bound by the bytes of the chosen experts' weights: 16 tokens, 384 experts of 7168 x 2048 390 us, 95% of
 // the copy bandwidth; one token 50 us, of which 8 pass before weights stream.  Eight warps of a CTA share an item's
 // panels and take a panel's K blocks in turn, each through a ring of its own: a block is one bulk copy.  A warp leaves its sums where its
 // last block of the item was and goes on to the next item; a finishing warp adds the eight up and gives the
@@ -187,7 +187,7 @@ __device__ __forceinline__ void choose(const W4MoeArgs &a, uint16_t *ids, float 
 // How many panels (log2) an item holds, shared out to the warps, so that a warp has more K blocks in a row and the items' own
 // cost (the first load of its activations, its sums, its signals) is spread over more of them.  That pays where a CTA takes many items; where it
 // takes few, smaller ones spread better.  Two panels / one: 59 tokens, 80 experts of 5280 x 352 (22 items of the down projection to a
-// CTA) 97 / 110 us, 32 tokens, 180 of 1256 x 1808 (26 and 9) 119 / 132; 1 token, 384 of 7168 x 2048 (2 and 3) 58 / 50.
+// CTA) 98 / 110 us, 32 tokens, 180 of 1256 x 1808 (26 and 9) 112 / 125; 1 token, 384 of 7168 x 2048 (2 and 3) 54 / 50.
 __device__ __forceinline__ int item_split(int slots, int panels, int ctas) {
   const int rounds = slots * panels / ctas;
   return rounds < 8 ? 0 : rounds < 32 ? 1 : 2;
@@ -198,7 +198,7 @@ __device__ void make_plan(const W4MoeArgs &a, Plan &plan, PlanScratch &s) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, entries = a.T * a.topk;
   if (entries > 32)
     for (int e = tid; e < a.E; e += kThreads) s.tokens[0][spread(e)] = s.tokens[1][spread(e)] = 0u;
-  // (with four places to a lane, where it has one expert, each choice ends in a search: 53 tokens, 28 experts, top 8 40 us instead of 34)
+  // (with four places to a lane, where it has one expert, each choice ends in a search: 53 tokens, 28 experts, top 8 37 us instead of 30)
   if (a.E <= 32)
     choose<1>(a, s.ids, plan.weight);
   else if (a.E <= 128)
@@ -393,8 +393,8 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
   const int split13 = item_split(slots, panels13, gridDim.x), split2 = item_split(slots, panels2, gridDim.x);
   const int items13 = (panels13 + (1 << split13) - 1) >> split13, items2 = (panels2 + (1 << split2) - 1) >> split2;  // of a slot
   // Stages of a warp's ring.  The producer claims an item a ring ahead of the products, which with few items leaves some to a CTA that
-  // is behind while others run out: two stages where items are few and small, else three.  Three / two: one token 51.2 /
-  // 50.0 us, 13 tokens, 24 experts of 1544 x 1000 38 / 36, 16 tokens, 384 of 7168 x 2048 399 / 409.
+  // is behind while others run out: two stages where items are few and small, else three.  Three / two: one token 51.3 /
+  // 49.7 us, 13 tokens, 24 experts of 1544 x 1000 36 / 34, 16 tokens, 384 of 7168 x 2048 390 / 402.
   const int depth = split2 == 0 ? 2 : most;
   int *counter = a.counters, *slot_done = counter + kW4MoeSlotDone, *row_power = counter + kW4MoeRowPower, *panel_done = counter + kW4MoeCounters;
   constexpr bool kPowers = T::kCode == NVFP4_DT_FP16;  // h may pass the type's range
@@ -667,7 +667,7 @@ __global__ void __launch_bounds__(kThreads, 2) w4_moe_experts_kernel(const W4Moe
   __syncwarp();
   asm volatile("bar.sync 1, %0;" ::"n"((kWarps + 1) * 32) : "memory");
   // Two or four columns to a thread: four are fewer turns where a panel has more than a pair for each thread (51 tokens, 116
-  // experts of 1384 x 184 55.6 -> 52.0 us), two 1% less time where it has not.
+  // experts of 1384 x 184 56.6 -> 51.8 us), two 1% less time where it has not.
   const int finished_rows = s_finished * a.T;
   auto add_up = [&](auto pair) {
     using V = decltype(pair);

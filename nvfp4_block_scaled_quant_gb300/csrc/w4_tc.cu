@@ -7,8 +7,8 @@
 // tokens.  Each group's product goes to an accumulator of its own, and the epilogue warps add it to fp32 registers
 // times the scale of their row, which they read from the ring: no weight is rounded.
 //
-// What a stage takes in turn (codes, dequantisation, commit, promotion) bounds it: 64 rows 7168 -> 7168 22.9 us (1.2 TB/s of
-// weights), 128 rows 28.3 (465 TF/s).
+// What a stage takes in turn (codes, dequantisation, commit, promotion) bounds it: 64 rows 7168 -> 7168 22.3 us (1.2 TB/s of
+// weights), 128 rows 27.7 (475 TF/s).
 // Warps: 0 = codes, 1 and 3 = MMA (3 also tensor memory), 2 = tokens, then the epilogue (four warps for each 64 tokens, one
 // 32-row quarter of tensor memory each) and the dequantising warps.  Every wait is bounded, as in the other
 // kernels; what hangs on the tokens waits for the previous launch first, whose time does not count.
