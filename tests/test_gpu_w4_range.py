@@ -135,3 +135,31 @@ def test_fp16_hidden_rows_past_the_range(T, H, I, E, topk, group, zeros):
     if T > 1:
         calm = torch.where(keep[:, None], x, x.clamp(-1, 1))
         assert torch.equal(run(calm)[keep], y[keep])
+
+
+def test_fp16_hidden_rows_past_the_range_captured_and_at_once():
+    """Replays with other tokens, some past the range and some not, and two streams at a time."""
+    x, router, cks, run = wide_layer(12, 1032, 520, 24, 4, 64, True, 3)
+    wants = [run(torch.roll(x, k, 0)) for k in range(len(SIZES))]
+    for k, w in enumerate(wants):
+        assert torch.equal(torch.roll(w, -k, 0), wants[0])
+    static = x.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        y = run(static)
+        z = run(torch.zeros_like(static))
+    for k, w in enumerate(wants):
+        static.copy_(torch.roll(x, k, 0))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, w) and not z.any()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for k in range(20):
+        for i in range(2):
+            with torch.cuda.stream(streams[i]):
+                got[i].append(run(x))
+    torch.cuda.synchronize()
+    assert all(torch.equal(v, wants[0]) for g in got for v in g)
+    assert ops.device_error() == (0, 0)
