@@ -500,7 +500,8 @@ NVFP4_API nvfp4_status nvfp4_residual_norm_backward(const void *dr_out, int64_t 
  * 4-bit integer weights with group scales, and 16-bit activations: for inference.  A checkpoint stores, for each row
  * of a matrix (N, K), codes c of 4 bits (two per byte, element 2 j in the low half; K / 2 bytes), and for each `group` (32,
  * 64 or 128) consecutive K elements, the last group of a row may be partial, a scale s in `dtype` and, optionally, a
- * zero point z (one byte, of which the low four bits count; 8 without zero points).  A weight is (c - z) s.
+ * zero point z (one byte, of which the low four bits count, so that a file that stores z - 1 has to be raised by its
+ * reader and its 15 stands for no z; 8 without zero points).  A weight is (c - z) s.
  * The conventions of the dense operators hold; x (rows, K) has a row stride ldx (a multiple of 8) and is bf16 or fp16
  * (`dtype`), the scales' type; K % 8 == 0.  Weights are never rounded: products with c - z are exact, a group's sum is fp32 and
  * multiplied by its scale in fp32.  A row of x that holds a NaN or an infinity has outputs that are not finite.

@@ -664,8 +664,8 @@ def w4_prepare(codes: torch.Tensor, scales: torch.Tensor, zeros: Optional[torch.
     """Lays out checkpoint weights (c - z) s, once, at load time.
 
     codes (N, K / 2) uint8 with element 2j in the low half of byte j, or (G, N, K / 2) for G matrices; scales
-    (..., N, ceil(K / group)) bf16 or fp16; zeros uint8 of the same shape, of which the low four bits count (None: 8
-    everywhere); group 32, 64 or 128.  ``gated``: the first N / 2 rows are a gate and the others the up projection of
+    (..., N, ceil(K / group)) bf16 or fp16; zeros uint8 of the same shape, z itself (not z - 1), of which the low four bits count
+    (None: 8 everywhere); group 32, 64 or 128.  ``gated``: the first N / 2 rows are a gate and the others the up projection of
     the same outputs (``w4_moe``'s w13).  K % 8 == 0.
     """
     st = _here(stream, codes, scales, zeros)
