@@ -503,8 +503,8 @@ NVFP4_API nvfp4_status nvfp4_residual_norm_backward(const void *dr_out, int64_t 
  * zero point z (one byte, of which the low four bits count, so that a file that stores z - 1 has to be raised by its
  * reader and its 15 stands for no z; 8 without zero points).  A weight is (c - z) s.
  * The conventions of the dense operators hold; x (rows, K) has a row stride ldx (a multiple of 8) and is bf16 or fp16
- * (`dtype`), the scales' type; K % 8 == 0.  Weights are never rounded: products with c - z are exact, a group's sum is fp32 and
- * multiplied by its scale in fp32.  A row of x that holds a NaN or an infinity has outputs that are not finite.
+ * (`dtype`), the scales' type; K % 8 == 0.  Weights are never rounded: products with c - z are exact, a group's sum is fp32 (of 2^-7 of its
+ * size in bf16, 2^-10 in fp16) and multiplied by its scale in fp32.  A row of x that holds a NaN or an infinity has outputs that are not finite.
  * ============================================================================ */
 
 /* Lays out G matrices for the products below, once, at load time: codes (G, N, K / 2), scales and zeros (G, N,
@@ -517,7 +517,7 @@ NVFP4_API nvfp4_status nvfp4_w4_prepare(const uint8_t *codes, const void *scales
                                         void *stream);
 
 /* y (M, N) = x (M, K) W^T, contiguous in `dtype`, W prepared without `gated`; any N, any M.  For few tokens the weights are read one
- * launch early, like those of nvfp4_linear, and no workspace is needed; for many it holds the weights as 16-bit integers
+ * launch early, like those of nvfp4_linear, and no workspace is needed; for many it holds the weights' codes in 16 bits
  * and the scales in fp32 (about 2 N K bytes).  The size returned for M rows is enough for every smaller number of rows too. */
 NVFP4_API size_t nvfp4_w4_linear_workspace_bytes(int64_t M, int64_t N, int64_t K, int group);
 NVFP4_API nvfp4_status nvfp4_w4_linear(const void *x, int dtype, int64_t M, int64_t K, int64_t ldx, int64_t N,

@@ -20,7 +20,7 @@
 //               longer than the other's MMAs.  Measured and left: four accumulators of 128 columns (two
 //               issuers; 8 warps 200 us, 16 warps 175 us), 16 epilogue warps on 256 columns, two batches
 //               of columns in flight, activation scales through a shared-memory ring.
-//   Op::kW4     A = the codes less their zero points (N, K) as 16-bit integers, B = x (M, K): the same promotion,
+//   Op::kW4     A = the codes less their zero points (N, K) in 16 bits, B = x (M, K): the same promotion,
 //               of every group of 32, 64 or 128 K (kAct) with its scale.  The operands are swapped, so that
 //               a thread's columns share the one scale of its row of A.  A group of 128 is two K blocks, one of
 //               32 half a block, which the two issuers share.  The output is written across: a lane's row is an
@@ -68,6 +68,7 @@ struct TileArgs {
   const float *sw; // kFp8: (ceil(N / 128), K blocks) weight scales
   void *out;       // 16-bit (M, N), row stride ldo; kW4: (N, M)
   int groups;      // kW4: of a row
+  float factor;    // kW4: of the sums, a power of two
   void *dwg, *dwu; // kGrad: the weight gradients, (dw_M / 2, N) each, row stride ldo
   const float *unscale;  // kGrad, fp16: factor of the sums (the inverse of dg's and du's power of two)
   int64_t ldo;
@@ -470,7 +471,7 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
               __syncwarp();
 #pragma unroll
               for (int j = 0; j < 32; j += 2) {
-                const uint32_t v = T::pack(sum[32 * c + j], sum[32 * c + j + 1]);
+                const uint32_t v = T::pack(sum[32 * c + j] * args.factor, sum[32 * c + j + 1] * args.factor);
                 place[j * 32 + lane] = static_cast<uint16_t>(v);
                 place[j * 32 + 32 + lane] = static_cast<uint16_t>(v >> 16);
               }
@@ -484,7 +485,7 @@ __global__ void __launch_bounds__(kTThreads<kOp>, 1)
           dst += out_n0 * args.ldo + out_row;
 #pragma unroll
           for (int i = 0; i < kBRows; ++i)
-            if (i < left) dst[i * args.ldo] = T::one(sum[i]);
+            if (i < left) dst[i * args.ldo] = T::one(sum[i] * args.factor);
         }
       } else if constexpr (kFp8) {
 #pragma unroll

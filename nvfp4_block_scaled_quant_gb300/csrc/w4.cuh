@@ -8,7 +8,8 @@
 // of a word's even bytes, one shift and the same masks those of the odd ones, and one multiplication and addition of
 // each pair takes the zero points off: nine operations for eight codes.  The result (c - z) 2^-kRest is exact in either type and
 // normal, so that activations go into the MMA as they are and the sums are multiplied by 2^kRest at the end.  Products are exact,
-// sums are fp32, scales apply to the fp32 sums of their group: no weight is rounded.
+// sums are fp32, scales apply to the fp32 sums of their group: no weight is rounded.  A group's sum may pass
+// fp32's range by 2^kRest.  (In bf16 2^-11 would hold every sum, but those of the smallest activations lose bits that outputs have.)
 // (Codes as they are, their sums less z sum x, are five operations, but c x and z x round apart where c = z: under an
 // activation of 10^9 times its neighbours, which meets weights of zero, nothing of the neighbours was left.)
 #pragma once
@@ -20,7 +21,7 @@
 
 namespace nvfp4 {
 
-// kStep: minus the exponent of the type's smallest subnormal; 2^kUp, a number of the type, brings a code to 2^-kRest of its size.
+// kStep: minus the exponent of the type's smallest subnormal; 2^kUp brings a code to 2^-kRest of its size.
 template <class T>
 struct W4Scale;
 template <>

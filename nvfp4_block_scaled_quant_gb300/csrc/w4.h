@@ -45,7 +45,7 @@ cudaError_t launch_w4_stream(const W4Args &a, int dtype, int group, bool zeros, 
 cudaError_t launch_w4_tc(const CUtensorMap &x, const W4Args &a, int dtype, int group, bool zeros, int tok, int splits,
                          cudaStream_t s);
 
-// Many tokens: the integers c - z of the prepared weights as a 16-bit matrix (N, K), the scales as (groups, lds) fp32, and
+// Many tokens: (c - z) 2^-kRest of the prepared weights as a 16-bit matrix (N, K), the scales as (groups, lds) fp32, and
 // the product of that matrix and x on CTA pairs.
 struct TileArgs;
 cudaError_t launch_w4_expand(const W4Args &a, int dtype, int group, bool zeros, uint16_t *out, float *scales, int64_t lds,

@@ -1,5 +1,5 @@
-// The linear layer on 4-bit weights for many tokens: the weights are written out once per call as the 16-bit integers
-// c - z (exact), which the CTA-pair GEMM takes as its operand; it applies the scales to each group's fp32 sums.
+// The linear layer on 4-bit weights for many tokens: the weights are written out once per call as the 16-bit numbers
+// (c - z) 2^-kRest (exact), which the CTA-pair GEMM takes as its operand; it applies the scales to each group's fp32 sums.
 #include "tile_gemm.cuh"
 #include "w4.cuh"
 
@@ -25,8 +25,6 @@ __global__ void __launch_bounds__(256) w4_expand_kernel(const uint8_t *w, int N,
     uint32_t zero = w4_zero<T>(8), p[4];
     if constexpr (kZeros) zero = w4_zero<T>(__ldg(src + kW4CodeBytes + 128 * kGpb + (gi * 8 + g) * 8 + 4 * pair + i), 0);
     w4_unpack<T>(word[i], zero, p);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) p[j] = mul2<T>(p[j], power_of_two2<T>(W4Scale<T>::kRest));  // in two steps: 2^kStep is out of the type's range
     if (row < N && k < K) *reinterpret_cast<uint4 *>(out + static_cast<int64_t>(row) * K + k) = make_uint4(p[0], p[1], p[2], p[3]);
   }
   if (tid < 64 * kGpb) {
@@ -47,7 +45,8 @@ cudaError_t expand_as(const W4Args &a, int group, bool zeros, uint16_t *out, flo
 }
 
 template <class T>
-cudaError_t gemm_as(const CUtensorMap &w, const CUtensorMap &x, const CUtensorMap &y, const TileArgs &args, int group, int cols, cudaStream_t s) {
+cudaError_t gemm_as(const CUtensorMap &w, const CUtensorMap &x, const CUtensorMap &y, TileArgs args, int group, int cols, cudaStream_t s) {
+  args.factor = static_cast<float>(1 << W4Scale<T>::kRest);
   if (group == 128) return launch_tile_gemm_as<TileOp::kW4, T, 128>(w, w, x, x, y, x, args, cols, s);
   if (group == 64) return launch_tile_gemm_as<TileOp::kW4, T, 64>(w, w, x, x, y, x, args, cols, s);
   return launch_tile_gemm_as<TileOp::kW4, T, 32>(w, w, x, x, y, x, args, cols, s);

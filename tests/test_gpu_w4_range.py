@@ -163,3 +163,34 @@ def test_fp16_hidden_rows_past_the_range_captured_and_at_once():
     torch.cuda.synchronize()
     assert all(torch.equal(v, wants[0]) for g in got for v in g)
     assert ops.device_error() == (0, 0)
+
+
+@pytest.mark.parametrize("group,zeros", [(32, True), (64, False), (128, True)])
+@pytest.mark.parametrize("M", [1, 9, 16, 40, 128, 1100])
+def test_large_activations(M, group, zeros):
+    """Rows of 2^121, all of one sign, under codes of one sign: a group's sum passes fp32's range, the output, under scales of
+    2^-20, does not."""
+    K, N = 392, 200
+    g = torch.Generator(device=DEV).manual_seed(M)
+    codes = torch.randint(0, 256, (N, K // 2), generator=g, device=DEV, dtype=torch.uint8) | 0xCC
+    scales = ((torch.rand(N, -(-K // group), generator=g, device=DEV) + 0.5) * 2.0 ** -20).to(BF)
+    ck = (codes, scales, torch.zeros(scales.shape, dtype=torch.uint8, device=DEV) if zeros else None)
+    x = torch.full((M, K), 2.0 ** 121, device=DEV, dtype=BF)
+    x[:, ::3] *= 0.5
+    want, err = product(x.to(F64), ck, group)
+    assert (want + err).amax() < torch.finfo(BF).max
+    assert (product(x.to(F64), (codes, torch.ones_like(scales), ck[2]), group)[0].amin() / (K / group)) > 2.0 ** 128 or group == 64
+    check(ops.w4_linear(x, ops.w4_prepare(*ck, group=group)), want, err, BF)
+
+
+@pytest.mark.parametrize("M", [1, 16, 40, 1100])
+def test_smallest_activations(M):
+    """Rows of bf16's smallest values under large scales."""
+    K, N, group = 392, 200, 64
+    g = torch.Generator(device=DEV).manual_seed(M)
+    codes, scales, z = checkpoint(g, (N, K), group, True, BF, DEV)
+    ck = (codes, (scales.float() * 2.0 ** 100).to(BF), z)
+    x = (torch.randint(-200, 201, (M, K), generator=g, device=DEV).float() * 2.0 ** -100 * 2.0 ** -33).to(BF)
+    assert (x != 0).any() and x.abs().max() < 2.0 ** -125
+    want, err = product(x.to(F64), ck, group)
+    check(ops.w4_linear(x, ops.w4_prepare(*ck, group=group)), want, err, BF)
