@@ -24,7 +24,7 @@
 //               of every group of 32, 64 or 128 K (kAct) with its scale.  The operands are swapped, so that
 //               a thread's columns share the one scale of its row of A.  A group of 128 is two K blocks, one of
 //               32 half a block, which the two issuers share.  The output is written across: a lane's row is an
-//               output column.  4096 x 7168 x 7168, groups of 128: 234 us, 1.80 PF/s, tensor pipe 86% busy.
+//               output column.  4096 x 7168 x 7168, groups of 128: 227 us, 1.85 PF/s, tensor pipe 86% busy.
 //   Op::kGated  A = x (M, K), B = rows of Wg (even CTA) and the matching rows of Wu (odd CTA):
 //               the first half of the accumulator's columns is g, the second u of the same outputs.
 //   Op::kGrad   two products in one launch.  dx = dg Wg + du Wu: A = [dg | du] in two segments of K = I,
